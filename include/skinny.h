@@ -319,6 +319,39 @@ SKINNY_API skinny_status skinny_moe_combine_run(int64_t m, int64_t d, int32_t to
                                      const float* weights, const void* shared_rows, const float* gate,
                                      int32_t rows_dtype, void* out, int32_t out_dtype, void* stream);
 
+/* --- 4-bit weights with group scales -------------------------------------- */
+
+/* A 4-bit weight [n][k] in groups of `group` (32, 64 or 128) elements along k:
+ *   weight (j, kk) = scale[j][kk/group] * (code(j, kk) - zero[j][kk/group])
+ * as a real number: no weight is rounded to 16 bits (the block formats Q4_0
+ * and Q2_0 above define theirs as rounded).
+ *   codes   uint8 [n][k/2], two unsigned 4-bit codes per byte, element kk in
+ *           byte kk/2, the low nibble for even kk; 16-byte aligned
+ *   scales  [n][k/group] in the 16-bit type of the rows; 2-byte aligned
+ *   zeros   uint8 [n][k/group], the zero points (0 .. 255; 0 .. 15 in use), or
+ *           NULL: 8 everywhere */
+typedef struct skinny_w4 {
+  const void* codes;
+  const void* scales;
+  const void* zeros;
+} skinny_w4;
+
+/* C[0:m, 0:n] = A[0:m, :] . W for a decode window's rows and a 4-bit grouped
+ * weight, in one launch that reads W once for all rows.  Products are exact
+ * and summed in fp32, the group's scale is applied to its sum; row i of C at
+ * any m equals the m = 1 call on that row bit for bit.
+ *   m        1 <= m <= SKINNY_GEMV_MAX_M
+ *   n, k     1 <= n < 2^31; k a multiple of group, < 2^31
+ *   A        [m][lda] SKINNY_F16 or SKINNY_BF16 (a_dtype); lda >= k a multiple
+ *            of 8 (0: k); 16-byte aligned
+ *   C        [m][ldc] SKINNY_F32, SKINNY_F16 or SKINNY_BF16 (c_dtype, rounded to
+ *            nearest even); ldc >= n (0: n); aligned to its element,
+ *            overlapping no input (else SKINNY_ERR_INVALID_ARG)
+ * All device pointers. */
+SKINNY_API skinny_status skinny_w4_mm_run(int64_t m, int64_t n, int64_t k, int32_t group, const void* A,
+                                          int64_t lda, int32_t a_dtype, const skinny_w4* W, void* C, int64_t ldc,
+                                          int32_t c_dtype, void* stream);
+
 /* Human-readable description of what a run with this m would launch: path,
  * tile or GEMV split, grid.  Writes a NUL-terminated string (truncated to
  * len). */

@@ -50,7 +50,7 @@ EXPORTS = (
     "skinny_mm_plan_info",
     "skinny_gemm_tile_count",
     "skinny_gemm_tile_name", "skinny_status_string", "skinny_abi_version", "skinny_cast_f32_bf16_run",
-    "skinny_moe_combine_run", "skinny_mm_run_static",
+    "skinny_moe_combine_run", "skinny_mm_run_static", "skinny_w4_mm_run",
 )
 STATIC_SCRATCH_BYTES = 32 << 20
 STATIC_COUNTER_BYTES = 1 << 20
@@ -71,6 +71,10 @@ class MMDesc(ctypes.Structure):
         ("tile_id", ctypes.c_int32),
         ("num_cus", ctypes.c_int32),
     ]
+
+
+class W4Desc(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("zeros", ctypes.c_void_p)]
 
 
 _vp, _i64, _i32, _sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
@@ -96,6 +100,8 @@ _lib.skinny_cast_f32_bf16_run.argtypes = [_i64, _vp, _vp, _vp]
 _lib.skinny_cast_f32_bf16_run.restype = ctypes.c_int
 _lib.skinny_moe_combine_run.argtypes = [_i64, _i64, _i32, _vp, _vp, _vp, _vp, _i32, _vp, _i32, _vp]
 _lib.skinny_moe_combine_run.restype = ctypes.c_int
+_lib.skinny_w4_mm_run.argtypes = [_i64, _i64, _i64, _i32, _vp, _i64, _i32, _vp, _vp, _i64, _i32, _vp]
+_lib.skinny_w4_mm_run.restype = ctypes.c_int
 _lib.skinny_mm_plan_info.argtypes = [_vp, _i64, ctypes.c_char_p, _sz]
 _lib.skinny_mm_plan_info.restype = ctypes.c_int
 _lib.skinny_gemm_tile_count.argtypes = []
@@ -420,4 +426,79 @@ def gate(A, W, max_m=None, out=None, stream=None):
     plan = get_plan(n, k, max_m or m, _dtype_code(A.dtype, "A"), _dtype_code(W.dtype, "W"),
                     _dtype_code(out.dtype, "C"), EPILOGUE_SIGMOID)
     plan.run(m, A, W, out, stream=stream)
+    return out
+
+
+class W4:
+    """A 4-bit grouped weight [n][k] (or a stack [e][n][k]): packed codes uint8
+    [n][k/2] (element kk in byte kk/2, the low nibble for even kk), scales
+    [n][k/g] in the rows' 16-bit type for groups of g = 32, 64 or 128 along k,
+    and zero points uint8 [n][k/g] (None: 8 everywhere);
+    weight = scale * (code - zero).  Checked once, here; the tensors are kept
+    alive and read at every call."""
+
+    __slots__ = ("codes", "scales", "zeros", "shape", "group", "dtype", "device", "_desc", "_addr")
+
+    def __init__(self, codes, scales, zeros=None):
+        if codes.dtype != torch.uint8 or scales.dtype not in (torch.float16, torch.bfloat16) or \
+                (zeros is not None and zeros.dtype != torch.uint8):
+            raise TypeError("W4: uint8 codes, float16 or bfloat16 scales, uint8 zero points (or None)")
+        if codes.dim() < 2 or scales.dim() != codes.dim() or codes.shape[:-1] != scales.shape[:-1]:
+            raise ValueError(f"W4: scales {tuple(scales.shape)} do not fit codes {tuple(codes.shape)}")
+        k, groups = 2 * codes.shape[-1], scales.shape[-1]
+        if groups < 1 or k % groups or k // groups not in (32, 64, 128):
+            raise ValueError(f"W4: {groups} scales for {k} elements: groups of 32, 64 or 128 are taken")
+        if zeros is not None and zeros.shape != scales.shape:
+            raise ValueError(f"W4: zero points {tuple(zeros.shape)} do not fit scales {tuple(scales.shape)}")
+        _dense("W4", codes=codes, scales=scales, zeros=zeros)
+        _on("W4", codes.device, scales, zeros)
+        self.codes, self.scales, self.zeros = codes, scales, zeros
+        self.shape, self.group = (*codes.shape[:-1], k), k // groups
+        self.dtype, self.device = scales.dtype, codes.device
+        self._desc = W4Desc(codes.data_ptr(), scales.data_ptr(), 0 if zeros is None else zeros.data_ptr())
+        self._addr = ctypes.addressof(self._desc)
+
+
+def _on(where, device, *tensors):
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError(f"{where}: every tensor must be on {device}, got one on {t.device}")
+
+
+def _rows(where, name, t):
+    """Row stride of a matrix whose rows are dense (a single row has any)."""
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{where}: {name} must be a matrix with contiguous rows")
+    return t.stride(0) if t.shape[0] > 1 else 0
+
+
+def _stream_of(device, stream):
+    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+
+
+def mm_w4(A, W, out=None, out_dtype=None, stream=None):
+    """C = A . W for A [m][k] (m <= 16, float16 or bfloat16, dense rows of any
+    stride that is a multiple of 8) and a 4-bit grouped weight W (a W4 whose
+    scales have A's type), in one launch; C is float32 unless `out` or
+    `out_dtype` says otherwise."""
+    lda = _rows("mm_w4", "A", A)
+    m, k = A.shape
+    if not isinstance(W, W4) or W.dtype != A.dtype:
+        raise TypeError(f"mm_w4: the weight must be a W4 with scales of A's type ({A.dtype})")
+    if len(W.shape) != 2 or W.shape[1] != k:
+        raise ValueError(f"mm_w4: a weight {W.shape} does not fit k = {k}")
+    n, device = W.shape[0], A.device
+    if W.device != device:
+        raise ValueError(f"mm_w4: A is on {device}, the weight on {W.device}")
+    if out is None:
+        out = torch.empty((m, n), dtype=out_dtype or torch.float32, device=device)
+        ldc = n
+    else:
+        ldc = _rows("mm_w4", "out", out)
+        if tuple(out.shape) != (m, n):
+            raise ValueError("mm_w4: out must be [m][n]")
+        _on("mm_w4", device, out)
+    _check(_lib.skinny_w4_mm_run(m, n, k, W.group, A.data_ptr(), lda, _dtype_code(A.dtype, "A"), W._addr,
+                                 out.data_ptr(), ldc, _dtype_code(out.dtype, "C"), _stream_of(device, stream)),
+           "skinny_w4_mm_run")
     return out

@@ -152,6 +152,28 @@ bool gemm_tile_foldable(int tile_id);
 hipError_t launch_splitk_reduce(const GemmArgs& args, int c_kind, hipStream_t stream);
 
 // ---------------------------------------------------------------------------
+// 4-bit grouped weights (w4.hip, moe.hip): codes [n][k/2] (element kk in byte
+// kk/2, the low nibble for even kk), scales [n][k/group] in the rows' type,
+// zero points uint8 [n][k/group] or null (8): W = s * (q - z)
+// ---------------------------------------------------------------------------
+struct W4Args {
+  const void* A;       // [m][lda] f16/bf16
+  int64_t lda;
+  const void* codes;
+  const void* scales;
+  const void* zeros;
+  int64_t n;
+  int64_t k;
+  void* C;             // [m][ldc]
+  int64_t ldc;
+  int32_t m;           // <= kGemvMaxM
+  int32_t c_kind;      // CK_*
+};
+
+// a_kind: CK_F16 or CK_BF16; group 32, 64 or 128
+hipError_t launch_w4_mm(const W4Args& args, int a_kind, int group, hipStream_t stream);
+
+// ---------------------------------------------------------------------------
 // The library's own scratch for skinny_mm_run_static: one file-scope device
 // array per GPU (static_scratch.hip), [counters: kStaticCounterBytes]
 // [data: the rest].  static_scratch() returns the current device's address of
