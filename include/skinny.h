@@ -96,7 +96,8 @@ typedef enum skinny_dtype {
   SKINNY_F32 = 3,
   SKINNY_Q8_0 = 4,
   SKINNY_Q4_0 = 5,
-  SKINNY_Q2_0 = 6
+  SKINNY_Q2_0 = 6,
+  SKINNY_W4 = 7 /* 4-bit grouped weights (skinny_w4; skinny_w4_mm_run and the MoE layer) */
 } skinny_dtype;
 
 /* desc.flags */
@@ -351,6 +352,93 @@ typedef struct skinny_w4 {
 SKINNY_API skinny_status skinny_w4_mm_run(int64_t m, int64_t n, int64_t k, int32_t group, const void* A,
                                           int64_t lda, int32_t a_dtype, const skinny_w4* W, void* C, int64_t ldc,
                                           int32_t c_dtype, void* stream);
+
+/* --- A whole mixture-of-experts layer for a decode window ------------------ */
+
+/* For each of m <= SKINNY_GEMV_MAX_M tokens x_t, with the router's weight
+ * Wr [experts][d], experts of inner length `inter` and an optional shared
+ * expert of inner length `shared_inter` behind a scalar gate:
+ *   l_t   = Wr x_t                              fp32 logits
+ *   S_t   = the topk largest of l_t (equal values by lower expert first)
+ *   p_te  = exp(l_te) / sum of exp(l_t.) over S_t (SKINNY_MOE_RENORM) or over
+ *           all experts
+ *   f_e(x) = Wd_e (silu(Wg_e x) * (Wu_e x)),    silu(v) = v / (1 + e^-v)
+ *   out_t = sum over e in S_t of p_te f_e(x_t)
+ *           + sigmoid(wg . x_t) f_shared(x_t)   (when shared_inter > 0)
+ * Products are summed in fp32; the inner values are carried in 22 bits (f16
+ * layers) or 24 (bf16 layers), the output rounded once (nearest even).  The
+ * distinct experts' weights are read once per window.  A token's output is
+ * the same bits at every m and beside any other tokens.
+ * In an f16 layer inner values past f16's range (65504) become infinite.
+ *   struct_size   sizeof(skinny_moe_desc)
+ *   dtype         SKINNY_F16 or SKINNY_BF16: x, the router, the gate's weight, the
+ *                 scales, and the weights unless they are 4-bit
+ *   w_dtype       the experts' and the shared expert's weights: dtype, or
+ *                 SKINNY_W4 with groups of `group` (32, 64 or 128; else 0)
+ *   out_dtype     SKINNY_F32, SKINNY_F16 or SKINNY_BF16
+ *   max_m         1 .. SKINNY_GEMV_MAX_M
+ *   d, inter, shared_inter   multiples of 32 (and of group), up to 2^20;
+ *                 shared_inter 0: no shared expert
+ *   experts       topk .. SKINNY_MOE_MAX_EXPERTS; topk 1 .. SKINNY_TOPK_MAX
+ *   ldx, ldo      row strides of x and out in elements, 0: d; ldx a multiple of 8
+ *   flags         SKINNY_MOE_RENORM or 0
+ *   num_cus       as in skinny_mm_desc */
+#define SKINNY_MOE_RENORM 0x1u
+#define SKINNY_MOE_MAX_EXPERTS 1024
+
+typedef struct skinny_moe_desc {
+  uint32_t struct_size;
+  int32_t dtype;
+  int32_t w_dtype;
+  int32_t out_dtype;
+  int32_t group;
+  int32_t topk;
+  int64_t max_m;
+  int64_t d;
+  int64_t inter;
+  int64_t shared_inter;
+  int64_t experts;
+  int64_t ldx;
+  int64_t ldo;
+  uint32_t flags;
+  int32_t num_cus;
+} skinny_moe_desc;
+
+/* Device pointers, 16-byte aligned (scales 2-byte; zeros any).  A 16-bit
+ * weight is given in `codes`, with scales and zeros NULL.
+ *   router       [experts][d]
+ *   w13          [experts][2 inter][d]: expert e's gate rows, then its up rows
+ *   w2           [experts][d][inter]
+ *   shared13, shared2   [2 shared_inter][d], [d][shared_inter] (or all NULL)
+ *   shared_gate  [d] (or NULL) */
+typedef struct skinny_moe_weights {
+  const void* router;
+  skinny_w4 w13;
+  skinny_w4 w2;
+  skinny_w4 shared13;
+  skinny_w4 shared2;
+  const void* shared_gate;
+} skinny_moe_weights;
+
+typedef struct skinny_moe_plan skinny_moe_plan;
+
+/* Validate `desc` and build a plan (host memory only, immutable). */
+SKINNY_API skinny_status skinny_moe_plan_create(const skinny_moe_desc* desc, skinny_moe_plan** out_plan);
+SKINNY_API void skinny_moe_plan_destroy(skinny_moe_plan* plan);
+
+/* Bytes of device workspace every run of this plan needs: 16-byte aligned,
+ * zero-filled once before its first use; a completed run leaves it ready for
+ * the next.  Two runs in flight at once must not share one. */
+SKINNY_API skinny_status skinny_moe_workspace_size(const skinny_moe_plan* plan, size_t* bytes);
+
+/* Enqueue the layer for m tokens (1 <= m <= max_m).
+ *   x            [m][ldx], 16-byte aligned
+ *   out          [m][ldo], aligned to its element, not overlapping x
+ *   topk_idx     int32 [m][topk], topk_weight f32 [m][topk]: S_t and p_te, the
+ *                largest logit first; 4-byte aligned; either may be NULL */
+SKINNY_API skinny_status skinny_moe_run(const skinny_moe_plan* plan, int64_t m, const void* x,
+                                        const skinny_moe_weights* weights, void* out, int32_t* topk_idx,
+                                        float* topk_weight, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Human-readable description of what a run with this m would launch: path,
  * tile or GEMV split, grid.  Writes a NUL-terminated string (truncated to

@@ -36,6 +36,7 @@ _lib = ctypes.CDLL(LIB_PATH)
 # --- C ABI mirror -----------------------------------------------------------
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_ALIGNMENT, ERR_SHAPE, ERR_HIP, ERR_WORKSPACE, ERR_SCRATCH = range(8)
 F16, BF16, F32, Q8_0, Q4_0, Q2_0 = 1, 2, 3, 4, 5, 6
+DTYPE_W4 = 7
 # stored codes per byte of the block-quantised weight kinds
 CODES_PER_BYTE = {Q8_0: 1, Q4_0: 2, Q2_0: 4}
 FORCE_GEMV, FORCE_GEMM, GEMM_SPLIT_LAUNCH, GEMM_ONE_LAUNCH = 0x1, 0x2, 0x4, 0x8
@@ -43,6 +44,8 @@ EPILOGUE_SIGMOID = 0x10
 GEMM_FOLD_LAUNCH = 0x20
 GEMV_MAX_M = 16
 TOPK_MAX = 32
+MOE_RENORM = 0x1
+MOE_MAX_EXPERTS = 1024
 
 EXPORTS = (
     "skinny_mm_plan", "skinny_mm_plan_destroy", "skinny_mm_workspace_size", "skinny_mm_run",
@@ -51,6 +54,7 @@ EXPORTS = (
     "skinny_gemm_tile_count",
     "skinny_gemm_tile_name", "skinny_status_string", "skinny_abi_version", "skinny_cast_f32_bf16_run",
     "skinny_moe_combine_run", "skinny_mm_run_static", "skinny_w4_mm_run",
+    "skinny_moe_plan_create", "skinny_moe_plan_destroy", "skinny_moe_workspace_size", "skinny_moe_run",
 )
 STATIC_SCRATCH_BYTES = 32 << 20
 STATIC_COUNTER_BYTES = 1 << 20
@@ -75,6 +79,31 @@ class MMDesc(ctypes.Structure):
 
 class W4Desc(ctypes.Structure):
     _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("zeros", ctypes.c_void_p)]
+
+
+class MoEDesc(ctypes.Structure):
+    _fields_ = [
+        ("struct_size", ctypes.c_uint32),
+        ("dtype", ctypes.c_int32),
+        ("w_dtype", ctypes.c_int32),
+        ("out_dtype", ctypes.c_int32),
+        ("group", ctypes.c_int32),
+        ("topk", ctypes.c_int32),
+        ("max_m", ctypes.c_int64),
+        ("d", ctypes.c_int64),
+        ("inter", ctypes.c_int64),
+        ("shared_inter", ctypes.c_int64),
+        ("experts", ctypes.c_int64),
+        ("ldx", ctypes.c_int64),
+        ("ldo", ctypes.c_int64),
+        ("flags", ctypes.c_uint32),
+        ("num_cus", ctypes.c_int32),
+    ]
+
+
+class MoEWeightsDesc(ctypes.Structure):
+    _fields_ = [("router", ctypes.c_void_p), ("w13", W4Desc), ("w2", W4Desc), ("shared13", W4Desc),
+                ("shared2", W4Desc), ("shared_gate", ctypes.c_void_p)]
 
 
 _vp, _i64, _i32, _sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
@@ -102,6 +131,14 @@ _lib.skinny_moe_combine_run.argtypes = [_i64, _i64, _i32, _vp, _vp, _vp, _vp, _i
 _lib.skinny_moe_combine_run.restype = ctypes.c_int
 _lib.skinny_w4_mm_run.argtypes = [_i64, _i64, _i64, _i32, _vp, _i64, _i32, _vp, _vp, _i64, _i32, _vp]
 _lib.skinny_w4_mm_run.restype = ctypes.c_int
+_lib.skinny_moe_plan_create.argtypes = [ctypes.POINTER(MoEDesc), ctypes.POINTER(_vp)]
+_lib.skinny_moe_plan_create.restype = ctypes.c_int
+_lib.skinny_moe_plan_destroy.argtypes = [_vp]
+_lib.skinny_moe_plan_destroy.restype = None
+_lib.skinny_moe_workspace_size.argtypes = [_vp, ctypes.POINTER(_sz)]
+_lib.skinny_moe_workspace_size.restype = ctypes.c_int
+_lib.skinny_moe_run.argtypes = [_vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]
+_lib.skinny_moe_run.restype = ctypes.c_int
 _lib.skinny_mm_plan_info.argtypes = [_vp, _i64, ctypes.c_char_p, _sz]
 _lib.skinny_mm_plan_info.restype = ctypes.c_int
 _lib.skinny_gemm_tile_count.argtypes = []
@@ -502,3 +539,119 @@ def mm_w4(A, W, out=None, out_dtype=None, stream=None):
                                  out.data_ptr(), ldc, _dtype_code(out.dtype, "C"), _stream_of(device, stream)),
            "skinny_w4_mm_run")
     return out
+
+
+class MoELayer:
+    """A whole mixture-of-experts layer for decode windows of up to max_m <= 16
+    tokens: router, top-k and softmax (renormalised over the top-k when
+    `renorm`), the routed experts' gated products silu(gate) * up, the optional
+    shared expert behind sigmoid(x . shared_gate), and the weighted sum.
+
+        layer = MoELayer(router, w13, w2, topk=10)
+        out = layer(x)                               # x [m][d] -> out [m][d]
+
+    router [experts][d] float16 or bfloat16; w13 [experts][2 inter][d] (each
+    expert's gate rows, then its up rows) and w2 [experts][d][inter], tensors
+    of the router's type or both W4 of one group length; shared13
+    [2 shared_inter][d] and shared2 [d][shared_inter] likewise, with
+    shared_gate [d].  x is contiguous and has the router's type; out has
+    out_dtype (x's type by default)."""
+
+    def __init__(self, router, w13, w2, topk, renorm=True, out_dtype=None, max_m=16, shared13=None, shared2=None,
+                 shared_gate=None, num_cus=0):
+        if router.dim() != 2 or router.dtype not in (torch.float16, torch.bfloat16):
+            raise TypeError("MoELayer: router must be a float16 or bfloat16 matrix [experts][d]")
+        experts, d = router.shape
+        dtype, device = router.dtype, router.device
+        w4 = isinstance(w13, W4)
+        if len(w13.shape) != 3 or w13.shape[1] % 2:
+            raise ValueError("MoELayer: w13 must be [experts][2 inter][d]")
+        inter = w13.shape[1] // 2
+        shared = [t is not None for t in (shared13, shared2, shared_gate)]
+        if any(shared) != all(shared):
+            raise ValueError("MoELayer: shared13, shared2 and shared_gate go together")
+        shared_inter = 0
+        if all(shared):
+            if len(shared13.shape) != 2 or shared13.shape[0] % 2 or shared13.shape[0] < 2:
+                raise ValueError("MoELayer: shared13 must be [2 shared_inter][d]")
+            shared_inter = shared13.shape[0] // 2
+            if tuple(shared_gate.shape) != (d,) or shared_gate.dtype != dtype:
+                raise ValueError("MoELayer: shared_gate must be [d] of the router's type")
+        group = w13.group if w4 else 0
+        descs = []
+        for name, w, shape in (("w13", w13, (experts, 2 * inter, d)), ("w2", w2, (experts, d, inter)),
+                               ("shared13", shared13, (2 * shared_inter, d)), ("shared2", shared2, (d, shared_inter))):
+            if w is None:
+                descs.append(W4Desc())
+                continue
+            if isinstance(w, W4) != w4 or w.dtype != dtype or (w4 and w.group != group):
+                raise TypeError(f"MoELayer: {name} must be a weight of the router's type, like the others")
+            if tuple(w.shape) != shape:
+                raise ValueError(f"MoELayer: {name} is {tuple(w.shape)}, not {shape}")
+            if not w4:
+                _dense("MoELayer", **{name: w})
+            _on("MoELayer", device, w)
+            descs.append(W4Desc(w._desc.codes, w._desc.scales, w._desc.zeros) if w4 else W4Desc(w.data_ptr()))
+        _dense("MoELayer", router=router, shared_gate=shared_gate)
+        _on("MoELayer", device, shared_gate)
+        self._keep = (router, w13, w2, shared13, shared2, shared_gate)
+        self.experts, self.d, self.inter, self.shared_inter, self.topk = experts, d, inter, shared_inter, topk
+        self.dtype, self.device, self.max_m = dtype, device, max_m
+        self.out_dtype = out_dtype or dtype
+        self._weights = MoEWeightsDesc(router.data_ptr(), *descs, shared_gate.data_ptr() if shared_inter else None)
+        code = _dtype_code(dtype, "router")
+        desc = MoEDesc(ctypes.sizeof(MoEDesc), code, DTYPE_W4 if w4 else code, _dtype_code(self.out_dtype, "out"), group,
+                       topk, max_m, d, inter, shared_inter, experts, 0, 0, MOE_RENORM if renorm else 0, num_cus)
+        self._h = None
+        h = ctypes.c_void_p()
+        _check(_lib.skinny_moe_plan_create(ctypes.byref(desc), ctypes.byref(h)), "skinny_moe_plan_create")
+        self._h = h
+        sz = ctypes.c_size_t()
+        _check(_lib.skinny_moe_workspace_size(h, ctypes.byref(sz)), "skinny_moe_workspace_size")
+        self.workspace_bytes = int(sz.value)
+        self._ws = {}
+
+    def workspace(self, stream=None):
+        """This layer's workspace for a stream (runs on different streams may be
+        in flight at once, so each has its own), allocated and zero-filled on it."""
+        if stream is None:
+            stream = torch.cuda.current_stream(self.device)
+        key = stream.cuda_stream
+        ws = self._ws.get(key)
+        if ws is None:
+            with torch.cuda.stream(stream):
+                ws = torch.zeros(self.workspace_bytes, dtype=torch.uint8, device=self.device)
+            self._ws[key] = ws
+        return ws
+
+    def __call__(self, x, out=None, topk_idx=None, topk_weight=None, stream=None):
+        """out [m][d]; topk_idx (int32 [m][topk]) and topk_weight (float32
+        [m][topk]) receive the routing when given."""
+        if x.dim() != 2 or x.shape[1] != self.d or x.dtype != self.dtype:
+            raise ValueError(f"MoELayer: x must be [m][{self.d}] of type {self.dtype}")
+        m = x.shape[0]
+        if out is None:
+            out = torch.empty((m, self.d), dtype=self.out_dtype, device=self.device)
+        elif tuple(out.shape) != (m, self.d) or out.dtype != self.out_dtype:
+            raise ValueError(f"MoELayer: out must be [{m}][{self.d}] of type {self.out_dtype}")
+        for name, t, dt in (("topk_idx", topk_idx, torch.int32), ("topk_weight", topk_weight, torch.float32)):
+            if t is not None and (tuple(t.shape) != (m, self.topk) or t.dtype != dt):
+                raise ValueError(f"MoELayer: {name} must be {dt} [{m}][{self.topk}]")
+        _dense("MoELayer", x=x, out=out, topk_idx=topk_idx, topk_weight=topk_weight)
+        _on("MoELayer", self.device, x, out, topk_idx, topk_weight)
+        if stream is None:
+            stream = torch.cuda.current_stream(self.device)
+        ws = self.workspace(stream)
+        _check(_lib.skinny_moe_run(self._h, m, x.data_ptr(), ctypes.addressof(self._weights), out.data_ptr(),
+                                   _ptr(topk_idx), _ptr(topk_weight), ws.data_ptr(), self.workspace_bytes,
+                                   stream.cuda_stream), "skinny_moe_run")
+        return out
+
+    def __del__(self):
+        h = getattr(self, "_h", None)
+        if h is not None and h.value and _lib is not None:
+            try:
+                _lib.skinny_moe_plan_destroy(h)
+            except Exception:  # interpreter shutdown
+                pass
+            self._h = None

@@ -1,7 +1,10 @@
 // abi_window.cpp -- the C ABI of the decode window's further operators
-// declared in include/skinny.h (4-bit grouped GEMV): argument validation, all
-// on the host and before any HIP call, and dispatch to the kernels in w4.hip.
+// declared in include/skinny.h (4-bit grouped GEMV, the MoE layer): argument
+// validation, all on the host and before any HIP call, and dispatch to the
+// kernels in w4.hip and moe.hip.
 #include <hip/hip_runtime_api.h>
+
+#include <new>
 
 #include "internal.h"
 #include "skinny.h"
@@ -32,7 +35,20 @@ bool group_ok(int32_t group) { return group == 32 || group == 64 || group == 128
 // bytes from the first element of row 0 to the last of row rows - 1
 int64_t span(int64_t rows, int64_t ld, int64_t len, int64_t size) { return ((rows - 1) * ld + len) * size; }
 
+int64_t round256(int64_t b) { return (b + 255) / 256 * 256; }
+
 }  // namespace
+
+static_assert(SKINNY_MOE_MAX_EXPERTS == kMoeMaxExperts, "expert limit");
+
+struct skinny_moe_plan {
+  skinny_moe_desc d;      // normalised copy (ldx / ldo filled in)
+  skinny_plan* router;    // the logits' GEMV
+  int64_t max_slots;      // distinct experts a window can reach
+  // workspace regions, in bytes from its start
+  int64_t router_ws;      // the router plan's own workspace comes first (its counters start at zero)
+  int64_t logits, nslots, slots, slot_w, h, bytes;
+};
 
 extern "C" {
 
@@ -67,6 +83,140 @@ skinny_status skinny_w4_mm_run(int64_t m, int64_t n, int64_t k, int32_t group, c
   g.m = (int32_t)m;
   g.c_kind = kind_of(c_dtype);
   return hip_status(launch_w4_mm(g, kind_of(a_dtype), group, (hipStream_t)stream));
+}
+
+skinny_status skinny_moe_plan_create(const skinny_moe_desc* desc, skinny_moe_plan** out_plan) {
+  if (desc == nullptr || out_plan == nullptr || desc->struct_size < sizeof(skinny_moe_desc))
+    return SKINNY_ERR_INVALID_ARG;
+  skinny_moe_desc d = *desc;
+  if (!half_type(d.dtype) || !float_type(d.out_dtype) || (d.w_dtype != d.dtype && d.w_dtype != SKINNY_W4) ||
+      (d.flags & ~SKINNY_MOE_RENORM) != 0)
+    return SKINNY_ERR_UNSUPPORTED;
+  if (d.w_dtype == SKINNY_W4 ? !group_ok(d.group) : d.group != 0) return SKINNY_ERR_UNSUPPORTED;
+  constexpr int64_t kMax = 1 << 20;
+  if (d.max_m < 1 || d.max_m > SKINNY_GEMV_MAX_M || d.topk < 1 || d.topk > SKINNY_TOPK_MAX || d.experts < d.topk ||
+      d.experts > SKINNY_MOE_MAX_EXPERTS || d.d < 1 || d.d > kMax || d.inter < 1 || d.inter > kMax ||
+      d.shared_inter < 0 || d.shared_inter > kMax || d.num_cus < 0)
+    return SKINNY_ERR_INVALID_ARG;
+  if (d.ldx == 0) d.ldx = d.d;
+  if (d.ldo == 0) d.ldo = d.d;
+  if (d.ldx > (1LL << 40) || d.ldo > (1LL << 40)) return SKINNY_ERR_INVALID_ARG;
+  const int64_t unit = d.group > 32 ? d.group : 32;
+  if (d.d % unit != 0 || d.inter % unit != 0 || d.shared_inter % unit != 0 || d.ldx < d.d || d.ldo < d.d)
+    return SKINNY_ERR_SHAPE;
+  if (d.ldx % 8 != 0) return SKINNY_ERR_ALIGNMENT;
+
+  skinny_mm_desc r{};
+  r.struct_size = sizeof(r);
+  r.a_dtype = d.dtype;
+  r.w_dtype = d.dtype;
+  r.c_dtype = SKINNY_F32;
+  r.max_m = d.max_m;
+  r.n = d.experts;
+  r.k = d.d;
+  r.lda = d.ldx;
+  r.tile_id = -1;
+  r.num_cus = d.num_cus;
+  skinny_plan* router = nullptr;
+  skinny_status st = skinny_mm_plan(&r, &router);
+  if (st != SKINNY_OK) return st;
+  size_t rws = 0;
+  skinny_mm_workspace_size(router, &rws);
+  skinny_moe_plan* p = new (std::nothrow) skinny_moe_plan;
+  if (p == nullptr) {
+    skinny_mm_plan_destroy(router);
+    return SKINNY_ERR_INVALID_ARG;
+  }
+  p->d = d;
+  p->router = router;
+  p->max_slots = d.max_m * d.topk < d.experts ? d.max_m * d.topk : d.experts;
+  const int64_t planes = moe_planes(kind_of(d.dtype));
+  int64_t at = 0;
+  auto region = [&at](int64_t bytes) {
+    const int64_t start = at;
+    at += round256(bytes);
+    return start;
+  };
+  p->router_ws = (int64_t)rws;
+  region(p->router_ws);
+  p->logits = region(d.max_m * d.experts * 4);
+  p->nslots = region(4);
+  p->slots = region(p->max_slots * 4);
+  p->slot_w = region((p->max_slots + 1) * kGemvMaxM * 4);
+  p->h = region((p->max_slots * d.inter + d.shared_inter) * kGemvMaxM * planes * 2);
+  p->bytes = at;
+  *out_plan = p;
+  return SKINNY_OK;
+}
+
+void skinny_moe_plan_destroy(skinny_moe_plan* plan) {
+  if (plan != nullptr) skinny_mm_plan_destroy(plan->router);
+  delete plan;
+}
+
+skinny_status skinny_moe_workspace_size(const skinny_moe_plan* plan, size_t* bytes) {
+  if (plan == nullptr || bytes == nullptr) return SKINNY_ERR_INVALID_ARG;
+  *bytes = (size_t)plan->bytes;
+  return SKINNY_OK;
+}
+
+skinny_status skinny_moe_run(const skinny_moe_plan* plan, int64_t m, const void* x, const skinny_moe_weights* weights,
+                             void* out, int32_t* topk_idx, float* topk_weight, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+  if (plan == nullptr || x == nullptr || weights == nullptr || out == nullptr) return SKINNY_ERR_INVALID_ARG;
+  const skinny_moe_desc& d = plan->d;
+  if (m < 1 || m > d.max_m) return SKINNY_ERR_INVALID_ARG;
+  const bool w4 = d.w_dtype == SKINNY_W4, shared = d.shared_inter > 0;
+  const skinny_w4* ws[4] = {&weights->w13, &weights->w2, &weights->shared13, &weights->shared2};
+  for (int i = 0; i < 4; ++i) {
+    const bool used = i < 2 || shared;
+    if (used ? ws[i]->codes == nullptr || (ws[i]->scales != nullptr) != w4 || (!w4 && ws[i]->zeros != nullptr)
+             : ws[i]->codes != nullptr || ws[i]->scales != nullptr || ws[i]->zeros != nullptr)
+      return SKINNY_ERR_INVALID_ARG;
+  }
+  if (weights->router == nullptr || (weights->shared_gate != nullptr) != shared) return SKINNY_ERR_INVALID_ARG;
+  for (int i = 0; i < 4; ++i)
+    if (!aligned(ws[i]->codes, 16) || !aligned(ws[i]->scales, 2)) return SKINNY_ERR_ALIGNMENT;
+  if (!aligned(x, 16) || !aligned(weights->router, 16) || !aligned(weights->shared_gate, 16) ||
+      !aligned(out, (uintptr_t)size_of(d.out_dtype)) || !aligned(topk_idx, 4) || !aligned(topk_weight, 4))
+    return SKINNY_ERR_ALIGNMENT;
+  if (overlap(out, span(m, d.ldo, d.d, size_of(d.out_dtype)), x, span(m, d.ldx, d.d, 2))) return SKINNY_ERR_INVALID_ARG;
+  if (workspace == nullptr || workspace_bytes < (size_t)plan->bytes) return SKINNY_ERR_WORKSPACE;
+  if (!aligned(workspace, 16)) return SKINNY_ERR_ALIGNMENT;
+
+  char* base = (char*)workspace;
+  float* logits = (float*)(base + plan->logits);
+  const skinny_status st = skinny_mm_run(plan->router, m, x, weights->router, nullptr, logits,
+                                         plan->router_ws > 0 ? base : nullptr, (size_t)plan->router_ws, stream);
+  if (st != SKINNY_OK) return st;
+  auto weight = [](const skinny_w4& w) { return MoeWeight{w.codes, w.scales, w.zeros}; };
+  MoeArgs a;
+  a.x = x;
+  a.ldx = d.ldx;
+  a.d = d.d;
+  a.inter = d.inter;
+  a.shared_inter = d.shared_inter;
+  a.w13 = weight(weights->w13);
+  a.w2 = weight(weights->w2);
+  a.s13 = weight(weights->shared13);
+  a.s2 = weight(weights->shared2);
+  a.shared_gate = weights->shared_gate;
+  a.logits = logits;
+  a.slots = (uint32_t*)(base + plan->slots);
+  a.nslots = (int32_t*)(base + plan->nslots);
+  a.slot_w = (float*)(base + plan->slot_w);
+  a.h = (uint16_t*)(base + plan->h);
+  a.topk_idx = topk_idx;
+  a.topk_weight = topk_weight;
+  a.out = out;
+  a.ldo = d.ldo;
+  a.m = (int32_t)m;
+  a.experts = (int32_t)d.experts;
+  a.topk = d.topk;
+  a.renorm = (d.flags & SKINNY_MOE_RENORM) != 0;
+  a.max_slots = (int32_t)plan->max_slots;
+  a.out_kind = kind_of(d.out_dtype);
+  return hip_status(launch_moe(a, kind_of(d.dtype), d.group, (hipStream_t)stream));
 }
 
 }  // extern "C"

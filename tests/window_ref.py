@@ -56,3 +56,91 @@ def w4_mm(a, w, kind):
     q, s, z = w4_parts(w, kind)
     A = f64(a, kind)
     return A @ (s * (q - z)).T, np.abs(A) @ (np.abs(s) * (32.0 + q + z)).T
+
+
+def _sigmoid(v):
+    return 1.0 / (1.0 + np.exp(-v))
+
+
+def _mm(a, w, kind, mag_w=None):
+    """a [m][k] (64 bits) . w [n][k]^T with the magnitudes that fp32 sums pass
+    through; w is (codes, scales, zeros) or bits."""
+    if isinstance(w, tuple):
+        q, s, z = w4_parts(w, kind)
+        return a @ (s * (q - z)).T, np.abs(a) @ (np.abs(s) * (32.0 + q + z)).T
+    W = f64(w, kind)
+    return a @ W.T, np.abs(a) @ np.abs(W).T
+
+
+def pick(w, e):
+    return tuple(None if t is None else t[e] for t in w) if isinstance(w, tuple) else w[e]
+
+
+EPS = 2.0 ** -24
+
+
+def _adds(k, w):
+    """Additions that follow one another on a path of a sum over k, at most."""
+    if isinstance(w, tuple):
+        g = 2 * w[0].shape[-1] // w[1].shape[-1]
+        return g + k // g + 12
+    return k + 16
+
+
+def _ffn(x, ex, w13, w2, p, ep, kind):
+    """p * f(x) of one row in 64 bits, and a bound on the error of the same in
+    fp32 sums, given x's error bound ex (0) and p's relative error ep:
+    |silu'| <= 1.1; silu, the product and the planes round by at most
+    16 * 2^-24 together."""
+    d = x.shape[1]
+    y, mag = _mm(x, w13, kind)
+    ey = _adds(d, w13) * EPS * mag
+    n = y.shape[1] // 2
+    g, u, eg, eu = y[:, :n], y[:, n:], ey[:, :n], ey[:, n:]
+    s = g * _sigmoid(g)
+    h = s * u * p
+    eh = p * (1.1 * eg * (np.abs(u) + eu) + np.abs(s) * eu) + np.abs(h) * (16 * EPS + ep)
+    o, _ = _mm(h, w2, kind)
+    _, mag = _mm(np.abs(h) + eh, w2, kind)
+    _, prop = _mm(eh, w2, kind)
+    return o, prop + _adds(n, w2) * EPS * mag, mag
+
+
+def moe(x, router, w13, w2, topk, renorm, shared, kind, out):
+    """(out, bound, ids, weights) of the layer in 64 bits; bound holds per
+    element for fp32 sums and the output type's rounding.  Asserts that the
+    logits leave no doubt about the top-k (inputs are chosen so)."""
+    X = f64(x, kind)
+    m, d = X.shape
+    lg, mag = _mm(X, router, kind)
+    el = (d + 16) * EPS * mag
+    experts = lg.shape[1]
+    ref = np.zeros((m, d))
+    err = np.zeros((m, d))
+    tot = np.zeros((m, d))
+    ids = np.zeros((m, topk), np.int64)
+    wts = np.zeros((m, topk))
+    for t in range(m):
+        order = sorted(range(experts), key=lambda e: (-lg[t, e], e))
+        for a, b in zip(order[:topk], order[1:topk + 1]):
+            assert lg[t, a] == lg[t, b] or lg[t, a] - lg[t, b] > 4e-6, "inputs with a doubtful top-k"
+        ids[t] = order[:topk]
+        p = np.exp(lg[t] - lg[t].max())
+        p /= p[ids[t]].sum() if renorm else p.sum()
+        wts[t] = p[ids[t]]
+        ep = 2 * float(el[t].max()) + (experts + 16) * EPS
+        for e in sorted(ids[t]):
+            o, eo, mg = _ffn(X[t:t + 1], 0.0, pick(w13, e), pick(w2, e), p[e], ep, kind)
+            ref[t] += o[0]
+            err[t] += eo[0]
+            tot[t] += mg[0]
+        if shared is not None:
+            s13, s2, sg = shared
+            v = float((X[t] * f64(sg, kind)).sum())
+            ev = (d + 16) * EPS * float((np.abs(X[t]) * np.abs(f64(sg, kind))).sum())
+            o, eo, mg = _ffn(X[t:t + 1], 0.0, s13, s2, _sigmoid(v), ev + 8 * EPS, kind)
+            ref[t] += o[0]
+            err[t] += eo[0]
+            tot[t] += mg[0]
+    err = err + (topk + 16) * EPS * tot
+    return ref, err * (1 + ULP[out]) + ULP[out] * np.abs(ref) + TINY[out], ids, wts
