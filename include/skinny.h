@@ -440,6 +440,41 @@ SKINNY_API skinny_status skinny_moe_run(const skinny_moe_plan* plan, int64_t m, 
                                         const skinny_moe_weights* weights, void* out, int32_t* topk_idx,
                                         float* topk_weight, void* workspace, size_t workspace_bytes, void* stream);
 
+/* --- Log probabilities of given tokens ------------------------------------- */
+
+/* For each row x of logits and its token t:
+ *   logprob   f32 [m]  x_t - ln sum exp(x_j)
+ *   entropy   f32 [m]  of the row's distribution, in nats
+ *   rank      int32 [m]  1 + #{j : x_j > x_t, or x_j = x_t and j < t}
+ *   top_ids   int32 [m][topk], top_logprobs f32 [m][topk]: the topk largest
+ *             logits, equal values (IEEE ==) by lower index first, and their
+ *             log probabilities
+ * Sums are held in fp32.  A logit of -inf (masked out) has probability 0; a
+ * row of nothing else gives log probabilities of -inf and an entropy of 0.  A
+ * row that holds a NaN or +inf gives NaN (its ids lie in the row or are -1).
+ * A token outside 0 .. vocab - 1 reads nothing: its logprob is NaN, its rank
+ * 0, the row's other results are given.  For m <= SKINNY_GEMV_MAX_M a row's
+ * results are the same bits at every m and wherever the row lies in memory.
+ *   m, vocab     1 <= m, vocab <= 2^30, m * vocab <= 2^50
+ *   logits       [m][ld] SKINNY_F32, SKINNY_F16 or SKINNY_BF16 (dtype), aligned to
+ *                its element; ld >= vocab (0: vocab), any value
+ *   tokens       [m] int32, or int64 when tokens64 is not 0; aligned to it
+ *   topk         0 .. min(vocab, SKINNY_TOPK_MAX); 0: top_ids and top_logprobs are
+ *                not written and may be NULL
+ *   outputs      4-byte aligned, overlapping neither one another nor the inputs
+ *   workspace    zero-initialised device scratch of at least
+ *                skinny_token_logprobs_workspace_size bytes, 16-byte aligned
+ *                (may be NULL when that is 0); a completed run leaves it ready
+ *                for the next, of any size it suffices for.  Two runs in
+ *                flight at once must not share one.
+ * All device pointers.  One launch. */
+SKINNY_API skinny_status skinny_token_logprobs_workspace_size(int64_t m, int64_t vocab, int32_t topk, size_t* bytes);
+SKINNY_API skinny_status skinny_token_logprobs_run(int64_t m, int64_t vocab, const void* logits, int64_t ld,
+                                                   int32_t dtype, const void* tokens, int32_t tokens64,
+                                                   int32_t topk, float* logprob, float* entropy, int32_t* rank,
+                                                   int32_t* top_ids, float* top_logprobs, void* workspace,
+                                                   size_t workspace_bytes, void* stream);
+
 /* Human-readable description of what a run with this m would launch: path,
  * tile or GEMV split, grid.  Writes a NUL-terminated string (truncated to
  * len). */

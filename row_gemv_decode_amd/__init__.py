@@ -16,6 +16,7 @@ W[k, n] in C[m, n] = A[m, k] . W[k, n].
 """
 import ctypes
 import os
+from typing import NamedTuple
 
 # torch first: it brings its own HIP runtime (soname libamdhip64.so.7); loaded
 # afterwards, libskinny.so binds to that same runtime, so torch's streams and
@@ -55,6 +56,7 @@ EXPORTS = (
     "skinny_gemm_tile_name", "skinny_status_string", "skinny_abi_version", "skinny_cast_f32_bf16_run",
     "skinny_moe_combine_run", "skinny_mm_run_static", "skinny_w4_mm_run",
     "skinny_moe_plan_create", "skinny_moe_plan_destroy", "skinny_moe_workspace_size", "skinny_moe_run",
+    "skinny_token_logprobs_workspace_size", "skinny_token_logprobs_run",
 )
 STATIC_SCRATCH_BYTES = 32 << 20
 STATIC_COUNTER_BYTES = 1 << 20
@@ -139,6 +141,11 @@ _lib.skinny_moe_workspace_size.argtypes = [_vp, ctypes.POINTER(_sz)]
 _lib.skinny_moe_workspace_size.restype = ctypes.c_int
 _lib.skinny_moe_run.argtypes = [_vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]
 _lib.skinny_moe_run.restype = ctypes.c_int
+_lib.skinny_token_logprobs_workspace_size.argtypes = [_i64, _i64, _i32, ctypes.POINTER(_sz)]
+_lib.skinny_token_logprobs_workspace_size.restype = ctypes.c_int
+_lib.skinny_token_logprobs_run.argtypes = [_i64, _i64, _vp, _i64, _i32, _vp, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _sz,
+                                           _vp]
+_lib.skinny_token_logprobs_run.restype = ctypes.c_int
 _lib.skinny_mm_plan_info.argtypes = [_vp, _i64, ctypes.c_char_p, _sz]
 _lib.skinny_mm_plan_info.restype = ctypes.c_int
 _lib.skinny_gemm_tile_count.argtypes = []
@@ -655,3 +662,59 @@ class MoELayer:
             except Exception:  # interpreter shutdown
                 pass
             self._h = None
+
+
+class TokenLogprobs(NamedTuple):
+    """What token_logprobs gives: per row the token's log probability, the
+    distribution's entropy in nats, the token's rank (1: the largest logit),
+    and the top alternatives' ids and log probabilities."""
+    logprob: "torch.Tensor"       # float32 [m]
+    entropy: "torch.Tensor"       # float32 [m]
+    rank: "torch.Tensor"          # int32 [m]
+    top_ids: "torch.Tensor"       # int32 [m][topk]
+    top_logprobs: "torch.Tensor"  # float32 [m][topk]
+
+
+_logprob_ws = {}
+
+
+def _logprob_workspace(nbytes, device, stream):
+    """The log probabilities' workspace of one (device, stream) pair, grown to
+    the largest run it has seen (a run leaves its counters at zero)."""
+    key = (device, stream.cuda_stream)
+    ws = _logprob_ws.get(key)
+    if ws is None or ws.numel() < nbytes:
+        with torch.cuda.stream(stream):
+            ws = torch.zeros(nbytes, dtype=torch.uint8, device=device)
+        _logprob_ws[key] = ws
+    return ws
+
+
+def token_logprobs(logits, tokens, topk=0, stream=None):
+    """Log probabilities of tokens[i] under softmax(logits[i]), with entropy,
+    rank and the topk <= 32 top alternatives (see TokenLogprobs), in one launch
+    that reads the logits once.  logits [m][vocab] float32, float16 or bfloat16
+    with dense rows of any stride; tokens [m] int64 or int32.  A logit of -inf
+    is masked out; a token outside the row gives NaN and rank 0."""
+    ld = _rows("token_logprobs", "logits", logits)
+    m, vocab = logits.shape
+    if tuple(tokens.shape) != (m,) or tokens.dtype not in (torch.int64, torch.int32):
+        raise ValueError(f"token_logprobs: tokens must be int64 or int32 [{m}]")
+    device = logits.device
+    _dense("token_logprobs", tokens=tokens)
+    _on("token_logprobs", device, tokens)
+    dtype = _dtype_code(logits.dtype, "logits")
+    sz = ctypes.c_size_t()
+    _check(_lib.skinny_token_logprobs_workspace_size(m, vocab, topk, ctypes.byref(sz)), "token_logprobs")
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    ws = _logprob_workspace(sz.value, device, stream) if sz.value else None
+    f = torch.empty((2 + topk, m), dtype=torch.float32, device=device)
+    i = torch.empty((1 + topk, m), dtype=torch.int32, device=device)
+    out = TokenLogprobs(f[0], f[1], i[0], i[1:].view(m, topk), f[2:].view(m, topk))
+    _check(_lib.skinny_token_logprobs_run(m, vocab, logits.data_ptr(), ld, dtype, tokens.data_ptr(),
+                                          int(tokens.dtype == torch.int64), topk, out.logprob.data_ptr(),
+                                          out.entropy.data_ptr(), out.rank.data_ptr(), out.top_ids.data_ptr(),
+                                          out.top_logprobs.data_ptr(), _ptr(ws), 0 if ws is None else ws.numel(),
+                                          stream.cuda_stream), "skinny_token_logprobs_run")
+    return out

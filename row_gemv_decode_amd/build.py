@@ -15,7 +15,7 @@ CSRC = os.path.join(PKG, "csrc")
 OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libskinny.so")
 ARCH = "gfx950"
-SOURCES = ["abi.cpp", "abi_window.cpp", "gemv.hip", "gemm.hip", "combine.hip", "w4.hip", "moe.hip",
+SOURCES = ["abi.cpp", "abi_window.cpp", "gemv.hip", "gemm.hip", "combine.hip", "w4.hip", "moe.hip", "logprobs.hip",
            "static_scratch.hip"]
 # sources compiled once per kernel family member: (source, object name, defines)
 INSTANCES = [

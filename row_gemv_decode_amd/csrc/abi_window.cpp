@@ -1,7 +1,7 @@
 // abi_window.cpp -- the C ABI of the decode window's further operators
-// declared in include/skinny.h (4-bit grouped GEMV, the MoE layer): argument
-// validation, all on the host and before any HIP call, and dispatch to the
-// kernels in w4.hip and moe.hip.
+// declared in include/skinny.h (4-bit grouped GEMV, the MoE layer, token
+// log probabilities): argument validation, all on the host and before any HIP
+// call, and dispatch to the kernels in w4.hip, moe.hip and logprobs.hip.
 #include <hip/hip_runtime_api.h>
 
 #include <new>
@@ -36,6 +36,33 @@ bool group_ok(int32_t group) { return group == 32 || group == 64 || group == 128
 int64_t span(int64_t rows, int64_t ld, int64_t len, int64_t size) { return ((rows - 1) * ld + len) * size; }
 
 int64_t round256(int64_t b) { return (b + 255) / 256 * 256; }
+
+// Workgroups per row of the log probabilities.  A window's rows (m <= 16) are
+// cut alike at every m, into at most 64 segments of at least 2048 logits; more
+// rows into as many as give about four workgroups per CU of 256.
+struct RowSegments {
+  int64_t count, len;
+};
+RowSegments row_segments(int64_t m, int64_t vocab) {
+  int64_t want = m <= SKINNY_GEMV_MAX_M ? kLogprobMaxSegments : (1024 + m - 1) / m;
+  const int64_t most = (vocab + 2047) / 2048;
+  if (want > most) want = most;
+  const int64_t len = ((vocab + want - 1) / want + 7) / 8 * 8;
+  return {(vocab + len - 1) / len, len};
+}
+// workspace: the rows' arrival counters, then the segments' partial results.
+// The counters' region has one fixed size, so that one workspace serves runs
+// of several sizes: no run's partial results touch another's counters.
+constexpr int64_t kRowCounterBytes = 1024 * 4;
+int64_t logprob_bytes(int64_t m, int64_t vocab, int32_t topk) {
+  const RowSegments s = row_segments(m, vocab);
+  return s.count == 1 ? 0 : kRowCounterBytes + round256(m * s.count * (4 + 2 * (int64_t)topk) * 4);
+}
+bool logprob_sizes_ok(int64_t m, int64_t vocab, int32_t topk) {
+  constexpr int64_t kMax = 1LL << 30;
+  return m >= 1 && m <= kMax && vocab >= 1 && vocab <= kMax && m <= (1LL << 50) / vocab && topk >= 0 &&
+         topk <= SKINNY_TOPK_MAX && topk <= vocab;
+}
 
 }  // namespace
 
@@ -217,6 +244,65 @@ skinny_status skinny_moe_run(const skinny_moe_plan* plan, int64_t m, const void*
   a.max_slots = (int32_t)plan->max_slots;
   a.out_kind = kind_of(d.out_dtype);
   return hip_status(launch_moe(a, kind_of(d.dtype), d.group, (hipStream_t)stream));
+}
+
+skinny_status skinny_token_logprobs_workspace_size(int64_t m, int64_t vocab, int32_t topk, size_t* bytes) {
+  if (bytes == nullptr || !logprob_sizes_ok(m, vocab, topk)) return SKINNY_ERR_INVALID_ARG;
+  *bytes = (size_t)logprob_bytes(m, vocab, topk);
+  return SKINNY_OK;
+}
+
+skinny_status skinny_token_logprobs_run(int64_t m, int64_t vocab, const void* logits, int64_t ld, int32_t dtype,
+                                        const void* tokens, int32_t tokens64, int32_t topk, float* logprob,
+                                        float* entropy, int32_t* rank, int32_t* top_ids, float* top_logprobs,
+                                        void* workspace, size_t workspace_bytes, void* stream) {
+  if (logits == nullptr || tokens == nullptr || logprob == nullptr || entropy == nullptr || rank == nullptr ||
+      !logprob_sizes_ok(m, vocab, topk) || (topk > 0 && (top_ids == nullptr || top_logprobs == nullptr)))
+    return SKINNY_ERR_INVALID_ARG;
+  if (!float_type(dtype)) return SKINNY_ERR_UNSUPPORTED;
+  if (ld == 0) ld = vocab;
+  if (ld > (1LL << 40)) return SKINNY_ERR_INVALID_ARG;
+  if (ld < vocab) return SKINNY_ERR_SHAPE;
+  if (!aligned(logits, (uintptr_t)size_of(dtype)) || !aligned(tokens, tokens64 != 0 ? 8 : 4) || !aligned(logprob, 4) ||
+      !aligned(entropy, 4) || !aligned(rank, 4) || !aligned(top_ids, 4) || !aligned(top_logprobs, 4))
+    return SKINNY_ERR_ALIGNMENT;
+  const int64_t tb = topk > 0 ? m * topk * 4 : 0;
+  const struct {
+    const void* p;
+    int64_t bytes;
+  } out[5] = {{logprob, m * 4}, {entropy, m * 4}, {rank, m * 4}, {tb > 0 ? top_ids : nullptr, tb},
+              {tb > 0 ? top_logprobs : nullptr, tb}};
+  for (int i = 0; i < 5; ++i) {
+    if (overlap(out[i].p, out[i].bytes, logits, span(m, ld, vocab, size_of(dtype))) ||
+        overlap(out[i].p, out[i].bytes, tokens, m * (tokens64 != 0 ? 8 : 4)))
+      return SKINNY_ERR_INVALID_ARG;
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i].p, out[i].bytes, out[j].p, out[j].bytes)) return SKINNY_ERR_INVALID_ARG;
+  }
+  const int64_t need = logprob_bytes(m, vocab, topk);
+  if (need > 0) {
+    if (workspace == nullptr || workspace_bytes < (size_t)need) return SKINNY_ERR_WORKSPACE;
+    if (!aligned(workspace, 16)) return SKINNY_ERR_ALIGNMENT;
+  }
+  const RowSegments seg = row_segments(m, vocab);
+  LogprobArgs a;
+  a.logits = logits;
+  a.ld = ld;
+  a.vocab = vocab;
+  a.m = m;
+  a.tokens = tokens;
+  a.tokens64 = tokens64 != 0;
+  a.topk = topk;
+  a.segments = (int32_t)seg.count;
+  a.seg_len = (int32_t)seg.len;
+  a.logprob = logprob;
+  a.entropy = entropy;
+  a.rank = rank;
+  a.top_ids = top_ids;
+  a.top_logprobs = top_logprobs;
+  a.counters = need > 0 ? (uint32_t*)workspace : nullptr;
+  a.partial = need > 0 ? (float*)((char*)workspace + kRowCounterBytes) : nullptr;
+  return hip_status(launch_logprobs(a, kind_of(dtype), (hipStream_t)stream));
 }
 
 }  // extern "C"

@@ -213,6 +213,32 @@ int moe_planes(int kind);  // 16-bit planes that hold one inner value
 hipError_t launch_moe(const MoeArgs& args, int kind, int group, hipStream_t stream);
 
 // ---------------------------------------------------------------------------
+// Token log probabilities (logprobs.hip)
+// ---------------------------------------------------------------------------
+constexpr int kLogprobMaxSegments = 64;
+
+struct LogprobArgs {
+  const void* logits;   // [m][ld]
+  int64_t ld;
+  int64_t vocab;        // <= 2^30
+  int64_t m;
+  const void* tokens;   // [m] int32 or (tokens64) int64
+  int32_t tokens64;
+  int32_t topk;
+  int32_t segments;     // workgroups per row, seg_len logits each (the last fewer)
+  int32_t seg_len;
+  float* logprob;       // [m]
+  float* entropy;       // [m]
+  int32_t* rank;        // [m]
+  int32_t* top_ids;     // [m][topk]
+  float* top_logprobs;  // [m][topk]
+  float* partial;       // segments > 1: [m][segments][4 + 2 topk]
+  uint32_t* counters;   // segments > 1: [m] arrivals, zero between calls
+};
+
+hipError_t launch_logprobs(const LogprobArgs& args, int x_kind, hipStream_t stream);
+
+// ---------------------------------------------------------------------------
 // The library's own scratch for skinny_mm_run_static: one file-scope device
 // array per GPU (static_scratch.hip), [counters: kStaticCounterBytes]
 // [data: the rest].  static_scratch() returns the current device's address of

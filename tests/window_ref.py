@@ -144,3 +144,49 @@ def moe(x, router, w13, w2, topk, renorm, shared, kind, out):
             tot[t] += mg[0]
     err = err + (topk + 16) * EPS * tot
     return ref, err * (1 + ULP[out]) + ULP[out] * np.abs(ref) + TINY[out], ids, wts
+
+
+def logprobs(x, tokens, topk):
+    """(logprob, entropy, rank, ids, top logprobs) of rows x [m][V] in 64 bits,
+    and error bounds of the fp32 evaluation for the two sums' results and, per
+    row, of any log probability x_j - M - ln S at distance |x_j - M|.
+
+    With d = x - M: t = d log2 e is off by 2 * 2^-24 |t|, so a term p = 2^t by
+    (2 |d| + 4) * 2^-23 relatively; a thread adds at most V/256 + 64 terms one
+    after another, each step rounding three times when its maximum grows."""
+    m, V = x.shape
+    adds = 4 * (V // 256 + 64) * EPS
+    lp = np.zeros(m)
+    ent = np.zeros(m)
+    rank = np.zeros(m, np.int64)
+    ids = np.zeros((m, topk), np.int64)
+    top = np.zeros((m, topk))
+    blp = np.zeros(m)
+    bent = np.zeros(m)
+    btop = np.zeros((m, topk))
+    for r in range(m):
+        v, t = x[r], int(tokens[r])
+        order = np.lexsort((np.arange(V), -v))[:topk]
+        ids[r] = order
+        known = 0 <= t < V
+        rank[r] = 1 + np.sum(v > v[t]) + np.sum(v[:t] == v[t]) if known else 0
+        M = v.max()
+        if M == -np.inf:
+            lp[r], ent[r], top[r] = (-np.inf if known else np.nan), 0.0, -np.inf
+            continue
+        d = v - M
+        p = np.exp(d)
+        S = p.sum()
+        p /= S
+        dz = np.where(np.isfinite(d), d, 0.0)
+        term = (2 * np.abs(dz) + 4) * 2 * EPS + adds
+        rs = float((p * term).sum())  # S's relative error
+        lnS = np.log(S)
+        ent[r] = lnS - (p * dz).sum()
+        mean = abs(float((p * dz).sum()))
+        bent[r] = rs + float((p * np.abs(dz) * term).sum()) + mean * rs + 8 * EPS * (lnS + mean + 1)
+        lp[r] = d[t] - lnS if known else np.nan
+        top[r] = d[order] - lnS
+        blp[r] = rs + 8 * EPS * (lnS + 1 + (abs(d[t]) if known and np.isfinite(d[t]) else 0))
+        btop[r] = rs + 8 * EPS * (lnS + 1 + np.where(np.isfinite(d[order]), np.abs(d[order]), 0))
+    return (lp, ent, rank, ids, top), (blp, bent, btop)
