@@ -54,7 +54,11 @@ EXPORTS = (
     "skinny_mm_plan_info",
     "skinny_gemm_tile_count",
     "skinny_gemm_tile_name", "skinny_status_string", "skinny_abi_version", "skinny_cast_f32_bf16_run",
-    "skinny_moe_combine_run", "skinny_mm_run_static", "skinny_w4_mm_run",
+    "skinny_moe_combine_run", "skinny_mm_run_static",
+)
+# the entry points of include/skinny_window.h
+WINDOW_EXPORTS = (
+    "skinny_w4_mm_run",
     "skinny_moe_plan_create", "skinny_moe_plan_destroy", "skinny_moe_workspace_size", "skinny_moe_run",
     "skinny_token_logprobs_workspace_size", "skinny_token_logprobs_run",
 )

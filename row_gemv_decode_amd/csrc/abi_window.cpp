@@ -1,13 +1,13 @@
 // abi_window.cpp -- the C ABI of the decode window's further operators
-// declared in include/skinny.h (4-bit grouped GEMV, the MoE layer, token
+// declared in include/skinny_window.h (4-bit grouped GEMV, the MoE layer, token
 // log probabilities): argument validation, all on the host and before any HIP
 // call, and dispatch to the kernels in w4.hip, moe.hip and logprobs.hip.
 #include <hip/hip_runtime_api.h>
 
 #include <new>
 
-#include "internal.h"
-#include "skinny.h"
+#include "skinny_window.h"
+#include "window.h"
 
 using namespace skinny;
 

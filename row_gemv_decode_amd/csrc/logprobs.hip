@@ -27,6 +27,7 @@
 // of the segments.
 #include "skinny.h"
 #include "wave_ops.h"
+#include "window.h"
 
 namespace skinny {
 

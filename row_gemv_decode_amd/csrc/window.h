@@ -1,0 +1,100 @@
+// window.h -- host-side interfaces between the C ABI of the decode window's
+// operators (abi_window.cpp) and their kernels (w4.hip, moe.hip,
+// logprobs.hip).  Not installed.
+#pragma once
+
+#include <hip/hip_runtime_api.h>
+#include <stdint.h>
+
+#include "internal.h"
+
+namespace skinny {
+
+// ---------------------------------------------------------------------------
+// 4-bit grouped weights (w4.hip, moe.hip): codes [n][k/2] (element kk in byte
+// kk/2, the low nibble for even kk), scales [n][k/group] in the rows' type,
+// zero points uint8 [n][k/group] or null (8): W = s * (q - z)
+// ---------------------------------------------------------------------------
+struct W4Args {
+  const void* A;       // [m][lda] f16/bf16
+  int64_t lda;
+  const void* codes;
+  const void* scales;
+  const void* zeros;
+  int64_t n;
+  int64_t k;
+  void* C;             // [m][ldc]
+  int64_t ldc;
+  int32_t m;           // <= kGemvMaxM
+  int32_t c_kind;      // CK_*
+};
+
+// a_kind: CK_F16 or CK_BF16; group 32, 64 or 128
+hipError_t launch_w4_mm(const W4Args& args, int a_kind, int group, hipStream_t stream);
+
+// ---------------------------------------------------------------------------
+// The whole MoE layer for a decode window (moe.hip): route, up, down launches
+// after the router's GEMV.
+// ---------------------------------------------------------------------------
+constexpr int kMoeMaxExperts = 1024;
+
+struct MoeWeight {     // 16-bit weights in `codes`, or a 4-bit grouped weight
+  const void* codes;
+  const void* scales;
+  const void* zeros;
+};
+
+struct MoeArgs {
+  const void* x;           // [m][ldx]
+  int64_t ldx;
+  int64_t d;               // row length
+  int64_t inter;           // an expert's inner length
+  int64_t shared_inter;    // the shared expert's, 0: none
+  MoeWeight w13, w2;       // [E][2 inter][d], [E][d][inter]
+  MoeWeight s13, s2;       // the shared expert's
+  const void* shared_gate; // [d]
+  const float* logits;     // [m][experts]
+  uint32_t* slots;         // distinct experts, ascending: expert | token mask << 16
+  int32_t* nslots;
+  float* slot_w;           // [max_slots + 1][16]: each slot's routing weight per token
+                           // (0: not routed), the shared expert's gates after the last
+  uint16_t* h;             // [max_slots][16][planes][inter], then [16][planes][shared_inter]
+  int32_t* topk_idx;       // [m][topk] or null
+  float* topk_weight;      // [m][topk] or null
+  void* out;               // [m][ldo]
+  int64_t ldo;
+  int32_t m, experts, topk, renorm, max_slots, out_kind;
+};
+
+int moe_planes(int kind);  // 16-bit planes that hold one inner value
+
+// kind: CK_F16 or CK_BF16; group: 0 (16-bit weights), 32, 64 or 128
+hipError_t launch_moe(const MoeArgs& args, int kind, int group, hipStream_t stream);
+
+// ---------------------------------------------------------------------------
+// Token log probabilities (logprobs.hip)
+// ---------------------------------------------------------------------------
+constexpr int kLogprobMaxSegments = 64;
+
+struct LogprobArgs {
+  const void* logits;   // [m][ld]
+  int64_t ld;
+  int64_t vocab;        // <= 2^30
+  int64_t m;
+  const void* tokens;   // [m] int32 or (tokens64) int64
+  int32_t tokens64;
+  int32_t topk;
+  int32_t segments;     // workgroups per row, seg_len logits each (the last fewer)
+  int32_t seg_len;
+  float* logprob;       // [m]
+  float* entropy;       // [m]
+  int32_t* rank;        // [m]
+  int32_t* top_ids;     // [m][topk]
+  float* top_logprobs;  // [m][topk]
+  float* partial;       // segments > 1: [m][segments][4 + 2 topk]
+  uint32_t* counters;   // segments > 1: [m] arrivals, zero between calls
+};
+
+hipError_t launch_logprobs(const LogprobArgs& args, int x_kind, hipStream_t stream);
+
+}  // namespace skinny

@@ -31,6 +31,7 @@
 #pragma once
 
 #include "device_common.h"
+#include "window.h"
 
 namespace skinny {
 

@@ -2,14 +2,27 @@
 grouped GEMV, MoE layer, token log probabilities): every refusal comes from
 the host before any HIP call, so these run without a GPU."""
 import ctypes
+import os
+import re
 
 import pytest
+
+from conftest import ROOT
 
 sk = pytest.importorskip("row_gemv_decode_amd")
 
 lib = sk.lib()
 P = 1 << 20  # made-up device addresses, far enough apart not to overlap
 A, CODES, SCALES, ZEROS, C = (i * (1 << 30) + P for i in range(1, 6))
+
+
+def test_exports_every_declared_symbol():
+    with open(os.path.join(ROOT, "include", "skinny_window.h")) as f:
+        text = re.sub(r"/\*.*?\*/", "", f.read(), flags=re.S)
+    names = re.findall(r"SKINNY_API\s+[\w ]+?\**\s*(\w+)\s*\(", text)
+    assert len(names) == 7 and set(names) == set(sk.WINDOW_EXPORTS)
+    for n in names:
+        assert hasattr(lib, n), n
 
 
 def w4_run(m=2, n=64, k=256, group=64, a=A, lda=0, a_dtype=sk.BF16, codes=CODES, scales=SCALES, zeros=ZEROS, c=C, ldc=0,
