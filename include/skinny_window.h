@@ -46,7 +46,7 @@ typedef struct skinny_w4 {
  * and summed in fp32, the group's scale is applied to its sum; row i of C at
  * any m equals the m = 1 call on that row bit for bit.
  *   m        1 <= m <= SKINNY_GEMV_MAX_M
- *   n, k     1 <= n < 2^31; k a multiple of group, < 2^31
+ *   n, k     1 <= n < 2^31; k a multiple of group, up to 2^24
  *   A        [m][lda] SKINNY_F16 or SKINNY_BF16 (a_dtype); lda >= k a multiple
  *            of 8 (0: k); 16-byte aligned
  *   C        [m][ldc] SKINNY_F32, SKINNY_F16 or SKINNY_BF16 (c_dtype, rounded to

@@ -85,7 +85,7 @@ skinny_status skinny_w4_mm_run(int64_t m, int64_t n, int64_t k, int32_t group, c
   if (A == nullptr || W == nullptr || C == nullptr || W->codes == nullptr || W->scales == nullptr)
     return SKINNY_ERR_INVALID_ARG;
   if (!half_type(a_dtype) || !float_type(c_dtype) || !group_ok(group)) return SKINNY_ERR_UNSUPPORTED;
-  if (m < 1 || m > SKINNY_GEMV_MAX_M || n < 1 || n > kMaxDim || k < 1 || k > kMaxDim) return SKINNY_ERR_INVALID_ARG;
+  if (m < 1 || m > SKINNY_GEMV_MAX_M || n < 1 || n > kMaxDim || k < 1 || k > kW4MaxK) return SKINNY_ERR_INVALID_ARG;
   if (lda == 0) lda = k;
   if (ldc == 0) ldc = n;
   if (lda > (1LL << 40) || ldc > (1LL << 40)) return SKINNY_ERR_INVALID_ARG;
@@ -100,9 +100,7 @@ skinny_status skinny_w4_mm_run(int64_t m, int64_t n, int64_t k, int32_t group, c
   W4Args g;
   g.A = A;
   g.lda = lda;
-  g.codes = W->codes;
-  g.scales = W->scales;
-  g.zeros = W->zeros;
+  g.w = WindowWeight{W->codes, W->scales, W->zeros};
   g.n = n;
   g.k = k;
   g.C = C;
@@ -216,7 +214,7 @@ skinny_status skinny_moe_run(const skinny_moe_plan* plan, int64_t m, const void*
   const skinny_status st = skinny_mm_run(plan->router, m, x, weights->router, nullptr, logits,
                                          plan->router_ws > 0 ? base : nullptr, (size_t)plan->router_ws, stream);
   if (st != SKINNY_OK) return st;
-  auto weight = [](const skinny_w4& w) { return MoeWeight{w.codes, w.scales, w.zeros}; };
+  auto weight = [](const skinny_w4& w) { return WindowWeight{w.codes, w.scales, w.zeros}; };
   MoeArgs a;
   a.x = x;
   a.ldx = d.ldx;

@@ -188,7 +188,7 @@ __global__ __launch_bounds__(64 * kMoeWaves) void moe_up_kernel(MoeArgs a) {
   const int64_t inter = shared ? a.shared_inter : a.inter;
   const uint32_t entry = shared ? 0xffff0000u : a.slots[slot];  // every token goes to the shared expert
   const int64_t e = (int64_t)(entry & 0xffffu);
-  const MoeWeight& W = shared ? a.s13 : a.w13;
+  const WindowWeight& W = shared ? a.s13 : a.w13;
 
   const int row = (lane & 15) < a.m ? (lane & 15) : a.m - 1;
   const uint16_t* arow = (const uint16_t*)a.x + row * a.ldx + 8 * h;

@@ -15,12 +15,19 @@ namespace skinny {
 // kk/2, the low nibble for even kk), scales [n][k/group] in the rows' type,
 // zero points uint8 [n][k/group] or null (8): W = s * (q - z)
 // ---------------------------------------------------------------------------
-struct W4Args {
-  const void* A;       // [m][lda] f16/bf16
-  int64_t lda;
+struct WindowWeight {     // 16-bit weights in `codes`, or a 4-bit grouped weight
   const void* codes;
   const void* scales;
   const void* zeros;
+};
+
+// largest k: a lane's offset into its tile of 16 columns has 32 bits
+constexpr int64_t kW4MaxK = 1 << 24;
+
+struct W4Args {
+  const void* A;       // [m][lda] f16/bf16
+  int64_t lda;
+  WindowWeight w;
   int64_t n;
   int64_t k;
   void* C;             // [m][ldc]
@@ -38,20 +45,14 @@ hipError_t launch_w4_mm(const W4Args& args, int a_kind, int group, hipStream_t s
 // ---------------------------------------------------------------------------
 constexpr int kMoeMaxExperts = 1024;
 
-struct MoeWeight {     // 16-bit weights in `codes`, or a 4-bit grouped weight
-  const void* codes;
-  const void* scales;
-  const void* zeros;
-};
-
 struct MoeArgs {
   const void* x;           // [m][ldx]
   int64_t ldx;
   int64_t d;               // row length
   int64_t inter;           // an expert's inner length
   int64_t shared_inter;    // the shared expert's, 0: none
-  MoeWeight w13, w2;       // [E][2 inter][d], [E][d][inter]
-  MoeWeight s13, s2;       // the shared expert's
+  WindowWeight w13, w2;       // [E][2 inter][d], [E][d][inter]
+  WindowWeight s13, s2;       // the shared expert's
   const void* shared_gate; // [d]
   const float* logits;     // [m][experts]
   uint32_t* slots;         // distinct experts, ascending: expert | token mask << 16
