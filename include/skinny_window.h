@@ -109,7 +109,8 @@ typedef struct skinny_moe_desc {
 } skinny_moe_desc;
 
 /* Device pointers, 16-byte aligned (scales 2-byte; zeros any).  A 16-bit
- * weight is given in `codes`, with scales and zeros NULL.
+ * weight is given in `codes`, with scales and zeros NULL; 4-bit weights come
+ * with zero points all or none (else SKINNY_ERR_UNSUPPORTED).
  *   router       [experts][d]
  *   w13          [experts][2 inter][d]: expert e's gate rows, then its up rows
  *   w2           [experts][d][inter]

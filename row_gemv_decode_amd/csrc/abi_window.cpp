@@ -74,7 +74,7 @@ struct skinny_moe_plan {
   int64_t max_slots;      // distinct experts a window can reach
   // workspace regions, in bytes from its start
   int64_t router_ws;      // the router plan's own workspace comes first (its counters start at zero)
-  int64_t logits, nslots, slots, slot_w, h, bytes;
+  int64_t counters, zero_page, logits, nslots, slots, slot_w, gates, partial, h, bytes;
 };
 
 extern "C" {
@@ -155,7 +155,8 @@ skinny_status skinny_moe_plan_create(const skinny_moe_desc* desc, skinny_moe_pla
   p->d = d;
   p->router = router;
   p->max_slots = d.max_m * d.topk < d.experts ? d.max_m * d.topk : d.experts;
-  const int64_t planes = moe_planes(kind_of(d.dtype));
+  const int64_t planes = moe_planes(kind_of(d.dtype), kind_of(d.out_dtype));
+  const int64_t splits = moe_down_splits(d.d);
   int64_t at = 0;
   auto region = [&at](int64_t bytes) {
     const int64_t start = at;
@@ -164,10 +165,14 @@ skinny_status skinny_moe_plan_create(const skinny_moe_desc* desc, skinny_moe_pla
   };
   p->router_ws = (int64_t)rws;
   region(p->router_ws);
+  p->counters = region(splits > 1 ? d.d / 32 * 4 : 0);
+  p->zero_page = region(256);
   p->logits = region(d.max_m * d.experts * 4);
   p->nslots = region(4);
   p->slots = region(p->max_slots * 4);
-  p->slot_w = region((p->max_slots + 1) * kGemvMaxM * 4);
+  p->slot_w = region(p->max_slots * kGemvMaxM * 4);
+  p->gates = region(kGemvMaxM * 4);
+  p->partial = region(splits > 1 ? splits * kGemvMaxM * d.d * 4 : 0);
   p->h = region((p->max_slots * d.inter + d.shared_inter) * kGemvMaxM * planes * 2);
   p->bytes = at;
   *out_plan = p;
@@ -199,6 +204,10 @@ skinny_status skinny_moe_run(const skinny_moe_plan* plan, int64_t m, const void*
              : ws[i]->codes != nullptr || ws[i]->scales != nullptr || ws[i]->zeros != nullptr)
       return SKINNY_ERR_INVALID_ARG;
   }
+  // zero points: with every 4-bit weight of the layer, or with none
+  const bool zeros = weights->w13.zeros != nullptr;
+  for (int i = 1; i < (shared ? 4 : 2); ++i)
+    if ((ws[i]->zeros != nullptr) != zeros) return SKINNY_ERR_UNSUPPORTED;
   if (weights->router == nullptr || (weights->shared_gate != nullptr) != shared) return SKINNY_ERR_INVALID_ARG;
   for (int i = 0; i < 4; ++i)
     if (!aligned(ws[i]->codes, 16) || !aligned(ws[i]->scales, 2)) return SKINNY_ERR_ALIGNMENT;
@@ -230,6 +239,11 @@ skinny_status skinny_moe_run(const skinny_moe_plan* plan, int64_t m, const void*
   a.slots = (uint32_t*)(base + plan->slots);
   a.nslots = (int32_t*)(base + plan->nslots);
   a.slot_w = (float*)(base + plan->slot_w);
+  a.gates = (float*)(base + plan->gates);
+  a.zero_page = (const uint16_t*)(base + plan->zero_page);
+  a.partial = (float*)(base + plan->partial);
+  a.counters = (uint32_t*)(base + plan->counters);
+  a.down_splits = moe_down_splits(d.d);
   a.h = (uint16_t*)(base + plan->h);
   a.topk_idx = topk_idx;
   a.topk_weight = topk_weight;

@@ -8,21 +8,26 @@
 //   out_t = sum over e in S_t of h_te . Wd_e  +  (sigmoid(x_t . wg) * h_t,shared) . Wd_shared
 //
 // HBM-bound on the distinct experts' weights, each read once per window.
-//   moe_route_kernel  one workgroup, one wave per token: top-k, softmax, the
-//                     shared expert's gate, and the list of distinct experts
-//                     in ascending order with each one's tokens
-//   moe_up_kernel     one workgroup per (distinct expert, 16 columns of h):
-//                     gate and up columns side by side against all rows of x
-//                     (a matrix-core tile holds 16 rows anyway, so tokens are
+//   moe_route_kernel  one workgroup, one wave per token: top-k, softmax and the
+//                     list of distinct experts in ascending order with each
+//                     one's tokens (a second workgroup: the shared expert's
+//                     gates)
+//   moe_up_kernel     one workgroup per (distinct expert, 16 or 32 columns of
+//                     h): gate and up columns side by side against all rows of
+//                     x (a matrix-core tile holds 16 rows anyway, so tokens are
 //                     not gathered), p and silu in the epilogue
-//   moe_down_kernel   one workgroup per 16 columns of the layer's output, over
-//                     all distinct experts: a row that an expert does not
+//   moe_down_kernel   one workgroup per 32 columns of the layer's output and
+//                     share of the experts' k: a row that an expert does not
 //                     serve is a row of zeros, so the matrix core adds the
 //                     experts of every token by itself, and the combine costs
-//                     nothing
-// h is kept exactly enough to lose nothing against fp32: as the sum of two
-// f16 (22 bits) or three bf16 (24 bits) planes, multiplied one after another;
-// the matrix cores have time for it while the weights stream.
+//                     nothing; the last workgroup of a column range to finish
+//                     adds the shares in order
+// h is kept as the sum of planes in the weights' type, multiplied one after
+// another (the matrix cores have time for it while the weights stream): two,
+// 16 (bf16) or 22 (f16) bits, under a 16-bit output, where one plane would add
+// as much error as the output's own rounding; three (bf16, 24 bits) under an
+// fp32 output.  For 4-bit weights h is stored in the pair order that their
+// decoding yields.
 //
 // Row invariance: which wave takes which part of k depends on the expert and
 // the part alone, each wave adds its experts in ascending order, and what the
@@ -36,11 +41,7 @@ namespace skinny {
 
 namespace {
 
-constexpr int kMoeWaves = 8;
-constexpr int kRouteCols = kMoeMaxExperts / 64;  // logits per lane
-
-template <int TK>
-constexpr int planes() { return TK == CK_F16 ? 2 : 3; }
+constexpr int kMoeWaves = 4;
 
 __device__ __forceinline__ float wave_sum_f32(float v) {
   v += dpp_mov<kDppXor1>(v);
@@ -53,74 +54,25 @@ __device__ __forceinline__ float wave_sum_f32(float v) {
   return fbits(r32[0]) + fbits(r32[1]);
 }
 
-// One workgroup of m waves.  Each round of a wave's top-k takes the largest
+// Workgroup 0, one wave per token: each round of the top-k takes the largest
 // remaining order key of the row (ties: the lowest column); lane i keeps the
 // i-th winner.  The softmax sums in a fixed order: over the winners lane by
-// lane, or over all logits.
-template <int TK>
+// lane, or over all logits.  Workgroup 1: the shared expert's gates.
+// NC: logits per lane.
+template <int TK, int NC>
 __global__ __launch_bounds__(1024) void moe_route_kernel(MoeArgs a) {
-  __shared__ uint32_t mask[kMoeMaxExperts];     // tokens of each expert
-  __shared__ int slot_of[kMoeMaxExperts];
-  __shared__ int win_e[kGemvMaxM][SKINNY_TOPK_MAX];
-  __shared__ float win_p[kGemvMaxM][SKINNY_TOPK_MAX];
-  __shared__ float gate[kGemvMaxM];
-  __shared__ int nslots_s;
+  __shared__ uint32_t mask[64 * NC];  // tokens of each expert
+  __shared__ int slot_of[64 * NC];
   const int tid = threadIdx.x;
   const int lane = tid & 63;
   const int t = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int E = a.experts;
-  for (int e = tid; e < E; e += blockDim.x) mask[e] = 0;
-  __syncthreads();
 
-  {
-    const float* row = a.logits + (int64_t)t * E;
-    float x[kRouteCols];
-    int key[kRouteCols];
-#pragma unroll
-    for (int u = 0; u < kRouteCols; ++u) x[u] = lane + 64 * u < E ? row[lane + 64 * u] : 0.0f;
-#pragma unroll
-    for (int u = 0; u < kRouteCols; ++u) key[u] = lane + 64 * u < E ? order_key(x[u]) : (int)0x80000000;
-    float top = 0.0f, mine = 0.0f;
-    int mine_e = 0;
-    for (int i = 0; i < a.topk; ++i) {
-      int best = key[0];
-#pragma unroll
-      for (int u = 1; u < kRouteCols; ++u) best = max(best, key[u]);
-      const int kmax = wave_max_i32(best);
-      int col = 0x7fffffff;
-#pragma unroll
-      for (int u = kRouteCols - 1; u >= 0; --u) col = key[u] == kmax ? lane + 64 * u : col;
-      // (a NaN logit may leave no column below E: keep the index in range)
-      const int e = min(wave_min_i32(col), E - 1);
-#pragma unroll
-      for (int u = 0; u < kRouteCols; ++u) key[u] = lane + 64 * u == e ? (int)0x80000000 : key[u];
-      const float v = row[e];
-      if (i == 0) top = v;
-      mine = lane == i ? v : mine;
-      mine_e = lane == i ? e : mine_e;
-    }
-    const float ex = lane < a.topk ? expf(mine - top) : 0.0f;
-    float total = 0.0f;
-    if (a.renorm) {
-      total = wave_sum_f32(ex);
-    } else {
-#pragma unroll
-      for (int u = 0; u < kRouteCols; ++u) total += lane + 64 * u < E ? expf(x[u] - top) : 0.0f;
-      total = wave_sum_f32(total);
-    }
-    const float p = ex / total;
-    if (lane < a.topk) {
-      win_e[t][lane] = mine_e;
-      win_p[t][lane] = p;
-      atomicOr(&mask[mine_e], 1u << t);
-      if (a.topk_idx != nullptr) a.topk_idx[t * a.topk + lane] = mine_e;
-      if (a.topk_weight != nullptr) a.topk_weight[t * a.topk + lane] = p;
-    }
-  }
-  if (a.shared_inter > 0) {
+  if (blockIdx.x == 1) {
     const uint16_t* xr = (const uint16_t*)a.x + t * a.ldx;
     const uint16_t* wr = (const uint16_t*)a.shared_gate;
     float s = 0.0f;
+#pragma unroll 4
     for (int c = lane * 8; c < a.d; c += 512) {
       const u32x4 xv = *(const u32x4*)(xr + c);
       const u32x4 wv = *(const u32x4*)(wr + c);
@@ -132,7 +84,59 @@ __global__ __launch_bounds__(1024) void moe_route_kernel(MoeArgs a) {
       }
     }
     s = wave_sum_f32(s);
-    if (lane == 0) gate[t] = 1.0f / (1.0f + expf(-s));
+    if (lane == 0) a.gates[t] = 1.0f / (1.0f + expf(-s));
+    return;
+  }
+
+  const float* row = a.logits + (int64_t)t * E;
+  float x[NC];
+#pragma unroll
+  for (int u = 0; u < NC; ++u) x[u] = lane + 64 * u < E ? row[lane + 64 * u] : 0.0f;
+  for (int e = tid; e < E; e += blockDim.x) mask[e] = 0;
+  __syncthreads();
+
+  int key[NC];
+#pragma unroll
+  for (int u = 0; u < NC; ++u) key[u] = lane + 64 * u < E ? order_key(x[u]) : (int)0x80000000;
+  int top = 0, mine = 0, mine_e = 0;
+  for (int i = 0; i < a.topk; ++i) {
+    int best = key[0];
+#pragma unroll
+    for (int u = 1; u < NC; ++u) best = max(best, key[u]);
+    const int kmax = wave_max_i32(best);
+    int col = lane + 64 * (NC - 1);
+#pragma unroll
+    for (int u = NC - 2; u >= 0; --u) col = key[u] == kmax ? lane + 64 * u : col;
+    const uint64_t b = __builtin_amdgcn_ballot_w64(best == kmax);
+    int e;
+    if ((b & (b - 1)) == 0) {  // uniform: one lane holds the maximum
+      e = (int)__builtin_amdgcn_readlane((uint32_t)col, (uint32_t)__builtin_ctzll(b));
+    } else {
+      e = wave_min_i32(best == kmax ? col : 0x7fffffff);
+    }
+    e = min(e, E - 1);  // (a NaN logit may leave no key above the lowest: keep the index in range)
+#pragma unroll
+    for (int u = 0; u < NC; ++u) key[u] = lane + 64 * u == e ? (int)0x80000000 : key[u];
+    if (i == 0) top = kmax;
+    mine = lane == i ? kmax : mine;
+    mine_e = lane == i ? e : mine_e;
+  }
+  const float vtop = key_value(top);
+  const float ex = lane < a.topk ? expf(key_value(mine) - vtop) : 0.0f;
+  float total;
+  if (a.renorm) {
+    total = wave_sum_f32(ex);
+  } else {
+    total = 0.0f;
+#pragma unroll
+    for (int u = 0; u < NC; ++u) total += lane + 64 * u < E ? expf(x[u] - vtop) : 0.0f;
+    total = wave_sum_f32(total);
+  }
+  const float p = ex / total;
+  if (lane < a.topk) {
+    atomicOr(&mask[mine_e], 1u << t);
+    if (a.topk_idx != nullptr) a.topk_idx[t * a.topk + lane] = mine_e;
+    if (a.topk_weight != nullptr) a.topk_weight[t * a.topk + lane] = p;
   }
   __syncthreads();
 
@@ -149,98 +153,80 @@ __global__ __launch_bounds__(1024) void moe_route_kernel(MoeArgs a) {
       }
       n += __builtin_popcountll(b);
     }
-    if (lane == 0) {
-      nslots_s = n;
-      *a.nslots = n;
-    }
+    if (lane == 0) *a.nslots = n;
   }
   __syncthreads();
-  const int n = nslots_s;
-  for (int i = tid; i < (n + 1) * kGemvMaxM; i += blockDim.x) {
-    // the shared expert's weights come last
-    const int row = i & (kGemvMaxM - 1);
-    a.slot_w[i] = (i >= n * kGemvMaxM && a.shared_inter > 0 && row < a.m) ? gate[row] : 0.0f;
-  }
-  __syncthreads();  // (orders this workgroup's global writes too: the next ones overwrite some)
-  if (lane < a.topk) a.slot_w[slot_of[win_e[t][lane]] * kGemvMaxM + t] = win_p[t][lane];
+  // (a weight is read for the tokens in the slot's mask only)
+  if (lane < a.topk) a.slot_w[slot_of[mine_e] * kGemvMaxM + t] = p;
 }
 
-// columns of w13: gate columns 0 .. inter - 1, up columns inter .. 2 inter - 1
-template <int TK, int WQ>
-__global__ __launch_bounds__(64 * kMoeWaves) void moe_up_kernel(MoeArgs a) {
-  constexpr int UB = WQ == kWFull ? 2 : 3;
-  constexpr int NP = planes<TK>();
-  __shared__ f32x4 red[kMoeWaves][2][64];
+// where column i of h lies in memory: for 4-bit weights each run of eight is
+// kept in the pair order of codes16
+template <int WQ>
+__device__ __forceinline__ int h_place(int i) {
+  if constexpr (WQ == kWFull) {
+    return i;
+  } else {
+    const int e = i & 7;
+    return (i & ~7) + (e < 4 ? 2 * e : 2 * e - 7);
+  }
+}
+
+// GT tiles of 16 columns of h: columns of w13 are the gate's 0 .. inter - 1,
+// then the up's
+template <int TK, int WQ, int NP, int GT>
+__global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_up_kernel(MoeArgs a) {
+  __shared__ f32x4 red[kMoeWaves][2 * GT][64];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int h = lane >> 4;
   const int k = (int)a.d;
   const int nslots = *a.nslots;
-  const int tiles = (int)a.inter / 16;
+  const int tiles = (int)a.inter / (16 * GT);
 
   // the shared expert's workgroups come first: they are sure to have work
-  const int shared_tiles = (int)a.shared_inter / 16;
+  const int shared_tiles = (int)a.shared_inter / (16 * GT);
   const bool shared = (int)blockIdx.x < shared_tiles;
   const int b = (int)blockIdx.x - shared_tiles;
-  const int slot = shared ? nslots : b / tiles;
+  const int slot = shared ? 0 : b / tiles;
   if (!shared && slot >= nslots) return;
   const int tile = shared ? (int)blockIdx.x : b - slot * tiles;
   const int64_t inter = shared ? a.shared_inter : a.inter;
   const uint32_t entry = shared ? 0xffff0000u : a.slots[slot];  // every token goes to the shared expert
-  const int64_t e = (int64_t)(entry & 0xffffu);
-  const WindowWeight& W = shared ? a.s13 : a.w13;
-
-  const int row = (lane & 15) < a.m ? (lane & 15) : a.m - 1;
-  const uint16_t* arow = (const uint16_t*)a.x + row * a.ldx + 8 * h;
-  WCol<WQ> col[2];
-  const int64_t j = e * 2 * inter + 16 * tile + (lane & 15);
-  col[0] = w_col<WQ>(W.codes, W.scales, W.zeros, j, a.d, h);
-  col[1] = w_col<WQ>(W.codes, W.scales, W.zeros, j + inter, a.d, h);
-  f32x4 tot[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
-
-  const int units = k / kUnit;
-  for (int u = wave; u < units; u += kMoeWaves * UB) {
-    WRaw<WQ> w[UB][2];
-    u32x4 x[UB][1][4];
+  const int64_t j0 = (int64_t)(entry & 0xffffu) * 2 * inter + 16 * GT * tile;
+  int64_t j[2 * GT];
+  f32x4 tot[2 * GT];
 #pragma unroll
-    for (int q = 0; q < UB; ++q) {
-      if (u + q * kMoeWaves < units) {  // wave-uniform
-        load_unit<WQ, false>(w[q][0], col[0], u + q * kMoeWaves, k, h);
-        load_unit<WQ, false>(w[q][1], col[1], u + q * kMoeWaves, k, h);
-        load_a_unit<false>(x[q][0], arow, u + q * kMoeWaves, k);
-      }
-    }
-    __builtin_amdgcn_sched_barrier(0);  // every load above is issued before the first product
+  for (int c = 0; c < GT; ++c) {
+    j[c] = j0 + 16 * c;
+    j[GT + c] = j0 + 16 * c + inter;
+    tot[c] = tot[GT + c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  }
+  const int row = min(lane & 15, a.m - 1);
+  const uint16_t* arow = (const uint16_t*)a.x + row * a.ldx + a_group<WQ>() * h;
+  WTiles<WQ, 2 * GT> t;
+  w_tiles<WQ, 2 * GT>(t, shared ? a.s13 : a.w13, j, k, 16, lane);
+  const WaveShare ws = wave_share<WQ, kMoeWaves>(k, wave);
+  stream_units<TK, WQ, 2 * GT>(tot, t, arow, ws.first, ws.n, ws.part, k, h);
 #pragma unroll
-    for (int q = 0; q < UB; ++q)
-      if (u + q * kMoeWaves < units) mul_unit<TK, WQ, 2, 1, false>(w[q], x[q], tot, u + q * kMoeWaves, k);
-  }
-  if (k % kUnit != 0 && wave == units % kMoeWaves) {
-    WRaw<WQ> w[2];
-    u32x4 x[1][4];
-    load_unit<WQ, true>(w[0], col[0], units, k, h);
-    load_unit<WQ, true>(w[1], col[1], units, k, h);
-    load_a_unit<true>(x[0], arow, units, k);
-    mul_unit<TK, WQ, 2, 1, true>(w, x, tot, units, k);
-  }
-  red[wave][0][lane] = tot[0];
-  red[wave][1][lane] = tot[1];
+  for (int c = 0; c < 2 * GT; ++c) red[wave][c][lane] = tot[c];
   __syncthreads();
-  if (wave == 0) {
-    f32x4 g = red[0][0][lane], up = red[0][1][lane];
+  if (wave < GT) {
+    f32x4 g = red[0][wave][lane], up = red[0][GT + wave][lane];
 #pragma unroll
     for (int w = 1; w < kMoeWaves; ++w) {
-      g += red[w][0][lane];
-      up += red[w][1][lane];
+      g += red[w][wave][lane];
+      up += red[w][GT + wave][lane];
     }
-    uint16_t* hb = a.h + (shared ? (int64_t)a.max_slots * kGemvMaxM * NP * a.inter : (int64_t)slot * kGemvMaxM * NP * inter);
+    const float* weight = shared ? a.gates : a.slot_w + slot * kGemvMaxM;
+    uint16_t* hb = a.h + (shared ? a.max_slots : slot) * (int64_t)(kGemvMaxM * NP) * a.inter;
+    hb += 16 * (tile * GT + wave) + h_place<WQ>(lane & 15);
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const int t = 4 * h + q;
-      if (t < a.m && ((entry >> (16 + t)) & 1u) != 0) {
-        const float p = a.slot_w[slot * kGemvMaxM + t];
-        float v = g[q] / (1.0f + expf(-g[q])) * up[q] * p;
-        uint16_t* o = hb + (int64_t)t * NP * inter + 16 * tile + (lane & 15);
+      const int tk = 4 * h + q;
+      if (tk < a.m && ((entry >> (16 + tk)) & 1u) != 0) {
+        float v = g[q] / (1.0f + expf(-g[q])) * up[q] * weight[tk];
+        uint16_t* o = hb + (int64_t)tk * NP * inter;
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
           const uint16_t bits = f32_half<TK>(v);
@@ -253,119 +239,305 @@ __global__ __launch_bounds__(64 * kMoeWaves) void moe_up_kernel(MoeArgs a) {
   }
 }
 
-// One expert's share of one wave: units u, u + kMoeWaves, ... of its k = inter
-template <int TK, int WQ>
-__device__ __forceinline__ void down_expert(const WCol<WQ>& col, const uint16_t* hrow, bool served, int64_t inter, int u0,
-                                            int h, f32x4 (&tot)[1]) {
-  constexpr int NP = planes<TK>();
-  const int k = (int)inter;
-  for (int u = u0; u * kUnit < k; u += kMoeWaves) {
-    const bool part = u * kUnit + kUnit > k;
-    WRaw<WQ> w[1];
-    u32x4 x[NP][4];
-#pragma unroll
-    for (int p = 0; p < NP; ++p)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) x[p][i] = u32x4{0u, 0u, 0u, 0u};
-    if (!part) {
-      load_unit<WQ, false>(w[0], col, u, k, h);
-      if (served) {
-#pragma unroll
-        for (int p = 0; p < NP; ++p) load_a_unit<false>(x[p], hrow + p * inter, u, k);
-      }
-      mul_unit<TK, WQ, 1, NP, false>(w, x, tot, u, k);
-    } else {
-      load_unit<WQ, true>(w[0], col, u, k, h);
-      if (served) {
-#pragma unroll
-        for (int p = 0; p < NP; ++p) load_a_unit<true>(x[p], hrow + p * inter, u, k);
-      }
-      mul_unit<TK, WQ, 1, NP, true>(w, x, tot, u, k);
-    }
-  }
-}
+// The items (expert, unit of its k) that wave `id` of `step` takes, expert by
+// expert in the list's order: unit u of expert e goes to wave (e * units + u)
+// mod step.  step is a power of two; the shared expert, last in the list,
+// counts as expert 0 with units of its own.
+struct DownItems {
+  const uint32_t* list;  // nslots entries, then the shared expert's, if any
+  int slots;             // entries in all
+  int shared_slot;       // its place, or one past the list
+  int units, shared_units, id, step;
+  int s, u;              // the current item
+  uint32_t entry;
 
-template <int TK, int WQ>
-__global__ __launch_bounds__(64 * kMoeWaves) void moe_down_kernel(MoeArgs a) {
-  constexpr int NP = planes<TK>();
-  __shared__ f32x4 red[kMoeWaves][64];
+  __device__ __forceinline__ int units_of(int slot) const { return slot == shared_slot ? shared_units : units; }
+  __device__ __forceinline__ int first_of(int slot, uint32_t en) const {
+    return (slot == shared_slot ? id : id - (int)(en & 0xffffu) * units) & (step - 1);
+  }
+  __device__ __forceinline__ int count(int lane) const {
+    int n = 0;
+    for (int q = lane; q < slots; q += 64) {
+      const int f = first_of(q, list[q]), un = units_of(q);
+      n += f < un ? (un - 1 - f) / step + 1 : 0;
+    }
+    return (int)wave_sum_f32((float)n);  // (exact: far below 2^24)
+  }
+  __device__ __forceinline__ void begin() {
+    s = -1;
+    u = 0;
+    entry = 0;
+    next();
+  }
+  // to the next item; past the last one it stays there
+  __device__ __forceinline__ void next() {
+    int ns = s, nu = u + step;
+    uint32_t ne = entry;
+    while (ns < 0 || nu >= units_of(ns)) {
+      if (ns + 1 >= slots) return;
+      ++ns;
+      ne = (uint32_t)__builtin_amdgcn_readfirstlane((int)list[ns]);
+      nu = first_of(ns, ne);
+    }
+    s = ns;
+    u = nu;
+    entry = ne;
+  }
+};
+
+template <int TK, int WQ, int NP>
+__global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_down_kernel(MoeArgs a) {
+  constexpr int CT = 2;
+  constexpr int NB = unit_blocks<WQ>();
+  constexpr int UL = unit_len<WQ>();
+  __shared__ f32x4 red[kMoeWaves][CT][64];
+  __shared__ uint32_t list[kGemvMaxM * SKINNY_TOPK_MAX + 1];
+  __shared__ int last_s;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int h = lane >> 4;
   const int row = lane & 15;
-  const int64_t j = (int64_t)blockIdx.x * 16 + (lane & 15);
-  const int nslots = *a.nslots;
-  const int units = (int)((a.inter + kUnit - 1) / kUnit);
-  f32x4 tot[1] = {{0.0f, 0.0f, 0.0f, 0.0f}};
-  for (int s = 0; s < nslots; ++s) {
-    const uint32_t entry = __builtin_amdgcn_readfirstlane(a.slots[s]);
-    const int e = (int)(entry & 0xffffu);
-    // wave (e * units + u) mod kMoeWaves takes unit u of expert e
-    const int u0 = (wave - e * units) & (kMoeWaves - 1);
-    const WCol<WQ> col = w_col<WQ>(a.w2.codes, a.w2.scales, a.w2.zeros, (int64_t)e * a.d + j, a.inter, h);
-    const uint16_t* hrow = a.h + ((int64_t)s * kGemvMaxM + row) * NP * a.inter + 8 * h;
-    down_expert<TK, WQ>(col, hrow, ((entry >> (16 + row)) & 1u) != 0, a.inter, u0, h, tot);
-  }
-  if (a.shared_inter > 0) {
-    const WCol<WQ> col = w_col<WQ>(a.s2.codes, a.s2.scales, a.s2.zeros, j, a.shared_inter, h);
-    const uint16_t* hrow =
-        a.h + (int64_t)a.max_slots * kGemvMaxM * NP * a.inter + (int64_t)row * NP * a.shared_inter + 8 * h;
-    down_expert<TK, WQ>(col, hrow, row < a.m, a.shared_inter, wave, h, tot);
-  }
-  red[wave][lane] = tot[0];
+  const int split = blockIdx.x % a.down_splits;
+  const int tile = blockIdx.x / a.down_splits;
+  const int64_t j0 = (int64_t)tile * (16 * CT);
+
+  int nslots = *a.nslots;
+  for (int i = threadIdx.x; i < a.max_slots; i += 64 * kMoeWaves) list[i] = a.slots[i];
+  nslots = __builtin_amdgcn_readfirstlane(nslots);
   __syncthreads();
-  if (wave == 0) {
-    f32x4 sum = red[0][lane];
+  if (threadIdx.x == 0 && a.shared_inter > 0) list[nslots] = 0xffff0000u;
+  __syncthreads();
+
+  DownItems it;
+  it.list = list;
+  it.slots = nslots + (a.shared_inter > 0 ? 1 : 0);
+  it.shared_slot = nslots;
+  it.units = (int)((a.inter + UL - 1) / UL);
+  it.shared_units = (int)((a.shared_inter + UL - 1) / UL);
+  it.id = wave + kMoeWaves * split;
+  it.step = kMoeWaves * a.down_splits;
+  const int n = __builtin_amdgcn_readfirstlane(it.count(lane));
+
+  f32x4 tot[CT];
 #pragma unroll
-    for (int w = 1; w < kMoeWaves; ++w) sum += red[w][lane];
+  for (int c = 0; c < CT; ++c) tot[c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+  struct Item {
+    WUnit<WQ, CT> w;
+    ScaleRaw<WQ, CT> s;
+    u32x4 a[NP][NB];
+  };
+  // Load the current item.  A row that the expert does not serve reads zeros,
+  // and so do all rows in blocks past the expert's k, where the weight reads
+  // the unit's first block instead: every item is then multiplied whole, with
+  // no branch between the matrix-core steps.
+  auto load = [&](Item& q) __attribute__((always_inline)) {
+    const bool shared = it.s == it.shared_slot;
+    const int k = (int)(shared ? a.shared_inter : a.inter);
+    const WindowWeight& W = shared ? a.s2 : a.w2;
+    const int64_t j[CT] = {(shared ? 0 : (int64_t)(it.entry & 0xffffu) * a.d) + j0,
+                           (shared ? 0 : (int64_t)(it.entry & 0xffffu) * a.d) + j0 + 16};
+    WTiles<WQ, CT> t;
+    w_tiles<WQ, CT>(t, W, j, k, 16, lane);
+    const bool part = it.u * UL + UL > k;
+    const bool served = row < a.m && ((it.entry >> (16 + row)) & 1u) != 0;
+    const uint16_t* hr = a.h + (shared ? a.max_slots : it.s) * (int64_t)(kGemvMaxM * NP) * a.inter +
+                         (int64_t)row * NP * k + it.u * UL + a_group<WQ>() * h;
+    if constexpr (WQ == kWFull) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-      if (4 * h + q < a.m) store_kind(a.out, (4 * h + q) * a.ldo + j, sum[q], a.out_kind);
+      for (int i = 0; i < 2; ++i) {
+        const int at = part && it.u * UL + 32 * i >= k ? 0 : 64 * i;
+#pragma unroll
+        for (int c = 0; c < CT; ++c) q.w.v[c][i] = *(const u32x4*)(t.codes[c] + (int64_t)it.u * 128 + t.off + at);
+      }
+    } else {
+      const int at = part && it.u * UL + 32 * h >= k ? -16 * h : 0;
+#pragma unroll
+      for (int c = 0; c < CT; ++c) q.w.v[c][0] = *(const u32x4*)(t.codes[c] + (int64_t)it.u * 64 + t.off + at);
+      load_scale(q.s, t, (it.u * UL + 32 * h) / group_len<WQ>());
+    }
+#pragma unroll
+    for (int p = 0; p < NP; ++p) {
+      const uint16_t* hp = served ? hr + (int64_t)p * k : a.zero_page;
+#pragma unroll
+      for (int i = 0; i < NB; ++i) {
+        const uint16_t* hi = part && it.u * UL + 32 * i >= k ? a.zero_page : hp + a_step<WQ>() * i;
+        q.a[p][i] = *(const u32x4*)hi;
+      }
+    }
+  };
+  auto mul = [&](const Item& q) __attribute__((always_inline)) {
+    u32x4 sz[CT];
+    if constexpr (WQ != kWFull) {
+#pragma unroll
+      for (int c = 0; c < CT; ++c) {
+        const uint32_t own = (uint32_t)q.s.s[c] | ((uint32_t)q.s.z[c] << 16);
+        if constexpr (group_len<WQ>() == 128) {
+          sz[c][0] = own;
+        } else if constexpr (group_len<WQ>() == 64) {
+          auto v = __builtin_amdgcn_permlane32_swap(own, own, false, false);
+          sz[c][0] = v[0];
+          sz[c][1] = v[1];
+        } else {
+          sz[c] = spread4(own);
+        }
+      }
+    }
+    mul_unit<TK, WQ, CT, NP, true, false>(q.w, sz, q.a, tot, 0, 0);
+  };
+
+  if (n > 0) {
+    Item i0, i1;
+    it.begin();
+    load(i0);
+    it.next();  // (past the last item: the last again)
+    load(i1);
+    int left = n;
+#pragma unroll 1
+    while (left >= 4) {
+      mul(i0);
+      __builtin_amdgcn_sched_barrier(0);
+      it.next();
+      load(i0);
+      __builtin_amdgcn_sched_barrier(0);
+      mul(i1);
+      __builtin_amdgcn_sched_barrier(0);
+      it.next();
+      load(i1);
+      __builtin_amdgcn_sched_barrier(0);
+      left -= 2;
+    }
+    mul(i0);
+    if (left == 3) {
+      it.next();
+      load(i0);
+    }
+    if (left >= 2) mul(i1);
+    if (left == 3) mul(i0);
+  }
+
+#pragma unroll
+  for (int c = 0; c < CT; ++c) red[wave][c][lane] = tot[c];
+  __syncthreads();
+  const int64_t jc = j0 + 16 * wave + row;  // waves 0 and 1: this thread's column
+  if (wave < CT) {
+    f32x4 sum = red[0][wave][lane];
+#pragma unroll
+    for (int w = 1; w < kMoeWaves; ++w) sum += red[w][wave][lane];
+    if (a.down_splits == 1) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (4 * h + q < a.m) store_kind(a.out, (4 * h + q) * a.ldo + jc, sum[q], a.out_kind);
+    } else {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (4 * h + q < a.m) st_dev(a.partial + ((int64_t)split * kGemvMaxM + 4 * h + q) * a.d + jc, sum[q]);
+      wait_mem();  // this share has reached the device-coherent level
+    }
+  }
+  if (a.down_splits > 1) {
+    __syncthreads();  // both waves' shares have
+    if (threadIdx.x == 0) last_s = atomicAdd(&a.counters[tile], 1u) == (uint32_t)(a.down_splits - 1);
+    __syncthreads();
+    if (last_s && wave < CT) {
+      // every share is there: add them in order
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        if (4 * h + q < a.m) {
+          const float* p = a.partial + (int64_t)(4 * h + q) * a.d + jc;
+          float v[kMoeMaxSplits];
+#pragma unroll
+          for (int i = 0; i < kMoeMaxSplits; ++i)
+            v[i] = ld_dev(p + (int64_t)(i < a.down_splits ? i : 0) * kGemvMaxM * a.d);
+          float sum = v[0];
+#pragma unroll
+          for (int i = 1; i < kMoeMaxSplits; ++i) sum = i < a.down_splits ? sum + v[i] : sum;
+          store_kind(a.out, (4 * h + q) * a.ldo + jc, sum, a.out_kind);
+        }
+      }
+      if (threadIdx.x == 0) a.counters[tile] = 0u;  // ready for the next call
+    }
   }
 }
 
 typedef void (*moe_fn)(MoeArgs);
 
 template <int TK>
-moe_fn pick_up(int group) {
-  return group == 0    ? moe_up_kernel<TK, kWFull>
-         : group == 32 ? moe_up_kernel<TK, 32>
-         : group == 64 ? moe_up_kernel<TK, 64>
-                       : moe_up_kernel<TK, 128>;
+moe_fn pick_route(int experts) {
+  return experts <= 64    ? moe_route_kernel<TK, 1>
+         : experts <= 128 ? moe_route_kernel<TK, 2>
+         : experts <= 256 ? moe_route_kernel<TK, 4>
+         : experts <= 512 ? moe_route_kernel<TK, 8>
+                          : moe_route_kernel<TK, 16>;
 }
 
-template <int TK>
-moe_fn pick_down(int group) {
-  return group == 0    ? moe_down_kernel<TK, kWFull>
-         : group == 32 ? moe_down_kernel<TK, 32>
-         : group == 64 ? moe_down_kernel<TK, 64>
-                       : moe_down_kernel<TK, 128>;
+template <int TK, int WQ, int NP>
+moe_fn pick_stage(bool up, bool wide) {
+  return !up ? moe_down_kernel<TK, WQ, NP> : wide ? moe_up_kernel<TK, WQ, NP, 2> : moe_up_kernel<TK, WQ, NP, 1>;
+}
+
+template <int TK, int NP>
+moe_fn pick_weight(int group, bool zeros, bool up, bool wide) {
+  switch (group + (zeros ? kZeros : 0)) {
+    case 0: return pick_stage<TK, kWFull, NP>(up, wide);
+    case 32: return pick_stage<TK, 32, NP>(up, wide);
+    case 64: return pick_stage<TK, 64, NP>(up, wide);
+    case 128: return pick_stage<TK, 128, NP>(up, wide);
+    case 32 + kZeros: return pick_stage<TK, 32 + kZeros, NP>(up, wide);
+    case 64 + kZeros: return pick_stage<TK, 64 + kZeros, NP>(up, wide);
+    default: return pick_stage<TK, 128 + kZeros, NP>(up, wide);
+  }
+}
+
+moe_fn pick(int kind, int np, int group, bool zeros, bool up, bool wide) {
+  return kind == CK_F16 ? pick_weight<CK_F16, 2>(group, zeros, up, wide)
+         : np == 2      ? pick_weight<CK_BF16, 2>(group, zeros, up, wide)
+                        : pick_weight<CK_BF16, 3>(group, zeros, up, wide);
 }
 
 }  // namespace
 
-int moe_planes(int kind) { return kind == CK_F16 ? planes<CK_F16>() : planes<CK_BF16>(); }
+int moe_planes(int kind, int out_kind) { return kind == CK_BF16 && out_kind == CK_F32 ? 3 : 2; }
+
+// Shares of the down product's k: enough workgroups for about ten waves per CU
+// of 256, a power of two; by the output's width alone, which also fixes every
+// row's order of additions.
+int moe_down_splits(int64_t d) {
+  int s = 1;
+  while (s < kMoeMaxSplits && (d / 32) * s < 640) s *= 2;
+  return s;
+}
 
 hipError_t launch_moe(const MoeArgs& a, int kind, int group, hipStream_t stream) {
   if (a.m < 1 || a.m > kGemvMaxM || a.experts < 1 || a.experts > kMoeMaxExperts || a.topk < 1 ||
       a.topk > SKINNY_TOPK_MAX || a.topk > a.experts || a.d % 32 != 0 || a.inter % 32 != 0 || a.shared_inter % 32 != 0 ||
       (group != 0 && group != 32 && group != 64 && group != 128) ||
       (group != 0 && (a.d % group != 0 || a.inter % group != 0 || a.shared_inter % group != 0)) ||
-      (kind != CK_F16 && kind != CK_BF16))
+      (kind != CK_F16 && kind != CK_BF16) || a.down_splits != moe_down_splits(a.d))
     return hipErrorInvalidValue;
   const int64_t slots = (int64_t)a.m * a.topk < a.experts ? (int64_t)a.m * a.topk : a.experts;
-  const int64_t up_blocks = slots * (a.inter / 16) + a.shared_inter / 16;
-  if (slots > a.max_slots || up_blocks > 0x7fffffff) return hipErrorInvalidValue;
+  if (slots > a.max_slots || a.max_slots > kGemvMaxM * SKINNY_TOPK_MAX) return hipErrorInvalidValue;
+  // two column tiles of h per workgroup where that still leaves many
+  // workgroups: the loads of x serve twice the columns (a column's arithmetic
+  // does not depend on it)
+  const bool wide = slots * (a.inter / 32) >= 2048;
+  const int64_t tile = wide ? 32 : 16;
+  const int64_t up_blocks = slots * (a.inter / tile) + a.shared_inter / tile;
+  const int64_t down_blocks = a.d / 32 * a.down_splits;
+  if (up_blocks > 0x7fffffff) return hipErrorInvalidValue;
+  const int np = moe_planes(kind, a.out_kind);
+  const bool zeros = a.w13.zeros != nullptr;
   const bool f16 = kind == CK_F16;
-  hipLaunchKernelGGL(f16 ? moe_route_kernel<CK_F16> : moe_route_kernel<CK_BF16>, dim3(1), dim3(64 * a.m), 0, stream, a);
+  hipLaunchKernelGGL(f16 ? pick_route<CK_F16>(a.experts) : pick_route<CK_BF16>(a.experts),
+                     dim3(a.shared_inter > 0 ? 2 : 1), dim3(64 * a.m), 0, stream, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(f16 ? pick_up<CK_F16>(group) : pick_up<CK_BF16>(group), dim3((unsigned)up_blocks),
-                     dim3(64 * kMoeWaves), 0, stream, a);
+  hipLaunchKernelGGL(pick(kind, np, group, zeros, true, wide), dim3((unsigned)up_blocks), dim3(64 * kMoeWaves), 0,
+                     stream, a);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(f16 ? pick_down<CK_F16>(group) : pick_down<CK_BF16>(group), dim3((unsigned)(a.d / 16)),
-                     dim3(64 * kMoeWaves), 0, stream, a);
+  hipLaunchKernelGGL(pick(kind, np, group, zeros, false, false), dim3((unsigned)down_blocks), dim3(64 * kMoeWaves), 0,
+                     stream, a);
   return hipGetLastError();
 }
 

@@ -35,6 +35,11 @@ __device__ __forceinline__ int order_key(float x) {
   return (int)(b ^ ((uint32_t)((int)b >> 31) & 0x7fffffffu));
 }
 
+// the float whose order key is `key` (-0 comes back as +0)
+__device__ __forceinline__ float key_value(int key) {
+  return fbits((uint32_t)key ^ ((uint32_t)(key >> 31) & 0x7fffffffu));
+}
+
 template <int CTRL>
 __device__ __forceinline__ int dpp_mov_i(int x) {
   return (int)__builtin_amdgcn_update_dpp(0u, (uint32_t)x, CTRL, 0xF, 0xF, false);
