@@ -485,7 +485,7 @@ class W4:
     weight = scale * (code - zero).  Checked once, here; the tensors are kept
     alive and read at every call."""
 
-    __slots__ = ("codes", "scales", "zeros", "shape", "group", "dtype", "device", "_desc", "_addr")
+    __slots__ = ("codes", "scales", "zeros", "shape", "group", "dtype", "device", "_desc", "_addr", "_index")
 
     def __init__(self, codes, scales, zeros=None):
         if codes.dtype != torch.uint8 or scales.dtype not in (torch.float16, torch.bfloat16) or \
@@ -505,6 +505,7 @@ class W4:
         self.dtype, self.device = scales.dtype, codes.device
         self._desc = W4Desc(codes.data_ptr(), scales.data_ptr(), 0 if zeros is None else zeros.data_ptr())
         self._addr = ctypes.addressof(self._desc)
+        self._index = codes.get_device()
 
 
 def _on(where, device, *tensors):
@@ -514,14 +515,35 @@ def _on(where, device, *tensors):
 
 
 def _rows(where, name, t):
-    """Row stride of a matrix whose rows are dense (a single row has any)."""
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+    """Row stride of a matrix whose rows are dense (0: a single row)."""
+    shape = t.shape
+    if len(shape) != 2 or (shape[1] > 1 and t.stride(1) != 1):
         raise ValueError(f"{where}: {name} must be a matrix with contiguous rows")
-    return t.stride(0) if t.shape[0] > 1 else 0
+    return t.stride(0) if shape[0] > 1 else 0
 
 
-def _stream_of(device, stream):
-    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+# A window's calls take a few microseconds on the GPU, so what the host does
+# for each of them counts: types are looked up, streams come as raw handles.
+_CODES = {torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32}
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _handle(index, stream):
+    """Raw handle of `stream`, or of the current stream of GPU `index`."""
+    return _raw_stream(index) if stream is None else stream.cuda_stream
+
+
+def _gpu(where, t):
+    index = t.get_device()
+    if index < 0:
+        raise ValueError(f"{where}: tensors must be on a GPU")
+    return index
+
+
+def _zeros_on(nbytes, index, stream):
+    """nbytes zero bytes on GPU `index`, allocated and filled on `stream` or its current stream."""
+    with torch.cuda.stream(torch.cuda.current_stream(index) if stream is None else stream):
+        return torch.zeros(nbytes, dtype=torch.uint8, device=torch.device("cuda", index))
 
 
 def mm_w4(A, W, out=None, out_dtype=None, stream=None):
@@ -531,24 +553,27 @@ def mm_w4(A, W, out=None, out_dtype=None, stream=None):
     `out_dtype` says otherwise."""
     lda = _rows("mm_w4", "A", A)
     m, k = A.shape
-    if not isinstance(W, W4) or W.dtype != A.dtype:
-        raise TypeError(f"mm_w4: the weight must be a W4 with scales of A's type ({A.dtype})")
+    dtype = A.dtype
+    if not isinstance(W, W4) or W.dtype is not dtype:
+        raise TypeError(f"mm_w4: the weight must be a W4 with scales of A's type ({dtype})")
     if len(W.shape) != 2 or W.shape[1] != k:
         raise ValueError(f"mm_w4: a weight {W.shape} does not fit k = {k}")
-    n, device = W.shape[0], A.device
-    if W.device != device:
-        raise ValueError(f"mm_w4: A is on {device}, the weight on {W.device}")
+    n = W.shape[0]
+    index = _gpu("mm_w4", A)
+    if W._index != index:
+        raise ValueError(f"mm_w4: A is on {A.device}, the weight on {W.device}")
     if out is None:
-        out = torch.empty((m, n), dtype=out_dtype or torch.float32, device=device)
+        out_dtype = out_dtype or torch.float32
+        out = torch.empty((m, n), dtype=out_dtype, device=W.device)
         ldc = n
     else:
         ldc = _rows("mm_w4", "out", out)
+        out_dtype = out.dtype
         if tuple(out.shape) != (m, n):
             raise ValueError("mm_w4: out must be [m][n]")
-        _on("mm_w4", device, out)
-    _check(_lib.skinny_w4_mm_run(m, n, k, W.group, A.data_ptr(), lda, _dtype_code(A.dtype, "A"), W._addr,
-                                 out.data_ptr(), ldc, _dtype_code(out.dtype, "C"), _stream_of(device, stream)),
-           "skinny_w4_mm_run")
+        _on("mm_w4", W.device, out)
+    _check(_lib.skinny_w4_mm_run(m, n, k, W.group, A.data_ptr(), lda, _CODES[dtype], W._addr, out.data_ptr(), ldc,
+                                 _CODES.get(out_dtype, 0), _handle(index, stream)), "skinny_w4_mm_run")
     return out
 
 
@@ -609,7 +634,9 @@ class MoELayer:
         self.experts, self.d, self.inter, self.shared_inter, self.topk = experts, d, inter, shared_inter, topk
         self.dtype, self.device, self.max_m = dtype, device, max_m
         self.out_dtype = out_dtype or dtype
+        self._index = _gpu("MoELayer", router)
         self._weights = MoEWeightsDesc(router.data_ptr(), *descs, shared_gate.data_ptr() if shared_inter else None)
+        self._weights_addr = ctypes.addressof(self._weights)
         code = _dtype_code(dtype, "router")
         desc = MoEDesc(ctypes.sizeof(MoEDesc), code, DTYPE_W4 if w4 else code, _dtype_code(self.out_dtype, "out"), group,
                        topk, max_m, d, inter, shared_inter, experts, 0, 0, MOE_RENORM if renorm else 0, num_cus)
@@ -622,40 +649,40 @@ class MoELayer:
         self.workspace_bytes = int(sz.value)
         self._ws = {}
 
-    def workspace(self, stream=None):
+    def _workspace(self, handle, stream):
         """This layer's workspace for a stream (runs on different streams may be
-        in flight at once, so each has its own), allocated and zero-filled on it."""
-        if stream is None:
-            stream = torch.cuda.current_stream(self.device)
-        key = stream.cuda_stream
-        ws = self._ws.get(key)
+        in flight at once, so each has its own)."""
+        ws = self._ws.get(handle)
         if ws is None:
-            with torch.cuda.stream(stream):
-                ws = torch.zeros(self.workspace_bytes, dtype=torch.uint8, device=self.device)
-            self._ws[key] = ws
+            ws = self._ws[handle] = _zeros_on(self.workspace_bytes, self._index, stream)
         return ws
 
     def __call__(self, x, out=None, topk_idx=None, topk_weight=None, stream=None):
         """out [m][d]; topk_idx (int32 [m][topk]) and topk_weight (float32
         [m][topk]) receive the routing when given."""
-        if x.dim() != 2 or x.shape[1] != self.d or x.dtype != self.dtype:
-            raise ValueError(f"MoELayer: x must be [m][{self.d}] of type {self.dtype}")
-        m = x.shape[0]
+        shape = x.shape
+        if len(shape) != 2 or shape[1] != self.d or x.dtype is not self.dtype or not x.is_contiguous():
+            raise ValueError(f"MoELayer: x must be contiguous [m][{self.d}] of type {self.dtype}")
+        if x.get_device() != self._index:
+            raise ValueError(f"MoELayer: x must be on {self.device}")
+        m = shape[0]
         if out is None:
             out = torch.empty((m, self.d), dtype=self.out_dtype, device=self.device)
-        elif tuple(out.shape) != (m, self.d) or out.dtype != self.out_dtype:
-            raise ValueError(f"MoELayer: out must be [{m}][{self.d}] of type {self.out_dtype}")
+        else:
+            if tuple(out.shape) != (m, self.d) or out.dtype != self.out_dtype:
+                raise ValueError(f"MoELayer: out must be [{m}][{self.d}] of type {self.out_dtype}")
+            _dense("MoELayer", out=out)
+            _on("MoELayer", self.device, out)
         for name, t, dt in (("topk_idx", topk_idx, torch.int32), ("topk_weight", topk_weight, torch.float32)):
-            if t is not None and (tuple(t.shape) != (m, self.topk) or t.dtype != dt):
-                raise ValueError(f"MoELayer: {name} must be {dt} [{m}][{self.topk}]")
-        _dense("MoELayer", x=x, out=out, topk_idx=topk_idx, topk_weight=topk_weight)
-        _on("MoELayer", self.device, x, out, topk_idx, topk_weight)
-        if stream is None:
-            stream = torch.cuda.current_stream(self.device)
-        ws = self.workspace(stream)
-        _check(_lib.skinny_moe_run(self._h, m, x.data_ptr(), ctypes.addressof(self._weights), out.data_ptr(),
-                                   _ptr(topk_idx), _ptr(topk_weight), ws.data_ptr(), self.workspace_bytes,
-                                   stream.cuda_stream), "skinny_moe_run")
+            if t is not None:
+                if tuple(t.shape) != (m, self.topk) or t.dtype != dt:
+                    raise ValueError(f"MoELayer: {name} must be {dt} [{m}][{self.topk}]")
+                _dense("MoELayer", **{name: t})
+                _on("MoELayer", self.device, t)
+        handle = _handle(self._index, stream)
+        ws = self._workspace(handle, stream)
+        _check(_lib.skinny_moe_run(self._h, m, x.data_ptr(), self._weights_addr, out.data_ptr(), _ptr(topk_idx),
+                                   _ptr(topk_weight), ws.data_ptr(), self.workspace_bytes, handle), "skinny_moe_run")
         return out
 
     def __del__(self):
@@ -671,7 +698,8 @@ class MoELayer:
 class TokenLogprobs(NamedTuple):
     """What token_logprobs gives: per row the token's log probability, the
     distribution's entropy in nats, the token's rank (1: the largest logit),
-    and the top alternatives' ids and log probabilities."""
+    and the top alternatives' ids and log probabilities.  The five share one
+    allocation."""
     logprob: "torch.Tensor"       # float32 [m]
     entropy: "torch.Tensor"       # float32 [m]
     rank: "torch.Tensor"          # int32 [m]
@@ -679,18 +707,16 @@ class TokenLogprobs(NamedTuple):
     top_logprobs: "torch.Tensor"  # float32 [m][topk]
 
 
+_logprob_need = {}  # (m, vocab, topk) -> workspace bytes
 _logprob_ws = {}
 
 
-def _logprob_workspace(nbytes, device, stream):
-    """The log probabilities' workspace of one (device, stream) pair, grown to
-    the largest run it has seen (a run leaves its counters at zero)."""
-    key = (device, stream.cuda_stream)
-    ws = _logprob_ws.get(key)
+def _logprob_workspace(nbytes, index, handle, stream):
+    """The log probabilities' workspace of one stream, grown to the largest run
+    it has seen (a run leaves its counters at zero)."""
+    ws = _logprob_ws.get((index, handle))
     if ws is None or ws.numel() < nbytes:
-        with torch.cuda.stream(stream):
-            ws = torch.zeros(nbytes, dtype=torch.uint8, device=device)
-        _logprob_ws[key] = ws
+        ws = _logprob_ws[index, handle] = _zeros_on(nbytes, index, stream)
     return ws
 
 
@@ -702,23 +728,29 @@ def token_logprobs(logits, tokens, topk=0, stream=None):
     is masked out; a token outside the row gives NaN and rank 0."""
     ld = _rows("token_logprobs", "logits", logits)
     m, vocab = logits.shape
-    if tuple(tokens.shape) != (m,) or tokens.dtype not in (torch.int64, torch.int32):
-        raise ValueError(f"token_logprobs: tokens must be int64 or int32 [{m}]")
-    device = logits.device
-    _dense("token_logprobs", tokens=tokens)
-    _on("token_logprobs", device, tokens)
-    dtype = _dtype_code(logits.dtype, "logits")
-    sz = ctypes.c_size_t()
-    _check(_lib.skinny_token_logprobs_workspace_size(m, vocab, topk, ctypes.byref(sz)), "token_logprobs")
-    if stream is None:
-        stream = torch.cuda.current_stream(device)
-    ws = _logprob_workspace(sz.value, device, stream) if sz.value else None
-    f = torch.empty((2 + topk, m), dtype=torch.float32, device=device)
-    i = torch.empty((1 + topk, m), dtype=torch.int32, device=device)
-    out = TokenLogprobs(f[0], f[1], i[0], i[1:].view(m, topk), f[2:].view(m, topk))
-    _check(_lib.skinny_token_logprobs_run(m, vocab, logits.data_ptr(), ld, dtype, tokens.data_ptr(),
-                                          int(tokens.dtype == torch.int64), topk, out.logprob.data_ptr(),
-                                          out.entropy.data_ptr(), out.rank.data_ptr(), out.top_ids.data_ptr(),
-                                          out.top_logprobs.data_ptr(), _ptr(ws), 0 if ws is None else ws.numel(),
-                                          stream.cuda_stream), "skinny_token_logprobs_run")
-    return out
+    t64 = tokens.dtype is torch.int64
+    if tuple(tokens.shape) != (m,) or not (t64 or tokens.dtype is torch.int32) or not tokens.is_contiguous():
+        raise ValueError(f"token_logprobs: tokens must be contiguous int64 or int32 [{m}]")
+    dtype = _CODES.get(logits.dtype)
+    if dtype is None:
+        raise TypeError(f"token_logprobs: unsupported dtype {logits.dtype}")
+    index = _gpu("token_logprobs", logits)
+    if tokens.get_device() != index:
+        raise ValueError("token_logprobs: logits and tokens must be on one GPU")
+    need = _logprob_need.get((m, vocab, topk))
+    if need is None:
+        sz = ctypes.c_size_t()
+        _check(_lib.skinny_token_logprobs_workspace_size(m, vocab, topk, ctypes.byref(sz)), "token_logprobs")
+        if len(_logprob_need) > 4096:
+            _logprob_need.clear()
+        need = _logprob_need[m, vocab, topk] = int(sz.value)
+    handle = _handle(index, stream)
+    ws = _logprob_workspace(need, index, handle, stream).data_ptr() if need else None
+    # one allocation for the five results, each at a multiple of 4 bytes
+    flat = torch.empty(m * (3 + 2 * topk), dtype=torch.float32, device=logits.device)
+    lp, ent, top, rank, ids = flat.split([m, m, m * topk, m, m * topk])
+    p = flat.data_ptr()
+    p_rank = p + 4 * m * (2 + topk)
+    _check(_lib.skinny_token_logprobs_run(m, vocab, logits.data_ptr(), ld, dtype, tokens.data_ptr(), t64, topk, p, p + 4 * m,
+                                          p_rank, p_rank + 4 * m, p + 8 * m, ws, need, handle), "skinny_token_logprobs_run")
+    return TokenLogprobs(lp, ent, rank.view(torch.int32), ids.view(torch.int32).view(m, topk), top.view(m, topk))

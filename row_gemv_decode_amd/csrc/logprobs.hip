@@ -14,13 +14,16 @@
 // rescales it when its maximum grows; nothing crosses lanes until the end of
 // the row.  Exponentials are base 2: S and U of exp2(d log2 e).
 //
-// Top-k: every wave keeps the best candidates it has seen in a list over its
-// lanes, lane i the i-th best, and the topk-th of them is a bar.  A chunk
-// without a lane whose maximum reaches the bar costs one comparison.  Entries
-// above it are inserted one by one: a ballot finds the place, a DPP shift
-// makes room.  When many lanes reach the bar at once (the first chunk, or
-// logits in rising order) the topk-th largest of the 64 lane maxima, found bit
-// by bit with ballots, is a better bar: at least topk entries are above it.
+// Top-k: every wave keeps the best entries it has seen in a list over its
+// lanes, lane i the i-th best, and the topk-th of them is a bar.  An entry is a
+// 64-bit key: the logit's order key above, the complement of its index below,
+// so one comparison ranks by value and then by lower index.  A chunk without a
+// lane whose maximum reaches the bar costs one comparison.  When many lanes
+// reach it (the first chunk, or logits in rising order) the topk-th largest of
+// the 64 lane maxima, found bit by bit with ballots, is a better bar: at least
+// topk entries are at or above it.  The entries that qualify are gathered in
+// LDS; when 64 have come together they are sorted over the lanes by a bitonic
+// network and merged with the list.
 //
 // Segments of one row leave their (M, S, U), rank count and list in the
 // workspace; the last workgroup of the row to arrive joins them, in the order
@@ -33,8 +36,6 @@ namespace skinny {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWaves = kThreads / 64;
 constexpr int kNone = 0x7fffff00;  // index of an entry that holds no logit (V stays below it)
 constexpr float kLowest = -3.402823466e38f;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -131,66 +132,147 @@ __device__ __forceinline__ Soft wave_join(Soft a) {
   return a;
 }
 
-// A wave's list: lane i holds the i-th best entry; (bar, bar_i) is its topk-th.
-struct List {
-  float v;
-  int i;
-  float bar;
-  int bar_i;
-};
+// --- entries and lists -------------------------------------------------------
+__device__ __forceinline__ uint64_t entry_of(float v, int i) {
+  return ((uint64_t)((uint32_t)order_key(v) ^ 0x80000000u) << 32) | (uint32_t)~i;
+}
+__device__ __forceinline__ float entry_value(uint64_t e) { return key_value((int)((uint32_t)(e >> 32) ^ 0x80000000u)); }
+__device__ __forceinline__ int entry_index(uint64_t e) { return (int)~(uint32_t)e; }
 
-__device__ __forceinline__ void list_clear(List& l) {
-  l.v = -__builtin_inff();
-  l.i = kNone;
-  l.bar = l.v;
-  l.bar_i = kNone;
+constexpr uint32_t kKeyNegInf = 0x007fffffu;  // upper half of -inf's entry
+constexpr uint32_t kKeyLowest = 0x00800000u;  // of kLowest's
+constexpr uint64_t kNoEntry = ((uint64_t)kKeyNegInf << 32) | (uint32_t)~kNone;
+
+__device__ __forceinline__ uint64_t join64(uint32_t lo, uint32_t hi) { return ((uint64_t)hi << 32) | lo; }
+
+// a DPP move that reads a lane for every lane: no old value is needed, which
+// saves the move that would set it
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_all(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, true);
 }
 
-__device__ __forceinline__ bool over_bar(const List& l, float v, int i) {
-  return v > l.bar || (v == l.bar && i < l.bar_i);
-}
-
-// insert the wave-uniform entry (v, i); it is over the bar
-__device__ __forceinline__ void list_insert(List& l, float v, int i, int topk, int lane) {
-  const uint64_t ahead = __builtin_amdgcn_ballot_w64(l.v > v || (l.v == v && l.i < i));
-  const int pos = __builtin_popcountll(ahead);
-  const float up_v = dpp_mov<0x138>(l.v);  // wave_shr:1, lane i takes lane i - 1's
-  const int up_i = dpp_mov_i<0x138>(l.i);
-  l.v = lane < pos ? l.v : lane == pos ? v : up_v;
-  l.i = lane < pos ? l.i : lane == pos ? i : up_i;
-  l.bar = fbits(__builtin_amdgcn_readlane(ubits(l.v), topk - 1));
-  l.bar_i = (int)__builtin_amdgcn_readlane((uint32_t)l.i, topk - 1);
-}
-
-// insert every lane's entry (v, i) that is over the bar and at least `least`
-__device__ __forceinline__ void list_add(List& l, float v, int i, float least, int topk, int lane) {
-  uint64_t b = __builtin_amdgcn_ballot_w64(v >= least && over_bar(l, v, i));
-  while (b != 0) {
-    const int from = __builtin_ctzll(b);
-    list_insert(l, fbits(__builtin_amdgcn_readlane(ubits(v), from)),
-                (int)__builtin_amdgcn_readlane((uint32_t)i, from), topk, lane);
-    b = (b & (b - 1)) & __builtin_amdgcn_ballot_w64(over_bar(l, v, i));
+// the value of lane ^ J
+template <int J>
+__device__ __forceinline__ uint32_t lane_xor(uint32_t v, int lane) {
+  if constexpr (J == 1) {
+    return dpp_all<kDppXor1>(v);
+  } else if constexpr (J == 2) {
+    return dpp_all<kDppXor2>(v);
+  } else if constexpr (J == 4) {  // 7 ^ 3
+    return dpp_all<0x1B>(dpp_all<kDppRowHalfMirror>(v));
+  } else if constexpr (J == 8) {  // a rotation by 8 in the row of 16
+    return dpp_all<0x128>(v);
+  } else if constexpr (J == 16) {
+    auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    return (lane & 16) != 0 ? r[0] : r[1];
+  } else {
+    auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    return (lane & 32) != 0 ? r[0] : r[1];
   }
 }
 
-// the topk-th largest of the lanes' values: its order key, bit by bit
-__device__ __forceinline__ float kth_of_lanes(float v, int topk) {
+// lanes that keep the larger of a pair at stride J of a network of blocks of K
+constexpr uint64_t keep_larger(int K, int J) {
+  uint64_t m = 0;
+  for (int l = 0; l < 64; ++l)
+    if (((l & J) == 0) == ((l & K) == 0)) m |= 1ull << l;
+  return m;
+}
+template <int K, int J>
+__device__ __forceinline__ uint64_t exchange(uint64_t v, int lane) {
+  const uint64_t o = join64(lane_xor<J>((uint32_t)v, lane), lane_xor<J>((uint32_t)(v >> 32), lane));
+  const uint64_t larger = __builtin_amdgcn_ballot_w64(v > o);
+  return __builtin_amdgcn_inverse_ballot_w64(~(larger ^ keep_larger(K, J))) ? v : o;
+}
+template <int K, int J>
+__device__ __forceinline__ uint64_t exchanges(uint64_t v, int lane) {
+  v = exchange<K, J>(v, lane);
+  if constexpr (J > 1) v = exchanges<K, J / 2>(v, lane);
+  return v;
+}
+// descending over the lanes
+__device__ __forceinline__ uint64_t lane_sort(uint64_t v, int lane) {
+  v = exchanges<2, 1>(v, lane);
+  v = exchanges<4, 2>(v, lane);
+  v = exchanges<8, 4>(v, lane);
+  v = exchanges<16, 8>(v, lane);
+  v = exchanges<32, 16>(v, lane);
+  return exchanges<64, 32>(v, lane);
+}
+// the value of lane 63 - lane
+__device__ __forceinline__ uint32_t lane_reverse(uint32_t v, int lane) {
+  return lane_xor<32>(lane_xor<16>(dpp_all<kDppRowMirror>(v), lane), lane);
+}
+
+// A wave's list: lane i holds the i-th best entry; `bar` is the topk-th, and no
+// logit below bar_value can be among the topk best any more (wave-uniform).
+struct List {
+  uint64_t e;
+  uint64_t bar;
+  float bar_value;
+};
+
+__device__ __forceinline__ void list_bar(List& l, int topk) {
+  l.bar = join64(__builtin_amdgcn_readlane((uint32_t)l.e, topk - 1),
+                 __builtin_amdgcn_readlane((uint32_t)(l.e >> 32), topk - 1));
+  l.bar_value = fmaxf(l.bar_value, entry_value(l.bar));
+}
+
+__device__ __forceinline__ void list_clear(List& l) {
+  l.e = l.bar = kNoEntry;
+  l.bar_value = -__builtin_inff();
+}
+
+// add 64 entries that descend over the lanes
+__device__ __forceinline__ void list_merge_sorted(List& l, uint64_t e, int topk, int lane) {
+  const uint64_t r = join64(lane_reverse((uint32_t)e, lane), lane_reverse((uint32_t)(e >> 32), lane));
+  l.e = exchanges<64, 32>(l.e > r ? l.e : r, lane);  // the 64 best of both, a bitonic sequence
+  list_bar(l, topk);
+}
+
+// entries waiting to be added: n in a wave's part of LDS
+constexpr int kPending = 64 + 4 * 64;
+struct Pending {
+  uint64_t* e;
+  int n;
+};
+
+__device__ __forceinline__ void wave_lds_order() {  // LDS writes of the wave before its later reads, and the reverse
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+__device__ __forceinline__ void list_flush(List& l, Pending& p, int topk, int lane) {
+  wave_lds_order();
+#pragma unroll 1
+  for (int i = 0; i < p.n; i += 64)
+    list_merge_sorted(l, lane_sort(i + lane < p.n ? p.e[i + lane] : kNoEntry, lane), topk, lane);
+  p.n = 0;
+  wave_lds_order();
+}
+
+// A bar from the lanes' values: at least topk of them are at or above it.  The
+// topk-th largest order key, found bit by bit in its upper 16 bits (the lower
+// ones would only save a few candidates).
+__device__ __forceinline__ float bar_of_lanes(float v, int topk) {
   const uint32_t key = (uint32_t)order_key(v) ^ 0x80000000u;
   uint32_t t = 0;
-  for (int bit = 31; bit >= 0; --bit) {
+#pragma unroll
+  for (int bit = 31; bit >= 16; --bit) {
     const uint32_t c = t | (1u << bit);
     t = __builtin_popcountll(__builtin_amdgcn_ballot_w64(key >= c)) >= topk ? c : t;
   }
-  const int k = (int)(t ^ 0x80000000u);
-  return fbits((uint32_t)k ^ ((uint32_t)(k >> 31) & 0x7fffffffu));
+  t = t <= kKeyLowest ? kKeyNegInf : t;  // a running maximum starts at kLowest: no logit stands for that
+  return key_value((int)(t ^ 0x80000000u));
 }
 
 // N logits per lane into the running state, the list and the rank count.
 // idx[q]: index of x[q * per], or kNone where a lane has none (x = -inf there).
 // where: -1 all indices lie before the token, 1 after it, 0 neither.
 template <int N, int PER>
-__device__ __forceinline__ void take(const float (&x)[N], const int (&idx)[N / PER], Soft& a, List& l, int& above,
-                                     float xt, int tok, int where, int topk, int lane) {
+__device__ __forceinline__ void take(const float (&x)[N], const int (&idx)[N / PER], Soft& a, List& l, Pending& pend,
+                                     int& above, float xt, int tok, int where, int topk, int lane) {
   float top = x[0];
 #pragma unroll
   for (int e = 1; e < N; ++e) top = fmaxf(top, x[e]);
@@ -215,38 +297,46 @@ __device__ __forceinline__ void take(const float (&x)[N], const int (&idx)[N / P
           __builtin_amdgcn_ballot_w64(x[e] > xt || (x[e] == xt && idx[e / PER] + e % PER < tok)));
   }
   if (topk > 0) {
-    const uint64_t b = __builtin_amdgcn_ballot_w64(top >= l.bar);
+    const uint64_t b = __builtin_amdgcn_ballot_w64(top >= l.bar_value);
     if (b != 0) {
-      const float least = __builtin_popcountll(b) > 8 ? kth_of_lanes(top, topk) : l.bar;
+      // Every lane's maximum so far, where it reaches the lanes' bar, has been
+      // gathered or is gathered below, and so have topk entries at least: the
+      // bar can replace a lower one before they reach the list.
+      if (__builtin_popcountll(b) > 8) l.bar_value = fmaxf(l.bar_value, bar_of_lanes(a.m, topk));
 #pragma unroll
-      for (int e = 0; e < N; ++e) list_add(l, x[e], idx[e / PER] + e % PER, least, topk, lane);
+      for (int e = 0; e < N; ++e) {
+        if (__builtin_amdgcn_ballot_w64(x[e] >= l.bar_value) != 0) {  // uniform
+          const uint64_t en = entry_of(x[e], idx[e / PER] + e % PER);
+          const bool in = x[e] >= l.bar_value && en > l.bar;  // (false for NaN)
+          const uint64_t q = __builtin_amdgcn_ballot_w64(in);
+          if (in) pend.e[pend.n + __builtin_popcountll(q & ((1ull << lane) - 1))] = en;
+          pend.n += __builtin_popcountll(q);
+        }
+        if (e % 4 == 3 && pend.n > 64) list_flush(l, pend, topk, lane);  // (room for four more times 64)
+      }
     }
   }
 }
 
-template <int XK>
-__global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobArgs g) {
+template <int XK, int kWaves>
+__global__ __launch_bounds__(64 * kWaves) void logprobs_kernel(LogprobArgs g) {
+  constexpr int kThreads = 64 * kWaves;
   constexpr int VE = vec_elems<XK>();
   constexpr int NV = 16 / VE;  // 16 logits per thread and step
   constexpr int ES = XK == CK_F32 ? 4 : 2;
   __shared__ Soft soft_s[kWaves];
   __shared__ int above_s[kWaves];
-  __shared__ float list_v[kWaves][SKINNY_TOPK_MAX];
-  __shared__ int list_i[kWaves][SKINNY_TOPK_MAX];
+  __shared__ uint64_t list_s[kWaves][SKINNY_TOPK_MAX];
+  __shared__ uint64_t pending_s[kWaves][kPending];
   __shared__ int last_s;
   const int tid = threadIdx.x;
   const int lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int topk = g.topk;
-  const int64_t r = (int64_t)blockIdx.x / g.segments;
-  const int seg = (int)((int64_t)blockIdx.x - r * g.segments);
+  const uint32_t row_index = blockIdx.x / (uint32_t)g.segments;
+  const int64_t r = row_index;
+  const int seg = (int)(blockIdx.x - row_index * (uint32_t)g.segments);
   const char* row = (const char*)g.logits + r * g.ld * ES;
-
-  // the token and its logit; a token outside the row has none
-  const int64_t token = g.tokens64 ? ((const int64_t*)g.tokens)[r] : (int64_t)((const int32_t*)g.tokens)[r];
-  const bool known = token >= 0 && token < g.vocab;
-  const int tok = known ? (int)token : 0;
-  const float xt = to_f32<XK>(row, tok);
 
   // this segment: first .. first + len - 1, in vectors of 16 bytes and, after
   // them, single logits.  A row may start at any element; its vectors are then
@@ -260,12 +350,19 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobArgs g) {
   Soft a = {kLowest, 0.0f, 0.0f};
   List l;
   list_clear(l);
+  Pending pend = {pending_s[wave], 0};
   int above = 0;
 
-  u32x4 raw[NV];
+  u32x4 raw[NV];  // the first loads are on their way before anything waits
 #pragma unroll
   for (int q = 0; q < NV; ++q)
     if (q * kThreads + tid < nvec) raw[q] = load16<ES>(vec + (int64_t)(q * kThreads + tid) * 16);
+  // the token and its logit; a token outside the row has none
+  const int64_t token = g.tokens64 ? ((const int64_t*)g.tokens)[r] : (int64_t)((const int32_t*)g.tokens)[r];
+  const bool known = token >= 0 && token < g.vocab;
+  const int tok = known ? (int)token : 0;
+  const float xt = to_f32<XK>(row, tok);
+
   for (int c = 0; c < nvec; c += NV * kThreads) {
     float x[NV * VE];
     int idx[NV];
@@ -274,10 +371,15 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobArgs g) {
       const int v = c + q * kThreads + tid;
       unpack<XK>(raw[q], &x[q * VE]);
       idx[q] = first + v * VE;
-      if (v >= nvec) {
-        idx[q] = kNone;
+    }
+    const bool full = c + NV * kThreads <= nvec;  // uniform: only the last step is not
+    if (!full) {
 #pragma unroll
-        for (int e = 0; e < VE; ++e) x[q * VE + e] = -__builtin_inff();
+      for (int q = 0; q < NV; ++q) {
+        const bool out = c + q * kThreads + tid >= nvec;
+        idx[q] = out ? kNone : idx[q];
+#pragma unroll
+        for (int e = 0; e < VE; ++e) x[q * VE + e] = out ? -__builtin_inff() : x[q * VE + e];
       }
     }
 #pragma unroll
@@ -285,18 +387,19 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobArgs g) {
       const int v = c + (NV + q) * kThreads + tid;
       if (v < nvec) raw[q] = load16<ES>(vec + (int64_t)v * 16);
     }
-    const bool full = c + NV * kThreads <= nvec;
     const int i0 = first + c * VE, i1 = i0 + NV * kThreads * VE;
     const int where = !full ? 0 : i1 <= tok ? -1 : i0 > tok ? 1 : 0;
-    take<NV * VE, VE>(x, idx, a, l, above, xt, tok, where, topk, lane);
+    take<NV * VE, VE>(x, idx, a, l, pend, above, xt, tok, where, topk, lane);
   }
   if (wave == 0 && len % VE != 0) {  // the last logits
     const int i = lane < len % VE ? first + nvec * VE + lane : kNone;
     float x[1] = {-__builtin_inff()};
     if (i != kNone) x[0] = to_f32<XK>(row, i);
     const int idx[1] = {i};
-    take<1, 1>(x, idx, a, l, above, xt, tok, 0, topk, lane);
+    take<1, 1>(x, idx, a, l, pend, above, xt, tok, 0, topk, lane);
   }
+
+  if (pend.n > 0) list_flush(l, pend, topk, lane);
 
   // join the waves in wave 0
   auto join_waves = [&]() __attribute__((always_inline)) {
@@ -305,10 +408,7 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobArgs g) {
       soft_s[wave] = a;
       above_s[wave] = above;
     }
-    if (wave > 0 && lane < topk) {
-      list_v[wave][lane] = l.v;
-      list_i[wave][lane] = l.i;
-    }
+    if (wave > 0 && lane < topk) list_s[wave][lane] = l.e;
     __syncthreads();
     if (wave == 0) {
       Soft b = {kLowest, 0.0f, 0.0f};
@@ -318,17 +418,12 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobArgs g) {
         n = above_s[lane];
       }
       a = wave_join(b);
-      above = n;
-      above += __builtin_amdgcn_readlane((uint32_t)n, 1) + __builtin_amdgcn_readlane((uint32_t)n, 2) +
-               __builtin_amdgcn_readlane((uint32_t)n, 3);
-      above = (int)__builtin_amdgcn_readfirstlane((uint32_t)above);
+      above = 0;
+#pragma unroll
+      for (int q = 0; q < kWaves; ++q) above += (int)__builtin_amdgcn_readlane((uint32_t)n, q);
       if (topk > 0) {
 #pragma unroll
-        for (int q = 1; q < kWaves; ++q) {
-          const float v = lane < topk ? list_v[q][lane] : -__builtin_inff();
-          const int i = lane < topk ? list_i[q][lane] : kNone;
-          list_add(l, v, i, l.bar, topk, lane);
-        }
+        for (int q = 1; q < kWaves; ++q) list_merge_sorted(l, lane < topk ? list_s[q][lane] : kNoEntry, topk, lane);
       }
     }
   };
@@ -346,8 +441,8 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobArgs g) {
         st_dev(mine + 3, fbits((uint32_t)above));
       }
       if (lane < topk) {
-        st_dev(mine + 4 + lane, l.v);
-        st_dev(mine + 4 + topk + lane, fbits((uint32_t)l.i));
+        st_dev(mine + 4 + lane, fbits((uint32_t)l.e));
+        st_dev(mine + 4 + topk + lane, fbits((uint32_t)(l.e >> 32)));
       }
       wait_mem();  // this segment has reached the device-coherent level
       if (lane == 0) last_s = atomicAdd(&g.counters[r], 1u) == (uint32_t)(g.segments - 1);
@@ -372,25 +467,19 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobArgs g) {
     above = (int)(__builtin_amdgcn_readlane((uint32_t)above, 0) + __builtin_amdgcn_readlane((uint32_t)above, 16) +
                   __builtin_amdgcn_readlane((uint32_t)above, 32) + __builtin_amdgcn_readlane((uint32_t)above, 48));
     if (topk > 0) {
-      // kMaxSegments * SKINNY_TOPK_MAX entries over kThreads threads
-      constexpr int R = kLogprobMaxSegments * SKINNY_TOPK_MAX / kThreads;
-      const int n = g.segments * topk;
-      float v[R];
-      int i[R];
+      // wave w takes segments w, w + kWaves, ...: each list descends over its lanes
+      constexpr int R = kLogprobMaxSegments / kWaves;
+      uint32_t lo[R], hi[R];
 #pragma unroll
-      for (int q = 0; q < R; ++q) {
-        const int e = q * kThreads + tid;
-        v[q] = -__builtin_inff();
-        i[q] = kNone;
-        if (e < n) {
-          const int s = e / topk;
-          const float* p = part + (int64_t)s * stride + 4 + (e - s * topk);
-          v[q] = ld_dev(p);
-          i[q] = (int)ubits(ld_dev(p + topk));
-        }
+      for (int q = 0; q < R; ++q) {  // every load before the first merge
+        const int sg = q * kWaves + wave;
+        const float* p = part + (int64_t)(sg < g.segments ? sg : 0) * stride + 4 + (lane < topk ? lane : 0);
+        lo[q] = ubits(ld_dev(p));
+        hi[q] = ubits(ld_dev(p + topk));
       }
 #pragma unroll
-      for (int q = 0; q < R; ++q) list_add(l, v[q], i[q], l.bar, topk, lane);
+      for (int q = 0; q < R; ++q)
+        if (q * kWaves + wave < g.segments) list_merge_sorted(l, lane < topk ? join64(lo[q], hi[q]) : kNoEntry, topk, lane);
     }
     __syncthreads();  // last_s and the waves' slots were read
     join_waves();
@@ -409,8 +498,9 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobArgs g) {
       g.rank[r] = known ? 1 + above : 0;
     }
     if (lane < topk) {
-      g.top_ids[r * topk + lane] = l.i == kNone ? -1 : l.i;
-      g.top_logprobs[r * topk + lane] = none ? ninf : (l.v - a.m) - ln_s;
+      const int i = entry_index(l.e);
+      g.top_ids[r * topk + lane] = i == kNone ? -1 : i;
+      g.top_logprobs[r * topk + lane] = none ? ninf : (entry_value(l.e) - a.m) - ln_s;
     }
   }
 }
@@ -423,10 +513,12 @@ hipError_t launch_logprobs(const LogprobArgs& a, int x_kind, hipStream_t stream)
       (int64_t)a.segments * a.seg_len < a.vocab || (int64_t)(a.segments - 1) * a.seg_len >= a.vocab ||
       a.m * a.segments > 0x7fffffff)
     return hipErrorInvalidValue;
-  const auto fn = x_kind == CK_F32   ? logprobs_kernel<CK_F32>
-                  : x_kind == CK_F16 ? logprobs_kernel<CK_F16>
-                                     : logprobs_kernel<CK_BF16>;
-  hipLaunchKernelGGL(fn, dim3((unsigned)(a.m * a.segments)), dim3(kThreads), 0, stream, a);
+  if (a.waves != 4 && a.waves != 8) return hipErrorInvalidValue;
+  const bool eight = a.waves == 8;
+  const auto fn = x_kind == CK_F32   ? (eight ? logprobs_kernel<CK_F32, 8> : logprobs_kernel<CK_F32, 4>)
+                  : x_kind == CK_F16 ? (eight ? logprobs_kernel<CK_F16, 8> : logprobs_kernel<CK_F16, 4>)
+                                     : (eight ? logprobs_kernel<CK_BF16, 8> : logprobs_kernel<CK_BF16, 4>);
+  hipLaunchKernelGGL(fn, dim3((unsigned)(a.m * a.segments)), dim3(64 * a.waves), 0, stream, a);
   return hipGetLastError();
 }
 

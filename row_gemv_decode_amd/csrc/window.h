@@ -80,7 +80,7 @@ hipError_t launch_moe(const MoeArgs& args, int kind, int group, hipStream_t stre
 // ---------------------------------------------------------------------------
 // Token log probabilities (logprobs.hip)
 // ---------------------------------------------------------------------------
-constexpr int kLogprobMaxSegments = 64;
+constexpr int kLogprobMaxSegments = 32;
 
 struct LogprobArgs {
   const void* logits;   // [m][ld]
@@ -92,6 +92,7 @@ struct LogprobArgs {
   int32_t topk;
   int32_t segments;     // workgroups per row, seg_len logits each (the last fewer)
   int32_t seg_len;
+  int32_t waves;        // per workgroup: 4 or 8
   float* logprob;       // [m]
   float* entropy;       // [m]
   int32_t* rank;        // [m]
