@@ -162,7 +162,7 @@ skinny_status skinny_moe_plan_create(const skinny_moe_desc* desc, skinny_moe_pla
   p->router = router;
   p->max_slots = d.max_m * d.topk < d.experts ? d.max_m * d.topk : d.experts;
   const int64_t planes = moe_planes(kind_of(d.dtype), kind_of(d.out_dtype));
-  const int64_t splits = moe_down_splits(d.d);
+  const int64_t splits = moe_down_splits(d.d, d.inter, d.shared_inter, d.topk, d.group);
   int64_t at = 0;
   auto region = [&at](int64_t bytes) {
     const int64_t start = at;
@@ -249,7 +249,7 @@ skinny_status skinny_moe_run(const skinny_moe_plan* plan, int64_t m, const void*
   a.zero_page = (const uint16_t*)(base + plan->zero_page);
   a.partial = (float*)(base + plan->partial);
   a.counters = (uint32_t*)(base + plan->counters);
-  a.down_splits = moe_down_splits(d.d);
+  a.down_splits = moe_down_splits(d.d, d.inter, d.shared_inter, d.topk, d.group);
   a.h = (uint16_t*)(base + plan->h);
   a.topk_idx = topk_idx;
   a.topk_weight = topk_weight;

@@ -153,6 +153,7 @@ __global__ __launch_bounds__(1024) void moe_route_kernel(MoeArgs a) {
       }
       n += __builtin_popcountll(b);
     }
+    for (int i = n + lane; i < a.max_slots; i += 64) a.slots[i] = 0;  // slots without a token
     if (lane == 0) *a.nslots = n;
   }
   __syncthreads();
@@ -177,11 +178,12 @@ __device__ __forceinline__ int h_place(int i) {
 template <int TK, int WQ, int NP, int GT>
 __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_up_kernel(MoeArgs a) {
   __shared__ f32x4 red[kMoeWaves][2 * GT][64];
+  __shared__ ScaleLds<WQ, 2 * GT> lds;
+  __shared__ u32x4 turn_s[kMoeWaves][turn_slots<WQ, 2 * GT, 1>() * 64];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int h = lane >> 4;
   const int k = (int)a.d;
-  const int nslots = *a.nslots;
   const int tiles = (int)a.inter / (16 * GT);
 
   // the shared expert's workgroups come first: they are sure to have work
@@ -189,10 +191,10 @@ __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_up_kernel(MoeArgs a) {
   const bool shared = (int)blockIdx.x < shared_tiles;
   const int b = (int)blockIdx.x - shared_tiles;
   const int slot = shared ? 0 : b / tiles;
-  if (!shared && slot >= nslots) return;
+  const uint32_t entry = shared ? 0xffff0000u : a.slots[slot];  // every token goes to the shared expert
+  if (entry < 0x10000u) return;  // no token: a slot past the window's experts
   const int tile = shared ? (int)blockIdx.x : b - slot * tiles;
   const int64_t inter = shared ? a.shared_inter : a.inter;
-  const uint32_t entry = shared ? 0xffff0000u : a.slots[slot];  // every token goes to the shared expert
   const int64_t j0 = (int64_t)(entry & 0xffffu) * 2 * inter + 16 * GT * tile;
   int64_t j[2 * GT];
   f32x4 tot[2 * GT];
@@ -202,12 +204,10 @@ __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_up_kernel(MoeArgs a) {
     j[GT + c] = j0 + 16 * c + inter;
     tot[c] = tot[GT + c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   }
-  const int row = min(lane & 15, a.m - 1);
-  const uint16_t* arow = (const uint16_t*)a.x + row * a.ldx + a_group<WQ>() * h;
-  WTiles<WQ, 2 * GT> t;
-  w_tiles<WQ, 2 * GT>(t, shared ? a.s13 : a.w13, j, k, 16, lane);
-  const WaveShare ws = wave_share<WQ, kMoeWaves>(k, wave);
-  stream_units<TK, WQ, 2 * GT>(tot, t, arow, ws.first, ws.n, ws.part, k, h);
+  const int row = min(lane >> 2, a.m - 1);
+  const uint16_t* arow = (const uint16_t*)a.x + row * a.ldx + 8 * (lane & 3);
+  block_product<TK, WQ, 2 * GT, kMoeWaves>(tot, lds, Turn(turn_s[wave], lane), shared ? a.s13 : a.w13, j, 16, arow, k,
+                                           wave, lane);
 #pragma unroll
   for (int c = 0; c < 2 * GT; ++c) red[wave][c][lane] = tot[c];
   __syncthreads();
@@ -240,9 +240,13 @@ __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_up_kernel(MoeArgs a) {
 }
 
 // The items (expert, unit of its k) that wave `id` of `step` takes, expert by
-// expert in the list's order: unit u of expert e goes to wave (e * units + u)
-// mod step.  step is a power of two; the shared expert, last in the list,
-// counts as expert 0 with units of its own.
+// expert in the list's order: run r of RUN consecutive units of expert e goes
+// to wave (e * runs + r) mod step.  RUN units of a column fill a cache line
+// (two units of codes, one of 16-bit weights): a line is read by one wave
+// (units of a line in two workgroups, on two XCDs, were read twice from memory).
+// step is a power of two; the shared expert, last in the list, counts as
+// expert 0 with runs of its own.
+template <int RUN>
 struct DownItems {
   const uint32_t* list;  // nslots entries, then the shared expert's, if any
   int slots;             // entries in all
@@ -252,27 +256,31 @@ struct DownItems {
   uint32_t entry;
 
   __device__ __forceinline__ int units_of(int slot) const { return slot == shared_slot ? shared_units : units; }
+  // the wave's first unit in a slot (perhaps past its last)
   __device__ __forceinline__ int first_of(int slot, uint32_t en) const {
-    return (slot == shared_slot ? id : id - (int)(en & 0xffffu) * units) & (step - 1);
+    const int runs = (units + RUN - 1) / RUN;
+    return ((slot == shared_slot ? id : id - (int)(en & 0xffffu) * runs) & (step - 1)) * RUN;
   }
   __device__ __forceinline__ int count(int lane) const {
     int n = 0;
     for (int q = lane; q < slots; q += 64) {
       const int f = first_of(q, list[q]), un = units_of(q);
-      n += f < un ? (un - 1 - f) / step + 1 : 0;
+      const int whole = f < un ? (un - f) / (step * RUN) : 0;  // rounds that hold a whole run
+      n += f < un ? whole * RUN + min(RUN, un - f - whole * step * RUN) : 0;
     }
     return (int)wave_sum_f32((float)n);  // (exact: far below 2^24)
   }
   __device__ __forceinline__ void begin() {
     s = -1;
-    u = 0;
+    u = RUN - 1;
     entry = 0;
     next();
   }
   // to the next item; past the last one it stays there
   __device__ __forceinline__ void next() {
-    int ns = s, nu = u + step;
+    int ns = s, nu = u + 1;
     uint32_t ne = entry;
+    if (nu % RUN == 0) nu += (step - 1) * RUN;
     while (ns < 0 || nu >= units_of(ns)) {
       if (ns + 1 >= slots) return;
       ++ns;
@@ -285,20 +293,110 @@ struct DownItems {
   }
 };
 
+// The scales and zero points of one unit of two adjacent tiles of 16 columns:
+// even lane groups fetch the first tile's, odd ones the second's, in one load
+// for the scales (2, 4 or 8 bytes of each column) and one for the zero points
+// (half as many).
+template <int WQ>
+struct UnitScales {
+  static constexpr int GU = 128 / group_len<WQ>();  // groups per unit
+  uint32_t s[2], z;
+  uint32_t shift;  // groups to drop at the low end
+
+  // j: the first column, col: the lane's column from there, u: the unit,
+  // groups: per column; rows: columns from j to the end of the weight (or 64,
+  // if there are more): a load that would pass the end is moved back
+  __device__ __forceinline__ void load(const WindowWeight& w, int64_t j, int col, int u, int groups, int rows) {
+    const int at = col * groups + u * GU;
+    const int from = min(at, rows * groups - GU);
+    shift = (uint32_t)(at - from);
+    const char* sp = (const char*)w.scales + j * groups * 2 + 2 * from;
+    if constexpr (GU == 1) {
+      s[0] = *(const uint16_t*)sp;
+    } else if constexpr (GU == 2) {
+      typedef uint32_t any __attribute__((aligned(2)));
+      s[0] = *(const any*)sp;
+    } else {
+      typedef uint64_t any __attribute__((aligned(2)));
+      const uint64_t q = *(const any*)sp;
+      s[0] = (uint32_t)q;
+      s[1] = (uint32_t)(q >> 32);
+    }
+    if constexpr ((WQ & kZeros) != 0) {
+      const char* zp = (const char*)w.zeros + j * groups + from;
+      if constexpr (GU == 1) {
+        z = *(const uint8_t*)zp;
+      } else if constexpr (GU == 2) {
+        typedef uint16_t any __attribute__((aligned(1)));
+        z = *(const any*)zp;
+      } else {
+        typedef uint32_t any __attribute__((aligned(1)));
+        z = *(const any*)zp;
+      }
+    }
+  }
+
+  // per tile and group: scale in the low half, zero point in the high half
+  __device__ __forceinline__ void get(u32x4 (&sz)[2]) const {
+    uint32_t lo = s[0], hi = 0, zz = 0;
+    if constexpr (GU == 4) {
+      const uint64_t q = (((uint64_t)s[1] << 32) | s[0]) >> (16 * shift);
+      lo = (uint32_t)q;
+      hi = (uint32_t)(q >> 32);
+    } else {
+      lo >>= 16 * shift;
+    }
+    const u32x4 l = spread4(lo);
+    u32x4 m = {0u, 0u, 0u, 0u}, zs = {0x08080808u, 0x08080808u, 0x08080808u, 0x08080808u};
+    if constexpr (GU == 4) m = spread4(hi);
+    if constexpr ((WQ & kZeros) != 0) {
+      zz = z >> (8 * shift);
+      zs = spread4(zz);
+    }
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int g = 0; g < GU; ++g) {
+        const uint32_t word = g < 2 ? (uint32_t)l[c] : (uint32_t)m[c];
+        const uint32_t sc = (g & 1) != 0 ? word >> 16 : word & 0xffffu;
+        const uint32_t zw = zs[c];
+        sz[c][g] = sc | (((zw >> (8 * g)) & 0xffu) << 16);
+      }
+  }
+};
+template <>
+struct UnitScales<kWFull> {
+  __device__ __forceinline__ void get(u32x4 (&)[2]) const {}
+};
+
 template <int TK, int WQ, int NP>
 __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_down_kernel(MoeArgs a) {
   constexpr int CT = 2;
   constexpr int NB = unit_blocks<WQ>();
   constexpr int UL = unit_len<WQ>();
   __shared__ f32x4 red[kMoeWaves][CT][64];
+  __shared__ u32x4 turn_s[kMoeWaves][turn_slots<WQ, CT, NP>() * 64];
   __shared__ uint32_t list[kGemvMaxM * SKINNY_TOPK_MAX + 1];
   __shared__ int last_s;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int h = lane >> 4;
   const int row = lane & 15;
-  const int split = blockIdx.x % a.down_splits;
-  const int tile = blockIdx.x / a.down_splits;
+  // Workgroups go to the eight XCDs in turn: the shares of one column range are
+  // eight apart, so they find each other's cache lines (a column's scales and
+  // its ends of code lines) in one L2.
+  int split, tile;
+  {
+    const int S = a.down_splits, b = blockIdx.x, tiles = (int)(gridDim.x / (unsigned)S);
+    const int whole = tiles / 8 * 8 * S;  // workgroups of whole sets of eight ranges
+    if (b < whole) {
+      split = b / 8 % S;
+      tile = b / (8 * S) * 8 + b % 8;
+    } else {
+      split = (b - whole) % S;
+      tile = whole / S + (b - whole) / S;
+    }
+  }
   const int64_t j0 = (int64_t)tile * (16 * CT);
 
   int nslots = *a.nslots;
@@ -308,7 +406,7 @@ __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_down_kernel(MoeArgs a) 
   if (threadIdx.x == 0 && a.shared_inter > 0) list[nslots] = 0xffff0000u;
   __syncthreads();
 
-  DownItems it;
+  DownItems<(WQ == kWFull ? 1 : 2)> it;
   it.list = list;
   it.slots = nslots + (a.shared_inter > 0 ? 1 : 0);
   it.shared_slot = nslots;
@@ -324,7 +422,7 @@ __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_down_kernel(MoeArgs a) 
 
   struct Item {
     WUnit<WQ, CT> w;
-    ScaleRaw<WQ, CT> s;
+    UnitScales<WQ> s;
     u32x4 a[NP][NB];
   };
   // Load the current item.  A row that the expert does not serve reads zeros,
@@ -335,14 +433,17 @@ __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_down_kernel(MoeArgs a) 
     const bool shared = it.s == it.shared_slot;
     const int k = (int)(shared ? a.shared_inter : a.inter);
     const WindowWeight& W = shared ? a.s2 : a.w2;
-    const int64_t j[CT] = {(shared ? 0 : (int64_t)(it.entry & 0xffffu) * a.d) + j0,
-                           (shared ? 0 : (int64_t)(it.entry & 0xffffu) * a.d) + j0 + 16};
+    const int64_t jb = (shared ? 0 : (int64_t)(it.entry & 0xffffu) * a.d) + j0;
+    int64_t j[CT];
+#pragma unroll
+    for (int c = 0; c < CT; ++c) j[c] = jb + 16 * c;
     WTiles<WQ, CT> t;
     w_tiles<WQ, CT>(t, W, j, k, 16, lane);
     const bool part = it.u * UL + UL > k;
-    const bool served = row < a.m && ((it.entry >> (16 + row)) & 1u) != 0;
+    const int tk = lane >> 2, piece = lane & 3;  // this lane's token (or column) and piece of each block
+    const bool served = tk < a.m && ((it.entry >> (16 + tk)) & 1u) != 0;
     const uint16_t* hr = a.h + (shared ? a.max_slots : it.s) * (int64_t)(kGemvMaxM * NP) * a.inter +
-                         (int64_t)row * NP * k + it.u * UL + a_group<WQ>() * h;
+                         (int64_t)tk * NP * k + it.u * UL + 8 * piece;
     if constexpr (WQ == kWFull) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -351,38 +452,27 @@ __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_down_kernel(MoeArgs a) 
         for (int c = 0; c < CT; ++c) q.w.v[c][i] = *(const u32x4*)(t.codes[c] + (int64_t)it.u * 128 + t.off + at);
       }
     } else {
-      const int at = part && it.u * UL + 32 * h >= k ? -16 * h : 0;
+      const int at = part && it.u * UL + 32 * piece >= k ? -16 * piece : 0;
 #pragma unroll
       for (int c = 0; c < CT; ++c) q.w.v[c][0] = *(const u32x4*)(t.codes[c] + (int64_t)it.u * 64 + t.off + at);
-      load_scale(q.s, t, (it.u * UL + 32 * h) / group_len<WQ>());
+      const int64_t rows = shared ? a.d - j0 : (a.experts - (int64_t)(it.entry & 0xffffu)) * a.d - j0;
+      q.s.load(W, jb, 16 * (h & 1) + row, it.u, k / group_len<WQ>(), (int)min(rows, (int64_t)64));
     }
 #pragma unroll
     for (int p = 0; p < NP; ++p) {
       const uint16_t* hp = served ? hr + (int64_t)p * k : a.zero_page;
 #pragma unroll
       for (int i = 0; i < NB; ++i) {
-        const uint16_t* hi = part && it.u * UL + 32 * i >= k ? a.zero_page : hp + a_step<WQ>() * i;
+        const uint16_t* hi = part && it.u * UL + 32 * i >= k ? a.zero_page : hp + 32 * i;
         q.a[p][i] = *(const u32x4*)hi;
       }
     }
   };
-  auto mul = [&](const Item& q) __attribute__((always_inline)) {
+  const Turn turn(turn_s[wave], lane);
+  auto mul = [&](Item& q) __attribute__((always_inline)) {
     u32x4 sz[CT];
-    if constexpr (WQ != kWFull) {
-#pragma unroll
-      for (int c = 0; c < CT; ++c) {
-        const uint32_t own = (uint32_t)q.s.s[c] | ((uint32_t)q.s.z[c] << 16);
-        if constexpr (group_len<WQ>() == 128) {
-          sz[c][0] = own;
-        } else if constexpr (group_len<WQ>() == 64) {
-          auto v = __builtin_amdgcn_permlane32_swap(own, own, false, false);
-          sz[c][0] = v[0];
-          sz[c][1] = v[1];
-        } else {
-          sz[c] = spread4(own);
-        }
-      }
-    }
+    q.s.get(sz);
+    turn_unit<WQ, CT, NP>(q.w, q.a, turn, lane);
     mul_unit<TK, WQ, CT, NP, true, false>(q.w, sz, q.a, tot, 0, 0);
   };
 
@@ -420,7 +510,8 @@ __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_down_kernel(MoeArgs a) 
   for (int c = 0; c < CT; ++c) red[wave][c][lane] = tot[c];
   __syncthreads();
   const int64_t jc = j0 + 16 * wave + row;  // waves 0 and 1: this thread's column
-  if (wave < CT) {
+  const bool mine = wave < CT;
+  if (mine) {
     f32x4 sum = red[0][wave][lane];
 #pragma unroll
     for (int w = 1; w < kMoeWaves; ++w) sum += red[w][wave][lane];
@@ -436,10 +527,10 @@ __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_down_kernel(MoeArgs a) 
     }
   }
   if (a.down_splits > 1) {
-    __syncthreads();  // both waves' shares have
+    __syncthreads();  // every wave's share has
     if (threadIdx.x == 0) last_s = atomicAdd(&a.counters[tile], 1u) == (uint32_t)(a.down_splits - 1);
     __syncthreads();
-    if (last_s && wave < CT) {
+    if (last_s && mine) {
       // every share is there: add them in order
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
@@ -455,8 +546,8 @@ __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_down_kernel(MoeArgs a) 
           store_kind(a.out, (4 * h + q) * a.ldo + jc, sum, a.out_kind);
         }
       }
-      if (threadIdx.x == 0) a.counters[tile] = 0u;  // ready for the next call
     }
+    if (last_s && threadIdx.x == 0) a.counters[tile] = 0u;  // ready for the next call
   }
 }
 
@@ -499,12 +590,14 @@ moe_fn pick(int kind, int np, int group, bool zeros, bool up, bool wide) {
 
 int moe_planes(int kind, int out_kind) { return kind == CK_BF16 && out_kind == CK_F32 ? 3 : 2; }
 
-// Shares of the down product's k: enough workgroups for about ten waves per CU
-// of 256, a power of two; by the output's width alone, which also fixes every
-// row's order of additions.
-int moe_down_splits(int64_t d) {
+// Shares of the down product's k, a power of two: enough workgroups for about
+// ten waves per CU of 256, but not more waves than one token's experts have
+// units.  By the layer alone, which also fixes every row's order of additions.
+int moe_down_splits(int64_t d, int64_t inter, int64_t shared_inter, int topk, int group) {
+  const int64_t unit = group == 0 ? 64 : 128;
+  const int64_t units = topk * ((inter + unit - 1) / unit) + (shared_inter + unit - 1) / unit;
   int s = 1;
-  while (s < kMoeMaxSplits && (d / 32) * s < 640) s *= 2;
+  while (s < kMoeMaxSplits && d / 32 * s < 640 && s * kMoeWaves < units) s *= 2;
   return s;
 }
 
@@ -513,7 +606,7 @@ hipError_t launch_moe(const MoeArgs& a, int kind, int group, hipStream_t stream)
       a.topk > SKINNY_TOPK_MAX || a.topk > a.experts || a.d % 32 != 0 || a.inter % 32 != 0 || a.shared_inter % 32 != 0 ||
       (group != 0 && group != 32 && group != 64 && group != 128) ||
       (group != 0 && (a.d % group != 0 || a.inter % group != 0 || a.shared_inter % group != 0)) ||
-      (kind != CK_F16 && kind != CK_BF16) || a.down_splits != moe_down_splits(a.d))
+      (kind != CK_F16 && kind != CK_BF16) || a.down_splits != moe_down_splits(a.d, a.inter, a.shared_inter, a.topk, group))
     return hipErrorInvalidValue;
   const int64_t slots = (int64_t)a.m * a.topk < a.experts ? (int64_t)a.m * a.topk : a.experts;
   if (slots > a.max_slots || a.max_slots > kGemvMaxM * SKINNY_TOPK_MAX) return hipErrorInvalidValue;

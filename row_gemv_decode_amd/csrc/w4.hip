@@ -21,6 +21,8 @@ constexpr int kW4Waves = 4;
 template <int TK, int WQ, int CT>
 __global__ __launch_bounds__(64 * kW4Waves, 2) void w4_rows_kernel(W4Args g) {
   __shared__ f32x4 red[kW4Waves][CT][64];
+  __shared__ ScaleLds<WQ, CT> lds;
+  __shared__ u32x4 turn_s[kW4Waves][turn_slots<WQ, CT, 1>() * 64];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int h = lane >> 4;
@@ -30,8 +32,8 @@ __global__ __launch_bounds__(64 * kW4Waves, 2) void w4_rows_kernel(W4Args g) {
   const int64_t j0 = CT > 1 && own > g.n - 16 * CT ? g.n - 16 * CT : own;
 
   // rows past m repeat row m - 1: their sums are never stored
-  const int row = min(lane & 15, g.m - 1);
-  const uint16_t* arow = (const uint16_t*)g.A + row * g.lda + a_group<WQ>() * h;
+  const int row = min(lane >> 2, g.m - 1);
+  const uint16_t* arow = (const uint16_t*)g.A + row * g.lda + 8 * (lane & 3);
   int64_t j[CT];
   f32x4 tot[CT];
 #pragma unroll
@@ -39,10 +41,8 @@ __global__ __launch_bounds__(64 * kW4Waves, 2) void w4_rows_kernel(W4Args g) {
     j[c] = j0 + 16 * c;
     tot[c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   }
-  WTiles<WQ, CT> t;
-  w_tiles<WQ, CT>(t, g.w, j, g.k, CT > 1 ? 16 : (int)min(g.n - j0, (int64_t)16), lane);
-  const WaveShare ws = wave_share<WQ, kW4Waves>(k, wave);
-  stream_units<TK, WQ, CT>(tot, t, arow, ws.first, ws.n, ws.part, k, h);
+  block_product<TK, WQ, CT, kW4Waves>(tot, lds, Turn(turn_s[wave], lane), g.w, j,
+                                      CT > 1 ? 16 : (int)min(g.n - j0, (int64_t)16), arow, k, wave, lane);
 
 #pragma unroll
   for (int c = 0; c < CT; ++c) red[wave][c][lane] = tot[c];

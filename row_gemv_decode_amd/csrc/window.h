@@ -44,7 +44,7 @@ hipError_t launch_w4_mm(const W4Args& args, int a_kind, int group, hipStream_t s
 // after the router's GEMV.
 // ---------------------------------------------------------------------------
 constexpr int kMoeMaxExperts = 1024;
-constexpr int kMoeMaxSplits = 8;
+constexpr int kMoeMaxSplits = 16;
 
 struct MoeArgs {
   const void* x;           // [m][ldx]
@@ -72,7 +72,7 @@ struct MoeArgs {
 };
 
 int moe_planes(int kind, int out_kind);  // 16-bit planes that hold one inner value
-int moe_down_splits(int64_t d);          // shares of the down product
+int moe_down_splits(int64_t d, int64_t inter, int64_t shared_inter, int topk, int group);  // shares of the down product
 
 // kind: CK_F16 or CK_BF16; group: 0 (16-bit weights), 32, 64 or 128
 hipError_t launch_moe(const MoeArgs& args, int kind, int group, hipStream_t stream);

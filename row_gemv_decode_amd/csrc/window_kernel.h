@@ -12,8 +12,8 @@
 //
 // 4-bit weights (one scale, and optionally one zero point, per group of G
 // elements along k; W = s * (q - z)):
-//   * Lane (column, h) loads 16 bytes, the 32 codes of block h of its unit:
-//     one wave load covers 16 columns x 64 bytes.  A 4 x 4 exchange between
+//   * A wave load covers 16 columns x 64 bytes, the codes of one unit; lane
+//     (column, h) needs the 16 bytes of block h.  A 4 x 4 exchange between
 //     the four lane groups and the four registers (two v_permlane32_swap, two
 //     v_permlane16_swap) then gives every lane group its eight codes of each
 //     block, so one MFMA sees one block of 32, hence one scale per column.
@@ -128,89 +128,82 @@ __device__ __forceinline__ u32x4 exchange4(u32x4 v) {
 }
 
 // ---------------------------------------------------------------------------
+// Loads and the turn.  The cache combines the accesses of consecutive lanes
+// only, so a load gives four consecutive lanes the 64 bytes of one row (a
+// column of the weight, or a token): lane l fetches piece l & 3 of row l >> 2.
+// The matrix core wants piece l >> 4 of row l & 15 in lane l.  Loading in that
+// order made every lane an access of its own, and the accesses, 61 for each
+// load, were what bounded the kernels (16 x 256 experts: the up product
+// took 175 us, the down product 130).  So each 1 KiB passes through a slot of
+// LDS that belongs to the wave: written as loaded, read as needed, no barrier.
+// A row's four pieces are stored rotated by f(row), which keeps the reads (and
+// the writes) free of bank conflicts.
+// ---------------------------------------------------------------------------
+struct Turn {
+  u32x4* slots;    // the wave's slots, 64 entries each
+  int put, get;    // the lane's entry to write, and to read
+
+  __device__ __forceinline__ Turn(u32x4* wave_slots, int lane) : slots(wave_slots) {
+    put = entry(lane >> 2, lane & 3);
+    get = entry(lane & 15, lane >> 4);
+  }
+  static __device__ __forceinline__ int entry(int row, int piece) { return row * 4 + (piece ^ ((row >> 1) & 3)); }
+};
+
+// order of a wave's LDS writes and its later reads by other lanes (the LDS
+// works in order; this keeps the compiler from moving them)
+__device__ __forceinline__ void wave_lds_order() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
 // A weight matrix as a wave sees it: CT tiles of 16 consecutive columns, each
 // from a wave-uniform address, and one 32-bit offset per lane that serves all
-// tiles (column l & 15 of a tile, block or elements of lane group h).
-// Loads are plain: two units share a cache line of every column, and a
-// non-temporal load gives the line's other half up (measured 5 to 20 % slower).
-// ---------------------------------------------------------------------------
+// tiles.  Weight loads are plain: two units share a cache line of every column,
+// and a non-temporal load gives the line's other half up (measured 5 to 20 %
+// slower).
 template <int WQ, int CT>
 struct WTiles {
-  const char* codes[CT];   // first column, k = 0 (16-bit weights or codes)
-  const char* scales[CT];
-  const char* zeros[CT];   // kZeros only
-  uint32_t off;            // lane's byte offset into codes
-  uint32_t col_groups;     // (l & 15) * groups per column
-  int groups;              // per column
+  const char* codes[CT];  // first column, k = 0 (16-bit weights or codes)
+  uint32_t off;           // lane's byte offset into codes
 };
 
 // tile c starts at column j[c] of a weight of row length k; cols: columns of a
 // tile that exist (lanes past them read the last one, their sums are not stored)
 template <int WQ, int CT>
-__device__ __forceinline__ void w_tiles(WTiles<WQ, CT>& t, const WindowWeight& w, const int64_t (&j)[CT], int64_t k, int cols,
-                                        int lane) {
-  const int h = lane >> 4;
-  const int col = min(lane & 15, cols - 1);
-  if constexpr (WQ == kWFull) {
+__device__ __forceinline__ void w_tiles(WTiles<WQ, CT>& t, const WindowWeight& w, const int64_t (&j)[CT], int64_t k,
+                                        int cols, int lane) {
+  const uint32_t row = (uint32_t)(WQ == kWFull ? k * 2 : k >> 1);  // bytes of a column
 #pragma unroll
-    for (int c = 0; c < CT; ++c) t.codes[c] = (const char*)w.codes + j[c] * k * 2;
-    t.off = (uint32_t)col * (uint32_t)(k * 2) + 16 * h;
-  } else {
-    t.groups = (int)(k / group_len<WQ>());
-#pragma unroll
-    for (int c = 0; c < CT; ++c) {
-      t.codes[c] = (const char*)w.codes + j[c] * (k >> 1);
-      t.scales[c] = (const char*)w.scales + j[c] * t.groups * 2;
-      t.zeros[c] = (const char*)w.zeros + ((WQ & kZeros) != 0 ? j[c] * t.groups : 0);
-    }
-    t.off = (uint32_t)col * (uint32_t)(k >> 1) + 16 * h;
-    t.col_groups = (uint32_t)(col * t.groups);
-  }
+  for (int c = 0; c < CT; ++c) t.codes[c] = (const char*)w.codes + j[c] * (int64_t)row;
+  t.off = (uint32_t)min(lane >> 2, cols - 1) * row + 16 * (lane & 3);
 }
 
-// loaded, not yet decoded weights of one unit
+// loaded, not yet turned and decoded weights of one unit
 template <int WQ, int CT>
 struct WUnit {
-  u32x4 v[CT][WQ == kWFull ? 2 : 1];
+  static constexpr int N = WQ == kWFull ? 2 : 1;  // loads per tile
+  u32x4 v[CT][N];
 };
 
 // Load unit u.  kPart: the last unit of a k that is no multiple of the unit
 // (k is one of 32): blocks past k are not read.
 template <int WQ, int CT, bool kPart>
-__device__ __forceinline__ void load_w(WUnit<WQ, CT>& r, const WTiles<WQ, CT>& t, int u, int k, int h) {
+__device__ __forceinline__ void load_w(WUnit<WQ, CT>& r, const WTiles<WQ, CT>& t, int u, int k, int lane) {
   if constexpr (WQ == kWFull) {
 #pragma unroll
     for (int i = 0; i < 2; ++i)
       if (!kPart || u * 64 + 32 * i < k) {
 #pragma unroll
-        for (int c = 0; c < CT; ++c)
-          r.v[c][i] = *(const u32x4*)(t.codes[c] + (int64_t)u * 128 + t.off + 64 * i);
+        for (int c = 0; c < CT; ++c) r.v[c][i] = *(const u32x4*)(t.codes[c] + (int64_t)u * 128 + t.off + 64 * i);
       }
   } else {
 #pragma unroll
     for (int c = 0; c < CT; ++c) {
       if (kPart) r.v[c][0] = u32x4{0u, 0u, 0u, 0u};
-      if (!kPart || u * 128 + 32 * h < k)
+      if (!kPart || u * 128 + 32 * (lane & 3) < k)
         r.v[c][0] = *(const u32x4*)(t.codes[c] + (int64_t)u * 64 + t.off);
     }
-  }
-}
-
-// The scale (low half) and zero point (high half) of group g of the lane's
-// column; g is clamped to the column's groups.
-template <int WQ, int CT>
-struct ScaleRaw {
-  uint16_t s[CT];
-  uint8_t z[CT];
-};
-template <int WQ, int CT>
-__device__ __forceinline__ void load_scale(ScaleRaw<WQ, CT>& r, const WTiles<WQ, CT>& t, int g) {
-  const uint32_t at = t.col_groups + (uint32_t)min(g, t.groups - 1);
-#pragma unroll
-  for (int c = 0; c < CT; ++c) {
-    r.s[c] = *(const uint16_t*)(t.scales[c] + 2 * at);
-    r.z[c] = 8;
-    if constexpr ((WQ & kZeros) != 0) r.z[c] = *(const uint8_t*)(t.zeros[c] + at);
   }
 }
 
@@ -222,20 +215,46 @@ __device__ __forceinline__ u32x4 spread4(uint32_t own) {
   return u32x4{lo[0], lo[1], hi[0], hi[1]};
 }
 
-// A's fragments of unit u from a row of 16-bit values.  `base` is the lane's
-// row at element 8h (or, for groups of 128, 32h: there a step of the matrix
-// core takes eight codes of each of the four blocks, so no exchange is needed).
-template <int WQ>
-constexpr int a_step() { return group_len<WQ>() == 128 ? 8 : 32; }   // elements from one fragment to the next
-template <int WQ>
-constexpr int a_group() { return group_len<WQ>() == 128 ? 32 : 8; }  // elements from one lane group to the next
-
+// A's blocks of unit u from a row of 16-bit values; `base` is the lane's row
+// (l >> 2) at piece l & 3 of block 0
 template <int WQ, bool kPart>
 __device__ __forceinline__ void load_a(u32x4 (&a)[unit_blocks<WQ>()], const uint16_t* base, int u, int k) {
 #pragma unroll
   for (int i = 0; i < unit_blocks<WQ>(); ++i)
-    if (!kPart || u * unit_len<WQ>() + 32 * i < k)
-      a[i] = *(const u32x4*)(base + (int64_t)u * unit_len<WQ>() + a_step<WQ>() * i);
+    if (!kPart || u * unit_len<WQ>() + 32 * i < k) a[i] = *(const u32x4*)(base + (int64_t)u * unit_len<WQ>() + 32 * i);
+}
+
+// Turn a unit: afterwards w.v and a.v hold, in lane l, piece l >> 4 of row
+// l & 15.  For groups of 128 A's fragment i is piece i of block l >> 4
+// instead: there a step of the matrix core takes eight codes of each of the
+// four blocks, so the codes need no exchange.
+template <int WQ, int CT, int NP>
+constexpr int turn_slots() { return CT * WUnit<WQ, CT>::N + NP * unit_blocks<WQ>(); }
+
+template <int WQ, int CT, int NP>
+__device__ __forceinline__ void turn_unit(WUnit<WQ, CT>& w, u32x4 (&a)[NP][unit_blocks<WQ>()], const Turn& t, int lane) {
+  constexpr int NW = WUnit<WQ, CT>::N, NB = unit_blocks<WQ>();
+  wave_lds_order();
+#pragma unroll
+  for (int c = 0; c < CT; ++c)
+#pragma unroll
+    for (int i = 0; i < NW; ++i) t.slots[(c * NW + i) * 64 + t.put] = w.v[c][i];
+  u32x4* as = t.slots + CT * NW * 64;
+#pragma unroll
+  for (int p = 0; p < NP; ++p)
+#pragma unroll
+    for (int i = 0; i < NB; ++i) as[(p * NB + i) * 64 + t.put] = a[p][i];
+  wave_lds_order();
+#pragma unroll
+  for (int c = 0; c < CT; ++c)
+#pragma unroll
+    for (int i = 0; i < NW; ++i) w.v[c][i] = t.slots[(c * NW + i) * 64 + t.get];
+#pragma unroll
+  for (int p = 0; p < NP; ++p)
+#pragma unroll
+    for (int i = 0; i < NB; ++i)
+      a[p][i] = group_len<WQ>() == 128 ? as[(p * NB + (lane >> 4)) * 64 + Turn::entry(lane & 15, i)]
+                                       : as[(p * NB + i) * 64 + t.get];
 }
 
 // tot[c] += A(unit) . W(unit) for CT column tiles; A is the sum of NP planes
@@ -298,145 +317,201 @@ __device__ __forceinline__ void mul_unit(const WUnit<WQ, CT>& w, const u32x4 (&s
   }
 }
 
-// Scales of the two units u and u + 1.  A lane group holds one group's: of
-// groups of 64 and 128 one load fetches both units' (and is issued a pair
-// ahead), of groups of 32 each unit has a load of its own.
+// ---------------------------------------------------------------------------
+// A workgroup's scales and zero points, in LDS as they lie in memory: column
+// by column, `groups` of each, for at most kSpanGroups groups at a time.  The
+// 16 columns of a tile lie together, so the workgroup fetches them with full
+// 16-byte loads; fetched by the lanes that use them, 2 and 1 bytes of 16
+// columns at a time, they cost the load path as much as a third of the codes
+// (16 x 256 experts, groups of 128: 198 us for the up product against 165
+// without any scale).
+// ---------------------------------------------------------------------------
+constexpr int kSpanGroups = 128;
 template <int WQ, int CT>
-struct PairScales {
-  ScaleRaw<WQ, CT> r[group_len<WQ>() == 32 ? 2 : 1];
+struct ScaleLds {
+  static constexpr int N = WQ == kWFull ? 8 : 16 * kSpanGroups;
+  uint16_t s[CT][N] __attribute__((aligned(16)));
+  uint8_t z[CT][(WQ & kZeros) != 0 ? N : 16] __attribute__((aligned(16)));
 };
-// with the pair: both units' scales
-template <int WQ, int CT>
-__device__ __forceinline__ void load_pair_scales(PairScales<WQ, CT>& p, const WTiles<WQ, CT>& t, int u, int h) {
-  if constexpr (group_len<WQ>() == 128) {
-    load_scale(p.r[0], t, u + (h >> 1));
-  } else if constexpr (group_len<WQ>() == 64) {
-    load_scale(p.r[0], t, 2 * u + h);
+
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(1)));
+
+// Staging in two steps, so that other loads can be issued between them: `load`
+// fetches, `store` writes to LDS.  g0, n: the span's groups; cols as in w_tiles.
+template <int WQ, int CT, int THREADS>
+struct ScaleStage {
+  static_assert(2 * kSpanGroups <= THREADS, "one 16-byte piece of a tile per thread");
+  u32x4 s[CT], z[CT];
+
+  // 16-byte pieces of a tile: of all columns in one run when the span is the
+  // whole k, else of each column's part; anything odder goes one by one
+  static __device__ __forceinline__ bool pieces(int n, int groups, int cols) {
+    return cols == 16 && (n == groups || n % 16 == 0);
   }
-}
-// with each unit: unit u as the first or second of its pair
-template <int WQ, int CT>
-__device__ __forceinline__ void load_unit_scales(PairScales<WQ, CT>& p, const WTiles<WQ, CT>& t, int u, int second, int h) {
-  if constexpr (group_len<WQ>() == 32) load_scale(p.r[second], t, 4 * u + h);
-}
-// unit `second` (0 or 1) of the pair
-template <int WQ, int CT>
-__device__ __forceinline__ void unit_scales(u32x4 (&sz)[CT], const PairScales<WQ, CT>& p, int second) {
-  if constexpr (WQ != kWFull) {
+  // byte offset of piece i; per: pieces per column, row: bytes of a column
+  static __device__ __forceinline__ uint32_t place(int i, bool run, int per, uint32_t row) {
+    return run ? 16u * i : (uint32_t)(i / per) * row + 16u * (uint32_t)(i % per);
+  }
+
+  __device__ __forceinline__ void load(const WindowWeight& w, const int64_t (&j)[CT], int g0, int n, int groups, int cols) {
+    if (!pieces(n, groups, cols)) return;
+    const bool run = n == groups;
 #pragma unroll
     for (int c = 0; c < CT; ++c) {
-      const ScaleRaw<WQ, CT>& r = p.r[group_len<WQ>() == 32 ? second : 0];
-      const uint32_t own = (uint32_t)r.s[c] | ((uint32_t)r.z[c] << 16);
-      if constexpr (group_len<WQ>() == 128) {
-        auto s = __builtin_amdgcn_permlane32_swap(own, own, false, false);
-        sz[c][0] = s[second];
-      } else {
-        const u32x4 s = spread4(own);
-        sz[c][0] = s[group_len<WQ>() == 64 ? 2 * second : 0];
-        sz[c][1] = s[group_len<WQ>() == 64 ? 2 * second + 1 : 1];
-        sz[c][2] = s[2];
-        sz[c][3] = s[3];
+      const int t = (int)(threadIdx.x + 64 * c) % THREADS;  // the tiles' pieces start at different waves
+      const char* sp = (const char*)w.scales + (j[c] * groups + g0) * 2;
+      if (t < 2 * n) s[c] = *(const u32x4_any*)(sp + place(t, run, n / 8, 2 * groups));
+      if constexpr ((WQ & kZeros) != 0) {
+        const char* zp = (const char*)w.zeros + j[c] * groups + g0;
+        if (t < n) z[c] = *(const u32x4_any*)(zp + place(t, run, n / 16, groups));
       }
     }
+  }
+
+  __device__ __forceinline__ void store(ScaleLds<WQ, CT>& lds, const WindowWeight& w, const int64_t (&j)[CT], int g0, int n,
+                                        int groups, int cols) {
+    if (pieces(n, groups, cols)) {
+#pragma unroll
+      for (int c = 0; c < CT; ++c) {
+        const int t = (int)(threadIdx.x + 64 * c) % THREADS;
+        if (t < 2 * n) ((u32x4*)lds.s[c])[t] = s[c];
+        if constexpr ((WQ & kZeros) != 0) {
+          if (t < n) ((u32x4*)lds.z[c])[t] = z[c];
+        }
+      }
+    } else {
+#pragma unroll 1
+      for (int c = 0; c < CT; ++c) {
+        const uint16_t* sp = (const uint16_t*)w.scales + j[c] * groups + g0;
+        const uint8_t* zp = (const uint8_t*)w.zeros + ((WQ & kZeros) != 0 ? j[c] * groups + g0 : 0);
+#pragma unroll 4
+        for (int i = threadIdx.x; i < cols * n; i += THREADS) {
+          const int col = i / n;
+          const int64_t at = (int64_t)col * groups + (i - col * n);
+          lds.s[c][i] = sp[at];
+          if constexpr ((WQ & kZeros) != 0) lds.z[c][i] = zp[at];
+        }
+      }
+    }
+  }
+};
+
+// the staged scales of the unit whose first group is the span's g-th: scale in
+// the low half, zero point in the high half
+template <int WQ, int CT>
+__device__ __forceinline__ void unit_scales(u32x4 (&sz)[CT], const ScaleLds<WQ, CT>& lds, int g, int row) {
+  if constexpr (WQ != kWFull) {
+#pragma unroll
+    for (int c = 0; c < CT; ++c)
+#pragma unroll
+      for (int i = 0; i < 128 / group_len<WQ>(); ++i) {
+        const uint32_t z = (WQ & kZeros) != 0 ? lds.z[c][row + g + i] : 8u;
+        sz[c][i] = (uint32_t)lds.s[c][row + g + i] | (z << 16);
+      }
   }
 }
 
 // ---------------------------------------------------------------------------
-// tot[c] += A . W over the units first .. first + n - 1 of k, and over the
-// partial unit `part` (negative: none).  Two units are in flight: each is
-// loaded again, two units on, as soon as it is used, so a wave always has
-// about CT x 4 KiB of loads under way, and loads are never issued under a
-// condition in the loop (a conditional load makes the compiler wait for more
-// than it needs).
+// tot[c] = A . W over a whole k, by NW waves that each end with a part of the
+// sum, to be added in the order of the waves.  k goes span by span (of
+// kSpanGroups groups; 16-bit weights have one span), and in a span wave w takes
+// a run of consecutive units; who sums what depends on k alone.  A wave has two
+// units in flight: each is loaded again, two units on, as soon as it is used,
+// and loads are never issued under a condition in the loop (a conditional load
+// makes the compiler wait for more than it needs).
 // ---------------------------------------------------------------------------
-template <int TK, int WQ, int CT>
-__device__ __forceinline__ void stream_units(f32x4 (&tot)[CT], const WTiles<WQ, CT>& t, const uint16_t* arow, int first,
-                                             int n, int part, int k, int h) {
+template <int TK, int WQ, int CT, int NW>
+__device__ __forceinline__ void block_product(f32x4 (&tot)[CT], ScaleLds<WQ, CT>& lds, const Turn& turn,
+                                              const WindowWeight& weight, const int64_t (&j)[CT], int cols,
+                                              const uint16_t* arow, int k, int wave, int lane) {
   constexpr int NB = unit_blocks<WQ>();
-  if (n > 0) {
+  constexpr int UL = unit_len<WQ>();
+  constexpr int GU = WQ == kWFull ? 0 : 128 / (WQ == kWFull ? 1 : group_len<WQ>());  // groups per unit
+  WTiles<WQ, CT> t;
+  w_tiles<WQ, CT>(t, weight, j, k, cols, lane);
+  const int groups = WQ == kWFull ? 0 : k / (WQ == kWFull ? 1 : group_len<WQ>());
+  const int span = WQ == kWFull ? k : kSpanGroups * group_len<WQ>();
+#pragma unroll 1
+  for (int k0 = 0; k0 < k; k0 += span) {
+    const int end = min(k, k0 + span);
+    const int u0 = k0 / UL, full = end / UL;  // full units end here
+    const int per = ((end + UL - 1) / UL - u0 + NW - 1) / NW;
+    const int first = min(u0 + wave * per, full);
+    const int n = min(u0 + wave * per + per, full) - first;
+    const bool part = end % UL != 0 && (full - u0) / per == wave;
+    const int g0 = u0 * GU, ng = min(kSpanGroups, groups - g0);
+    const int row = min(lane & 15, cols - 1) * ng - g0;
+
     WUnit<WQ, CT> w0, w1;
     u32x4 a0[1][NB], a1[1][NB], sz[CT];
-    PairScales<WQ, CT> s, sn;
-    int u = first;
-    // unit v into the first or second of the two buffers
-    auto load0 = [&](int v) __attribute__((always_inline)) {
-      load_unit_scales(s, t, v, 0, h);
-      load_w<WQ, CT, false>(w0, t, v, k, h);
-      load_a<WQ, false>(a0[0], arow, v, k);
+    auto load0 = [&](int u) __attribute__((always_inline)) {
+      load_w<WQ, CT, false>(w0, t, u, k, lane);
+      load_a<WQ, false>(a0[0], arow, u, k);
     };
-    auto load1 = [&](int v) __attribute__((always_inline)) {
-      load_unit_scales(s, t, v, 1, h);
-      load_w<WQ, CT, false>(w1, t, v, k, h);
-      load_a<WQ, false>(a1[0], arow, v, k);
+    auto load1 = [&](int u) __attribute__((always_inline)) {
+      load_w<WQ, CT, false>(w1, t, u, k, lane);
+      load_a<WQ, false>(a1[0], arow, u, k);
     };
-    load_pair_scales(s, t, u, h);
-    load0(u);
-    load1(n > 1 ? u + 1 : u);
-    int left = n;
-#pragma unroll 1
-    while (left >= 4) {
-      load_pair_scales(sn, t, u + 2, h);
-      __builtin_amdgcn_sched_barrier(0);
-      unit_scales(sz, s, 0);
+    const int second = n > 1 ? first + 1 : first;
+    auto mul0 = [&](int u) __attribute__((always_inline)) {
+      unit_scales(sz, lds, u * GU, row);
+      turn_unit<WQ, CT, 1>(w0, a0, turn, lane);
       mul_unit<TK, WQ, CT, 1, false, false>(w0, sz, a0, tot, u, k);
-      __builtin_amdgcn_sched_barrier(0);  // used up before it is loaded again: same registers, no copies
-      load0(u + 2);
-      __builtin_amdgcn_sched_barrier(0);
-      unit_scales(sz, s, 1);
-      mul_unit<TK, WQ, CT, 1, false, false>(w1, sz, a1, tot, u + 1, k);
-      __builtin_amdgcn_sched_barrier(0);
-      load1(u + 3);
-      __builtin_amdgcn_sched_barrier(0);
-      if constexpr (group_len<WQ>() != 32) s = sn;
-      u += 2;
-      left -= 2;
-    }
-    __builtin_amdgcn_sched_barrier(0);
-    unit_scales(sz, s, 0);
-    mul_unit<TK, WQ, CT, 1, false, false>(w0, sz, a0, tot, u, k);
-    if (left == 3) {
-      load_pair_scales(sn, t, u + 2, h);
-      load0(u + 2);
-    }
-    if (left >= 2) {
-      unit_scales(sz, s, 1);
-      mul_unit<TK, WQ, CT, 1, false, false>(w1, sz, a1, tot, u + 1, k);
-    }
-    if (left == 3) {
-      if constexpr (group_len<WQ>() == 32) {
-        unit_scales(sz, s, 0);
-      } else {
-        unit_scales(sz, sn, 0);
+    };
+    auto mul1 = [&](int u) __attribute__((always_inline)) {
+      unit_scales(sz, lds, u * GU, row);
+      turn_unit<WQ, CT, 1>(w1, a1, turn, lane);
+      mul_unit<TK, WQ, CT, 1, false, false>(w1, sz, a1, tot, u, k);
+    };
+    if constexpr (WQ != kWFull) {
+      // the scales first, then the first units' codes, and the scales to LDS
+      // while those are on their way
+      ScaleStage<WQ, CT, 64 * NW> st;
+      st.load(weight, j, g0, ng, groups, cols);
+      if (n > 0) {
+        load_w<WQ, CT, false>(w0, t, first, k, lane);
+        load_w<WQ, CT, false>(w1, t, second, k, lane);
       }
-      mul_unit<TK, WQ, CT, 1, false, false>(w0, sz, a0, tot, u + 2, k);
+      if (k0 > 0) __syncthreads();  // every wave is done with the span before
+      st.store(lds, weight, j, g0, ng, groups, cols);
+      if (n > 0) {
+        load_a<WQ, false>(a0[0], arow, first, k);
+        load_a<WQ, false>(a1[0], arow, second, k);
+      }
+      __syncthreads();
+    } else if (n > 0) {
+      load0(first);
+      load1(second);
+    }
+    if (n > 0) {
+      int u = first;
+      int left = n;
+#pragma unroll 1
+      while (left >= 4) {
+        mul0(u);
+        __builtin_amdgcn_sched_barrier(0);  // used up before it is loaded again: same registers, no copies
+        load0(u + 2);
+        __builtin_amdgcn_sched_barrier(0);
+        mul1(u + 1);
+        __builtin_amdgcn_sched_barrier(0);
+        load1(u + 3);
+        __builtin_amdgcn_sched_barrier(0);
+        u += 2;
+        left -= 2;
+      }
+      mul0(u);
+      if (left == 3) load0(u + 2);
+      if (left >= 2) mul1(u + 1);
+      if (left == 3) mul0(u + 2);
+    }
+    if (part) {  // (groups past k are not staged: mul_unit does not use them)
+      load_w<WQ, CT, true>(w0, t, full, k, lane);
+      load_a<WQ, true>(a0[0], arow, full, k);
+      unit_scales(sz, lds, full * GU, row);
+      turn_unit<WQ, CT, 1>(w0, a0, turn, lane);
+      mul_unit<TK, WQ, CT, 1, false, true>(w0, sz, a0, tot, full, k);
     }
   }
-  if (part >= 0) {
-    WUnit<WQ, CT> w;
-    u32x4 a[1][NB], sz[CT];
-    PairScales<WQ, CT> s;
-    load_pair_scales(s, t, part, h);
-    load_unit_scales(s, t, part, 0, h);
-    load_w<WQ, CT, true>(w, t, part, k, h);
-    load_a<WQ, true>(a[0], arow, part, k);
-    unit_scales(sz, s, 0);
-    mul_unit<TK, WQ, CT, 1, false, true>(w, sz, a, tot, part, k);
-  }
-}
-
-// how NW waves share k: wave w takes the full units first .. first + n - 1 and
-// perhaps the partial one; depends on k alone
-struct WaveShare {
-  int first, n, part;
-};
-template <int WQ, int NW>
-__device__ __forceinline__ WaveShare wave_share(int k, int wave) {
-  const int full = k / unit_len<WQ>();
-  const int all = (k + unit_len<WQ>() - 1) / unit_len<WQ>();
-  const int per = (all + NW - 1) / NW;
-  const int first = min(wave * per, full);
-  const int last = min(wave * per + per, full);
-  return {first, last - first, all > full && full / per == wave ? full : -1};
 }
 
 // store one fp32 value as the output kind (uniform runtime kind)
