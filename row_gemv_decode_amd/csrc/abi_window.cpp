@@ -80,7 +80,7 @@ struct skinny_moe_plan {
   int64_t max_slots;      // distinct experts a window can reach
   // workspace regions, in bytes from its start
   int64_t router_ws;      // the router plan's own workspace comes first (its counters start at zero)
-  int64_t counters, zero_page, logits, nslots, slots, slot_w, gates, partial, h, bytes;
+  int64_t logits, slots, slot_w, slot_rank, gates, h, y, bytes;
 };
 
 extern "C" {
@@ -162,7 +162,6 @@ skinny_status skinny_moe_plan_create(const skinny_moe_desc* desc, skinny_moe_pla
   p->router = router;
   p->max_slots = d.max_m * d.topk < d.experts ? d.max_m * d.topk : d.experts;
   const int64_t planes = moe_planes(kind_of(d.dtype), kind_of(d.out_dtype));
-  const int64_t splits = moe_down_splits(d.d, d.inter, d.shared_inter, d.topk, d.group);
   int64_t at = 0;
   auto region = [&at](int64_t bytes) {
     const int64_t start = at;
@@ -171,15 +170,13 @@ skinny_status skinny_moe_plan_create(const skinny_moe_desc* desc, skinny_moe_pla
   };
   p->router_ws = (int64_t)rws;
   region(p->router_ws);
-  p->counters = region(splits > 1 ? d.d / 32 * 4 : 0);
-  p->zero_page = region(256);
   p->logits = region(d.max_m * d.experts * 4);
-  p->nslots = region(4);
   p->slots = region(p->max_slots * 4);
   p->slot_w = region(p->max_slots * kGemvMaxM * 4);
+  p->slot_rank = region(p->max_slots * kGemvMaxM * 4);
   p->gates = region(kGemvMaxM * 4);
-  p->partial = region(splits > 1 ? splits * kGemvMaxM * d.d * 4 : 0);
   p->h = region((p->max_slots * d.inter + d.shared_inter) * kGemvMaxM * planes * 2);
+  p->y = region(d.max_m * (d.topk + 1) * d.d * 4);
   p->bytes = at;
   *out_plan = p;
   return SKINNY_OK;
@@ -243,14 +240,11 @@ skinny_status skinny_moe_run(const skinny_moe_plan* plan, int64_t m, const void*
   a.shared_gate = weights->shared_gate;
   a.logits = logits;
   a.slots = (uint32_t*)(base + plan->slots);
-  a.nslots = (int32_t*)(base + plan->nslots);
   a.slot_w = (float*)(base + plan->slot_w);
+  a.slot_rank = (int32_t*)(base + plan->slot_rank);
   a.gates = (float*)(base + plan->gates);
-  a.zero_page = (const uint16_t*)(base + plan->zero_page);
-  a.partial = (float*)(base + plan->partial);
-  a.counters = (uint32_t*)(base + plan->counters);
-  a.down_splits = moe_down_splits(d.d, d.inter, d.shared_inter, d.topk, d.group);
   a.h = (uint16_t*)(base + plan->h);
+  a.y = (float*)(base + plan->y);
   a.topk_idx = topk_idx;
   a.topk_weight = topk_weight;
   a.out = out;

@@ -7,7 +7,8 @@
 //   h_te  = silu(x_t . Wg_e) * (x_t . Wu_e) * p_te
 //   out_t = sum over e in S_t of h_te . Wd_e  +  (sigmoid(x_t . wg) * h_t,shared) . Wd_shared
 //
-// HBM-bound on the distinct experts' weights, each read once per window.
+// HBM-bound on the distinct experts' weights, each read once per window (the
+// down weight of an expert that serves more than 8 tokens twice).
 //   moe_route_kernel  one workgroup, one wave per token: top-k, softmax and the
 //                     list of distinct experts in ascending order with each
 //                     one's tokens (a second workgroup: the shared expert's
@@ -16,23 +17,19 @@
 //                     h): gate and up columns side by side against all rows of
 //                     x (a matrix-core tile holds 16 rows anyway, so tokens are
 //                     not gathered), p and silu in the epilogue
-//   moe_down_kernel   one workgroup per 32 columns of the layer's output and
-//                     share of the experts' k: a row that an expert does not
-//                     serve is a row of zeros, so the matrix core adds the
-//                     experts of every token by itself, and the combine costs
-//                     nothing; the last workgroup of a column range to finish
-//                     adds the shares in order
-// h is kept as the sum of planes in the weights' type, multiplied one after
-// another (the matrix cores have time for it while the weights stream): two,
+//   moe_down_kernel   per distinct expert, the output rows of the tokens it serves
+//   moe_combine_kernel  adds each token's rows
+// h is kept as the sum of planes in the weights' type, multiplied in rows of the
+// same matrix-core step: two,
 // 16 (bf16) or 22 (f16) bits, under a 16-bit output, where one plane would add
 // as much error as the output's own rounding; three (bf16, 24 bits) under an
 // fp32 output.  For 4-bit weights h is stored in the pair order that their
 // decoding yields.
 //
-// Row invariance: which wave takes which part of k depends on the expert and
-// the part alone, each wave adds its experts in ascending order, and what the
-// other tokens' experts add to a row is an exact zero; so a token's output is
-// the same bits in every window.
+// Row invariance: which wave takes which part of k depends on the layer alone, a
+// matrix-core row does not depend on the other rows, and a token's experts are
+// added in the order of its own choice; so a token's output is the same bits in
+// every window.
 #include "skinny.h"
 #include "wave_ops.h"
 #include "window_kernel.h"
@@ -95,9 +92,11 @@ __global__ __launch_bounds__(1024) void moe_route_kernel(MoeArgs a) {
   for (int e = tid; e < E; e += blockDim.x) mask[e] = 0;
   __syncthreads();
 
+  // (a NaN may have the lowest key: it is moved up, so that no expert is taken twice)
+  constexpr int kTaken = (int)0x80000000;
   int key[NC];
 #pragma unroll
-  for (int u = 0; u < NC; ++u) key[u] = lane + 64 * u < E ? order_key(x[u]) : (int)0x80000000;
+  for (int u = 0; u < NC; ++u) key[u] = lane + 64 * u < E ? max(order_key(x[u]), kTaken + 1) : kTaken;
   int top = 0, mine = 0, mine_e = 0;
   for (int i = 0; i < a.topk; ++i) {
     int best = key[0];
@@ -114,9 +113,8 @@ __global__ __launch_bounds__(1024) void moe_route_kernel(MoeArgs a) {
     } else {
       e = wave_min_i32(best == kmax ? col : 0x7fffffff);
     }
-    e = min(e, E - 1);  // (a NaN logit may leave no key above the lowest: keep the index in range)
 #pragma unroll
-    for (int u = 0; u < NC; ++u) key[u] = lane + 64 * u == e ? (int)0x80000000 : key[u];
+    for (int u = 0; u < NC; ++u) key[u] = lane + 64 * u == e ? kTaken : key[u];
     if (i == 0) top = kmax;
     mine = lane == i ? kmax : mine;
     mine_e = lane == i ? e : mine_e;
@@ -154,11 +152,13 @@ __global__ __launch_bounds__(1024) void moe_route_kernel(MoeArgs a) {
       n += __builtin_popcountll(b);
     }
     for (int i = n + lane; i < a.max_slots; i += 64) a.slots[i] = 0;  // slots without a token
-    if (lane == 0) *a.nslots = n;
   }
   __syncthreads();
-  // (a weight is read for the tokens in the slot's mask only)
-  if (lane < a.topk) a.slot_w[slot_of[mine_e] * kGemvMaxM + t] = p;
+  // (read for the tokens in the slot's mask only)
+  if (lane < a.topk) {
+    a.slot_w[slot_of[mine_e] * kGemvMaxM + t] = p;
+    a.slot_rank[slot_of[mine_e] * kGemvMaxM + t] = lane;
+  }
 }
 
 // where column i of h lies in memory: for 4-bit weights each run of eight is
@@ -171,6 +171,34 @@ __device__ __forceinline__ int h_place(int i) {
     const int e = i & 7;
     return (i & ~7) + (e < 4 ? 2 * e : 2 * e - 7);
   }
+}
+
+// Waves that share a column's sum in the down product: more than one where k has
+// many units, or where one token's experts would leave most of the chip idle.  By
+// the layer alone, so that every window adds in the same order.  Every wave has
+// a unit.
+__host__ __device__ __forceinline__ int down_waves(int units, int64_t d, int topk) {
+  int n = 1;
+  while (n < kMoeWaves && (units > 8 * n || topk * (d / 16) * n < 1024) &&
+         (2 * n - 1) * ((units + 2 * n - 1) / (2 * n)) < units)
+    n *= 2;
+  return n;
+}
+
+// column tiles of a wave in the down product.  Measured (us, 1 / 2 / 4 tiles):
+// 16-bit weights, 1 of 256 experts (d = 5120, inter = 896) 21.1 / 22.9 / 25.0;
+// 4 bits, 16 of 256 110 / 83 / 82, 3 of 256 33 / 27 / 29, 5 of 512 (d = 2560,
+// inter = 672) 31 / 27 / 26, 1 of 8 (d = 4096, inter = 8192) 16.4 / 15.5 / 19.5
+template <int WQ>
+constexpr int down_tiles() { return WQ == kWFull ? 1 : 2; }
+
+__device__ const u32x4 kZeroLine = {0u, 0u, 0u, 0u};
+
+// The row that a lane of token tk reads: its own if the expert serves it, else
+// one that is read anyway (whose sums are then not stored for tk)
+__device__ __forceinline__ int served_row(uint32_t entry, int tk, int m) {
+  const uint32_t mask = (entry >> 16) & ((1u << m) - 1);
+  return ((mask >> tk) & 1u) != 0 ? tk : __builtin_ctz(mask);
 }
 
 // GT tiles of 16 columns of h: columns of w13 are the gate's 0 .. inter - 1,
@@ -204,8 +232,7 @@ __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_up_kernel(MoeArgs a) {
     j[GT + c] = j0 + 16 * c + inter;
     tot[c] = tot[GT + c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   }
-  const int row = min(lane >> 2, a.m - 1);
-  const uint16_t* arow = (const uint16_t*)a.x + row * a.ldx + 8 * (lane & 3);
+  const uint16_t* arow = (const uint16_t*)a.x + served_row(entry, lane >> 2, a.m) * a.ldx + 8 * (lane & 3);
   block_product<TK, WQ, 2 * GT, kMoeWaves>(tot, lds, Turn(turn_s[wave], lane), shared ? a.s13 : a.w13, j, 16, arow, k,
                                            wave, lane);
 #pragma unroll
@@ -239,65 +266,10 @@ __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_up_kernel(MoeArgs a) {
   }
 }
 
-// The items (expert, unit of its k) that wave `id` of `step` takes, expert by
-// expert in the list's order: run r of RUN consecutive units of expert e goes
-// to wave (e * runs + r) mod step.  RUN units of a column fill a cache line
-// (two units of codes, one of 16-bit weights): a line is read by one wave
-// (units of a line in two workgroups, on two XCDs, were read twice from memory).
-// step is a power of two; the shared expert, last in the list, counts as
-// expert 0 with runs of its own.
-template <int RUN>
-struct DownItems {
-  const uint32_t* list;  // nslots entries, then the shared expert's, if any
-  int slots;             // entries in all
-  int shared_slot;       // its place, or one past the list
-  int units, shared_units, id, step;
-  int s, u;              // the current item
-  uint32_t entry;
-
-  __device__ __forceinline__ int units_of(int slot) const { return slot == shared_slot ? shared_units : units; }
-  // the wave's first unit in a slot (perhaps past its last)
-  __device__ __forceinline__ int first_of(int slot, uint32_t en) const {
-    const int runs = (units + RUN - 1) / RUN;
-    return ((slot == shared_slot ? id : id - (int)(en & 0xffffu) * runs) & (step - 1)) * RUN;
-  }
-  __device__ __forceinline__ int count(int lane) const {
-    int n = 0;
-    for (int q = lane; q < slots; q += 64) {
-      const int f = first_of(q, list[q]), un = units_of(q);
-      const int whole = f < un ? (un - f) / (step * RUN) : 0;  // rounds that hold a whole run
-      n += f < un ? whole * RUN + min(RUN, un - f - whole * step * RUN) : 0;
-    }
-    return (int)wave_sum_f32((float)n);  // (exact: far below 2^24)
-  }
-  __device__ __forceinline__ void begin() {
-    s = -1;
-    u = RUN - 1;
-    entry = 0;
-    next();
-  }
-  // to the next item; past the last one it stays there
-  __device__ __forceinline__ void next() {
-    int ns = s, nu = u + 1;
-    uint32_t ne = entry;
-    if (nu % RUN == 0) nu += (step - 1) * RUN;
-    while (ns < 0 || nu >= units_of(ns)) {
-      if (ns + 1 >= slots) return;
-      ++ns;
-      ne = (uint32_t)__builtin_amdgcn_readfirstlane((int)list[ns]);
-      nu = first_of(ns, ne);
-    }
-    s = ns;
-    u = nu;
-    entry = ne;
-  }
-};
-
-// The scales and zero points of one unit of two adjacent tiles of 16 columns:
-// even lane groups fetch the first tile's, odd ones the second's, in one load
-// for the scales (2, 4 or 8 bytes of each column) and one for the zero points
-// (half as many).
-template <int WQ>
+// The scales and zero points of one unit of CT adjacent tiles of 16 columns:
+// lane group h fetches tile h mod CT's, in one load for the scales (2, 4 or 8
+// bytes of each column) and one for the zero points (half as many).
+template <int WQ, int CT>
 struct UnitScales {
   static constexpr int GU = 128 / group_len<WQ>();  // groups per unit
   uint32_t s[2], z;
@@ -336,8 +308,9 @@ struct UnitScales {
     }
   }
 
-  // per tile and group: scale in the low half, zero point in the high half
-  __device__ __forceinline__ void get(u32x4 (&sz)[2]) const {
+  // per tile and group: scale in the low half, zero point in the high half; a
+  // group past the unit's n has scale 0
+  __device__ __forceinline__ void get(u32x4 (&sz)[CT], int n) const {
     uint32_t lo = s[0], hi = 0, zz = 0;
     if constexpr (GU == 4) {
       const uint64_t q = (((uint64_t)s[1] << 32) | s[0]) >> (16 * shift);
@@ -354,201 +327,228 @@ struct UnitScales {
       zs = spread4(zz);
     }
 #pragma unroll
-    for (int c = 0; c < 2; ++c)
+    for (int c = 0; c < CT; ++c)
 #pragma unroll
       for (int g = 0; g < GU; ++g) {
         const uint32_t word = g < 2 ? (uint32_t)l[c] : (uint32_t)m[c];
         const uint32_t sc = (g & 1) != 0 ? word >> 16 : word & 0xffffu;
         const uint32_t zw = zs[c];
-        sz[c][g] = sc | (((zw >> (8 * g)) & 0xffu) << 16);
+        const uint32_t v = sc | (((zw >> (8 * g)) & 0xffu) << 16);
+        sz[c][g] = GU > 1 && g >= n ? 0u : v;
       }
   }
 };
-template <>
-struct UnitScales<kWFull> {
-  __device__ __forceinline__ void get(u32x4 (&)[2]) const {}
+template <int CT>
+struct UnitScales<kWFull, CT> {
+  __device__ __forceinline__ void get(u32x4 (&)[CT], int) const {}
 };
 
+// The experts' outputs, as fp32 rows y for the tokens that each expert serves.
+// A wave owns CT tiles of 16 columns (KS = 1), or KS waves share them, each with
+// a run of the units of k.  Few experts serve many tokens, so the rows of the
+// matrix-core tile hold the planes of h: 16 / PS tokens, plane p in the rows from
+// p * (16 / PS), and one step multiplies all planes; an expert that serves more
+// tokens takes further workgroups (blockIdx.y), which read its weight again.
+// Bound by what a wave does per byte, not by memory alone: with the planes in
+// turn, h for 16 tokens and the waves splitting k, 16 of 256 experts (d = 5120,
+// inter = 896, 4 bits) took 130 to 170 us; so, 83 (3.5 TB/s).
 template <int TK, int WQ, int NP>
 __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_down_kernel(MoeArgs a) {
-  constexpr int CT = 2;
+  constexpr int CT = down_tiles<WQ>();
   constexpr int NB = unit_blocks<WQ>();
   constexpr int UL = unit_len<WQ>();
-  __shared__ f32x4 red[kMoeWaves][CT][64];
-  __shared__ u32x4 turn_s[kMoeWaves][turn_slots<WQ, CT, NP>() * 64];
-  __shared__ uint32_t list[kGemvMaxM * SKINNY_TOPK_MAX + 1];
-  __shared__ int last_s;
+  constexpr int PS = NP == 2 ? 2 : 4, TT = 16 / PS;  // rows for a token's planes, tokens
+  constexpr int GU = WQ == kWFull ? 1 : 128 / (WQ == kWFull ? 1 : group_len<WQ>());
+  __shared__ u32x4 turn_s[kMoeWaves][turn_slots<WQ, CT, 1>() * 64];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int h = lane >> 4;
   const int row = lane & 15;
-  // Workgroups go to the eight XCDs in turn: the shares of one column range are
-  // eight apart, so they find each other's cache lines (a column's scales and
-  // its ends of code lines) in one L2.
-  int split, tile;
+  const int sets = (int)a.d / 16 / CT;  // (d is a multiple of 16 CT)
+
+  // the workgroup's expert and sets of columns; the shared expert's come first
+  const int KS0 = a.shared_inter > 0 ? down_waves((int)((a.shared_inter + UL - 1) / UL), a.d, a.topk) : 1;
+  const int per0 = kMoeWaves / KS0;
+  const int blocks0 = a.shared_inter > 0 ? (sets + per0 - 1) / per0 : 0;
+  const bool shared = (int)blockIdx.x < blocks0;
+  const int KS = shared ? KS0 : down_waves((int)((a.inter + UL - 1) / UL), a.d, a.topk);
+  const int per = kMoeWaves / KS;  // sets of a workgroup
+  const int blocks = (sets + per - 1) / per;
+  const int b = (int)blockIdx.x - (shared ? 0 : blocks0);
+  const int slot = shared ? a.max_slots : b / blocks;  // (the shared expert's h lies after the slots')
+  const uint32_t entry = shared ? 0xffff0000u : a.slots[slot];
+  // the tokens of this workgroup: the TT served ones from blockIdx.y * TT on
+  uint32_t mask = (entry >> 16) & ((1u << a.m) - 1);
+  for (int i = 0; i < (int)blockIdx.y * TT && mask != 0; ++i) mask &= mask - 1;
+  if (mask == 0) return;  // none, or a slot past the window's experts
+  const int set = (shared ? b : b - slot * blocks) * per + wave / KS;
+  const int k = (int)(shared ? a.shared_inter : a.inter);
+  const int units = (k + UL - 1) / UL;
+  const int run = (units + KS - 1) / KS;  // every wave has a unit
+  const int first = wave % KS * run, n = min(run, units - first);
+
+  // lane group l >> 2 reads row l >> 2: a plane of a token, or one that is read
+  // anyway; this lane's four results' tokens follow
+  int tk = 0;
+  int64_t yrow[4];
   {
-    const int S = a.down_splits, b = blockIdx.x, tiles = (int)(gridDim.x / (unsigned)S);
-    const int whole = tiles / 8 * 8 * S;  // workgroups of whole sets of eight ranges
-    if (b < whole) {
-      split = b / 8 % S;
-      tile = b / (8 * S) * 8 + b % 8;
-    } else {
-      split = (b - whole) % S;
-      tile = whole / S + (b - whole) / S;
+    uint32_t left = mask;
+    const int last = __builtin_ctz(mask);
+    tk = last;
+#pragma unroll
+    for (int i = 0; i < TT; ++i) {
+      const int t = left != 0 ? __builtin_ctz(left) : -1;
+      if (t >= 0 && (lane >> 2) % TT == i) tk = t;
+      if (i / 4 == (lane >> 4) % (TT / 4)) {
+        const int rank = t < 0 || shared ? a.topk : a.slot_rank[slot * kGemvMaxM + t];
+        yrow[i % 4] = t < 0 ? -1 : ((int64_t)t * (a.topk + 1) + rank) * a.d;
+      }
+      left &= left - 1;
     }
   }
-  const int64_t j0 = (int64_t)tile * (16 * CT);
+  const int plane = min((lane >> 2) / TT, NP - 1);
 
-  int nslots = *a.nslots;
-  for (int i = threadIdx.x; i < a.max_slots; i += 64 * kMoeWaves) list[i] = a.slots[i];
-  nslots = __builtin_amdgcn_readfirstlane(nslots);
-  __syncthreads();
-  if (threadIdx.x == 0 && a.shared_inter > 0) list[nslots] = 0xffff0000u;
-  __syncthreads();
-
-  DownItems<(WQ == kWFull ? 1 : 2)> it;
-  it.list = list;
-  it.slots = nslots + (a.shared_inter > 0 ? 1 : 0);
-  it.shared_slot = nslots;
-  it.units = (int)((a.inter + UL - 1) / UL);
-  it.shared_units = (int)((a.shared_inter + UL - 1) / UL);
-  it.id = wave + kMoeWaves * split;
-  it.step = kMoeWaves * a.down_splits;
-  const int n = __builtin_amdgcn_readfirstlane(it.count(lane));
-
-  f32x4 tot[CT];
-#pragma unroll
-  for (int c = 0; c < CT; ++c) tot[c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  const WindowWeight& W = shared ? a.s2 : a.w2;
+  const int64_t e0 = (int64_t)(entry & 0xffffu) * a.d;  // the expert's first column
+  const uint32_t cbytes = (uint32_t)(WQ == kWFull ? k * 2 : k >> 1);
+  const uint32_t coff = (uint32_t)(lane >> 2) * cbytes + 16 * (lane & 3);
+  const uint16_t* hbase = a.h + slot * (int64_t)(kGemvMaxM * NP) * a.inter;
+  const uint32_t hoff = (uint32_t)((tk * NP + plane) * k + 8 * (lane & 3));
+  const int groups = k / (WQ == kWFull ? 1 : group_len<WQ>());
+  const int col = 16 * ((lane >> 4) % CT) + row;
 
   struct Item {
     WUnit<WQ, CT> w;
-    UnitScales<WQ> s;
-    u32x4 a[NP][NB];
+    UnitScales<WQ, CT> s;
+    u32x4 a[1][NB];
   };
-  // Load the current item.  A row that the expert does not serve reads zeros,
-  // and so do all rows in blocks past the expert's k, where the weight reads
-  // the unit's first block instead: every item is then multiplied whole, with
+  const int64_t j = e0 + (int64_t)min(set, sets - 1) * (16 * CT);  // (a wave past the last set repeats it)
+  const char* cset = (const char*)W.codes + j * cbytes;
+  // A k that is no multiple of the unit: blocks past k read zeros for h and the
+  // unit's first block for the weight, so every item is multiplied whole, with
   // no branch between the matrix-core steps.
-  auto load = [&](Item& q) __attribute__((always_inline)) {
-    const bool shared = it.s == it.shared_slot;
-    const int k = (int)(shared ? a.shared_inter : a.inter);
-    const WindowWeight& W = shared ? a.s2 : a.w2;
-    const int64_t jb = (shared ? 0 : (int64_t)(it.entry & 0xffffu) * a.d) + j0;
-    int64_t j[CT];
-#pragma unroll
-    for (int c = 0; c < CT; ++c) j[c] = jb + 16 * c;
-    WTiles<WQ, CT> t;
-    w_tiles<WQ, CT>(t, W, j, k, 16, lane);
-    const bool part = it.u * UL + UL > k;
-    const int tk = lane >> 2, piece = lane & 3;  // this lane's token (or column) and piece of each block
-    const bool served = tk < a.m && ((it.entry >> (16 + tk)) & 1u) != 0;
-    const uint16_t* hr = a.h + (shared ? a.max_slots : it.s) * (int64_t)(kGemvMaxM * NP) * a.inter +
-                         (int64_t)tk * NP * k + it.u * UL + 8 * piece;
+  auto load = [&](Item& q, int u) __attribute__((always_inline)) {
+    const int rest = k - u * UL;
     if constexpr (WQ == kWFull) {
+      const char* cu = cset + (int64_t)u * 128;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int at = part && it.u * UL + 32 * i >= k ? 0 : 64 * i;
+        const int off = 32 * i >= rest ? 0 : 64 * i;
 #pragma unroll
-        for (int c = 0; c < CT; ++c) q.w.v[c][i] = *(const u32x4*)(t.codes[c] + (int64_t)it.u * 128 + t.off + at);
+        for (int c = 0; c < CT; ++c) q.w.v[c][i] = *(const u32x4*)(cu + (coff + (uint32_t)(c * 16) * cbytes) + off);
       }
     } else {
-      const int at = part && it.u * UL + 32 * piece >= k ? -16 * piece : 0;
+      const char* cu = cset + (int64_t)u * 64;
+      const uint32_t off = coff - (group_len<WQ>() != 128 && 32 * (lane & 3) >= rest ? 16u * (lane & 3) : 0u);
 #pragma unroll
-      for (int c = 0; c < CT; ++c) q.w.v[c][0] = *(const u32x4*)(t.codes[c] + (int64_t)it.u * 64 + t.off + at);
-      const int64_t rows = shared ? a.d - j0 : (a.experts - (int64_t)(it.entry & 0xffffu)) * a.d - j0;
-      q.s.load(W, jb, 16 * (h & 1) + row, it.u, k / group_len<WQ>(), (int)min(rows, (int64_t)64));
+      for (int c = 0; c < CT; ++c) q.w.v[c][0] = *(const u32x4*)(cu + (off + (uint32_t)(c * 16) * cbytes));
+      const int64_t rows = shared ? a.d - j : a.experts * a.d - j;
+      q.s.load(W, j, col, u, groups, (int)min(rows, (int64_t)64));
     }
+    const uint16_t* hu = hbase + (int64_t)u * UL;
 #pragma unroll
-    for (int p = 0; p < NP; ++p) {
-      const uint16_t* hp = served ? hr + (int64_t)p * k : a.zero_page;
-#pragma unroll
-      for (int i = 0; i < NB; ++i) {
-        const uint16_t* hi = part && it.u * UL + 32 * i >= k ? a.zero_page : hp + 32 * i;
-        q.a[p][i] = *(const u32x4*)hi;
-      }
+    for (int i = 0; i < NB; ++i) {
+      const uint16_t* at = hu + hoff + 32 * i;
+      if (group_len<WQ>() != 128 && 32 * i >= rest) at = (const uint16_t*)&kZeroLine;
+      q.a[0][i] = *(const u32x4*)at;
     }
-  };
-  const Turn turn(turn_s[wave], lane);
-  auto mul = [&](Item& q) __attribute__((always_inline)) {
-    u32x4 sz[CT];
-    q.s.get(sz);
-    turn_unit<WQ, CT, NP>(q.w, q.a, turn, lane);
-    mul_unit<TK, WQ, CT, NP, true, false>(q.w, sz, q.a, tot, 0, 0);
   };
 
-  if (n > 0) {
-    Item i0, i1;
-    it.begin();
-    load(i0);
-    it.next();  // (past the last item: the last again)
-    load(i1);
-    int left = n;
+  const Turn turn(turn_s[wave], lane);
+  f32x4 tot[CT];
+#pragma unroll
+  for (int c = 0; c < CT; ++c) tot[c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  auto mul = [&](Item& q, int u) __attribute__((always_inline)) {
+    u32x4 sz[CT];
+    q.s.get(sz, groups - u * GU);
+    turn_unit<WQ, CT, 1>(q.w, q.a, turn, lane);
+    if constexpr (WQ == kWFull) {
+      // (the matrix core's results are read in the straight line of code that
+      // forms them: for a read behind a branch the compiler has left out the wait)
+      f32x4 acc[CT];
+#pragma unroll
+      for (int c = 0; c < CT; ++c) acc[c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      mul_unit<TK, WQ, CT, 1, true, false>(q.w, sz, q.a, acc, 0, 0);
+#pragma unroll
+      for (int c = 0; c < CT; ++c) tot[c] += acc[c];
+    } else {
+      mul_unit<TK, WQ, CT, 1, true, false>(q.w, sz, q.a, tot, 0, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);  // used up before it is loaded again: same registers, no copies
+  };
+  {
+    Item q0, q1;
+    int u = first, left = n;
+    load(q0, u);
+    load(q1, n > 1 ? u + 1 : u);
 #pragma unroll 1
     while (left >= 4) {
-      mul(i0);
+      mul(q0, u);
+      load(q0, u + 2);
       __builtin_amdgcn_sched_barrier(0);
-      it.next();
-      load(i0);
+      mul(q1, u + 1);
+      load(q1, u + 3);
       __builtin_amdgcn_sched_barrier(0);
-      mul(i1);
-      __builtin_amdgcn_sched_barrier(0);
-      it.next();
-      load(i1);
-      __builtin_amdgcn_sched_barrier(0);
+      u += 2;
       left -= 2;
     }
-    mul(i0);
-    if (left == 3) {
-      it.next();
-      load(i0);
-    }
-    if (left >= 2) mul(i1);
-    if (left == 3) mul(i0);
+    mul(q0, u);
+    if (left == 3) load(q0, u + 2);
+    if (left >= 2) mul(q1, u + 1);
+    if (left == 3) mul(q0, u + 2);
   }
 
+  if (KS > 1) {
+    f32x4* red = (f32x4*)turn_s[wave];
+    wave_lds_order();
 #pragma unroll
-  for (int c = 0; c < CT; ++c) red[wave][c][lane] = tot[c];
-  __syncthreads();
-  const int64_t jc = j0 + 16 * wave + row;  // waves 0 and 1: this thread's column
-  const bool mine = wave < CT;
-  if (mine) {
-    f32x4 sum = red[0][wave][lane];
-#pragma unroll
-    for (int w = 1; w < kMoeWaves; ++w) sum += red[w][wave][lane];
-    if (a.down_splits == 1) {
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        if (4 * h + q < a.m) store_kind(a.out, (4 * h + q) * a.ldo + jc, sum[q], a.out_kind);
-    } else {
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        if (4 * h + q < a.m) st_dev(a.partial + ((int64_t)split * kGemvMaxM + 4 * h + q) * a.d + jc, sum[q]);
-      wait_mem();  // this share has reached the device-coherent level
-    }
-  }
-  if (a.down_splits > 1) {
-    __syncthreads();  // every wave's share has
-    if (threadIdx.x == 0) last_s = atomicAdd(&a.counters[tile], 1u) == (uint32_t)(a.down_splits - 1);
+    for (int c = 0; c < CT; ++c) red[c * 64 + lane] = tot[c];
     __syncthreads();
-    if (last_s && mine) {
-      // every share is there: add them in order
+    if (wave % KS == 0) {
+      for (int w = 1; w < KS; ++w)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        if (4 * h + q < a.m) {
-          const float* p = a.partial + (int64_t)(4 * h + q) * a.d + jc;
-          float v[kMoeMaxSplits];
-#pragma unroll
-          for (int i = 0; i < kMoeMaxSplits; ++i)
-            v[i] = ld_dev(p + (int64_t)(i < a.down_splits ? i : 0) * kGemvMaxM * a.d);
-          float sum = v[0];
-#pragma unroll
-          for (int i = 1; i < kMoeMaxSplits; ++i) sum = i < a.down_splits ? sum + v[i] : sum;
-          store_kind(a.out, (4 * h + q) * a.ldo + jc, sum, a.out_kind);
-        }
-      }
+        for (int c = 0; c < CT; ++c) tot[c] += ((const f32x4*)turn_s[wave + w])[c * 64 + lane];
     }
-    if (last_s && threadIdx.x == 0) a.counters[tile] = 0u;  // ready for the next call
   }
+  // the planes' sums: the groups of TT rows, in order
+#pragma unroll
+  for (int c = 0; c < CT; ++c)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      float v = tot[c][q];
+      auto s32 = __builtin_amdgcn_permlane32_swap(ubits(v), ubits(v), false, false);
+      if constexpr (PS == 2) {
+        v = fbits(s32[0]) + fbits(s32[1]);  // (lane groups h and h + 2)
+      } else {
+        auto lo = __builtin_amdgcn_permlane16_swap(s32[0], s32[0], false, false);  // planes 0 and 1
+        auto hi = __builtin_amdgcn_permlane16_swap(s32[1], s32[1], false, false);  // plane 2
+        v = (fbits(lo[0]) + fbits(lo[1])) + fbits(hi[0]);
+      }
+      tot[c][q] = v;
+    }
+  if (wave % KS == 0 && set < sets && lane < 16 * 4 / PS) {
+    float* y = a.y + (int64_t)set * (16 * CT) + row;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (yrow[q] >= 0) {
+#pragma unroll
+        for (int c = 0; c < CT; ++c) y[yrow[q] + 16 * c] = tot[c][q];
+      }
+  }
+}
+
+// out[t] = the sum of token t's experts' rows, largest logit first, then the
+// shared expert's; a thread adds four columns
+__global__ __launch_bounds__(64) void moe_combine_kernel(MoeArgs a) {
+  const int64_t j = 4 * (int64_t)(blockIdx.x * 64 + threadIdx.x);
+  const int t = blockIdx.y;
+  if (j >= a.d) return;
+  const float* y = a.y + (int64_t)t * (a.topk + 1) * a.d + j;
+  const int n = a.topk + (a.shared_inter > 0 ? 1 : 0);
+  f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 8
+  for (int i = 0; i < n; ++i) sum += *(const f32x4*)(y + (int64_t)i * a.d);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) store_kind(a.out, t * a.ldo + j + e, sum[e], a.out_kind);
 }
 
 typedef void (*moe_fn)(MoeArgs);
@@ -590,23 +590,12 @@ moe_fn pick(int kind, int np, int group, bool zeros, bool up, bool wide) {
 
 int moe_planes(int kind, int out_kind) { return kind == CK_BF16 && out_kind == CK_F32 ? 3 : 2; }
 
-// Shares of the down product's k, a power of two: enough workgroups for about
-// ten waves per CU of 256, but not more waves than one token's experts have
-// units.  By the layer alone, which also fixes every row's order of additions.
-int moe_down_splits(int64_t d, int64_t inter, int64_t shared_inter, int topk, int group) {
-  const int64_t unit = group == 0 ? 64 : 128;
-  const int64_t units = topk * ((inter + unit - 1) / unit) + (shared_inter + unit - 1) / unit;
-  int s = 1;
-  while (s < kMoeMaxSplits && d / 32 * s < 640 && s * kMoeWaves < units) s *= 2;
-  return s;
-}
-
 hipError_t launch_moe(const MoeArgs& a, int kind, int group, hipStream_t stream) {
   if (a.m < 1 || a.m > kGemvMaxM || a.experts < 1 || a.experts > kMoeMaxExperts || a.topk < 1 ||
       a.topk > SKINNY_TOPK_MAX || a.topk > a.experts || a.d % 32 != 0 || a.inter % 32 != 0 || a.shared_inter % 32 != 0 ||
       (group != 0 && group != 32 && group != 64 && group != 128) ||
       (group != 0 && (a.d % group != 0 || a.inter % group != 0 || a.shared_inter % group != 0)) ||
-      (kind != CK_F16 && kind != CK_BF16) || a.down_splits != moe_down_splits(a.d, a.inter, a.shared_inter, a.topk, group))
+      (kind != CK_F16 && kind != CK_BF16))
     return hipErrorInvalidValue;
   const int64_t slots = (int64_t)a.m * a.topk < a.experts ? (int64_t)a.m * a.topk : a.experts;
   if (slots > a.max_slots || a.max_slots > kGemvMaxM * SKINNY_TOPK_MAX) return hipErrorInvalidValue;
@@ -615,10 +604,18 @@ hipError_t launch_moe(const MoeArgs& a, int kind, int group, hipStream_t stream)
   // does not depend on it)
   const bool wide = slots * (a.inter / 32) >= 2048;
   const int64_t tile = wide ? 32 : 16;
-  const int64_t up_blocks = slots * (a.inter / tile) + a.shared_inter / tile;
-  const int64_t down_blocks = a.d / 32 * a.down_splits;
-  if (up_blocks > 0x7fffffff) return hipErrorInvalidValue;
   const int np = moe_planes(kind, a.out_kind);
+  const int64_t up_blocks = slots * (a.inter / tile) + a.shared_inter / tile;
+  // the down product: as in its kernel
+  const int unit = group == 0 ? unit_len<kWFull>() : unit_len<128>();
+  const int64_t sets = a.d / 16 / (group == 0 ? down_tiles<kWFull>() : down_tiles<128>());
+  auto blocks = [&](int64_t inter) {
+    const int per = kMoeWaves / down_waves((int)((inter + unit - 1) / unit), a.d, a.topk);
+    return (sets + per - 1) / per;
+  };
+  const int64_t down_blocks = slots * blocks(a.inter) + (a.shared_inter > 0 ? blocks(a.shared_inter) : 0);
+  const int tokens = np == 2 ? 8 : 4;  // of a workgroup
+  if (up_blocks > 0x7fffffff || down_blocks > 0x7fffffff) return hipErrorInvalidValue;
   const bool zeros = a.w13.zeros != nullptr;
   const bool f16 = kind == CK_F16;
   hipLaunchKernelGGL(f16 ? pick_route<CK_F16>(a.experts) : pick_route<CK_BF16>(a.experts),
@@ -629,8 +626,11 @@ hipError_t launch_moe(const MoeArgs& a, int kind, int group, hipStream_t stream)
                      stream, a);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(pick(kind, np, group, zeros, false, false), dim3((unsigned)down_blocks), dim3(64 * kMoeWaves), 0,
+  hipLaunchKernelGGL(pick(kind, np, group, zeros, false, false), dim3((unsigned)down_blocks, (unsigned)((a.m + tokens - 1) / tokens)), dim3(64 * kMoeWaves), 0,
                      stream, a);
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(moe_combine_kernel, dim3((unsigned)((a.d + 255) / 256), (unsigned)a.m), dim3(64), 0, stream, a);
   return hipGetLastError();
 }
 

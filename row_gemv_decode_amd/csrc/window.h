@@ -40,11 +40,10 @@ struct W4Args {
 hipError_t launch_w4_mm(const W4Args& args, int a_kind, int group, hipStream_t stream);
 
 // ---------------------------------------------------------------------------
-// The whole MoE layer for a decode window (moe.hip): route, up, down launches
-// after the router's GEMV.
+// The whole MoE layer for a decode window (moe.hip): route, up, down, combine
+// launches after the router's GEMV.
 // ---------------------------------------------------------------------------
 constexpr int kMoeMaxExperts = 1024;
-constexpr int kMoeMaxSplits = 16;
 
 struct MoeArgs {
   const void* x;           // [m][ldx]
@@ -57,22 +56,19 @@ struct MoeArgs {
   const void* shared_gate; // [d]
   const float* logits;     // [m][experts]
   uint32_t* slots;         // distinct experts, ascending: expert | token mask << 16
-  int32_t* nslots;
   float* slot_w;           // [max_slots][16]: each slot's routing weight per token it serves
+  int32_t* slot_rank;      // [max_slots][16]: and its place among the token's experts
   float* gates;            // [16]: the shared expert's gates
-  const uint16_t* zero_page;  // 256 bytes of zeros
-  float* partial;          // down_splits > 1: [down_splits][16][d] shares of the output
-  uint32_t* counters;      // down_splits > 1: [d / 32] arrivals, zero between calls
   uint16_t* h;             // [max_slots][16][planes][inter], then [16][planes][shared_inter]
+  float* y;                // [m][topk + 1][d]: the experts' outputs, the shared expert's last
   int32_t* topk_idx;       // [m][topk] or null
   float* topk_weight;      // [m][topk] or null
   void* out;               // [m][ldo]
   int64_t ldo;
-  int32_t m, experts, topk, renorm, max_slots, out_kind, down_splits;
+  int32_t m, experts, topk, renorm, max_slots, out_kind;
 };
 
 int moe_planes(int kind, int out_kind);  // 16-bit planes that hold one inner value
-int moe_down_splits(int64_t d, int64_t inter, int64_t shared_inter, int topk, int group);  // shares of the down product
 
 // kind: CK_F16 or CK_BF16; group: 0 (16-bit weights), 32, 64 or 128
 hipError_t launch_moe(const MoeArgs& args, int kind, int group, hipStream_t stream);

@@ -132,9 +132,9 @@ __device__ __forceinline__ u32x4 exchange4(u32x4 v) {
 // only, so a load gives four consecutive lanes the 64 bytes of one row (a
 // column of the weight, or a token): lane l fetches piece l & 3 of row l >> 2.
 // The matrix core wants piece l >> 4 of row l & 15 in lane l.  Loading in that
-// order made every lane an access of its own, and the accesses, 61 for each
-// load, were what bounded the kernels (16 x 256 experts: the up product
-// took 175 us, the down product 130).  So each 1 KiB passes through a slot of
+// order makes every lane an access of its own, and the accesses, some 30 for each
+// load, were what bounded the kernels (MoE, 16 of 256 experts: the up product
+// took 175 us for 137).  So each 1 KiB passes through a slot of
 // LDS that belongs to the wave: written as loaded, read as needed, no barrier.
 // A row's four pieces are stored rotated by f(row), which keeps the reads (and
 // the writes) free of bank conflicts.
@@ -147,7 +147,9 @@ struct Turn {
     put = entry(lane >> 2, lane & 3);
     get = entry(lane & 15, lane >> 4);
   }
-  static __device__ __forceinline__ int entry(int row, int piece) { return row * 4 + (piece ^ ((row >> 1) & 3)); }
+  static __device__ __forceinline__ int entry(int row, int piece) {
+    return row * 4 + (piece ^ ((row >> 1) & 3) ^ (row >> 3));
+  }
 };
 
 // order of a wave's LDS writes and its later reads by other lanes (the LDS
