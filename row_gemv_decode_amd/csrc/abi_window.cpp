@@ -37,21 +37,22 @@ int64_t span(int64_t rows, int64_t ld, int64_t len, int64_t size) { return ((row
 
 int64_t round256(int64_t b) { return (b + 255) / 256 * 256; }
 
-// Workgroups per row of the log probabilities.  A window's rows (m <= 16) are
-// cut alike at every m, into at most 32 segments of at least 8192 logits; more
-// rows into as many as give about four workgroups of four waves per CU of 256,
-// and from 256 rows on a row is one workgroup's, of eight waves up to 1023 rows
-// and four from there on.  Measured (us): 16 x 131071 bf16, top 20, segments of
-// at least 4096 / 8192 / 16384: 18.0 / 15.4 / 17.5; 1 x 32000 fp32 10.5 / 11.7 /
-// 14.9; 512 x 50021 f16 with four / eight waves 26.6 / 23.5, 300 x 100003 bf16
-// 43 / 37, 2048 x 32000 bf16 45 / 54.
+// Workgroups per row of the log probabilities: as many as give four workgroups of
+// four waves per CU of 256, but at most 16 (which cuts a window's rows alike at
+// every m), each of at least 4096 logits; from 256 rows on a row is one
+// workgroup's, of eight waves up to 1023 rows and four from there on.  Measured
+// (us): at most 16 / 32 segments, 16 x 131071 bf16, top 20, 15.4 / 17.9, 1 x 151000
+// bf16 12.3 / 13.0; segments of at least 4096 / 8192, 1 x 32000 fp32 10.5 / 11.7,
+// 4 x 50000 11.5 / 12.8; 512 x 50021 f16 with four / eight waves 26.6 / 23.5, 300 x
+// 100003 bf16 43 / 37, 2048 x 32000 bf16 45 / 54.
 struct RowSegments {
   int64_t count, len;
   int waves;
 };
 RowSegments row_segments(int64_t m, int64_t vocab) {
-  int64_t want = m <= SKINNY_GEMV_MAX_M ? kLogprobMaxSegments : m < 256 ? (1024 + m - 1) / m : 1;
-  const int64_t most = (vocab + 8191) / 8192;
+  int64_t want = m < 256 ? (1024 + m - 1) / m : 1;
+  if (want > kLogprobMaxSegments) want = kLogprobMaxSegments;
+  const int64_t most = (vocab + 4095) / 4096;
   if (want > most) want = most;
   const int64_t len = ((vocab + want - 1) / want + 7) / 8 * 8;
   return {(vocab + len - 1) / len, len, m >= 256 && m < 1024 ? 8 : 4};

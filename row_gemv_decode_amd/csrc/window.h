@@ -76,7 +76,7 @@ hipError_t launch_moe(const MoeArgs& args, int kind, int group, hipStream_t stre
 // ---------------------------------------------------------------------------
 // Token log probabilities (logprobs.hip)
 // ---------------------------------------------------------------------------
-constexpr int kLogprobMaxSegments = 32;
+constexpr int kLogprobMaxSegments = 16;
 
 struct LogprobArgs {
   const void* logits;   // [m][ld]

@@ -70,6 +70,13 @@ def test_lp_row_counts(m, kind):
     check(x, t, 6, kind, t64=m % 2 == 0)
 
 
+@pytest.mark.parametrize("m,V", [(17, 300007), (31, 270001), (1, 600011)])
+def test_lp_long_rows(m, V):
+    """More logits than the segments' least length times their number."""
+    x, t = normal(m, V, 9290 + m)
+    check(x, t, 6, "bf16")
+
+
 @pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("offset", [0, 1, 2, 3, 5, 7])
 def test_lp_alignment_and_strides(offset, kind):
