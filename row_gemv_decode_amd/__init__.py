@@ -540,10 +540,26 @@ def _gpu(where, t):
     return index
 
 
-def _zeros_on(nbytes, index, stream):
-    """nbytes zero bytes on GPU `index`, allocated and filled on `stream` or its current stream."""
-    with torch.cuda.stream(torch.cuda.current_stream(index) if stream is None else stream):
-        return torch.zeros(nbytes, dtype=torch.uint8, device=torch.device("cuda", index))
+def _empty(shape, dtype, device, stream):
+    """An output, allocated on the stream that writes it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _stream_workspace(cache, key, nbytes, index, stream):
+    """The workspace of at least nbytes that `cache` holds for a stream, made
+    and zeroed on that stream (a run leaves its counters at zero).  One made
+    while the stream is captured belongs to the graph, which zeroes it at every
+    replay, and is not kept."""
+    ws = cache.get(key)
+    if ws is None or ws.numel() < nbytes:
+        with torch.cuda.stream(torch.cuda.current_stream(index) if stream is None else stream):
+            ws = torch.zeros(nbytes, dtype=torch.uint8, device=torch.device("cuda", index))
+            if not torch.cuda.is_current_stream_capturing():
+                cache[key] = ws
+    return ws
 
 
 def mm_w4(A, W, out=None, out_dtype=None, stream=None):
@@ -564,7 +580,7 @@ def mm_w4(A, W, out=None, out_dtype=None, stream=None):
         raise ValueError(f"mm_w4: A is on {A.device}, the weight on {W.device}")
     if out is None:
         out_dtype = out_dtype or torch.float32
-        out = torch.empty((m, n), dtype=out_dtype, device=W.device)
+        out = _empty((m, n), out_dtype, W.device, stream)
         ldc = n
     else:
         ldc = _rows("mm_w4", "out", out)
@@ -649,14 +665,6 @@ class MoELayer:
         self.workspace_bytes = int(sz.value)
         self._ws = {}
 
-    def _workspace(self, handle, stream):
-        """This layer's workspace for a stream (runs on different streams may be
-        in flight at once, so each has its own)."""
-        ws = self._ws.get(handle)
-        if ws is None:
-            ws = self._ws[handle] = _zeros_on(self.workspace_bytes, self._index, stream)
-        return ws
-
     def __call__(self, x, out=None, topk_idx=None, topk_weight=None, stream=None):
         """out [m][d]; topk_idx (int32 [m][topk]) and topk_weight (float32
         [m][topk]) receive the routing when given."""
@@ -667,7 +675,7 @@ class MoELayer:
             raise ValueError(f"MoELayer: x must be on {self.device}")
         m = shape[0]
         if out is None:
-            out = torch.empty((m, self.d), dtype=self.out_dtype, device=self.device)
+            out = _empty((m, self.d), self.out_dtype, self.device, stream)
         else:
             if tuple(out.shape) != (m, self.d) or out.dtype != self.out_dtype:
                 raise ValueError(f"MoELayer: out must be [{m}][{self.d}] of type {self.out_dtype}")
@@ -680,7 +688,8 @@ class MoELayer:
                 _dense("MoELayer", **{name: t})
                 _on("MoELayer", self.device, t)
         handle = _handle(self._index, stream)
-        ws = self._workspace(handle, stream)
+        # (runs on different streams may be in flight at once: each has its own)
+        ws = _stream_workspace(self._ws, handle, self.workspace_bytes, self._index, stream)
         _check(_lib.skinny_moe_run(self._h, m, x.data_ptr(), self._weights_addr, out.data_ptr(), _ptr(topk_idx),
                                    _ptr(topk_weight), ws.data_ptr(), self.workspace_bytes, handle), "skinny_moe_run")
         return out
@@ -711,15 +720,6 @@ _logprob_need = {}  # (m, vocab, topk) -> workspace bytes
 _logprob_ws = {}
 
 
-def _logprob_workspace(nbytes, index, handle, stream):
-    """The log probabilities' workspace of one stream, grown to the largest run
-    it has seen (a run leaves its counters at zero)."""
-    ws = _logprob_ws.get((index, handle))
-    if ws is None or ws.numel() < nbytes:
-        ws = _logprob_ws[index, handle] = _zeros_on(nbytes, index, stream)
-    return ws
-
-
 def token_logprobs(logits, tokens, topk=0, stream=None):
     """Log probabilities of tokens[i] under softmax(logits[i]), with entropy,
     rank and the topk <= 32 top alternatives (see TokenLogprobs), in one launch
@@ -745,12 +745,13 @@ def token_logprobs(logits, tokens, topk=0, stream=None):
             _logprob_need.clear()
         need = _logprob_need[m, vocab, topk] = int(sz.value)
     handle = _handle(index, stream)
-    ws = _logprob_workspace(need, index, handle, stream).data_ptr() if need else None
+    ws = _stream_workspace(_logprob_ws, (index, handle), need, index, stream) if need else None
     # one allocation for the five results, each at a multiple of 4 bytes
-    flat = torch.empty(m * (3 + 2 * topk), dtype=torch.float32, device=logits.device)
+    flat = _empty(m * (3 + 2 * topk), torch.float32, logits.device, stream)
     lp, ent, top, rank, ids = flat.split([m, m, m * topk, m, m * topk])
     p = flat.data_ptr()
     p_rank = p + 4 * m * (2 + topk)
     _check(_lib.skinny_token_logprobs_run(m, vocab, logits.data_ptr(), ld, dtype, tokens.data_ptr(), t64, topk, p, p + 4 * m,
-                                          p_rank, p_rank + 4 * m, p + 8 * m, ws, need, handle), "skinny_token_logprobs_run")
+                                          p_rank, p_rank + 4 * m, p + 8 * m, None if ws is None else ws.data_ptr(), need, handle),
+           "skinny_token_logprobs_run")
     return TokenLogprobs(lp, ent, rank.view(torch.int32), ids.view(torch.int32).view(m, topk), top.view(m, topk))

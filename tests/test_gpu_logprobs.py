@@ -220,6 +220,28 @@ def test_lp_graph_replay():
         assert all(torch.equal(a, b) and torch.equal(c, b) for a, b, c in zip(out, want, eager))
 
 
+def test_lp_captured_before_a_run():
+    """A capture on a stream without a workspace: the graph carries its own, and
+    eager runs on that stream get theirs."""
+    x, t = normal(2, 50000, 10300)
+    dev, tok, want = check(x, t, 7, "f32")
+    s = torch.cuda.Stream()
+    sk._logprob_ws.pop((dev.get_device(), s.cuda_stream), None)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        out = sk.token_logprobs(dev, tok, topk=7)
+    for _ in range(3):
+        eager = sk.token_logprobs(dev, tok, topk=7, stream=s)
+        s.synchronize()
+        for o in out:
+            o.zero_()
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) and torch.equal(c, b) for a, b, c in zip(out, want, eager))
+
+
 def test_lp_refusals():
     x = torch.zeros((2, 100), device="cuda")
     t = torch.zeros(2, dtype=torch.int64, device="cuda")

@@ -182,6 +182,26 @@ def test_moe_graph_replay():
         assert torch.equal(out, got) and torch.equal(eager, got)
 
 
+def test_moe_captured_before_a_run():
+    """A capture on a stream that the layer has not run on: the graph carries a
+    workspace of its own, and eager runs on that stream get theirs."""
+    c = Case(3, 20, 4, 256, 128, shared=64, group=64, seed=9050)
+    layer, x, got = c.check()
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        out = layer(x)
+    for _ in range(3):
+        eager = layer(x, stream=s)
+        s.synchronize()
+        out.zero_()
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, got) and torch.equal(eager, got)
+
+
 def test_moe_refusals():
     c = Case(2, 8, 2, 128, 64, shared=32, seed=9100)
     router, w13, w2 = c.dev(c.router), c.dev(c.w13), c.dev(c.w2)
