@@ -205,7 +205,6 @@ __device__ __forceinline__ int served_row(uint32_t entry, int tk, int m) {
 // then the up's
 template <int TK, int WQ, int NP, int GT>
 __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_up_kernel(MoeArgs a) {
-  __shared__ f32x4 red[kMoeWaves][2 * GT][64];
   __shared__ ScaleLds<WQ, 2 * GT> lds;
   __shared__ u32x4 turn_s[kMoeWaves][turn_slots<WQ, 2 * GT, 1>() * 64];
   const int lane = threadIdx.x & 63;
@@ -235,16 +234,10 @@ __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_up_kernel(MoeArgs a) {
   const uint16_t* arow = (const uint16_t*)a.x + served_row(entry, lane >> 2, a.m) * a.ldx + 8 * (lane & 3);
   block_product<TK, WQ, 2 * GT, kMoeWaves>(tot, lds, Turn(turn_s[wave], lane), shared ? a.s13 : a.w13, j, 16, arow, k,
                                            wave, lane);
-#pragma unroll
-  for (int c = 0; c < 2 * GT; ++c) red[wave][c][lane] = tot[c];
+  put_sums(turn_s[wave], tot, lane);
   __syncthreads();
   if (wave < GT) {
-    f32x4 g = red[0][wave][lane], up = red[0][GT + wave][lane];
-#pragma unroll
-    for (int w = 1; w < kMoeWaves; ++w) {
-      g += red[w][wave][lane];
-      up += red[w][GT + wave][lane];
-    }
+    const f32x4 g = wave_sums(turn_s, wave, lane), up = wave_sums(turn_s, GT + wave, lane);
     const float* weight = shared ? a.gates : a.slot_w + slot * kGemvMaxM;
     uint16_t* hb = a.h + (shared ? a.max_slots : slot) * (int64_t)(kGemvMaxM * NP) * a.inter;
     hb += 16 * (tile * GT + wave) + h_place<WQ>(lane & 15);
@@ -308,10 +301,10 @@ struct UnitScales {
     }
   }
 
-  // per tile and group: scale in the low half, zero point in the high half; a
-  // group past the unit's n has scale 0
-  __device__ __forceinline__ void get(u32x4 (&sz)[CT], int n) const {
-    uint32_t lo = s[0], hi = 0, zz = 0;
+  // the pairs that the product takes; a group past the unit's n has scale 0
+  template <int TK>
+  __device__ __forceinline__ void get(f32x4 (&sv)[CT], f32x4 (&zv)[CT], int n) const {
+    uint32_t lo = s[0], hi = 0;
     if constexpr (GU == 4) {
       const uint64_t q = (((uint64_t)s[1] << 32) | s[0]) >> (16 * shift);
       lo = (uint32_t)q;
@@ -322,25 +315,22 @@ struct UnitScales {
     const u32x4 l = spread4(lo);
     u32x4 m = {0u, 0u, 0u, 0u}, zs = {0x08080808u, 0x08080808u, 0x08080808u, 0x08080808u};
     if constexpr (GU == 4) m = spread4(hi);
-    if constexpr ((WQ & kZeros) != 0) {
-      zz = z >> (8 * shift);
-      zs = spread4(zz);
-    }
+    if constexpr ((WQ & kZeros) != 0) zs = spread4(z >> (8 * shift));
 #pragma unroll
     for (int c = 0; c < CT; ++c)
 #pragma unroll
       for (int g = 0; g < GU; ++g) {
-        const uint32_t word = g < 2 ? (uint32_t)l[c] : (uint32_t)m[c];
-        const uint32_t sc = (g & 1) != 0 ? word >> 16 : word & 0xffffu;
-        const uint32_t zw = zs[c];
-        const uint32_t v = sc | (((zw >> (8 * g)) & 0xffu) << 16);
-        sz[c][g] = GU > 1 && g >= n ? 0u : v;
+        const uint32_t word = g < 2 ? (uint32_t)l[c] : (uint32_t)m[c], zw = zs[c];
+        const float f = half_f32<TK>((uint16_t)((g & 1) != 0 ? word >> 16 : word));
+        sv[c][g] = GU > 1 && g >= n ? 0.0f : f;
+        zv[c][g] = -16.0f - (float)((zw >> (8 * g)) & 0xffu);
       }
   }
 };
 template <int CT>
 struct UnitScales<kWFull, CT> {
-  __device__ __forceinline__ void get(u32x4 (&)[CT], int) const {}
+  template <int TK>
+  __device__ __forceinline__ void get(f32x4 (&)[CT], f32x4 (&)[CT], int) const {}
 };
 
 // The experts' outputs, as fp32 rows y for the tokens that each expert serves.
@@ -458,8 +448,8 @@ __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_down_kernel(MoeArgs a) 
 #pragma unroll
   for (int c = 0; c < CT; ++c) tot[c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   auto mul = [&](Item& q, int u) __attribute__((always_inline)) {
-    u32x4 sz[CT];
-    q.s.get(sz, groups - u * GU);
+    f32x4 sv[CT], zv[CT];
+    q.s.template get<TK>(sv, zv, groups - u * GU);
     turn_unit<WQ, CT, 1>(q.w, q.a, turn, lane);
     if constexpr (WQ == kWFull) {
       // (the matrix core's results are read in the straight line of code that
@@ -467,11 +457,11 @@ __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_down_kernel(MoeArgs a) 
       f32x4 acc[CT];
 #pragma unroll
       for (int c = 0; c < CT; ++c) acc[c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-      mul_unit<TK, WQ, CT, 1, true, false>(q.w, sz, q.a, acc, 0, 0);
+      mul_unit<TK, WQ, CT, 1, true, false>(q.w, sv, zv, q.a, acc, 0, 0);
 #pragma unroll
       for (int c = 0; c < CT; ++c) tot[c] += acc[c];
     } else {
-      mul_unit<TK, WQ, CT, 1, true, false>(q.w, sz, q.a, tot, 0, 0);
+      mul_unit<TK, WQ, CT, 1, true, false>(q.w, sv, zv, q.a, tot, 0, 0);
     }
     __builtin_amdgcn_sched_barrier(0);  // used up before it is loaded again: same registers, no copies
   };

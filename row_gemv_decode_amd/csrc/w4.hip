@@ -20,7 +20,6 @@ constexpr int kW4Waves = 4;
 
 template <int TK, int WQ, int CT>
 __global__ __launch_bounds__(64 * kW4Waves, 2) void w4_rows_kernel(W4Args g) {
-  __shared__ f32x4 red[kW4Waves][CT][64];
   __shared__ ScaleLds<WQ, CT> lds;
   __shared__ u32x4 turn_s[kW4Waves][turn_slots<WQ, CT, 1>() * 64];
   const int lane = threadIdx.x & 63;
@@ -44,13 +43,10 @@ __global__ __launch_bounds__(64 * kW4Waves, 2) void w4_rows_kernel(W4Args g) {
   block_product<TK, WQ, CT, kW4Waves>(tot, lds, Turn(turn_s[wave], lane), g.w, j,
                                       CT > 1 ? 16 : (int)min(g.n - j0, (int64_t)16), arow, k, wave, lane);
 
-#pragma unroll
-  for (int c = 0; c < CT; ++c) red[wave][c][lane] = tot[c];
+  put_sums(turn_s[wave], tot, lane);
   __syncthreads();
   if (wave < CT) {
-    f32x4 sum = red[0][wave][lane];
-#pragma unroll
-    for (int w = 1; w < kW4Waves; ++w) sum += red[w][wave][lane];
+    const f32x4 sum = wave_sums(turn_s, wave, lane);
     const int64_t col = j0 + 16 * wave + (lane & 15);
     if (col >= own && col < g.n) {
 #pragma unroll

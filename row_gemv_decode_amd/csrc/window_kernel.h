@@ -152,6 +152,13 @@ struct Turn {
   }
 };
 
+// barrier of a workgroup that shares LDS only: loads from memory stay in flight
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
 // order of a wave's LDS writes and its later reads by other lanes (the LDS
 // works in order; this keeps the compiler from moving them)
 __device__ __forceinline__ void wave_lds_order() {
@@ -260,10 +267,10 @@ __device__ __forceinline__ void turn_unit(WUnit<WQ, CT>& w, u32x4 (&a)[NP][unit_
 }
 
 // tot[c] += A(unit) . W(unit) for CT column tiles; A is the sum of NP planes
-// (kOrdered: their elements are in pair order already).  sz[c][g]: scale and
-// zero point of the unit's group g.
+// (kOrdered: their elements are in pair order already).  sv[c][g], zv[c][g]: the
+// unit's group g's scale and -(16 + zero point).
 template <int TK, int WQ, int CT, int NP, bool kOrdered, bool kPart>
-__device__ __forceinline__ void mul_unit(const WUnit<WQ, CT>& w, const u32x4 (&sz)[CT],
+__device__ __forceinline__ void mul_unit(const WUnit<WQ, CT>& w, const f32x4 (&sv)[CT], const f32x4 (&zv)[CT],
                                          const u32x4 (&a)[NP][unit_blocks<WQ>()], f32x4 (&tot)[CT], int u, int k) {
   if constexpr (WQ == kWFull) {
 #pragma unroll
@@ -307,9 +314,7 @@ __device__ __forceinline__ void mul_unit(const WUnit<WQ, CT>& w, const u32x4 (&s
       }
 #pragma unroll
       for (int c = 0; c < CT; ++c) {
-        const uint32_t szg = sz[c][g];
-        const float s = half_f32<TK>((uint16_t)(szg & 0xffffu));
-        const float z = -16.0f - (float)(szg >> 16);
+        const float s = sv[c][g], z = zv[c][g];
 #pragma unroll
         for (int e = 0; e < 4; ++e) tot[c][e] = __builtin_fmaf(s, __builtin_fmaf(z, sa[e], acc[c][e]), tot[c][e]);
       }
@@ -320,65 +325,80 @@ __device__ __forceinline__ void mul_unit(const WUnit<WQ, CT>& w, const u32x4 (&s
 }
 
 // ---------------------------------------------------------------------------
-// A workgroup's scales and zero points, in LDS as they lie in memory: column
-// by column, `groups` of each, for at most kSpanGroups groups at a time.  The
-// 16 columns of a tile lie together, so the workgroup fetches them with full
-// 16-byte loads; fetched by the lanes that use them, 2 and 1 bytes of 16
-// columns at a time, they cost the load path as much as a third of the codes
-// (16 x 256 experts, groups of 128: 198 us for the up product against 165
-// without any scale).
+// A workgroup's scales and zero points, in LDS as the fp32 pairs (s, -(16 + z))
+// that the product takes: column by column, `groups` of each, for at most
+// kSpanGroups groups at a time.  The 16 columns of a tile lie together in memory,
+// so the workgroup fetches them with full 16-byte loads; fetched by the lanes
+// that use them, 2 and 1 bytes of 16 columns at a time, they cost the load path
+// as much as a third of the codes (16 of 256 experts, groups of 128: 198 us for
+// the up product against 165 without any scale).  Converted once here, a pair
+// serves every unit without further instructions.
 // ---------------------------------------------------------------------------
-constexpr int kSpanGroups = 128;
+constexpr int kSpanGroups = 80;  // (four tiles' pairs and the slots of the turn: two workgroups per CU)
+typedef float f32x2 __attribute__((ext_vector_type(2)));
 template <int WQ, int CT>
 struct ScaleLds {
-  static constexpr int N = WQ == kWFull ? 8 : 16 * kSpanGroups;
-  uint16_t s[CT][N] __attribute__((aligned(16)));
-  uint8_t z[CT][(WQ & kZeros) != 0 ? N : 16] __attribute__((aligned(16)));
+  f32x2 v[CT][WQ == kWFull ? 1 : 16 * (kSpanGroups + 2)] __attribute__((aligned(16)));
 };
-
-typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(1)));
+// pairs from a column to the next: twice an odd number, so that the 16 columns'
+// reads of 16 bytes meet no bank conflict
+__device__ __forceinline__ int scale_stride(int n) {
+  const int even = (n + 1) & ~1;
+  return (even & 2) != 0 ? even : even + 2;
+}
 
 // Staging in two steps, so that other loads can be issued between them: `load`
 // fetches, `store` writes to LDS.  g0, n: the span's groups; cols as in w_tiles.
-template <int WQ, int CT, int THREADS>
+template <int TK, int WQ, int CT, int THREADS>
 struct ScaleStage {
-  static_assert(2 * kSpanGroups <= THREADS, "one 16-byte piece of a tile per thread");
-  u32x4 s[CT], z[CT];
+  static_assert(2 * kSpanGroups <= THREADS, "one piece of 8 groups of a tile per thread");
+  u32x4 s[CT];
+  uint64_t z[CT];
 
-  // 16-byte pieces of a tile: of all columns in one run when the span is the
+  // pieces of 8 groups of a tile: of all columns in one run when the span is the
   // whole k, else of each column's part; anything odder goes one by one
   static __device__ __forceinline__ bool pieces(int n, int groups, int cols) {
-    return cols == 16 && (n == groups || n % 16 == 0);
-  }
-  // byte offset of piece i; per: pieces per column, row: bytes of a column
-  static __device__ __forceinline__ uint32_t place(int i, bool run, int per, uint32_t row) {
-    return run ? 16u * i : (uint32_t)(i / per) * row + 16u * (uint32_t)(i % per);
+    return cols == 16 && (n == groups || n % 8 == 0);
   }
 
   __device__ __forceinline__ void load(const WindowWeight& w, const int64_t (&j)[CT], int g0, int n, int groups, int cols) {
     if (!pieces(n, groups, cols)) return;
-    const bool run = n == groups;
 #pragma unroll
     for (int c = 0; c < CT; ++c) {
-      const int t = (int)(threadIdx.x + 64 * c) % THREADS;  // the tiles' pieces start at different waves
-      const char* sp = (const char*)w.scales + (j[c] * groups + g0) * 2;
-      if (t < 2 * n) s[c] = *(const u32x4_any*)(sp + place(t, run, n / 8, 2 * groups));
-      if constexpr ((WQ & kZeros) != 0) {
-        const char* zp = (const char*)w.zeros + j[c] * groups + g0;
-        if (t < n) z[c] = *(const u32x4_any*)(zp + place(t, run, n / 16, groups));
+      const int t = (int)(threadIdx.x + 128 * c) % THREADS;  // the tiles' pieces start at different waves
+      const int per = n / 8;  // pieces of a column's part
+      const int64_t at = j[c] * groups + g0 + (n == groups ? 8 * t : t / per * groups + t % per * 8);
+      typedef u32x4 any16 __attribute__((aligned(2)));
+      typedef uint64_t any8 __attribute__((aligned(1)));
+      if (t < 2 * n) {
+        s[c] = *(const any16*)((const uint16_t*)w.scales + at);
+        if constexpr ((WQ & kZeros) != 0) z[c] = *(const any8*)((const uint8_t*)w.zeros + at);
       }
     }
   }
 
+  static __device__ __forceinline__ f32x2 pair(uint32_t s, uint32_t z) {
+    return f32x2{half_f32<TK>((uint16_t)s), (WQ & kZeros) != 0 ? -16.0f - (float)z : -24.0f};
+  }
+
   __device__ __forceinline__ void store(ScaleLds<WQ, CT>& lds, const WindowWeight& w, const int64_t (&j)[CT], int g0, int n,
                                         int groups, int cols) {
+    const int stride = scale_stride(n);
     if (pieces(n, groups, cols)) {
 #pragma unroll
       for (int c = 0; c < CT; ++c) {
-        const int t = (int)(threadIdx.x + 64 * c) % THREADS;
-        if (t < 2 * n) ((u32x4*)lds.s[c])[t] = s[c];
-        if constexpr ((WQ & kZeros) != 0) {
-          if (t < n) ((u32x4*)lds.z[c])[t] = z[c];
+        const int t = (int)(threadIdx.x + 128 * c) % THREADS;
+        if (t < 2 * n) {
+          int col = 8 * t / n, g = 8 * t - col * n;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t word = s[c][i / 2];
+            lds.v[c][col * stride + g] = pair(word >> (16 * (i & 1)), (uint32_t)(z[c] >> (8 * i)) & 0xffu);
+            if (++g == n) {
+              g = 0;
+              ++col;
+            }
+          }
         }
       }
     } else {
@@ -388,34 +408,43 @@ struct ScaleStage {
         const uint8_t* zp = (const uint8_t*)w.zeros + ((WQ & kZeros) != 0 ? j[c] * groups + g0 : 0);
 #pragma unroll 4
         for (int i = threadIdx.x; i < cols * n; i += THREADS) {
-          const int col = i / n;
-          const int64_t at = (int64_t)col * groups + (i - col * n);
-          lds.s[c][i] = sp[at];
-          if constexpr ((WQ & kZeros) != 0) lds.z[c][i] = zp[at];
+          const int col = i / n, g = i - col * n;
+          const int64_t at = (int64_t)col * groups + g;
+          lds.v[c][col * stride + g] = pair(sp[at], (WQ & kZeros) != 0 ? zp[at] : 0u);
         }
       }
     }
   }
 };
 
-// the staged scales of the unit whose first group is the span's g-th: scale in
-// the low half, zero point in the high half
+// the staged scales of the unit whose first pair in a column is at `at`
 template <int WQ, int CT>
-__device__ __forceinline__ void unit_scales(u32x4 (&sz)[CT], const ScaleLds<WQ, CT>& lds, int g, int row) {
+__device__ __forceinline__ void unit_scales(f32x4 (&sv)[CT], f32x4 (&zv)[CT], const ScaleLds<WQ, CT>& lds, int at) {
   if constexpr (WQ != kWFull) {
+    constexpr int GU = 128 / group_len<WQ>();
 #pragma unroll
-    for (int c = 0; c < CT; ++c)
+    for (int c = 0; c < CT; ++c) {
+      if constexpr (GU == 1) {
+        const f32x2 v = lds.v[c][at];
+        sv[c][0] = v[0];
+        zv[c][0] = v[1];
+      } else {
 #pragma unroll
-      for (int i = 0; i < 128 / group_len<WQ>(); ++i) {
-        const uint32_t z = (WQ & kZeros) != 0 ? lds.z[c][row + g + i] : 8u;
-        sz[c][i] = (uint32_t)lds.s[c][row + g + i] | (z << 16);
+        for (int i = 0; i < GU; i += 2) {
+          const f32x4 v = *(const f32x4*)&lds.v[c][at + i];
+          sv[c][i] = v[0];
+          zv[c][i] = v[1];
+          sv[c][i + 1] = v[2];
+          zv[c][i + 1] = v[3];
+        }
       }
+    }
   }
 }
 
 // ---------------------------------------------------------------------------
 // tot[c] = A . W over a whole k, by NW waves that each end with a part of the
-// sum, to be added in the order of the waves.  k goes span by span (of
+// sum, to be added in the order of the waves.  k goes span by span (of at most
 // kSpanGroups groups; 16-bit weights have one span), and in a span wave w takes
 // a run of consecutive units; who sums what depends on k alone.  A wave has two
 // units in flight: each is loaded again, two units on, as soon as it is used,
@@ -432,7 +461,13 @@ __device__ __forceinline__ void block_product(f32x4 (&tot)[CT], ScaleLds<WQ, CT>
   WTiles<WQ, CT> t;
   w_tiles<WQ, CT>(t, weight, j, k, cols, lane);
   const int groups = WQ == kWFull ? 0 : k / (WQ == kWFull ? 1 : group_len<WQ>());
-  const int span = WQ == kWFull ? k : kSpanGroups * group_len<WQ>();
+  int span = k;
+  if constexpr (WQ != kWFull) {  // as few spans as hold k, of about one length, each for all waves
+    constexpr int most = kSpanGroups * group_len<WQ>() / UL;
+    static_assert(most % NW == 0, "");
+    const int units = (k + UL - 1) / UL, spans = (units + most - 1) / most;
+    span = (((units + spans - 1) / spans + NW - 1) / NW * NW) * UL;
+  }
 #pragma unroll 1
   for (int k0 = 0; k0 < k; k0 += span) {
     const int end = min(k, k0 + span);
@@ -442,10 +477,11 @@ __device__ __forceinline__ void block_product(f32x4 (&tot)[CT], ScaleLds<WQ, CT>
     const int n = min(u0 + wave * per + per, full) - first;
     const bool part = end % UL != 0 && (full - u0) / per == wave;
     const int g0 = u0 * GU, ng = min(kSpanGroups, groups - g0);
-    const int row = min(lane & 15, cols - 1) * ng - g0;
+    const int row = min(lane & 15, cols - 1) * scale_stride(ng) - g0;
 
     WUnit<WQ, CT> w0, w1;
-    u32x4 a0[1][NB], a1[1][NB], sz[CT];
+    u32x4 a0[1][NB], a1[1][NB];
+    f32x4 sv[CT], zv[CT];
     auto load0 = [&](int u) __attribute__((always_inline)) {
       load_w<WQ, CT, false>(w0, t, u, k, lane);
       load_a<WQ, false>(a0[0], arow, u, k);
@@ -456,31 +492,31 @@ __device__ __forceinline__ void block_product(f32x4 (&tot)[CT], ScaleLds<WQ, CT>
     };
     const int second = n > 1 ? first + 1 : first;
     auto mul0 = [&](int u) __attribute__((always_inline)) {
-      unit_scales(sz, lds, u * GU, row);
+      unit_scales(sv, zv, lds, row + u * GU);
       turn_unit<WQ, CT, 1>(w0, a0, turn, lane);
-      mul_unit<TK, WQ, CT, 1, false, false>(w0, sz, a0, tot, u, k);
+      mul_unit<TK, WQ, CT, 1, false, false>(w0, sv, zv, a0, tot, u, k);
     };
     auto mul1 = [&](int u) __attribute__((always_inline)) {
-      unit_scales(sz, lds, u * GU, row);
+      unit_scales(sv, zv, lds, row + u * GU);
       turn_unit<WQ, CT, 1>(w1, a1, turn, lane);
-      mul_unit<TK, WQ, CT, 1, false, false>(w1, sz, a1, tot, u, k);
+      mul_unit<TK, WQ, CT, 1, false, false>(w1, sv, zv, a1, tot, u, k);
     };
     if constexpr (WQ != kWFull) {
       // the scales first, then the first units' codes, and the scales to LDS
       // while those are on their way
-      ScaleStage<WQ, CT, 64 * NW> st;
+      ScaleStage<TK, WQ, CT, 64 * NW> st;
       st.load(weight, j, g0, ng, groups, cols);
       if (n > 0) {
         load_w<WQ, CT, false>(w0, t, first, k, lane);
         load_w<WQ, CT, false>(w1, t, second, k, lane);
       }
-      if (k0 > 0) __syncthreads();  // every wave is done with the span before
-      st.store(lds, weight, j, g0, ng, groups, cols);
       if (n > 0) {
         load_a<WQ, false>(a0[0], arow, first, k);
         load_a<WQ, false>(a1[0], arow, second, k);
       }
-      __syncthreads();
+      if (k0 > 0) lds_barrier();  // every wave is done with the span before
+      st.store(lds, weight, j, g0, ng, groups, cols);
+      lds_barrier();
     } else if (n > 0) {
       load0(first);
       load1(second);
@@ -509,11 +545,27 @@ __device__ __forceinline__ void block_product(f32x4 (&tot)[CT], ScaleLds<WQ, CT>
     if (part) {  // (groups past k are not staged: mul_unit does not use them)
       load_w<WQ, CT, true>(w0, t, full, k, lane);
       load_a<WQ, true>(a0[0], arow, full, k);
-      unit_scales(sz, lds, full * GU, row);
+      unit_scales(sv, zv, lds, row + full * GU);
       turn_unit<WQ, CT, 1>(w0, a0, turn, lane);
-      mul_unit<TK, WQ, CT, 1, false, true>(w0, sz, a0, tot, full, k);
+      mul_unit<TK, WQ, CT, 1, false, true>(w0, sv, zv, a0, tot, full, k);
     }
   }
+}
+
+// The waves' sums: each writes its own into its slots of the turn (used up by
+// then), and after a barrier any wave adds a tile's in the order of the waves.
+template <int CT>
+__device__ __forceinline__ void put_sums(u32x4* wave_slots, const f32x4 (&tot)[CT], int lane) {
+  wave_lds_order();
+#pragma unroll
+  for (int c = 0; c < CT; ++c) ((f32x4*)wave_slots)[c * 64 + lane] = tot[c];
+}
+template <int NW, int N>
+__device__ __forceinline__ f32x4 wave_sums(const u32x4 (&slots)[NW][N], int c, int lane) {
+  f32x4 sum = ((const f32x4*)slots[0])[c * 64 + lane];
+#pragma unroll
+  for (int w = 1; w < NW; ++w) sum += ((const f32x4*)slots[w])[c * 64 + lane];
+  return sum;
 }
 
 // store one fp32 value as the output kind (uniform runtime kind)
