@@ -527,16 +527,26 @@ __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_down_kernel(MoeArgs a) 
 }
 
 // out[t] = the sum of token t's experts' rows, largest logit first, then the
-// shared expert's; a thread adds four columns
+// shared expert's; a thread adds four columns.  Twelve rows are fetched before
+// the first is added (loads past the last row repeat it), so the kernel waits
+// for memory once for up to twelve (1 of 64 experts, top 4: 2.4 us, and 2.7 row by
+// row; of the 4.6 us of 5 of 512 most is reading rows that other XCDs wrote).
 __global__ __launch_bounds__(64) void moe_combine_kernel(MoeArgs a) {
+  constexpr int R = 12;
   const int64_t j = 4 * (int64_t)(blockIdx.x * 64 + threadIdx.x);
   const int t = blockIdx.y;
   if (j >= a.d) return;
   const float* y = a.y + (int64_t)t * (a.topk + 1) * a.d + j;
   const int n = a.topk + (a.shared_inter > 0 ? 1 : 0);
   f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 8
-  for (int i = 0; i < n; ++i) sum += *(const f32x4*)(y + (int64_t)i * a.d);
+#pragma unroll 1
+  for (int i0 = 0; i0 < n; i0 += R) {
+    f32x4 v[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) v[i] = *(const f32x4*)(y + (int64_t)min(i0 + i, n - 1) * a.d);
+#pragma unroll
+    for (int i = 0; i < R; ++i) sum = i0 + i < n ? sum + v[i] : sum;
+  }
 #pragma unroll
   for (int e = 0; e < 4; ++e) store_kind(a.out, t * a.ldo + j + e, sum[e], a.out_kind);
 }
