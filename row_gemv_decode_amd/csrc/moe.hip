@@ -18,7 +18,7 @@
 //                     x (a matrix-core tile holds 16 rows anyway, so tokens are
 //                     not gathered), p and silu in the epilogue
 //   moe_down_kernel   per distinct expert, the output rows of the tokens it serves
-//   moe_combine_kernel  adds each token's rows
+//   moe_sum_kernel    adds each token's rows
 // h is kept as the sum of planes in the weights' type, multiplied in rows of the
 // same matrix-core step: two,
 // 16 (bf16) or 22 (f16) bits, under a 16-bit output, where one plane would add
@@ -531,7 +531,7 @@ __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_down_kernel(MoeArgs a) 
 // the first is added (loads past the last row repeat it), so the kernel waits
 // for memory once for up to twelve (1 of 64 experts, top 4: 2.4 us, and 2.7 row by
 // row; of the 4.6 us of 5 of 512 most is reading rows that other XCDs wrote).
-__global__ __launch_bounds__(64) void moe_combine_kernel(MoeArgs a) {
+__global__ __launch_bounds__(64) void moe_sum_kernel(MoeArgs a) {
   constexpr int R = 12;
   const int64_t j = 4 * (int64_t)(blockIdx.x * 64 + threadIdx.x);
   const int t = blockIdx.y;
@@ -599,9 +599,11 @@ hipError_t launch_moe(const MoeArgs& a, int kind, int group, hipStream_t stream)
     return hipErrorInvalidValue;
   const int64_t slots = (int64_t)a.m * a.topk < a.experts ? (int64_t)a.m * a.topk : a.experts;
   if (slots > a.max_slots || a.max_slots > kGemvMaxM * SKINNY_TOPK_MAX) return hipErrorInvalidValue;
-  // two column tiles of h per workgroup where that still leaves many
-  // workgroups: the loads of x serve twice the columns (a column's arithmetic
-  // does not depend on it)
+  // Two column tiles of h per workgroup where that still leaves many workgroups:
+  // the loads of x serve twice the columns (a column's arithmetic does not depend
+  // on it).  Measured (us, one / two tiles; sets of 32 columns): 4480 (16 of 256
+  // experts) 154 / 146, 2048 (16 of 8, inter = 8192) 78 / 74, 1050 (5 of 512) 36 / 40,
+  // 280 (1 of 256 bf16) 42 / 49
   const bool wide = slots * (a.inter / 32) >= 2048;
   const int64_t tile = wide ? 32 : 16;
   const int np = moe_planes(kind, a.out_kind);
@@ -630,7 +632,7 @@ hipError_t launch_moe(const MoeArgs& a, int kind, int group, hipStream_t stream)
                      stream, a);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(moe_combine_kernel, dim3((unsigned)((a.d + 255) / 256), (unsigned)a.m), dim3(64), 0, stream, a);
+  hipLaunchKernelGGL(moe_sum_kernel, dim3((unsigned)((a.d + 255) / 256), (unsigned)a.m), dim3(64), 0, stream, a);
   return hipGetLastError();
 }
 

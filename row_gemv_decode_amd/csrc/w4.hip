@@ -4,8 +4,10 @@
 //   C[r][j] = sum over groups g of  s[j][g] * sum over kk in g of (q[j][kk] - z[j][g]) * A[r][kk]
 //
 // for r < m <= 16.  HBM-bound: the codes and scales are read once per call for
-// all rows.  A workgroup of four waves owns CT tiles of 16 columns; each wave
-// takes a quarter of k (a run of units of 128) and streams it with two units
+// all rows (3 x 100003 x 5120, groups of 128, 265 MB: 71 us, 3.7 TB/s, where a
+// large copy moves 4.9 TB/s; below about 10 MB the launch and one round trip to
+// HBM are the time).  A workgroup of four waves owns CT tiles of 16 columns; each
+// wave takes a quarter of k (a run of units of 128) and streams it with two units
 // in flight, and the four sums are added in LDS in the order of the waves.
 // The split of k depends on k alone, so row i of any window equals the one-row
 // call bit for bit.
@@ -14,7 +16,6 @@
 namespace skinny {
 
 namespace {
-
 
 constexpr int kW4Waves = 4;
 
@@ -76,10 +77,10 @@ hipError_t launch_w4_mm(const W4Args& args, int a_kind, int group, hipStream_t s
     return hipErrorInvalidValue;
   const int64_t tiles = (args.n + 15) / 16;
   // Column tiles per wave: more tiles share the loads of A, fewer make more
-  // workgroups.  Measured (us, 1 / 2 / 4 tiles; m = 16, groups of 128 unless
-  // noted): n x k = 512 x 2560 (m = 4) 5.0 / 5.9 / 8.3; 4864 x 896 (m = 1, groups
-  // of 32) 4.2 / 4.3 / 5.8; 5120 x 5120 16.1 / 12.2 / 17.7; 7680 x 2560 9.8 / 8.1 /
-  // 11.0; 32000 x 4096 53 / 42 / 38; 100003 x 5120 168 / 123 / 101
+  // workgroups.  Measured (us, 1 / 2 / 4 tiles): n x k = 512 x 2560 (m = 4, groups
+  // of 64) 5.7 / 6.8 / 9.3; 4864 x 896 (m = 1, 32) 4.8 / 5.1 / 6.6; 5120 x 5120 (m = 1,
+  // 128) 10.5 / 10.1 / 14.2; 7680 x 2560 (m = 16, 128) 8.5 / 8.5 / 10.8; 32000 x 4096
+  // (m = 16, 32) 33 / 31 / 29; 100003 x 5120 (m = 16, 128) 107 / 84 / 80
   const int ct = tiles >= 1536 ? 4 : tiles >= 312 ? 2 : 1;
   const w4_fn fn = args.w.zeros == nullptr
                        ? (a_kind == CK_F16 ? w4_pick<CK_F16, 0>(group, ct) : w4_pick<CK_BF16, 0>(group, ct))

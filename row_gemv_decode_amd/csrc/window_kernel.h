@@ -7,8 +7,8 @@
 // of each block of 32; of the 16 x 16 result it holds column l & 15, rows
 // 4h .. 4h + 3.  All 16 rows cost the same as one, and a row's sums do not
 // depend on the other rows, so row i of any window equals the one-row call bit
-// for bit.  A weight is read once for the whole window, straight from HBM to
-// registers: no weight is used by two waves, so LDS would only add a copy.
+// for bit.  A weight is read once for the whole window, by the wave that
+// multiplies it.
 //
 // 4-bit weights (one scale, and optionally one zero point, per group of G
 // elements along k; W = s * (q - z)):
