@@ -206,7 +206,7 @@ __device__ __forceinline__ int served_row(uint32_t entry, int tk, int m) {
 template <int TK, int WQ, int NP, int GT>
 __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_up_kernel(MoeArgs a) {
   __shared__ ScaleLds<WQ, 2 * GT> lds;
-  __shared__ u32x4 turn_s[kMoeWaves][turn_slots<WQ, 2 * GT, 1>() * 64];
+  __shared__ u32x4 turn_s[kMoeWaves][turn_slots<WQ, 2 * GT>() * 64];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int h = lane >> 4;
@@ -349,7 +349,7 @@ __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_down_kernel(MoeArgs a) 
   constexpr int UL = unit_len<WQ>();
   constexpr int PS = NP == 2 ? 2 : 4, TT = 16 / PS;  // rows for a token's planes, tokens
   constexpr int GU = WQ == kWFull ? 1 : 128 / (WQ == kWFull ? 1 : group_len<WQ>());
-  __shared__ u32x4 turn_s[kMoeWaves][turn_slots<WQ, CT, 1>() * 64];
+  __shared__ u32x4 turn_s[kMoeWaves][turn_slots<WQ, CT>() * 64];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int row = lane & 15;
@@ -409,7 +409,7 @@ __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_down_kernel(MoeArgs a) 
   struct Item {
     WUnit<WQ, CT> w;
     UnitScales<WQ, CT> s;
-    u32x4 a[1][NB];
+    u32x4 a[NB];
   };
   const int64_t j = e0 + (int64_t)min(set, sets - 1) * (16 * CT);  // (a wave past the last set repeats it)
   const char* cset = (const char*)W.codes + j * cbytes;
@@ -439,7 +439,7 @@ __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_down_kernel(MoeArgs a) 
     for (int i = 0; i < NB; ++i) {
       const uint16_t* at = hu + hoff + 32 * i;
       if (group_len<WQ>() != 128 && 32 * i >= rest) at = (const uint16_t*)&kZeroLine;
-      q.a[0][i] = *(const u32x4*)at;
+      q.a[i] = *(const u32x4*)at;
     }
   };
 
@@ -450,18 +450,18 @@ __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_down_kernel(MoeArgs a) 
   auto mul = [&](Item& q, int u) __attribute__((always_inline)) {
     f32x4 sv[CT], zv[CT];
     q.s.template get<TK>(sv, zv, groups - u * GU);
-    turn_unit<WQ, CT, 1>(q.w, q.a, turn, lane);
+    turn_unit<WQ, CT>(q.w, q.a, turn, lane);
     if constexpr (WQ == kWFull) {
       // (the matrix core's results are read in the straight line of code that
       // forms them: for a read behind a branch the compiler has left out the wait)
       f32x4 acc[CT];
 #pragma unroll
       for (int c = 0; c < CT; ++c) acc[c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-      mul_unit<TK, WQ, CT, 1, true, false>(q.w, sv, zv, q.a, acc, 0, 0);
+      mul_unit<TK, WQ, CT, true, false>(q.w, sv, zv, q.a, acc, 0, 0);
 #pragma unroll
       for (int c = 0; c < CT; ++c) tot[c] += acc[c];
     } else {
-      mul_unit<TK, WQ, CT, 1, true, false>(q.w, sv, zv, q.a, tot, 0, 0);
+      mul_unit<TK, WQ, CT, true, false>(q.w, sv, zv, q.a, tot, 0, 0);
     }
     __builtin_amdgcn_sched_barrier(0);  // used up before it is loaded again: same registers, no copies
   };

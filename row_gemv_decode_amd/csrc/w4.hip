@@ -22,7 +22,7 @@ constexpr int kW4Waves = 4;
 template <int TK, int WQ, int CT>
 __global__ __launch_bounds__(64 * kW4Waves, 2) void w4_rows_kernel(W4Args g) {
   __shared__ ScaleLds<WQ, CT> lds;
-  __shared__ u32x4 turn_s[kW4Waves][turn_slots<WQ, CT, 1>() * 64];
+  __shared__ u32x4 turn_s[kW4Waves][turn_slots<WQ, CT>() * 64];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int h = lane >> 4;

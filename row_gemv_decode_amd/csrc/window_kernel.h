@@ -237,11 +237,11 @@ __device__ __forceinline__ void load_a(u32x4 (&a)[unit_blocks<WQ>()], const uint
 // l & 15.  For groups of 128 A's fragment i is piece i of block l >> 4
 // instead: there a step of the matrix core takes eight codes of each of the
 // four blocks, so the codes need no exchange.
-template <int WQ, int CT, int NP>
-constexpr int turn_slots() { return CT * WUnit<WQ, CT>::N + NP * unit_blocks<WQ>(); }
+template <int WQ, int CT>
+constexpr int turn_slots() { return CT * WUnit<WQ, CT>::N + unit_blocks<WQ>(); }
 
-template <int WQ, int CT, int NP>
-__device__ __forceinline__ void turn_unit(WUnit<WQ, CT>& w, u32x4 (&a)[NP][unit_blocks<WQ>()], const Turn& t, int lane) {
+template <int WQ, int CT>
+__device__ __forceinline__ void turn_unit(WUnit<WQ, CT>& w, u32x4 (&a)[unit_blocks<WQ>()], const Turn& t, int lane) {
   constexpr int NW = WUnit<WQ, CT>::N, NB = unit_blocks<WQ>();
   wave_lds_order();
 #pragma unroll
@@ -250,36 +250,28 @@ __device__ __forceinline__ void turn_unit(WUnit<WQ, CT>& w, u32x4 (&a)[NP][unit_
     for (int i = 0; i < NW; ++i) t.slots[(c * NW + i) * 64 + t.put] = w.v[c][i];
   u32x4* as = t.slots + CT * NW * 64;
 #pragma unroll
-  for (int p = 0; p < NP; ++p)
-#pragma unroll
-    for (int i = 0; i < NB; ++i) as[(p * NB + i) * 64 + t.put] = a[p][i];
+  for (int i = 0; i < NB; ++i) as[i * 64 + t.put] = a[i];
   wave_lds_order();
 #pragma unroll
   for (int c = 0; c < CT; ++c)
 #pragma unroll
     for (int i = 0; i < NW; ++i) w.v[c][i] = t.slots[(c * NW + i) * 64 + t.get];
 #pragma unroll
-  for (int p = 0; p < NP; ++p)
-#pragma unroll
-    for (int i = 0; i < NB; ++i)
-      a[p][i] = group_len<WQ>() == 128 ? as[(p * NB + (lane >> 4)) * 64 + Turn::entry(lane & 15, i)]
-                                       : as[(p * NB + i) * 64 + t.get];
+  for (int i = 0; i < NB; ++i)
+    a[i] = group_len<WQ>() == 128 ? as[(lane >> 4) * 64 + Turn::entry(lane & 15, i)] : as[i * 64 + t.get];
 }
-
-// tot[c] += A(unit) . W(unit) for CT column tiles; A is the sum of NP planes
-// (kOrdered: their elements are in pair order already).  sv[c][g], zv[c][g]: the
-// unit's group g's scale and -(16 + zero point).
-template <int TK, int WQ, int CT, int NP, bool kOrdered, bool kPart>
+// tot[c] += A(unit) . W(unit) for CT column tiles (kOrdered: A's elements are in
+// pair order already).  sv[c][g], zv[c][g]: the unit's group g's scale and
+// -(16 + zero point).
+template <int TK, int WQ, int CT, bool kOrdered, bool kPart>
 __device__ __forceinline__ void mul_unit(const WUnit<WQ, CT>& w, const f32x4 (&sv)[CT], const f32x4 (&zv)[CT],
-                                         const u32x4 (&a)[NP][unit_blocks<WQ>()], f32x4 (&tot)[CT], int u, int k) {
+                                         const u32x4 (&a)[unit_blocks<WQ>()], f32x4 (&tot)[CT], int u, int k) {
   if constexpr (WQ == kWFull) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       if (kPart && u * 64 + 32 * i >= k) break;
 #pragma unroll
-      for (int p = 0; p < NP; ++p)
-#pragma unroll
-        for (int c = 0; c < CT; ++c) tot[c] = mfma16<TK>(a[p][i], w.v[c][i], tot[c]);
+      for (int c = 0; c < CT; ++c) tot[c] = mfma16<TK>(a[i], w.v[c][i], tot[c]);
     }
   } else {
     constexpr int NB = group_len<WQ>() / 32;  // blocks per group
@@ -298,18 +290,12 @@ __device__ __forceinline__ void mul_unit(const WUnit<WQ, CT>& w, const f32x4 (&s
       for (int c = 0; c < CT; ++c) acc[c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int i = g * NB; i < g * NB + NB; ++i) {
-        u32x4 ap[NP];
-#pragma unroll
-        for (int p = 0; p < NP; ++p) {
-          ap[p] = kOrdered ? a[p][i] : pair_order(a[p][i]);
-          sa = mfma16<TK>(ap[p], ones, sa);
-        }
+        const u32x4 ap = kOrdered ? a[i] : pair_order(a[i]);
+        sa = mfma16<TK>(ap, ones, sa);
 #pragma unroll
         for (int c = 0; c < CT; ++c) {
           const uint32_t qi = q[c][i];
-          const u32x4 b = codes16<TK>(qi, bits);
-#pragma unroll
-          for (int p = 0; p < NP; ++p) acc[c] = mfma16<TK>(ap[p], b, acc[c]);
+          acc[c] = mfma16<TK>(ap, codes16<TK>(qi, bits), acc[c]);
         }
       }
 #pragma unroll
@@ -480,26 +466,26 @@ __device__ __forceinline__ void block_product(f32x4 (&tot)[CT], ScaleLds<WQ, CT>
     const int row = min(lane & 15, cols - 1) * scale_stride(ng) - g0;
 
     WUnit<WQ, CT> w0, w1;
-    u32x4 a0[1][NB], a1[1][NB];
+    u32x4 a0[NB], a1[NB];
     f32x4 sv[CT], zv[CT];
     auto load0 = [&](int u) __attribute__((always_inline)) {
       load_w<WQ, CT, false>(w0, t, u, k, lane);
-      load_a<WQ, false>(a0[0], arow, u, k);
+      load_a<WQ, false>(a0, arow, u, k);
     };
     auto load1 = [&](int u) __attribute__((always_inline)) {
       load_w<WQ, CT, false>(w1, t, u, k, lane);
-      load_a<WQ, false>(a1[0], arow, u, k);
+      load_a<WQ, false>(a1, arow, u, k);
     };
     const int second = n > 1 ? first + 1 : first;
     auto mul0 = [&](int u) __attribute__((always_inline)) {
       unit_scales(sv, zv, lds, row + u * GU);
-      turn_unit<WQ, CT, 1>(w0, a0, turn, lane);
-      mul_unit<TK, WQ, CT, 1, false, false>(w0, sv, zv, a0, tot, u, k);
+      turn_unit<WQ, CT>(w0, a0, turn, lane);
+      mul_unit<TK, WQ, CT, false, false>(w0, sv, zv, a0, tot, u, k);
     };
     auto mul1 = [&](int u) __attribute__((always_inline)) {
       unit_scales(sv, zv, lds, row + u * GU);
-      turn_unit<WQ, CT, 1>(w1, a1, turn, lane);
-      mul_unit<TK, WQ, CT, 1, false, false>(w1, sv, zv, a1, tot, u, k);
+      turn_unit<WQ, CT>(w1, a1, turn, lane);
+      mul_unit<TK, WQ, CT, false, false>(w1, sv, zv, a1, tot, u, k);
     };
     if constexpr (WQ != kWFull) {
       // the scales first, then the first units' codes, and the scales to LDS
@@ -511,8 +497,8 @@ __device__ __forceinline__ void block_product(f32x4 (&tot)[CT], ScaleLds<WQ, CT>
         load_w<WQ, CT, false>(w1, t, second, k, lane);
       }
       if (n > 0) {
-        load_a<WQ, false>(a0[0], arow, first, k);
-        load_a<WQ, false>(a1[0], arow, second, k);
+        load_a<WQ, false>(a0, arow, first, k);
+        load_a<WQ, false>(a1, arow, second, k);
       }
       if (k0 > 0) lds_barrier();  // every wave is done with the span before
       st.store(lds, weight, j, g0, ng, groups, cols);
@@ -544,10 +530,10 @@ __device__ __forceinline__ void block_product(f32x4 (&tot)[CT], ScaleLds<WQ, CT>
     }
     if (part) {  // (groups past k are not staged: mul_unit does not use them)
       load_w<WQ, CT, true>(w0, t, full, k, lane);
-      load_a<WQ, true>(a0[0], arow, full, k);
+      load_a<WQ, true>(a0, arow, full, k);
       unit_scales(sv, zv, lds, row + full * GU);
-      turn_unit<WQ, CT, 1>(w0, a0, turn, lane);
-      mul_unit<TK, WQ, CT, 1, false, true>(w0, sv, zv, a0, tot, full, k);
+      turn_unit<WQ, CT>(w0, a0, turn, lane);
+      mul_unit<TK, WQ, CT, false, true>(w0, sv, zv, a0, tot, full, k);
     }
   }
 }
