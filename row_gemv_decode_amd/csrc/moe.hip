@@ -7,8 +7,8 @@
 //   h_te  = silu(x_t . Wg_e) * (x_t . Wu_e) * p_te
 //   out_t = sum over e in S_t of h_te . Wd_e  +  (sigmoid(x_t . wg) * h_t,shared) . Wd_shared
 //
-// HBM-bound on the distinct experts' weights, each read once per window (the
-// down weight of an expert that serves more than 8 tokens twice).
+// HBM-bound on the distinct experts' weights, each read once per window (an
+// expert's down weight once per 8 tokens that it serves, or 4 with three planes).
 //   moe_route_kernel  one workgroup, one wave per token: top-k, softmax and the
 //                     list of distinct experts in ascending order with each
 //                     one's tokens (a second workgroup: the shared expert's
@@ -20,11 +20,10 @@
 //   moe_down_kernel   per distinct expert, the output rows of the tokens it serves
 //   moe_sum_kernel    adds each token's rows
 // h is kept as the sum of planes in the weights' type, multiplied in rows of the
-// same matrix-core step: two,
-// 16 (bf16) or 22 (f16) bits, under a 16-bit output, where one plane would add
-// as much error as the output's own rounding; three (bf16, 24 bits) under an
-// fp32 output.  For 4-bit weights h is stored in the pair order that their
-// decoding yields.
+// same matrix-core step: two, 16 (bf16) or 22 (f16) bits, under a 16-bit output,
+// where one plane would add as much error as the output's own rounding; three
+// (bf16, 24 bits) under an fp32 output.  For 4-bit weights h is stored in the pair
+// order that their decoding yields.
 //
 // Row invariance: which wave takes which part of k depends on the layer alone, a
 // matrix-core row does not depend on the other rows, and a token's experts are

@@ -376,13 +376,24 @@ struct ScaleStage {
         const int t = (int)(threadIdx.x + 128 * c) % THREADS;
         if (t < 2 * n) {
           int col = 8 * t / n, g = 8 * t - col * n;
+          f32x2 v[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const uint32_t word = s[c][i / 2];
-            lds.v[c][col * stride + g] = pair(word >> (16 * (i & 1)), (uint32_t)(z[c] >> (8 * i)) & 0xffu);
-            if (++g == n) {
-              g = 0;
-              ++col;
+            v[i] = pair(word >> (16 * (i & 1)), (uint32_t)(z[c] >> (8 * i)) & 0xffu);
+          }
+          if (n % 8 == 0) {  // a piece is of one column
+#pragma unroll
+            for (int i = 0; i < 8; i += 2)
+              *(f32x4*)&lds.v[c][col * stride + g + i] = f32x4{v[i][0], v[i][1], v[i + 1][0], v[i + 1][1]};
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              lds.v[c][col * stride + g] = v[i];
+              if (++g == n) {
+                g = 0;
+                ++col;
+              }
             }
           }
         }
