@@ -748,7 +748,7 @@ def token_logprobs(logits, tokens, topk=0, stream=None):
     ws = _stream_workspace(_logprob_ws, (index, handle), need, index, stream) if need else None
     # one allocation for the five results, each at a multiple of 4 bytes
     flat = _empty(m * (3 + 2 * topk), torch.float32, logits.device, stream)
-    lp, ent, top, rank, ids = flat.split([m, m, m * topk, m, m * topk])
+    lp, ent, top, rank, ids = flat.split_with_sizes((m, m, m * topk, m, m * topk))
     p = flat.data_ptr()
     p_rank = p + 4 * m * (2 + topk)
     _check(_lib.skinny_token_logprobs_run(m, vocab, logits.data_ptr(), ld, dtype, tokens.data_ptr(), t64, topk, p, p + 4 * m,

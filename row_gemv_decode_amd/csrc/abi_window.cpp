@@ -41,10 +41,10 @@ int64_t round256(int64_t b) { return (b + 255) / 256 * 256; }
 // four waves per CU of 256, but at most 16 (which cuts a window's rows alike at
 // every m), each of at least 4096 logits; from 256 rows on a row is one
 // workgroup's, of eight waves up to 1023 rows and four from there on.  Measured
-// (us): at most 16 / 32 segments, 16 x 131071 bf16, top 20, 15.4 / 17.9, 1 x 151000
-// bf16 12.3 / 13.0; segments of at least 4096 / 8192, 1 x 32000 fp32 10.5 / 11.7,
-// 4 x 50000 11.5 / 12.8; 512 x 50021 f16 with four / eight waves 26.6 / 23.5, 300 x
-// 100003 bf16 43 / 37, 2048 x 32000 bf16 45 / 54.
+// (us): at most 16 / 32 segments, 16 x 131071 bf16, top 20, 15.1 / 17.9, 1 x 151000
+// bf16 11.3 / 13.0; segments of at least 4096 / 8192, 1 x 32000 fp32 9.3 / 10.7,
+// 4 x 50000 10.6 / 11.9; 512 x 50021 f16 with four / eight waves 26.6 / 22.0, 2048 x
+// 32000 bf16 45 / 54; two segments of four waves for 512 x 50021 25.6.
 struct RowSegments {
   int64_t count, len;
   int waves;

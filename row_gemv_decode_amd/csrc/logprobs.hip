@@ -338,7 +338,7 @@ __global__ __launch_bounds__(64 * kWaves) void logprobs_kernel(LogprobArgs g) {
   __shared__ uint32_t bar_s[kLogprobMaxSegments];  // (segments or waves)
   __shared__ int pool_n;
   __shared__ int last_s;
-  static_assert(kPool >= kLogprobMaxSegments * kPoolTopk && kLogprobMaxSegments >= kWaves && kPendingEnd >= 0,
+  static_assert(kPool >= kLogprobMaxSegments * kPoolTopk && kLogprobMaxSegments >= kWaves,
                 "the pool holds the waves' entries, or the segments'");
   const int tid = threadIdx.x;
   const int lane = tid & 63;
