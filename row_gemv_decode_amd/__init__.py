@@ -681,12 +681,13 @@ class MoELayer:
                 raise ValueError(f"MoELayer: out must be [{m}][{self.d}] of type {self.out_dtype}")
             _dense("MoELayer", out=out)
             _on("MoELayer", self.device, out)
-        for name, t, dt in (("topk_idx", topk_idx, torch.int32), ("topk_weight", topk_weight, torch.float32)):
-            if t is not None:
-                if tuple(t.shape) != (m, self.topk) or t.dtype != dt:
-                    raise ValueError(f"MoELayer: {name} must be {dt} [{m}][{self.topk}]")
-                _dense("MoELayer", **{name: t})
-                _on("MoELayer", self.device, t)
+        if topk_idx is not None or topk_weight is not None:
+            for name, t, dt in (("topk_idx", topk_idx, torch.int32), ("topk_weight", topk_weight, torch.float32)):
+                if t is not None:
+                    if tuple(t.shape) != (m, self.topk) or t.dtype != dt:
+                        raise ValueError(f"MoELayer: {name} must be {dt} [{m}][{self.topk}]")
+                    _dense("MoELayer", **{name: t})
+                    _on("MoELayer", self.device, t)
         handle = _handle(self._index, stream)
         # (runs on different streams may be in flight at once: each has its own)
         ws = _stream_workspace(self._ws, handle, self.workspace_bytes, self._index, stream)
