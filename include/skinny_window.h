@@ -70,10 +70,9 @@ SKINNY_API skinny_status skinny_w4_mm_run(int64_t m, int64_t n, int64_t k, int32
  *   out_t = sum over e in S_t of p_te f_e(x_t)
  *           + sigmoid(wg . x_t) f_shared(x_t)   (when shared_inter > 0)
  * Products are summed in fp32; the inner values are carried in 22 bits (f16
- * layers), 16 (bf16 layers with a 16-bit output) or 24 (bf16 layers with an fp32
- * output), the output rounded once (nearest even).  The distinct experts'
- * weights are read once per window, an expert's down weight once per 8 tokens
- * that it serves (4 in a bf16 layer with an fp32 output).  A token's output is
+ * layers) or 24 (bf16 layers), the output rounded once (nearest even).  The
+ * distinct experts' weights are read once per window, an expert's down weight
+ * once per 8 tokens that it serves (4 in a bf16 layer).  A token's output is
  * the same bits at every m and beside any other tokens.
  * In an f16 layer inner values past f16's range (65504) become infinite.
  *   struct_size   sizeof(skinny_moe_desc)

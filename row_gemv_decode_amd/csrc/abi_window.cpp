@@ -162,7 +162,7 @@ skinny_status skinny_moe_plan_create(const skinny_moe_desc* desc, skinny_moe_pla
   p->d = d;
   p->router = router;
   p->max_slots = d.max_m * d.topk < d.experts ? d.max_m * d.topk : d.experts;
-  const int64_t planes = moe_planes(kind_of(d.dtype), kind_of(d.out_dtype));
+  const int64_t planes = moe_planes(kind_of(d.dtype));
   int64_t at = 0;
   auto region = [&at](int64_t bytes) {
     const int64_t start = at;

@@ -20,10 +20,10 @@
 //   moe_down_kernel   per distinct expert, the output rows of the tokens it serves
 //   moe_sum_kernel    adds each token's rows
 // h is kept as the sum of planes in the weights' type, multiplied in rows of the
-// same matrix-core step: two, 16 (bf16) or 22 (f16) bits, under a 16-bit output,
-// where one plane would add as much error as the output's own rounding; three
-// (bf16, 24 bits) under an fp32 output.  For 4-bit weights h is stored in the pair
-// order that their decoding yields.
+// same matrix-core step: three in bf16, which hold the 24 bits of fp32, two in f16
+// (22 bits).  (With two planes in bf16, 3 in 1000 bf16 outputs came out a step of
+// the type away.)  For 4-bit weights h is stored in the pair order
+// that their decoding yields.
 //
 // Row invariance: which wave takes which part of k depends on the layer alone, a
 // matrix-core row does not depend on the other rows, and a token's experts are
@@ -579,15 +579,14 @@ moe_fn pick_weight(int group, bool zeros, bool up, bool wide) {
   }
 }
 
-moe_fn pick(int kind, int np, int group, bool zeros, bool up, bool wide) {
+moe_fn pick(int kind, int group, bool zeros, bool up, bool wide) {
   return kind == CK_F16 ? pick_weight<CK_F16, 2>(group, zeros, up, wide)
-         : np == 2      ? pick_weight<CK_BF16, 2>(group, zeros, up, wide)
                         : pick_weight<CK_BF16, 3>(group, zeros, up, wide);
 }
 
 }  // namespace
 
-int moe_planes(int kind, int out_kind) { return kind == CK_BF16 && out_kind == CK_F32 ? 3 : 2; }
+int moe_planes(int kind) { return kind == CK_BF16 ? 3 : 2; }
 
 hipError_t launch_moe(const MoeArgs& a, int kind, int group, hipStream_t stream) {
   if (a.m < 1 || a.m > kGemvMaxM || a.experts < 1 || a.experts > kMoeMaxExperts || a.topk < 1 ||
@@ -605,7 +604,7 @@ hipError_t launch_moe(const MoeArgs& a, int kind, int group, hipStream_t stream)
   // 280 (1 of 256 bf16) 42 / 49
   const bool wide = slots * (a.inter / 32) >= 2048;
   const int64_t tile = wide ? 32 : 16;
-  const int np = moe_planes(kind, a.out_kind);
+  const int np = moe_planes(kind);
   const int64_t up_blocks = slots * (a.inter / tile) + a.shared_inter / tile;
   // the down product: as in its kernel
   const int unit = group == 0 ? unit_len<kWFull>() : unit_len<128>();
@@ -623,11 +622,11 @@ hipError_t launch_moe(const MoeArgs& a, int kind, int group, hipStream_t stream)
                      dim3(a.shared_inter > 0 ? 2 : 1), dim3(64 * a.m), 0, stream, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(pick(kind, np, group, zeros, true, wide), dim3((unsigned)up_blocks), dim3(64 * kMoeWaves), 0,
+  hipLaunchKernelGGL(pick(kind, group, zeros, true, wide), dim3((unsigned)up_blocks), dim3(64 * kMoeWaves), 0,
                      stream, a);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(pick(kind, np, group, zeros, false, false), dim3((unsigned)down_blocks, (unsigned)((a.m + tokens - 1) / tokens)), dim3(64 * kMoeWaves), 0,
+  hipLaunchKernelGGL(pick(kind, group, zeros, false, false), dim3((unsigned)down_blocks, (unsigned)((a.m + tokens - 1) / tokens)), dim3(64 * kMoeWaves), 0,
                      stream, a);
   e = hipGetLastError();
   if (e != hipSuccess) return e;

@@ -68,7 +68,7 @@ struct MoeArgs {
   int32_t m, experts, topk, renorm, max_slots, out_kind;
 };
 
-int moe_planes(int kind, int out_kind);  // 16-bit planes that hold one inner value
+int moe_planes(int kind);  // 16-bit planes that hold one inner value
 
 // kind: CK_F16 or CK_BF16; group: 0 (16-bit weights), 32, 64 or 128
 hipError_t launch_moe(const MoeArgs& args, int kind, int group, hipStream_t stream);

@@ -82,6 +82,17 @@ def test_moe_output_types_and_plain_softmax(kind):
         Case(3, 40, 6, 256, 128, kind=kind, out=out, renorm=False, seed=8100).check()
 
 
+@pytest.mark.parametrize("group", [0, 128])
+def test_moe_16_bit_output_is_the_fp32_output_rounded(group):
+    """The inner values lose no bit under a 16-bit output that they keep under
+    fp32: the outputs are those of the fp32 layer, rounded once."""
+    kw = dict(shared=128, group=group, zeros=group > 0, kind="bf16", seed=8150)
+    _, _, wide = Case(16, 24, 4, 768, 256, out="f32", **kw).check()
+    for out in ("bf16", "f16"):
+        _, _, got = Case(16, 24, 4, 768, 256, out=out, **kw).check()
+        assert torch.equal(got, wide.to(DT[out]))
+
+
 @pytest.mark.parametrize("experts,topk", [(1, 1), (2, 2), (32, 32), (63, 3), (64, 10), (65, 10), (300, 7), (1024, 32)])
 def test_moe_expert_counts(experts, topk):
     Case(4, experts, topk, 128, 64, shared=32, seed=8200 + experts).check()
