@@ -515,11 +515,30 @@ def _on(where, device, *tensors):
 
 
 def _rows(where, name, t):
-    """Row stride of a matrix whose rows are dense (0: a single row)."""
+    """Row stride of a matrix whose rows are dense and lie apart (0: a single
+    row, which the library takes as a dense one)."""
     shape = t.shape
     if len(shape) != 2 or (shape[1] > 1 and t.stride(1) != 1):
         raise ValueError(f"{where}: {name} must be a matrix with contiguous rows")
-    return t.stride(0) if shape[0] > 1 else 0
+    if shape[0] < 2:
+        return 0
+    ld = t.stride(0)
+    if ld < shape[1]:
+        raise ValueError(f"{where}: {name}'s rows of {shape[1]} elements share memory (row stride {ld})")
+    return ld
+
+
+def _input_rows(where, name, t, stream):
+    """(t, its row stride) of an input.  Rows that share memory (a row expanded
+    to several, windows that overlap) are copied apart on the stream that reads
+    them: the library takes no row stride below the rows' length."""
+    if len(t.shape) == 2 and t.shape[0] > 1 and t.stride(0) < t.shape[1] and t.stride(1) == 1:
+        if stream is None:
+            t = t.contiguous()
+        else:
+            with torch.cuda.stream(stream):
+                t = t.contiguous()
+    return t, _rows(where, name, t)
 
 
 # A window's calls take a few microseconds on the GPU, so what the host does
@@ -566,8 +585,9 @@ def mm_w4(A, W, out=None, out_dtype=None, stream=None):
     """C = A . W for A [m][k] (m <= 16, float16 or bfloat16, dense rows of any
     stride that is a multiple of 8) and a 4-bit grouped weight W (a W4 whose
     scales have A's type), in one launch; C is float32 unless `out` or
-    `out_dtype` says otherwise."""
-    lda = _rows("mm_w4", "A", A)
+    `out_dtype` says otherwise.  Rows of A that share memory (A.expand(m, k) of
+    one row) are copied apart first; those of `out` must not."""
+    A, lda = _input_rows("mm_w4", "A", A, stream)
     m, k = A.shape
     dtype = A.dtype
     if not isinstance(W, W4) or W.dtype is not dtype:
@@ -725,9 +745,11 @@ def token_logprobs(logits, tokens, topk=0, stream=None):
     """Log probabilities of tokens[i] under softmax(logits[i]), with entropy,
     rank and the topk <= 32 top alternatives (see TokenLogprobs), in one launch
     that reads the logits once.  logits [m][vocab] float32, float16 or bfloat16
-    with dense rows of any stride; tokens [m] int64 or int32.  A logit of -inf
-    is masked out; a token outside the row gives NaN and rank 0."""
-    ld = _rows("token_logprobs", "logits", logits)
+    with dense rows of any stride (rows that share memory, as in scoring several
+    tokens of one row by row.expand(m, vocab), are copied apart first); tokens
+    [m] int64 or int32.  A logit of -inf is masked out; a token outside the row
+    gives NaN and rank 0."""
+    logits, ld = _input_rows("token_logprobs", "logits", logits, stream)
     m, vocab = logits.shape
     t64 = tokens.dtype is torch.int64
     if tuple(tokens.shape) != (m,) or not (t64 or tokens.dtype is torch.int32) or not tokens.is_contiguous():

@@ -261,3 +261,17 @@ def test_lp_refusals():
         sk.token_logprobs(x[:, :4], t, topk=5)
     with pytest.raises(sk.SkinnyError):
         sk.token_logprobs(x[:, :0], t)
+
+
+@pytest.mark.parametrize("V", [40, 5003, 70001])
+def test_lp_several_tokens_of_one_row(V):
+    """A row expanded to one row per token: the results of its copies."""
+    x, _ = normal(1, V, 10400)
+    dev, _ = store(x, "f32")
+    tok = torch.arange(16, device="cuda") * (V // 16)
+    want = sk.token_logprobs(dev.repeat(16, 1), tok, topk=3)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = [sk.token_logprobs(dev.expand(16, -1), tok, topk=3), sk.token_logprobs(dev.expand(16, -1), tok, topk=3, stream=s)]
+    s.synchronize()
+    assert all(torch.equal(a, b) for g in got for a, b in zip(g, want))

@@ -181,3 +181,22 @@ def test_w4_refusals():
         sk.mm_w4(torch.zeros((2, 130), dtype=torch.bfloat16, device="cuda")[:, :128], W)  # lda % 8
     with pytest.raises(ValueError):
         sk.mm_w4(A, W, out=torch.zeros((2, 9), device="cuda"))
+
+
+def test_w4_rows_that_share_memory():
+    """One row expanded to several, and windows that overlap: as their copies."""
+    _, W, _ = check(2, 300, 512, 64, "bf16", "f32", True, 7800)
+    one = torch.randn((1, 512), generator=torch.Generator().manual_seed(7801)).to(torch.bfloat16).cuda()
+    over = torch.randn(1024, generator=torch.Generator().manual_seed(7802)).to(torch.bfloat16).cuda().as_strided((5, 512), (128, 1))
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    for a in (one.expand(16, -1), over):
+        want = sk.mm_w4(a.contiguous(), W)
+        assert torch.equal(sk.mm_w4(a, W), want)
+        b = sk.mm_w4(a, W, stream=s)
+        s.synchronize()
+        assert torch.equal(b, want)
+    with pytest.raises(ValueError):
+        sk.mm_w4(one, W, out=torch.zeros(300, device="cuda").expand(1, -1)[:, :299])
+    with pytest.raises(ValueError):
+        sk.mm_w4(one.expand(3, -1), W, out=torch.zeros(300, device="cuda").expand(3, -1))

@@ -1,0 +1,115 @@
+"""The Python side of the decode-window operators, on the host: what the
+binding hands to the library, recorded by a stand-in for it.  Tensors lie in
+host memory and no kernel runs."""
+import ctypes
+
+import pytest
+
+torch = pytest.importorskip("torch")
+sk = pytest.importorskip("row_gemv_decode_amd")
+
+
+class Recorder:
+    """Stands in for the library: keeps the arguments of every call."""
+
+    def __init__(self):
+        self.calls = []
+        self.during = None  # called within each run
+
+    def __getattr__(self, name):
+        def call(*args):
+            if name == "skinny_token_logprobs_workspace_size":
+                args[3]._obj.value = 0
+            else:
+                self.calls.append((name, args))
+            if self.during is not None:
+                self.during(name, args)
+            return sk.OK
+
+        return call
+
+
+@pytest.fixture
+def lib(monkeypatch):
+    rec = Recorder()
+    monkeypatch.setattr(sk, "_lib", rec)
+    monkeypatch.setattr(sk, "_gpu", lambda where, t: -1)
+    monkeypatch.setattr(sk, "_handle", lambda index, stream: 0)
+    monkeypatch.setattr(sk, "_logprob_need", {})
+    return rec
+
+
+def head(n=8, k=64):
+    return sk.W4(torch.zeros((n, k // 2), dtype=torch.uint8), torch.ones((n, k // 32), dtype=torch.bfloat16))
+
+
+def shared_rows(m, length, dtype):
+    """Matrices of m rows whose memory holds fewer: one row for all, and rows
+    that begin half a row apart."""
+    one = torch.arange(length, dtype=torch.float32).to(dtype)
+    half = torch.arange((m + 1) * length // 2, dtype=torch.float32).to(dtype)
+    return one.expand(m, -1), half.as_strided((m, length), (length // 2, 1))
+
+
+def test_w4_rows_that_share_memory_are_copied(lib):
+    for a in shared_rows(4, 64, torch.bfloat16):
+        seen = []
+
+        def during(name, args, a=a, seen=seen):
+            m, _, k, _, ptr, lda = args[:6]
+            assert ptr != a.data_ptr(), "read as rows that lie apart"
+            lda = lda or k
+            raw = ctypes.string_at(ptr, 2 * ((m - 1) * lda + k))
+            got = torch.frombuffer(bytearray(raw), dtype=torch.bfloat16).as_strided((m, k), (lda, 1))
+            seen.append(torch.equal(got, a))
+
+        lib.during = during
+        sk.mm_w4(a, head())
+        assert seen == [True]
+
+
+def test_logprobs_rows_that_share_memory_are_copied(lib):
+    for x in shared_rows(3, 50, torch.float32):
+        seen = []
+
+        def during(name, args, x=x, seen=seen):
+            if name != "skinny_token_logprobs_run":
+                return
+            m, vocab, ptr, ld = args[:4]
+            assert ptr != x.data_ptr(), "read as rows that lie apart"
+            ld = ld or vocab
+            raw = ctypes.string_at(ptr, 4 * ((m - 1) * ld + vocab))
+            got = torch.frombuffer(bytearray(raw), dtype=torch.float32).as_strided((m, vocab), (ld, 1))
+            seen.append(torch.equal(got, x))
+
+        lib.during = during
+        sk.token_logprobs(x, torch.zeros(3, dtype=torch.int64), topk=2)
+        assert seen == [True]
+
+
+def test_w4_output_rows_that_share_memory_are_refused(lib):
+    a = torch.zeros((4, 64), dtype=torch.bfloat16)
+    for n, out in ((8, torch.zeros(8).expand(4, -1)), (8, torch.zeros(40).as_strided((4, 8), (4, 1))),
+                   (1, torch.zeros((1, 1)).expand(4, 1))):
+        with pytest.raises(ValueError, match="share memory"):
+            sk.mm_w4(a, head(n), out=out)
+    assert lib.calls == []
+
+
+def test_columns_that_lie_apart_are_refused(lib):
+    for a in (torch.zeros((64, 4), dtype=torch.bfloat16).t(), torch.zeros((4, 1), dtype=torch.bfloat16).expand(4, 64)):
+        with pytest.raises(ValueError, match="contiguous rows"):
+            sk.mm_w4(a, head())
+    assert lib.calls == []
+
+
+def test_rows_that_lie_apart_are_read_where_they_are(lib):
+    a = torch.zeros((4, 80), dtype=torch.bfloat16)[:, :64]
+    x = torch.zeros((3, 60))[:, :50]
+    sk.mm_w4(a, head())
+    sk.mm_w4(a[:1], head())
+    sk.token_logprobs(x, torch.zeros(3, dtype=torch.int64))
+    got = [args for name, args in lib.calls]
+    assert (got[0][4], got[0][5]) == (a.data_ptr(), 80)
+    assert (got[1][4], got[1][5]) == (a.data_ptr(), 0)
+    assert (got[2][2], got[2][3]) == (x.data_ptr(), 60)
