@@ -24,6 +24,12 @@
 extern "C" {
 #endif
 
+/* A workspace of these operators starts with arrival counters.  Only they have
+ * to be zero before its first use: the first SKINNY_WINDOW_COUNTER_BYTES, or
+ * nothing for a MoE layer whose router needs no workspace of its own
+ * (skinny_mm_workspace_size of its plan for n = experts, k = d). */
+#define SKINNY_WINDOW_COUNTER_BYTES 4096
+
 /* --- 4-bit weights with group scales -------------------------------------- */
 
 /* A 4-bit weight [n][k] in groups of `group` (32, 64 or 128) elements along k:
@@ -133,8 +139,9 @@ SKINNY_API skinny_status skinny_moe_plan_create(const skinny_moe_desc* desc, ski
 SKINNY_API void skinny_moe_plan_destroy(skinny_moe_plan* plan);
 
 /* Bytes of device workspace every run of this plan needs: 16-byte aligned,
- * zero-filled once before its first use; a completed run leaves it ready for
- * the next.  Two runs in flight at once must not share one. */
+ * zero-filled (see SKINNY_WINDOW_COUNTER_BYTES) once before its first use; a
+ * completed run leaves it ready for the next.  Two runs in flight at once must
+ * not share one, and a graph that is replayed beside other runs needs its own. */
 SKINNY_API skinny_status skinny_moe_workspace_size(const skinny_moe_plan* plan, size_t* bytes);
 
 /* Enqueue the layer for m tokens (1 <= m <= max_m).
@@ -168,7 +175,7 @@ SKINNY_API skinny_status skinny_moe_run(const skinny_moe_plan* plan, int64_t m, 
  *   topk         0 .. min(vocab, SKINNY_TOPK_MAX); 0: top_ids and top_logprobs are
  *                not written and may be NULL
  *   outputs      4-byte aligned, overlapping neither one another nor the inputs
- *   workspace    zero-initialised device scratch of at least
+ *   workspace    zero-initialised (see SKINNY_WINDOW_COUNTER_BYTES) device scratch of at least
  *                skinny_token_logprobs_workspace_size bytes, 16-byte aligned
  *                (may be NULL when that is 0); a completed run leaves it ready
  *                for the next, of any size it suffices for.  Two runs in

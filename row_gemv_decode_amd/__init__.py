@@ -47,6 +47,7 @@ GEMV_MAX_M = 16
 TOPK_MAX = 32
 MOE_RENORM = 0x1
 MOE_MAX_EXPERTS = 1024
+WINDOW_COUNTER_BYTES = 4096
 
 EXPORTS = (
     "skinny_mm_plan", "skinny_mm_plan_destroy", "skinny_mm_workspace_size", "skinny_mm_run",
@@ -567,17 +568,33 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _stream_workspace(cache, key, nbytes, index, stream):
+def _capturing(handle, stream):
+    """Whether the stream that a call runs on is being captured (the default
+    stream, handle 0, cannot be)."""
+    if handle == 0:
+        return False
+    if stream is None:
+        return torch.cuda.is_current_stream_capturing()
+    with torch.cuda.stream(stream):
+        return torch.cuda.is_current_stream_capturing()
+
+
+def _stream_workspace(cache, key, nbytes, counters, device, handle, stream):
     """The workspace of at least nbytes that `cache` holds for a stream, made
-    and zeroed on that stream (a run leaves its counters at zero).  One made
-    while the stream is captured belongs to the graph, which zeroes it at every
-    replay, and is not kept."""
-    ws = cache.get(key)
+    and zeroed on that stream (a run leaves its counters at zero).  A capture
+    always gets one of its own, from the graph's memory, whose first `counters`
+    bytes the graph zeroes at every replay: the stream's may be replaced by a
+    larger one, and eager runs may use it, while the graph lives."""
+    capturing = _capturing(handle, stream)
+    ws = None if capturing else cache.get(key)
     if ws is None or ws.numel() < nbytes:
-        with torch.cuda.stream(torch.cuda.current_stream(index) if stream is None else stream):
-            ws = torch.zeros(nbytes, dtype=torch.uint8, device=torch.device("cuda", index))
-            if not torch.cuda.is_current_stream_capturing():
-                cache[key] = ws
+        with torch.cuda.stream(torch.cuda.current_stream(device) if stream is None else stream):
+            if capturing:
+                ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+                if counters:
+                    ws[:counters].zero_()
+            else:
+                ws = cache[key] = torch.zeros(nbytes, dtype=torch.uint8, device=device)
     return ws
 
 
@@ -683,6 +700,8 @@ class MoELayer:
         sz = ctypes.c_size_t()
         _check(_lib.skinny_moe_workspace_size(h, ctypes.byref(sz)), "skinny_moe_workspace_size")
         self.workspace_bytes = int(sz.value)
+        # (the layer's only counters are its router GEMV's, where that splits k over workgroups)
+        self._counters = WINDOW_COUNTER_BYTES if Plan(experts, d, max_m, code, code, F32).workspace_bytes else 0
         self._ws = {}
 
     def __call__(self, x, out=None, topk_idx=None, topk_weight=None, stream=None):
@@ -710,7 +729,7 @@ class MoELayer:
                     _on("MoELayer", self.device, t)
         handle = _handle(self._index, stream)
         # (runs on different streams may be in flight at once: each has its own)
-        ws = _stream_workspace(self._ws, handle, self.workspace_bytes, self._index, stream)
+        ws = _stream_workspace(self._ws, handle, self.workspace_bytes, self._counters, self.device, handle, stream)
         _check(_lib.skinny_moe_run(self._h, m, x.data_ptr(), self._weights_addr, out.data_ptr(), _ptr(topk_idx),
                                    _ptr(topk_weight), ws.data_ptr(), self.workspace_bytes, handle), "skinny_moe_run")
         return out
@@ -768,7 +787,9 @@ def token_logprobs(logits, tokens, topk=0, stream=None):
             _logprob_need.clear()
         need = _logprob_need[m, vocab, topk] = int(sz.value)
     handle = _handle(index, stream)
-    ws = _stream_workspace(_logprob_ws, (index, handle), need, index, stream) if need else None
+    ws = None
+    if need:
+        ws = _stream_workspace(_logprob_ws, (index, handle), need, WINDOW_COUNTER_BYTES, logits.device, handle, stream)
     # one allocation for the five results, each at a multiple of 4 bytes
     flat = _empty(m * (3 + 2 * topk), torch.float32, logits.device, stream)
     lp, ent, top, rank, ids = flat.split_with_sizes((m, m, m * topk, m, m * topk))

@@ -60,7 +60,7 @@ RowSegments row_segments(int64_t m, int64_t vocab) {
 // workspace: the rows' arrival counters, then the segments' partial results.
 // The counters' region has one fixed size, so that one workspace serves runs
 // of several sizes: no run's partial results touch another's counters.
-constexpr int64_t kRowCounterBytes = 1024 * 4;
+constexpr int64_t kRowCounterBytes = SKINNY_WINDOW_COUNTER_BYTES;
 int64_t logprob_bytes(int64_t m, int64_t vocab, int32_t topk) {
   const RowSegments s = row_segments(m, vocab);
   return s.count == 1 ? 0 : kRowCounterBytes + round256(m * s.count * (4 + 2 * (int64_t)topk) * 4);
@@ -74,6 +74,8 @@ bool logprob_sizes_ok(int64_t m, int64_t vocab, int32_t topk) {
 }  // namespace
 
 static_assert(SKINNY_MOE_MAX_EXPERTS == kMoeMaxExperts, "expert limit");
+// (the router's GEMV counts arrivals per range of columns, so at most one per expert)
+static_assert(SKINNY_MOE_MAX_EXPERTS * 4 <= SKINNY_WINDOW_COUNTER_BYTES, "the router's counters");
 
 struct skinny_moe_plan {
   skinny_moe_desc d;      // normalised copy (ldx / ldo filled in)

@@ -275,3 +275,35 @@ def test_lp_several_tokens_of_one_row(V):
     got = [sk.token_logprobs(dev.expand(16, -1), tok, topk=3), sk.token_logprobs(dev.expand(16, -1), tok, topk=3, stream=s)]
     s.synchronize()
     assert all(torch.equal(a, b) for g in got for a, b in zip(g, want))
+
+
+def test_lp_graph_outlives_the_streams_workspace():
+    """A stream's workspace is replaced by a larger one after a capture on that
+    stream: the graph's replays neither need the old one nor write to the
+    tensors that lie there now, also beside eager calls on the stream."""
+    x, t = normal(4, 60000, 10500)
+    dev, tok, want = check(x, t, 4, "f32")
+    big, bt = store(normal(16, 70000, 10501)[0], "f32")[0], torch.arange(16, device="cuda")
+    bwant = sk.token_logprobs(big, bt, topk=32)
+    s, other = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    sk.token_logprobs(dev, tok, topk=4, stream=s)
+    s.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        out = sk.token_logprobs(dev, tok, topk=4)
+    sk.token_logprobs(big, bt, topk=32, stream=s)
+    with torch.cuda.stream(s):
+        near = [torch.full((n,), 1 + n % 100, dtype=torch.uint8, device="cuda") for n in (512, 4096, 8192, 20000, 60000) * 4]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for o in out:
+            o.zero_()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(other):
+            g.replay()
+        eager = [sk.token_logprobs(big, bt, topk=32, stream=s) for _ in range(3)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
+        assert all(torch.equal(a, b) for e in eager for a, b in zip(e, bwant))
+        assert all(bool((n == 1 + n.numel() % 100).all()) for n in near)

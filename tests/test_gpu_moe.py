@@ -241,3 +241,29 @@ def test_moe_refusals():
         sk.MoELayer(router, w13, w2, topk=9)
     with pytest.raises(sk.SkinnyError):
         sk.MoELayer(router, w13, w2, topk=2, max_m=17)
+
+
+@pytest.mark.parametrize("d", [256, 8320])
+def test_moe_graph_beside_eager_runs_on_its_stream(d):
+    """A graph captured on a stream that the layer has run on, replayed on
+    another stream while the first one runs the layer on other tokens (with d
+    past 8192 the router's arrival counters are part of the workspace)."""
+    c = Case(6, 20, 4, d, 64, shared=32, seed=9200)
+    layer, x, got = c.check()
+    y = x.flip(0).contiguous()
+    want = layer(y)
+    s, other = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    layer(y, stream=s)
+    s.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        out = layer(x)
+    for _ in range(4):
+        out.zero_()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(other):
+            g.replay()
+        eager = [layer(y, stream=s) for _ in range(8)]
+        torch.cuda.synchronize()
+        assert torch.equal(out, got) and all(torch.equal(e, want) for e in eager)

@@ -1,6 +1,7 @@
 """The Python side of the decode-window operators, on the host: what the
 binding hands to the library, recorded by a stand-in for it.  Tensors lie in
 host memory and no kernel runs."""
+import contextlib
 import ctypes
 
 import pytest
@@ -14,12 +15,13 @@ class Recorder:
 
     def __init__(self):
         self.calls = []
+        self.need = 0  # workspace bytes
         self.during = None  # called within each run
 
     def __getattr__(self, name):
         def call(*args):
             if name == "skinny_token_logprobs_workspace_size":
-                args[3]._obj.value = 0
+                args[3]._obj.value = self.need
             else:
                 self.calls.append((name, args))
             if self.during is not None:
@@ -113,3 +115,38 @@ def test_rows_that_lie_apart_are_read_where_they_are(lib):
     assert (got[0][4], got[0][5]) == (a.data_ptr(), 80)
     assert (got[1][4], got[1][5]) == (a.data_ptr(), 0)
     assert (got[2][2], got[2][3]) == (x.data_ptr(), 60)
+
+
+@pytest.mark.parametrize("stream", [None, object()])
+def test_a_capture_never_takes_the_streams_workspace(lib, monkeypatch, stream):
+    """A graph outlives the stream's workspace, which a larger call replaces:
+    it gets one of its own, with zeroed counters, and leaves the stream's."""
+    lib.need = 3 * sk.WINDOW_COUNTER_BYTES
+    cached = torch.zeros(lib.need, dtype=torch.uint8)
+    cache = {(-1, 5): cached}
+    capturing = [True]
+    monkeypatch.setattr(sk, "_logprob_ws", cache)
+    monkeypatch.setattr(sk, "_handle", lambda index, stream: 5)
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: contextlib.nullcontext())
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda d=None: None)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: capturing[0])
+    used = []
+
+    def during(name, args):
+        if name == "skinny_token_logprobs_run":
+            used.append(args[13])
+            if capturing[0]:
+                assert args[14] == lib.need
+                assert ctypes.string_at(args[13], sk.WINDOW_COUNTER_BYTES) == bytes(sk.WINDOW_COUNTER_BYTES)
+
+    lib.during = during
+    x, t = torch.zeros((2, 50)), torch.zeros(2, dtype=torch.int64)
+    sk.token_logprobs(x, t, stream=stream)
+    assert used[0] != cached.data_ptr() and cache == {(-1, 5): cached}
+    capturing[0] = False
+    sk.token_logprobs(x, t, stream=stream)
+    assert used[1] == cached.data_ptr()
+    monkeypatch.setattr(sk, "_logprob_need", {})
+    lib.need *= 2
+    sk.token_logprobs(x, t, stream=stream)  # a larger call replaces the stream's
+    assert used[2] != cached.data_ptr() and cache[-1, 5].numel() == lib.need
