@@ -141,7 +141,9 @@ SKINNY_API void skinny_moe_plan_destroy(skinny_moe_plan* plan);
 /* Bytes of device workspace every run of this plan needs: 16-byte aligned,
  * zero-filled (see SKINNY_WINDOW_COUNTER_BYTES) once before its first use; a
  * completed run leaves it ready for the next.  Two runs in flight at once must
- * not share one, and a graph that is replayed beside other runs needs its own. */
+ * not share one, and a graph that is replayed beside other runs needs its own.
+ * A run is several launches: two host threads must not enqueue runs on one
+ * workspace at once, not even on one stream. */
 SKINNY_API skinny_status skinny_moe_workspace_size(const skinny_moe_plan* plan, size_t* bytes);
 
 /* Enqueue the layer for m tokens (1 <= m <= max_m).

@@ -16,6 +16,7 @@ W[k, n] in C[m, n] = A[m, k] . W[k, n].
 """
 import ctypes
 import os
+import threading
 from typing import NamedTuple
 
 # torch first: it brings its own HIP runtime (soname libamdhip64.so.7); loaded
@@ -644,7 +645,7 @@ class MoELayer:
     of the router's type or both W4 of one group length; shared13
     [2 shared_inter][d] and shared2 [d][shared_inter] likewise, with
     shared_gate [d].  x is contiguous and has the router's type; out has
-    out_dtype (x's type by default)."""
+    out_dtype (x's type by default).  Several threads may call a layer at once."""
 
     def __init__(self, router, w13, w2, topk, renorm=True, out_dtype=None, max_m=16, shared13=None, shared2=None,
                  shared_gate=None, num_cus=0):
@@ -703,6 +704,7 @@ class MoELayer:
         # (the layer's only counters are its router GEMV's, where that splits k over workgroups)
         self._counters = WINDOW_COUNTER_BYTES if Plan(experts, d, max_m, code, code, F32).workspace_bytes else 0
         self._ws = {}
+        self._lock = threading.Lock()
 
     def __call__(self, x, out=None, topk_idx=None, topk_weight=None, stream=None):
         """out [m][d]; topk_idx (int32 [m][topk]) and topk_weight (float32
@@ -728,10 +730,13 @@ class MoELayer:
                     _dense("MoELayer", **{name: t})
                     _on("MoELayer", self.device, t)
         handle = _handle(self._index, stream)
-        # (runs on different streams may be in flight at once: each has its own)
-        ws = _stream_workspace(self._ws, handle, self.workspace_bytes, self._counters, self.device, handle, stream)
-        _check(_lib.skinny_moe_run(self._h, m, x.data_ptr(), self._weights_addr, out.data_ptr(), _ptr(topk_idx),
-                                   _ptr(topk_weight), ws.data_ptr(), self.workspace_bytes, handle), "skinny_moe_run")
+        # Runs on different streams may be in flight at once: each stream has its
+        # own workspace.  A run is several launches over it, so two threads on one
+        # stream must not interleave theirs.
+        with self._lock:
+            ws = _stream_workspace(self._ws, handle, self.workspace_bytes, self._counters, self.device, handle, stream)
+            _check(_lib.skinny_moe_run(self._h, m, x.data_ptr(), self._weights_addr, out.data_ptr(), _ptr(topk_idx),
+                                       _ptr(topk_weight), ws.data_ptr(), self.workspace_bytes, handle), "skinny_moe_run")
         return out
 
     def __del__(self):

@@ -3,6 +3,8 @@
 layer: the additions of each sum times 2^-24 of the magnitudes added, the
 activation's slope, the softmax's dependence on the logits, the output type's
 rounding)."""
+import threading
+
 import numpy as np
 import pytest
 
@@ -267,3 +269,23 @@ def test_moe_graph_beside_eager_runs_on_its_stream(d):
         eager = [layer(y, stream=s) for _ in range(8)]
         torch.cuda.synchronize()
         assert torch.equal(out, got) and all(torch.equal(e, want) for e in eager)
+
+
+def test_moe_from_several_threads():
+    """Threads that call one layer on one stream get their own tokens' outputs."""
+    c = Case(16, 24, 4, 256, 96, shared=32, seed=9300)
+    layer, x, _ = c.check()
+    xs = [x[i:i + 3].contiguous() for i in range(8)]
+    want = [layer(v) for v in xs]
+    got = [None] * 8
+
+    def work(i):
+        got[i] = [layer(xs[i]) for _ in range(40)]
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(8)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, w) for g, w in zip(got, want) for o in g)

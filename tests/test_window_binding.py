@@ -3,6 +3,8 @@ binding hands to the library, recorded by a stand-in for it.  Tensors lie in
 host memory and no kernel runs."""
 import contextlib
 import ctypes
+import threading
+import time
 
 import pytest
 
@@ -20,8 +22,8 @@ class Recorder:
 
     def __getattr__(self, name):
         def call(*args):
-            if name == "skinny_token_logprobs_workspace_size":
-                args[3]._obj.value = self.need
+            if name.endswith("workspace_size"):
+                args[-1]._obj.value = self.need
             else:
                 self.calls.append((name, args))
             if self.during is not None:
@@ -150,3 +152,33 @@ def test_a_capture_never_takes_the_streams_workspace(lib, monkeypatch, stream):
     lib.need *= 2
     sk.token_logprobs(x, t, stream=stream)  # a larger call replaces the stream's
     assert used[2] != cached.data_ptr() and cache[-1, 5].numel() == lib.need
+
+
+def moe_layer(d=64, inter=32, experts=4):
+    half = torch.bfloat16
+    return sk.MoELayer(torch.zeros((experts, d), dtype=half), torch.zeros((experts, 2 * inter, d), dtype=half),
+                       torch.zeros((experts, d, inter), dtype=half), topk=2)
+
+
+def test_threads_do_not_enqueue_a_layers_runs_at_once(lib, monkeypatch):
+    """A run is several launches over one workspace: another thread's must not
+    come between them."""
+    monkeypatch.setattr(sk, "_stream_workspace", lambda *a: torch.zeros(16, dtype=torch.uint8))
+    layer = moe_layer()
+    inside, most = [0], [0]
+
+    def during(name, args):
+        if name == "skinny_moe_run":
+            inside[0] += 1
+            most[0] = max(most[0], inside[0])
+            time.sleep(0.05)  # (as the library's call does, without the interpreter's lock)
+            inside[0] -= 1
+
+    lib.during = during
+    x = torch.zeros((3, 64), dtype=torch.bfloat16)
+    threads = [threading.Thread(target=layer, args=(x,)) for _ in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert sum(name == "skinny_moe_run" for name, _ in lib.calls) == 4 and most[0] == 1
