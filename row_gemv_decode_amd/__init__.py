@@ -534,7 +534,11 @@ def _input_rows(where, name, t, stream):
     """(t, its row stride) of an input.  Rows that share memory (a row expanded
     to several, windows that overlap) are copied apart on the stream that reads
     them: the library takes no row stride below the rows' length."""
-    if len(t.shape) == 2 and t.shape[0] > 1 and t.stride(0) < t.shape[1] and t.stride(1) == 1:
+    shape = t.shape
+    if len(shape) == 2 and shape[0] > 1 and t.stride(1) == 1:
+        ld = t.stride(0)
+        if ld >= shape[1]:
+            return t, ld
         if stream is None:
             t = t.contiguous()
         else:
@@ -547,6 +551,9 @@ def _input_rows(where, name, t, stream):
 # for each of them counts: types are looked up, streams come as raw handles.
 _CODES = {torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32}
 _raw_stream = torch._C._cuda_getCurrentRawStream
+# (the library launches on the current device: a call whose tensors lie on
+# another GPU makes that one current first)
+_current_device = torch._C._cuda_getDevice
 
 
 def _handle(index, stream):
@@ -616,6 +623,9 @@ def mm_w4(A, W, out=None, out_dtype=None, stream=None):
     index = _gpu("mm_w4", A)
     if W._index != index:
         raise ValueError(f"mm_w4: A is on {A.device}, the weight on {W.device}")
+    if _current_device() != index:
+        with torch.cuda.device(index):
+            return mm_w4(A, W, out, out_dtype, stream)
     if out is None:
         out_dtype = out_dtype or torch.float32
         out = _empty((m, n), out_dtype, W.device, stream)
@@ -714,6 +724,9 @@ class MoELayer:
             raise ValueError(f"MoELayer: x must be contiguous [m][{self.d}] of type {self.dtype}")
         if x.get_device() != self._index:
             raise ValueError(f"MoELayer: x must be on {self.device}")
+        if _current_device() != self._index:
+            with torch.cuda.device(self._index):
+                return self(x, out, topk_idx, topk_weight, stream)
         m = shape[0]
         if out is None:
             out = _empty((m, self.d), self.out_dtype, self.device, stream)
@@ -784,6 +797,9 @@ def token_logprobs(logits, tokens, topk=0, stream=None):
     index = _gpu("token_logprobs", logits)
     if tokens.get_device() != index:
         raise ValueError("token_logprobs: logits and tokens must be on one GPU")
+    if _current_device() != index:
+        with torch.cuda.device(index):
+            return token_logprobs(logits, tokens, topk, stream)
     need = _logprob_need.get((m, vocab, topk))
     if need is None:
         sz = ctypes.c_size_t()

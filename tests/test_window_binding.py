@@ -39,6 +39,7 @@ def lib(monkeypatch):
     monkeypatch.setattr(sk, "_lib", rec)
     monkeypatch.setattr(sk, "_gpu", lambda where, t: -1)
     monkeypatch.setattr(sk, "_handle", lambda index, stream: 0)
+    monkeypatch.setattr(sk, "_current_device", lambda: -1, raising=False)
     monkeypatch.setattr(sk, "_logprob_need", {})
     return rec
 
@@ -182,3 +183,25 @@ def test_threads_do_not_enqueue_a_layers_runs_at_once(lib, monkeypatch):
     for t in threads:
         t.join()
     assert sum(name == "skinny_moe_run" for name, _ in lib.calls) == 4 and most[0] == 1
+
+
+def test_the_tensors_gpu_is_current_during_a_call(lib, monkeypatch):
+    """The library launches on the current device, whatever the stream's."""
+    monkeypatch.setattr(sk, "_stream_workspace", lambda *a: torch.zeros(16, dtype=torch.uint8))
+    layer = moe_layer()
+    current, seen = [3], []
+
+    @contextlib.contextmanager
+    def device(index):
+        was, current[0] = current[0], index
+        yield
+        current[0] = was
+
+    monkeypatch.setattr(sk, "_current_device", lambda: current[0], raising=False)
+    monkeypatch.setattr(torch.cuda, "device", device)
+    lib.during = lambda name, args: seen.append((name, current[0])) if name.endswith("_run") else None
+    sk.mm_w4(torch.zeros((2, 64), dtype=torch.bfloat16), head())
+    layer(torch.zeros((2, 64), dtype=torch.bfloat16))
+    sk.token_logprobs(torch.zeros((2, 50)), torch.zeros(2, dtype=torch.int64), topk=1)
+    assert seen == [("skinny_w4_mm_run", -1), ("skinny_moe_run", -1), ("skinny_token_logprobs_run", -1)]
+    assert current == [3]
