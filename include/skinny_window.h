@@ -75,12 +75,13 @@ SKINNY_API skinny_status skinny_w4_mm_run(int64_t m, int64_t n, int64_t k, int32
  *   f_e(x) = Wd_e (silu(Wg_e x) * (Wu_e x)),    silu(v) = v / (1 + e^-v)
  *   out_t = sum over e in S_t of p_te f_e(x_t)
  *           + sigmoid(wg . x_t) f_shared(x_t)   (when shared_inter > 0)
- * Products are summed in fp32; the inner values are carried in 22 bits (f16
- * layers) or 24 (bf16 layers), the output rounded once (nearest even).  The
- * distinct experts' weights are read once per window, an expert's down weight
- * once per 8 tokens that it serves (4 in a bf16 layer).  A token's output is
- * the same bits at every m and beside any other tokens.
- * In an f16 layer inner values past f16's range (65504) become infinite.
+ * Products are summed in fp32; the inner values silu(.) * (.) are carried in 24
+ * bits, the output rounded once (nearest even).  In an f16 layer with 16-bit
+ * weights that holds for inner values from 2^-12 to 2^18 in magnitude: products
+ * of smaller ones lose a bit for every power of two, larger ones become
+ * infinite.  The distinct experts' weights are read once per window, an expert's
+ * down weight once per 4 tokens that it serves.  A token's output is the same
+ * bits at every m and beside any other tokens.
  *   struct_size   sizeof(skinny_moe_desc)
  *   dtype         SKINNY_F16 or SKINNY_BF16: x, the router, the gate's weight, the
  *                 scales, and the weights unless they are 4-bit

@@ -83,7 +83,7 @@ struct skinny_moe_plan {
   int64_t max_slots;      // distinct experts a window can reach
   // workspace regions, in bytes from its start
   int64_t router_ws;      // the router plan's own workspace comes first (its counters start at zero)
-  int64_t logits, slots, slot_w, slot_rank, gates, h, y, bytes;
+  int64_t logits, slots, slot_rank, weights, h, y, bytes;
 };
 
 extern "C" {
@@ -164,7 +164,7 @@ skinny_status skinny_moe_plan_create(const skinny_moe_desc* desc, skinny_moe_pla
   p->d = d;
   p->router = router;
   p->max_slots = d.max_m * d.topk < d.experts ? d.max_m * d.topk : d.experts;
-  const int64_t planes = moe_planes(kind_of(d.dtype));
+  const int64_t planes = moe_planes();
   int64_t at = 0;
   auto region = [&at](int64_t bytes) {
     const int64_t start = at;
@@ -175,9 +175,8 @@ skinny_status skinny_moe_plan_create(const skinny_moe_desc* desc, skinny_moe_pla
   region(p->router_ws);
   p->logits = region(d.max_m * d.experts * 4);
   p->slots = region(p->max_slots * 4);
-  p->slot_w = region(p->max_slots * kGemvMaxM * 4);
   p->slot_rank = region(p->max_slots * kGemvMaxM * 4);
-  p->gates = region(kGemvMaxM * 4);
+  p->weights = region(d.max_m * (d.topk + 1) * 4);
   p->h = region((p->max_slots * d.inter + d.shared_inter) * kGemvMaxM * planes * 2);
   p->y = region(d.max_m * (d.topk + 1) * d.d * 4);
   p->bytes = at;
@@ -243,9 +242,8 @@ skinny_status skinny_moe_run(const skinny_moe_plan* plan, int64_t m, const void*
   a.shared_gate = weights->shared_gate;
   a.logits = logits;
   a.slots = (uint32_t*)(base + plan->slots);
-  a.slot_w = (float*)(base + plan->slot_w);
   a.slot_rank = (int32_t*)(base + plan->slot_rank);
-  a.gates = (float*)(base + plan->gates);
+  a.weights = (float*)(base + plan->weights);
   a.h = (uint16_t*)(base + plan->h);
   a.y = (float*)(base + plan->y);
   a.topk_idx = topk_idx;

@@ -4,11 +4,11 @@
 //   l_t   = x_t . Wr                                   (router logits, by the GEMV)
 //   S_t   = the topk largest of l_t (equal values by lower expert first)
 //   p_te  = exp(l_te) / sum over S_t (or over all experts) of exp(l_t.)
-//   h_te  = silu(x_t . Wg_e) * (x_t . Wu_e) * p_te
-//   out_t = sum over e in S_t of h_te . Wd_e  +  (sigmoid(x_t . wg) * h_t,shared) . Wd_shared
+//   h_te  = silu(x_t . Wg_e) * (x_t . Wu_e)
+//   out_t = sum over e in S_t of p_te (h_te . Wd_e)  +  sigmoid(x_t . wg) (h_t,shared . Wd_shared)
 //
 // HBM-bound on the distinct experts' weights, each read once per window (an
-// expert's down weight once per 8 tokens that it serves, or 4 with three planes).
+// expert's down weight once per 4 tokens that it serves).
 //   moe_route_kernel  one workgroup, one wave per token: top-k, softmax and the
 //                     list of distinct experts in ascending order with each
 //                     one's tokens (a second workgroup: the shared expert's
@@ -16,14 +16,20 @@
 //   moe_up_kernel     one workgroup per (distinct expert, 16 or 32 columns of
 //                     h): gate and up columns side by side against all rows of
 //                     x (a matrix-core tile holds 16 rows anyway, so tokens are
-//                     not gathered), p and silu in the epilogue
+//                     not gathered), silu in the epilogue
 //   moe_down_kernel   per distinct expert, the output rows of the tokens it serves
-//   moe_sum_kernel    adds each token's rows
-// h is kept as the sum of planes in the weights' type, multiplied in rows of the
-// same matrix-core step: three in bf16, which hold the 24 bits of fp32, two in f16
-// (22 bits).  (With two planes in bf16, 3 in 1000 bf16 outputs came out a step of
-// the type away.)  For 4-bit weights h is stored in the pair order
-// that their decoding yields.
+//   moe_sum_kernel    adds each token's rows, times p
+// h is kept as the sum of three 16-bit planes, multiplied in rows of the same
+// matrix-core step, which hold the 24 bits of fp32.  (With two planes in bf16, 3 in
+// 1000 bf16 outputs came out a step of the type away.)  The planes are bf16 where
+// the weights can be, that is in bf16 layers and with 4-bit weights.  In f16 layers
+// with 16-bit weights they are f16, which has few exponents: h is scaled by 2^-2,
+// and each plane is the remainder of the one before times 2^11.  That is as good as
+// fp32 for |h| from 2^-12 to 2^18; below, the first plane is subnormal, which the
+// matrix core multiplies with as many fewer bits (inputs of 1e-3, h about 2^-20: a
+// relative error of 3e-6).  p stays out of h for the same reason.  (Two planes of
+// h p as they are: 3e-5 at inputs of 2^-4, 7e-3 at 2^-8, infinity past 65504.)  For
+// 4-bit weights h is stored in the pair order that their decoding yields.
 //
 // Row invariance: which wave takes which part of k depends on the layer alone, a
 // matrix-core row does not depend on the other rows, and a token's experts are
@@ -38,6 +44,7 @@ namespace skinny {
 namespace {
 
 constexpr int kMoeWaves = 4;
+constexpr int kMoeDownTokens = 4;  // of a workgroup of the down product: 16 rows hold their planes
 
 __device__ __forceinline__ float wave_sum_f32(float v) {
   v += dpp_mov<kDppXor1>(v);
@@ -80,7 +87,7 @@ __global__ __launch_bounds__(1024) void moe_route_kernel(MoeArgs a) {
       }
     }
     s = wave_sum_f32(s);
-    if (lane == 0) a.gates[t] = 1.0f / (1.0f + expf(-s));
+    if (lane == 0) a.weights[t * (a.topk + 1) + a.topk] = 1.0f / (1.0f + expf(-s));
     return;
   }
 
@@ -132,6 +139,7 @@ __global__ __launch_bounds__(1024) void moe_route_kernel(MoeArgs a) {
   const float p = ex / total;
   if (lane < a.topk) {
     atomicOr(&mask[mine_e], 1u << t);
+    a.weights[t * (a.topk + 1) + lane] = p;
     if (a.topk_idx != nullptr) a.topk_idx[t * a.topk + lane] = mine_e;
     if (a.topk_weight != nullptr) a.topk_weight[t * a.topk + lane] = p;
   }
@@ -154,10 +162,7 @@ __global__ __launch_bounds__(1024) void moe_route_kernel(MoeArgs a) {
   }
   __syncthreads();
   // (read for the tokens in the slot's mask only)
-  if (lane < a.topk) {
-    a.slot_w[slot_of[mine_e] * kGemvMaxM + t] = p;
-    a.slot_rank[slot_of[mine_e] * kGemvMaxM + t] = lane;
-  }
+  if (lane < a.topk) a.slot_rank[slot_of[mine_e] * kGemvMaxM + t] = lane;
 }
 
 // where column i of h lies in memory: for 4-bit weights each run of eight is
@@ -200,9 +205,18 @@ __device__ __forceinline__ int served_row(uint32_t entry, int tk, int m) {
   return ((mask >> tk) & 1u) != 0 ? tk : __builtin_ctz(mask);
 }
 
+// h's planes (see above): their type PK, and the scales
+constexpr int kPlanes = 3;
+template <int TK, int WQ>
+constexpr int plane_kind() { return WQ == kWFull ? TK : CK_BF16; }
+template <int PK>
+constexpr float inner_scale() { return PK == CK_F16 ? 0.25f : 1.0f; }
+template <int PK>
+constexpr float plane_step() { return PK == CK_F16 ? 2048.0f : 1.0f; }
+
 // GT tiles of 16 columns of h: columns of w13 are the gate's 0 .. inter - 1,
 // then the up's
-template <int TK, int WQ, int NP, int GT>
+template <int TK, int WQ, int GT>
 __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_up_kernel(MoeArgs a) {
   __shared__ ScaleLds<WQ, 2 * GT> lds;
   __shared__ u32x4 turn_s[kMoeWaves][turn_slots<WQ, 2 * GT>() * 64];
@@ -237,21 +251,21 @@ __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_up_kernel(MoeArgs a) {
   __syncthreads();
   if (wave < GT) {
     const f32x4 g = wave_sums(turn_s, wave, lane), up = wave_sums(turn_s, GT + wave, lane);
-    const float* weight = shared ? a.gates : a.slot_w + slot * kGemvMaxM;
-    uint16_t* hb = a.h + (shared ? a.max_slots : slot) * (int64_t)(kGemvMaxM * NP) * a.inter;
+    constexpr int PK = plane_kind<TK, WQ>();
+    uint16_t* hb = a.h + (shared ? a.max_slots : slot) * (int64_t)(kGemvMaxM * kPlanes) * a.inter;
     hb += 16 * (tile * GT + wave) + h_place<WQ>(lane & 15);
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const int tk = 4 * h + q;
       if (tk < a.m && ((entry >> (16 + tk)) & 1u) != 0) {
-        float v = g[q] / (1.0f + expf(-g[q])) * up[q] * weight[tk];
-        uint16_t* o = hb + (int64_t)tk * NP * inter;
+        float v = g[q] / (1.0f + expf(-g[q])) * up[q] * inner_scale<PK>();
+        uint16_t* o = hb + (int64_t)tk * kPlanes * inter;
 #pragma unroll
-        for (int i = 0; i < NP; ++i) {
-          const uint16_t bits = f32_half<TK>(v);
+        for (int i = 0; i < kPlanes; ++i) {
+          const uint16_t bits = f32_half<PK>(v);
           o[i * inter] = bits;
-          const float part = half_f32<TK>(bits);
-          v = __builtin_isfinite(part) ? v - part : 0.0f;  // exact: the remainder of the rounding
+          const float part = half_f32<PK>(bits);
+          v = __builtin_isfinite(part) ? (v - part) * plane_step<PK>() : 0.0f;  // exact: the remainder of the rounding
         }
       }
     }
@@ -335,18 +349,19 @@ struct UnitScales<kWFull, CT> {
 // The experts' outputs, as fp32 rows y for the tokens that each expert serves.
 // A wave owns CT tiles of 16 columns (KS = 1), or KS waves share them, each with
 // a run of the units of k.  Few experts serve many tokens, so the rows of the
-// matrix-core tile hold the planes of h: 16 / PS tokens, plane p in the rows from
-// p * (16 / PS), and one step multiplies all planes; an expert that serves more
+// matrix-core tile hold the planes of h: 4 tokens, plane p in the rows from 4 p
+// (the last plane twice), and one step multiplies all planes; an expert that serves more
 // tokens takes further workgroups (blockIdx.y), which read its weight again.
 // Bound by what a wave does per byte, not by memory alone: with the planes in
 // turn, h for 16 tokens and the waves splitting k, 16 of 256 experts (d = 5120,
 // inter = 896, 4 bits) took 130 to 170 us; so, 83 (3.5 TB/s).
-template <int TK, int WQ, int NP>
+template <int TK, int WQ>
 __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_down_kernel(MoeArgs a) {
   constexpr int CT = down_tiles<WQ>();
   constexpr int NB = unit_blocks<WQ>();
   constexpr int UL = unit_len<WQ>();
-  constexpr int PS = NP == 2 ? 2 : 4, TT = 16 / PS;  // rows for a token's planes, tokens
+  constexpr int TT = kMoeDownTokens;
+  constexpr int PK = plane_kind<TK, WQ>();
   constexpr int GU = WQ == kWFull ? 1 : 128 / (WQ == kWFull ? 1 : group_len<WQ>());
   __shared__ u32x4 turn_s[kMoeWaves][turn_slots<WQ, CT>() * 64];
   const int lane = threadIdx.x & 63;
@@ -378,7 +393,7 @@ __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_down_kernel(MoeArgs a) 
   // lane group l >> 2 reads row l >> 2: a plane of a token, or one that is read
   // anyway; this lane's four results' tokens follow
   int tk = 0;
-  int64_t yrow[4];
+  int64_t yrow[TT];
   {
     uint32_t left = mask;
     const int last = __builtin_ctz(mask);
@@ -387,21 +402,19 @@ __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_down_kernel(MoeArgs a) 
     for (int i = 0; i < TT; ++i) {
       const int t = left != 0 ? __builtin_ctz(left) : -1;
       if (t >= 0 && (lane >> 2) % TT == i) tk = t;
-      if (i / 4 == (lane >> 4) % (TT / 4)) {
-        const int rank = t < 0 || shared ? a.topk : a.slot_rank[slot * kGemvMaxM + t];
-        yrow[i % 4] = t < 0 ? -1 : ((int64_t)t * (a.topk + 1) + rank) * a.d;
-      }
+      const int rank = t < 0 || shared ? a.topk : a.slot_rank[slot * kGemvMaxM + t];
+      yrow[i] = t < 0 ? -1 : ((int64_t)t * (a.topk + 1) + rank) * a.d;
       left &= left - 1;
     }
   }
-  const int plane = min((lane >> 2) / TT, NP - 1);
+  const int plane = min((lane >> 2) / TT, kPlanes - 1);
 
   const WindowWeight& W = shared ? a.s2 : a.w2;
   const int64_t e0 = (int64_t)(entry & 0xffffu) * a.d;  // the expert's first column
   const uint32_t cbytes = (uint32_t)(WQ == kWFull ? k * 2 : k >> 1);
   const uint32_t coff = (uint32_t)(lane >> 2) * cbytes + 16 * (lane & 3);
-  const uint16_t* hbase = a.h + slot * (int64_t)(kGemvMaxM * NP) * a.inter;
-  const uint32_t hoff = (uint32_t)((tk * NP + plane) * k + 8 * (lane & 3));
+  const uint16_t* hbase = a.h + slot * (int64_t)(kGemvMaxM * kPlanes) * a.inter;
+  const uint32_t hoff = (uint32_t)((tk * kPlanes + plane) * k + 8 * (lane & 3));
   const int groups = k / (WQ == kWFull ? 1 : group_len<WQ>());
   const int col = 16 * ((lane >> 4) % CT) + row;
 
@@ -456,11 +469,11 @@ __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_down_kernel(MoeArgs a) 
       f32x4 acc[CT];
 #pragma unroll
       for (int c = 0; c < CT; ++c) acc[c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-      mul_unit<TK, WQ, CT, true, false>(q.w, sv, zv, q.a, acc, 0, 0);
+      mul_unit<PK, WQ, CT, true, false>(q.w, sv, zv, q.a, acc, 0, 0);
 #pragma unroll
       for (int c = 0; c < CT; ++c) tot[c] += acc[c];
     } else {
-      mul_unit<TK, WQ, CT, true, false>(q.w, sv, zv, q.a, tot, 0, 0);
+      mul_unit<PK, WQ, CT, true, false>(q.w, sv, zv, q.a, tot, 0, 0);
     }
     __builtin_amdgcn_sched_barrier(0);  // used up before it is loaded again: same registers, no copies
   };
@@ -498,26 +511,23 @@ __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_down_kernel(MoeArgs a) 
         for (int c = 0; c < CT; ++c) tot[c] += ((const f32x4*)turn_s[wave + w])[c * 64 + lane];
     }
   }
-  // the planes' sums: the groups of TT rows, in order
+  // the planes' sums, lane group h plane h's, to one
+  constexpr float down = 1.0f / plane_step<PK>();
 #pragma unroll
   for (int c = 0; c < CT; ++c)
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      float v = tot[c][q];
+      const float v = tot[c][q];
       auto s32 = __builtin_amdgcn_permlane32_swap(ubits(v), ubits(v), false, false);
-      if constexpr (PS == 2) {
-        v = fbits(s32[0]) + fbits(s32[1]);  // (lane groups h and h + 2)
-      } else {
-        auto lo = __builtin_amdgcn_permlane16_swap(s32[0], s32[0], false, false);  // planes 0 and 1
-        auto hi = __builtin_amdgcn_permlane16_swap(s32[1], s32[1], false, false);  // plane 2
-        v = (fbits(lo[0]) + fbits(lo[1])) + fbits(hi[0]);
-      }
-      tot[c][q] = v;
+      auto lo = __builtin_amdgcn_permlane16_swap(s32[0], s32[0], false, false);  // planes 0 and 1
+      auto hi = __builtin_amdgcn_permlane16_swap(s32[1], s32[1], false, false);  // plane 2
+      const float rest = __builtin_fmaf(down, fbits(hi[0]), fbits(lo[1]));
+      tot[c][q] = __builtin_fmaf(down, rest, fbits(lo[0])) * (1.0f / inner_scale<PK>());
     }
-  if (wave % KS == 0 && set < sets && lane < 16 * 4 / PS) {
+  if (wave % KS == 0 && set < sets && lane < 16) {
     float* y = a.y + (int64_t)set * (16 * CT) + row;
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
+    for (int q = 0; q < TT; ++q)
       if (yrow[q] >= 0) {
 #pragma unroll
         for (int c = 0; c < CT; ++c) y[yrow[q] + 16 * c] = tot[c][q];
@@ -526,7 +536,7 @@ __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_down_kernel(MoeArgs a) 
 }
 
 // out[t] = the sum of token t's experts' rows, largest logit first, then the
-// shared expert's; a thread adds four columns.  Twelve rows are fetched before
+// shared expert's, each times its weight; a thread adds four columns.  Twelve rows are fetched before
 // the first is added (loads past the last row repeat it), so the kernel waits
 // for memory once for up to twelve (1 of 64 experts, top 4: 2.4 us, and 2.7 row by
 // row; of the 4.6 us of 5 of 512 most is reading rows that other XCDs wrote).
@@ -536,15 +546,22 @@ __global__ __launch_bounds__(64) void moe_sum_kernel(MoeArgs a) {
   const int t = blockIdx.y;
   if (j >= a.d) return;
   const float* y = a.y + (int64_t)t * (a.topk + 1) * a.d + j;
+  const float* w = a.weights + t * (a.topk + 1);
   const int n = a.topk + (a.shared_inter > 0 ? 1 : 0);
   f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 1
   for (int i0 = 0; i0 < n; i0 += R) {
     f32x4 v[R];
+    float p[R];
 #pragma unroll
-    for (int i = 0; i < R; ++i) v[i] = *(const f32x4*)(y + (int64_t)min(i0 + i, n - 1) * a.d);
+    for (int i = 0; i < R; ++i) {
+      v[i] = *(const f32x4*)(y + (int64_t)min(i0 + i, n - 1) * a.d);
+      p[i] = w[min(i0 + i, n - 1)];
+    }
 #pragma unroll
-    for (int i = 0; i < R; ++i) sum = i0 + i < n ? sum + v[i] : sum;
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum[e] = i0 + i < n ? __builtin_fmaf(p[i], v[i][e], sum[e]) : sum[e];
   }
 #pragma unroll
   for (int e = 0; e < 4; ++e) store_kind(a.out, t * a.ldo + j + e, sum[e], a.out_kind);
@@ -561,32 +578,31 @@ moe_fn pick_route(int experts) {
                           : moe_route_kernel<TK, 16>;
 }
 
-template <int TK, int WQ, int NP>
+template <int TK, int WQ>
 moe_fn pick_stage(bool up, bool wide) {
-  return !up ? moe_down_kernel<TK, WQ, NP> : wide ? moe_up_kernel<TK, WQ, NP, 2> : moe_up_kernel<TK, WQ, NP, 1>;
+  return !up ? moe_down_kernel<TK, WQ> : wide ? moe_up_kernel<TK, WQ, 2> : moe_up_kernel<TK, WQ, 1>;
 }
 
-template <int TK, int NP>
+template <int TK>
 moe_fn pick_weight(int group, bool zeros, bool up, bool wide) {
   switch (group + (zeros ? kZeros : 0)) {
-    case 0: return pick_stage<TK, kWFull, NP>(up, wide);
-    case 32: return pick_stage<TK, 32, NP>(up, wide);
-    case 64: return pick_stage<TK, 64, NP>(up, wide);
-    case 128: return pick_stage<TK, 128, NP>(up, wide);
-    case 32 + kZeros: return pick_stage<TK, 32 + kZeros, NP>(up, wide);
-    case 64 + kZeros: return pick_stage<TK, 64 + kZeros, NP>(up, wide);
-    default: return pick_stage<TK, 128 + kZeros, NP>(up, wide);
+    case 0: return pick_stage<TK, kWFull>(up, wide);
+    case 32: return pick_stage<TK, 32>(up, wide);
+    case 64: return pick_stage<TK, 64>(up, wide);
+    case 128: return pick_stage<TK, 128>(up, wide);
+    case 32 + kZeros: return pick_stage<TK, 32 + kZeros>(up, wide);
+    case 64 + kZeros: return pick_stage<TK, 64 + kZeros>(up, wide);
+    default: return pick_stage<TK, 128 + kZeros>(up, wide);
   }
 }
 
 moe_fn pick(int kind, int group, bool zeros, bool up, bool wide) {
-  return kind == CK_F16 ? pick_weight<CK_F16, 2>(group, zeros, up, wide)
-                        : pick_weight<CK_BF16, 3>(group, zeros, up, wide);
+  return kind == CK_F16 ? pick_weight<CK_F16>(group, zeros, up, wide) : pick_weight<CK_BF16>(group, zeros, up, wide);
 }
 
 }  // namespace
 
-int moe_planes(int kind) { return kind == CK_BF16 ? 3 : 2; }
+int moe_planes() { return kPlanes; }
 
 hipError_t launch_moe(const MoeArgs& a, int kind, int group, hipStream_t stream) {
   if (a.m < 1 || a.m > kGemvMaxM || a.experts < 1 || a.experts > kMoeMaxExperts || a.topk < 1 ||
@@ -604,7 +620,6 @@ hipError_t launch_moe(const MoeArgs& a, int kind, int group, hipStream_t stream)
   // 280 (1 of 256 bf16) 42 / 49
   const bool wide = slots * (a.inter / 32) >= 2048;
   const int64_t tile = wide ? 32 : 16;
-  const int np = moe_planes(kind);
   const int64_t up_blocks = slots * (a.inter / tile) + a.shared_inter / tile;
   // the down product: as in its kernel
   const int unit = group == 0 ? unit_len<kWFull>() : unit_len<128>();
@@ -614,7 +629,7 @@ hipError_t launch_moe(const MoeArgs& a, int kind, int group, hipStream_t stream)
     return (sets + per - 1) / per;
   };
   const int64_t down_blocks = slots * blocks(a.inter) + (a.shared_inter > 0 ? blocks(a.shared_inter) : 0);
-  const int tokens = np == 2 ? 8 : 4;  // of a workgroup
+  const int tokens = kMoeDownTokens;
   if (up_blocks > 0x7fffffff || down_blocks > 0x7fffffff) return hipErrorInvalidValue;
   const bool zeros = a.w13.zeros != nullptr;
   const bool f16 = kind == CK_F16;

@@ -56,9 +56,8 @@ struct MoeArgs {
   const void* shared_gate; // [d]
   const float* logits;     // [m][experts]
   uint32_t* slots;         // distinct experts, ascending: expert | token mask << 16
-  float* slot_w;           // [max_slots][16]: each slot's routing weight per token it serves
-  int32_t* slot_rank;      // [max_slots][16]: and its place among the token's experts
-  float* gates;            // [16]: the shared expert's gates
+  int32_t* slot_rank;      // [max_slots][16]: each slot's place among the experts of a token it serves
+  float* weights;          // [m][topk + 1]: routing weights, the shared expert's gate last
   uint16_t* h;             // [max_slots][16][planes][inter], then [16][planes][shared_inter]
   float* y;                // [m][topk + 1][d]: the experts' outputs, the shared expert's last
   int32_t* topk_idx;       // [m][topk] or null
@@ -68,7 +67,7 @@ struct MoeArgs {
   int32_t m, experts, topk, renorm, max_slots, out_kind;
 };
 
-int moe_planes(int kind);  // 16-bit planes that hold one inner value
+int moe_planes();  // 16-bit planes that hold one inner value
 
 // kind: CK_F16 or CK_BF16; group: 0 (16-bit weights), 32, 64 or 128
 hipError_t launch_moe(const MoeArgs& args, int kind, int group, hipStream_t stream);

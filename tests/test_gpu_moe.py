@@ -84,11 +84,12 @@ def test_moe_output_types_and_plain_softmax(kind):
         Case(3, 40, 6, 256, 128, kind=kind, out=out, renorm=False, seed=8100).check()
 
 
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
 @pytest.mark.parametrize("group", [0, 128])
-def test_moe_16_bit_output_is_the_fp32_output_rounded(group):
+def test_moe_16_bit_output_is_the_fp32_output_rounded(group, kind):
     """The inner values lose no bit under a 16-bit output that they keep under
     fp32: the outputs are those of the fp32 layer, rounded once."""
-    kw = dict(shared=128, group=group, zeros=group > 0, kind="bf16", seed=8150)
+    kw = dict(shared=128, group=group, zeros=group > 0, kind=kind, seed=8150)
     _, _, wide = Case(16, 24, 4, 768, 256, out="f32", **kw).check()
     for out in ("bf16", "f16"):
         _, _, got = Case(16, 24, 4, 768, 256, out=out, **kw).check()
@@ -289,3 +290,67 @@ def test_moe_from_several_threads():
         t.join()
     torch.cuda.synchronize()
     assert all(torch.equal(o, w) for g, w in zip(got, want) for o in g)
+
+
+@pytest.mark.parametrize("kind,group", [("f16", 0), ("f16", 32), ("f16", 128), ("bf16", 0), ("bf16", 64)])
+def test_moe_inner_values_of_every_size(kind, group):
+    """Up rows times a power of two: the inner values and the outputs scale
+    with them, from about 2^-17 (k = -14) to past f16's 65504 (k = 17).  The
+    weights are small integers times a power of two, which every k leaves exact.
+    The outputs then differ by the sums' rounding alone: over the inner length
+    of 128 at most 160 additions of 2^-24 of the magnitudes, which are less than
+    16 times the largest output: 2^-12.6.  That is worst case; roundings of
+    either sign give its square root's share, and 2^-16 is asserted."""
+    rng = np.random.default_rng(9400)
+    E, d, n, topk = 6, 256, 128, 3
+
+    def grid(*shape):
+        return rng.integers(-7, 8, size=shape) * 2.0 ** -7
+
+    def weight(v, k):  # v * 2^k
+        if group == 0:
+            return to_dev(WL.to_bits(v * 2.0 ** k, kind), kind)
+        q = (v * 2.0 ** 7 + 8).astype(np.uint8)
+        codes = (q[..., 0::2] | (q[..., 1::2] << 4)).astype(np.uint8)
+        shape = (*v.shape[:-1], v.shape[-1] // group)
+        return sk.W4(to_dev(codes, "u8"), to_dev(WL.to_bits(np.broadcast_to(2.0 ** (k - 7.0), shape), kind), kind))
+
+    def stack(rows, k):  # gate rows as they are, up rows times 2^k
+        gate, up = rows[..., :n, :], rows[..., n:, :]
+        a, b = weight(gate, 0), weight(up, k)
+        if group == 0:
+            return torch.cat((a, b), dim=-2)
+        return sk.W4(torch.cat((a.codes, b.codes), dim=-2), torch.cat((a.scales, b.scales), dim=-2))
+
+    x = to_dev(WL.gen_matrix((5, d), kind, ("normal", 1.0), 9401), kind)
+    router = to_dev(WL.gen_matrix((E, d), kind, ("normal", 0.06), 9402), kind)
+    gate = to_dev(WL.gen_matrix((d,), kind, ("normal", 0.06), 9403), kind)
+    w13, w2, s13, s2 = grid(E, 2 * n, d), grid(E, d, n), grid(2 * n, d), grid(d, n)
+
+    def run(k):
+        layer = sk.MoELayer(router, stack(w13, k), weight(w2, 0), topk=topk, renorm=False, out_dtype=torch.float32,
+                            shared13=stack(s13, k), shared2=weight(s2, 0), shared_gate=gate)
+        return layer(x).double()
+
+    base = run(0)
+    for k in (-14, -10, -6, -2, 5, 11, 17):
+        off = (run(k) * 2.0 ** -k - base).abs().max() / base.abs().max()
+        print(f"moe {kind} group={group} k={k} off {float(off):.1e}", flush=True)
+        assert float(off) <= 2.0 ** -16
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("scale", [1.0, 1e-2, 1e-3])
+def test_moe_small_inputs(scale, kind):
+    """Inputs of 1e-2 and 1e-3 (the router's weight grows as they shrink, so the
+    routing stays the same) under a plain softmax and an fp32 output, in root mean
+    square against 64 bits.  A sum of n terms of either sign in fp32 is off by
+    about sqrt(n) * 2^-24 of its own size; 2 sqrt(d) + sqrt(inter) + 16 stands for
+    gate, up, down and the rest."""
+    c = Case(4, 64, 6, 768, 256, shared=128, kind=kind, out="f32", renorm=False, seed=9500)
+    c.x = WL.gen_matrix((4, 768), kind, ("normal", scale), 9501)
+    c.router = WL.gen_matrix((64, 768), kind, ("normal", 1.4 / np.sqrt(768) / scale), 9502)
+    got = c.layer()(c.dev(c.x)).double().cpu().numpy()
+    ref, _, _, _ = R.moe(c.x, c.router, c.w13, c.w2, 6, False, c.sh, kind, "f32")
+    off = np.sqrt(((got - ref) ** 2).mean() / (ref ** 2).mean())
+    assert off <= (2 * np.sqrt(768) + np.sqrt(256) + 16) * 2.0 ** -24
