@@ -177,8 +177,8 @@ skinny_status skinny_moe_plan_create(const skinny_moe_desc* desc, skinny_moe_pla
   p->slots = region(p->max_slots * 4);
   p->slot_rank = region(p->max_slots * kGemvMaxM * 4);
   p->weights = region(d.max_m * (d.topk + 1) * 4);
-  p->h = region((p->max_slots * d.inter + d.shared_inter) * kGemvMaxM * planes * 2);
-  p->y = region(d.max_m * (d.topk + 1) * d.d * 4);
+  p->h = region(d.max_m * (d.topk * d.inter + d.shared_inter) * planes * 2);
+  p->y = region(d.max_m * (d.topk + (d.shared_inter > 0 ? 1 : 0)) * d.d * 4);
   p->bytes = at;
   *out_plan = p;
   return SKINNY_OK;

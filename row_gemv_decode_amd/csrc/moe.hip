@@ -214,6 +214,10 @@ constexpr float inner_scale() { return PK == CK_F16 ? 0.25f : 1.0f; }
 template <int PK>
 constexpr float plane_step() { return PK == CK_F16 ? 2048.0f : 1.0f; }
 
+// Rows of h, kPlanes * inter long: token t's i-th expert's is row t * topk + i; the
+// shared expert's rows, one per token, lie after them.  The rows of y likewise.
+__device__ __forceinline__ int64_t shared_h(const MoeArgs& a) { return (int64_t)a.m * a.topk * kPlanes * a.inter; }
+
 // GT tiles of 16 columns of h: columns of w13 are the gate's 0 .. inter - 1,
 // then the up's
 template <int TK, int WQ, int GT>
@@ -252,14 +256,14 @@ __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_up_kernel(MoeArgs a) {
   if (wave < GT) {
     const f32x4 g = wave_sums(turn_s, wave, lane), up = wave_sums(turn_s, GT + wave, lane);
     constexpr int PK = plane_kind<TK, WQ>();
-    uint16_t* hb = a.h + (shared ? a.max_slots : slot) * (int64_t)(kGemvMaxM * kPlanes) * a.inter;
-    hb += 16 * (tile * GT + wave) + h_place<WQ>(lane & 15);
+    uint16_t* hb = a.h + (shared ? shared_h(a) : 0) + 16 * (tile * GT + wave) + h_place<WQ>(lane & 15);
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const int tk = 4 * h + q;
       if (tk < a.m && ((entry >> (16 + tk)) & 1u) != 0) {
         float v = g[q] / (1.0f + expf(-g[q])) * up[q] * inner_scale<PK>();
-        uint16_t* o = hb + (int64_t)tk * kPlanes * inter;
+        const int hrow = shared ? tk : tk * a.topk + a.slot_rank[slot * kGemvMaxM + tk];
+        uint16_t* o = hb + (int64_t)hrow * kPlanes * inter;
 #pragma unroll
         for (int i = 0; i < kPlanes; ++i) {
           const uint16_t bits = f32_half<PK>(v);
@@ -378,7 +382,7 @@ __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_down_kernel(MoeArgs a) 
   const int per = kMoeWaves / KS;  // sets of a workgroup
   const int blocks = (sets + per - 1) / per;
   const int b = (int)blockIdx.x - (shared ? 0 : blocks0);
-  const int slot = shared ? a.max_slots : b / blocks;  // (the shared expert's h lies after the slots')
+  const int slot = shared ? 0 : b / blocks;
   const uint32_t entry = shared ? 0xffff0000u : a.slots[slot];
   // the tokens of this workgroup: the TT served ones from blockIdx.y * TT on
   uint32_t mask = (entry >> 16) & ((1u << a.m) - 1);
@@ -392,18 +396,16 @@ __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_down_kernel(MoeArgs a) 
 
   // lane group l >> 2 reads row l >> 2: a plane of a token, or one that is read
   // anyway; this lane's four results' tokens follow
-  int tk = 0;
+  int hrow = 0;
   int64_t yrow[TT];
   {
     uint32_t left = mask;
-    const int last = __builtin_ctz(mask);
-    tk = last;
 #pragma unroll
     for (int i = 0; i < TT; ++i) {
       const int t = left != 0 ? __builtin_ctz(left) : -1;
-      if (t >= 0 && (lane >> 2) % TT == i) tk = t;
-      const int rank = t < 0 || shared ? a.topk : a.slot_rank[slot * kGemvMaxM + t];
-      yrow[i] = t < 0 ? -1 : ((int64_t)t * (a.topk + 1) + rank) * a.d;
+      const int own = t < 0 || shared ? t : t * a.topk + a.slot_rank[slot * kGemvMaxM + t];
+      if (i == 0 || (t >= 0 && (lane >> 2) % TT == i)) hrow = own;
+      yrow[i] = t < 0 ? -1 : (int64_t)(shared ? a.m * a.topk + own : own) * a.d;
       left &= left - 1;
     }
   }
@@ -413,8 +415,8 @@ __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_down_kernel(MoeArgs a) 
   const int64_t e0 = (int64_t)(entry & 0xffffu) * a.d;  // the expert's first column
   const uint32_t cbytes = (uint32_t)(WQ == kWFull ? k * 2 : k >> 1);
   const uint32_t coff = (uint32_t)(lane >> 2) * cbytes + 16 * (lane & 3);
-  const uint16_t* hbase = a.h + slot * (int64_t)(kGemvMaxM * kPlanes) * a.inter;
-  const uint32_t hoff = (uint32_t)((tk * kPlanes + plane) * k + 8 * (lane & 3));
+  const uint16_t* hbase = a.h + (shared ? shared_h(a) : 0);
+  const uint32_t hoff = (uint32_t)((hrow * kPlanes + plane) * k + 8 * (lane & 3));
   const int groups = k / (WQ == kWFull ? 1 : group_len<WQ>());
   const int col = 16 * ((lane >> 4) % CT) + row;
 
@@ -545,7 +547,8 @@ __global__ __launch_bounds__(64) void moe_sum_kernel(MoeArgs a) {
   const int64_t j = 4 * (int64_t)(blockIdx.x * 64 + threadIdx.x);
   const int t = blockIdx.y;
   if (j >= a.d) return;
-  const float* y = a.y + (int64_t)t * (a.topk + 1) * a.d + j;
+  const float* y = a.y + (int64_t)t * a.topk * a.d + j;
+  const float* ys = a.y + (int64_t)(a.m * a.topk + t) * a.d + j;  // the shared expert's
   const float* w = a.weights + t * (a.topk + 1);
   const int n = a.topk + (a.shared_inter > 0 ? 1 : 0);
   f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -555,8 +558,9 @@ __global__ __launch_bounds__(64) void moe_sum_kernel(MoeArgs a) {
     float p[R];
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      v[i] = *(const f32x4*)(y + (int64_t)min(i0 + i, n - 1) * a.d);
-      p[i] = w[min(i0 + i, n - 1)];
+      const int at = min(i0 + i, n - 1);
+      v[i] = *(const f32x4*)(at < a.topk ? y + (int64_t)at * a.d : ys);
+      p[i] = w[at];
     }
 #pragma unroll
     for (int i = 0; i < R; ++i)

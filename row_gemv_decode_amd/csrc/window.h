@@ -58,8 +58,8 @@ struct MoeArgs {
   uint32_t* slots;         // distinct experts, ascending: expert | token mask << 16
   int32_t* slot_rank;      // [max_slots][16]: each slot's place among the experts of a token it serves
   float* weights;          // [m][topk + 1]: routing weights, the shared expert's gate last
-  uint16_t* h;             // [max_slots][16][planes][inter], then [16][planes][shared_inter]
-  float* y;                // [m][topk + 1][d]: the experts' outputs, the shared expert's last
+  uint16_t* h;             // [m][topk][planes][inter], then [m][planes][shared_inter]
+  float* y;                // the experts' outputs, [m][topk][d], then the shared expert's, [m][d]
   int32_t* topk_idx;       // [m][topk] or null
   float* topk_weight;      // [m][topk] or null
   void* out;               // [m][ldo]

@@ -171,3 +171,18 @@ def test_logprobs_workspace_size():
     for bad in ((0, 10, 0), (1, 0, 0), (1, 10, 11), (1, 10, -1)):
         assert lib.skinny_token_logprobs_workspace_size(*bad, ctypes.byref(n)) == sk.ERR_INVALID_ARG
     assert lib.skinny_token_logprobs_workspace_size(1, 10, 0, None) == sk.ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("topk,experts,shared_inter", [(10, 256, 1792), (4, 64, 0), (32, 512, 1024)])
+def test_moe_workspace_holds_a_row_per_tokens_expert(topk, experts, shared_inter):
+    """The inner values and outputs of the m * topk rows that a window has (three
+    16-bit planes, and fp32), not of 16 rows for each expert that it may reach."""
+    d, inter, m = 5120, 896, 16
+    st, h = moe_create(d=d, inter=inter, topk=topk, experts=experts, shared_inter=shared_inter, w_dtype=sk.DTYPE_W4, group=128)
+    assert st == sk.OK
+    n = ctypes.c_size_t()
+    assert lib.skinny_moe_workspace_size(h, ctypes.byref(n)) == sk.OK
+    lib.skinny_moe_plan_destroy(h)
+    rows = m * (topk * (inter * 6 + d * 4) + (shared_inter * 6 + d * 4 if shared_inter else 0))
+    lists = m * experts * 4 + m * topk * 128  # logits, routing
+    assert rows <= n.value <= rows + lists + (1 << 14)
