@@ -83,7 +83,7 @@ struct skinny_moe_plan {
   int64_t max_slots;      // distinct experts a window can reach
   // workspace regions, in bytes from its start
   int64_t router_ws;      // the router plan's own workspace comes first (its counters start at zero)
-  int64_t logits, slots, slot_rank, weights, h, y, bytes;
+  int64_t logits, slots, slot_rank, parts, weights, h, y, bytes;
 };
 
 extern "C" {
@@ -176,6 +176,7 @@ skinny_status skinny_moe_plan_create(const skinny_moe_desc* desc, skinny_moe_pla
   p->logits = region(d.max_m * d.experts * 4);
   p->slots = region(p->max_slots * 4);
   p->slot_rank = region(p->max_slots * kGemvMaxM * 4);
+  p->parts = region(d.max_m * d.topk * 16);  // (at most one for each token's expert)
   p->weights = region(d.max_m * (d.topk + 1) * 4);
   p->h = region(d.max_m * (d.topk * d.inter + d.shared_inter) * planes * 2);
   p->y = region(d.max_m * (d.topk + (d.shared_inter > 0 ? 1 : 0)) * d.d * 4);
@@ -243,6 +244,7 @@ skinny_status skinny_moe_run(const skinny_moe_plan* plan, int64_t m, const void*
   a.logits = logits;
   a.slots = (uint32_t*)(base + plan->slots);
   a.slot_rank = (int32_t*)(base + plan->slot_rank);
+  a.parts = (uint32_t*)(base + plan->parts);
   a.weights = (float*)(base + plan->weights);
   a.h = (uint16_t*)(base + plan->h);
   a.y = (float*)(base + plan->y);

@@ -11,13 +11,13 @@
 // expert's down weight once per 4 tokens that it serves).
 //   moe_route_kernel  one workgroup, one wave per token: top-k, softmax and the
 //                     list of distinct experts in ascending order with each
-//                     one's tokens (a second workgroup: the shared expert's
-//                     gates)
+//                     one's tokens, whole and in parts of four (a second
+//                     workgroup: the shared expert's gates)
 //   moe_up_kernel     one workgroup per (distinct expert, 16 or 32 columns of
 //                     h): gate and up columns side by side against all rows of
 //                     x (a matrix-core tile holds 16 rows anyway, so tokens are
 //                     not gathered), silu in the epilogue
-//   moe_down_kernel   per distinct expert, the output rows of the tokens it serves
+//   moe_down_kernel   per distinct expert and part of its tokens, their output rows
 //   moe_sum_kernel    adds each token's rows, times p
 // h is kept as the sum of three 16-bit planes, multiplied in rows of the same
 // matrix-core step, which hold the 24 bits of fp32.  (With two planes in bf16, 3 in
@@ -65,7 +65,7 @@ __device__ __forceinline__ float wave_sum_f32(float v) {
 template <int TK, int NC>
 __global__ __launch_bounds__(1024) void moe_route_kernel(MoeArgs a) {
   __shared__ uint32_t mask[64 * NC];  // tokens of each expert
-  __shared__ int slot_of[64 * NC];
+  __shared__ int slot_of[64 * NC];      // its slot | its first part << 16
   const int tid = threadIdx.x;
   const int lane = tid & 63;
   const int t = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -146,23 +146,43 @@ __global__ __launch_bounds__(1024) void moe_route_kernel(MoeArgs a) {
   __syncthreads();
 
   if (t == 0) {  // the distinct experts, ascending
-    int n = 0;
-    for (int e0 = 0; e0 < E; e0 += 64) {
-      const int e = e0 + lane;
-      const uint32_t mk = e < E ? mask[e] : 0u;
+    int n = 0, np = 0;
+    uint32_t masks[NC];
+#pragma unroll
+    for (int u = 0; u < NC; ++u) masks[u] = lane + 64 * u < E ? mask[lane + 64 * u] : 0u;
+#pragma unroll
+    for (int u = 0; u < NC; ++u) {
+      const int e = lane + 64 * u;
+      const uint32_t mk = masks[u];
+      const uint64_t lower = (1ull << lane) - 1;
       const uint64_t b = __builtin_amdgcn_ballot_w64(mk != 0);
-      const int slot = n + __builtin_popcountll(b & ((1ull << lane) - 1));
+      const int slot = n + __builtin_popcountll(b & lower);
+      const int parts = (__builtin_popcount(mk) + kMoeDownTokens - 1) / kMoeDownTokens;  // at most 4
+      const uint64_t b1 = __builtin_amdgcn_ballot_w64((parts & 1) != 0);
+      const uint64_t b2 = __builtin_amdgcn_ballot_w64((parts & 2) != 0);
+      const uint64_t b4 = __builtin_amdgcn_ballot_w64((parts & 4) != 0);
+      const int part = np + __builtin_popcountll(b1 & lower) + 2 * __builtin_popcountll(b2 & lower) +
+                       4 * __builtin_popcountll(b4 & lower);
       if (mk != 0) {
-        slot_of[e] = slot;
+        slot_of[e] = slot | (part << 16);
         a.slots[slot] = (uint32_t)e | (mk << 16);
+        for (int q = 0, left = __builtin_popcount(mk); q < parts; ++q, left -= kMoeDownTokens)
+          a.parts[4 * (part + q)] = (uint32_t)e | ((uint32_t)min(left, kMoeDownTokens) << 16);
       }
       n += __builtin_popcountll(b);
+      np += __builtin_popcountll(b1) + 2 * __builtin_popcountll(b2) + 4 * __builtin_popcountll(b4);
     }
     for (int i = n + lane; i < a.max_slots; i += 64) a.slots[i] = 0;  // slots without a token
+    for (int i = np + lane; i < a.max_parts; i += 64) a.parts[4 * i] = 0;
   }
   __syncthreads();
-  // (read for the tokens in the slot's mask only)
-  if (lane < a.topk) a.slot_rank[slot_of[mine_e] * kGemvMaxM + t] = lane;
+  if (lane < a.topk) {
+    const int at = slot_of[mine_e];
+    a.slot_rank[(at & 0xffff) * kGemvMaxM + t] = lane;  // (read for the tokens in the slot's mask only)
+    const int place = __builtin_popcount(mask[mine_e] & ((1u << t) - 1));  // of the expert's tokens
+    uint32_t* part = a.parts + 4 * ((at >> 16) + place / kMoeDownTokens);
+    ((uint16_t*)(part + 1))[place % kMoeDownTokens] = (uint16_t)(t * a.topk + lane);
+  }
 }
 
 // where column i of h lies in memory: for 4-bit weights each run of eight is
@@ -354,8 +374,10 @@ struct UnitScales<kWFull, CT> {
 // A wave owns CT tiles of 16 columns (KS = 1), or KS waves share them, each with
 // a run of the units of k.  Few experts serve many tokens, so the rows of the
 // matrix-core tile hold the planes of h: 4 tokens, plane p in the rows from 4 p
-// (the last plane twice), and one step multiplies all planes; an expert that serves more
-// tokens takes further workgroups (blockIdx.y), which read its weight again.
+// (the last plane twice), and one step multiplies all planes.  An expert that serves
+// more tokens has further parts, which read its weight again.  The parts come as a
+// list: as further workgroups of every slot, most of which had no token, they took
+// 16 of 256 experts 20 us more.
 // Bound by what a wave does per byte, not by memory alone: with the planes in
 // turn, h for 16 tokens and the waves splitting k, 16 of 256 experts (d = 5120,
 // inter = 896, 4 bits) took 130 to 170 us; so, 83 (3.5 TB/s).
@@ -376,43 +398,45 @@ __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_down_kernel(MoeArgs a) 
   // the workgroup's expert and sets of columns; the shared expert's come first
   const int KS0 = a.shared_inter > 0 ? down_waves((int)((a.shared_inter + UL - 1) / UL), a.d, a.topk) : 1;
   const int per0 = kMoeWaves / KS0;
-  const int blocks0 = a.shared_inter > 0 ? (sets + per0 - 1) / per0 : 0;
+  const int blocks0 = a.shared_inter > 0 ? (a.m + TT - 1) / TT * ((sets + per0 - 1) / per0) : 0;
   const bool shared = (int)blockIdx.x < blocks0;
   const int KS = shared ? KS0 : down_waves((int)((a.inter + UL - 1) / UL), a.d, a.topk);
   const int per = kMoeWaves / KS;  // sets of a workgroup
   const int blocks = (sets + per - 1) / per;
+  // its part: the expert and its tokens' rows of h
   const int b = (int)blockIdx.x - (shared ? 0 : blocks0);
-  const int slot = shared ? 0 : b / blocks;
-  const uint32_t entry = shared ? 0xffff0000u : a.slots[slot];
-  // the tokens of this workgroup: the TT served ones from blockIdx.y * TT on
-  uint32_t mask = (entry >> 16) & ((1u << a.m) - 1);
-  for (int i = 0; i < (int)blockIdx.y * TT && mask != 0; ++i) mask &= mask - 1;
-  if (mask == 0) return;  // none, or a slot past the window's experts
-  const int set = (shared ? b : b - slot * blocks) * per + wave / KS;
+  const int part = b / blocks;
+  uint32_t expert = 0;
+  int tokens, hrows[TT];
+  if (shared) {  // (every token goes to the shared expert)
+    tokens = min(a.m - TT * part, TT);
+#pragma unroll
+    for (int i = 0; i < TT; ++i) hrows[i] = TT * part + i;
+  } else {
+    const u32x4 p = ((const u32x4*)a.parts)[part];
+    const uint32_t head = p[0], r01 = p[1], r23 = p[2];
+    expert = head & 0xffffu;
+    tokens = (int)(head >> 16);
+    if (tokens == 0) return;  // a part past the window's last
+    hrows[0] = (int)(r01 & 0xffffu);
+    hrows[1] = (int)(r01 >> 16);
+    hrows[2] = (int)(r23 & 0xffffu);
+    hrows[3] = (int)(r23 >> 16);
+  }
+  const int set = (b - part * blocks) * per + wave / KS;
   const int k = (int)(shared ? a.shared_inter : a.inter);
   const int units = (k + UL - 1) / UL;
   const int run = (units + KS - 1) / KS;  // every wave has a unit
   const int first = wave % KS * run, n = min(run, units - first);
 
-  // lane group l >> 2 reads row l >> 2: a plane of a token, or one that is read
-  // anyway; this lane's four results' tokens follow
-  int hrow = 0;
-  int64_t yrow[TT];
-  {
-    uint32_t left = mask;
+  // lane group l >> 2 reads row l >> 2: a plane of a token, or of the first one
+  int hrow = hrows[0];
 #pragma unroll
-    for (int i = 0; i < TT; ++i) {
-      const int t = left != 0 ? __builtin_ctz(left) : -1;
-      const int own = t < 0 || shared ? t : t * a.topk + a.slot_rank[slot * kGemvMaxM + t];
-      if (i == 0 || (t >= 0 && (lane >> 2) % TT == i)) hrow = own;
-      yrow[i] = t < 0 ? -1 : (int64_t)(shared ? a.m * a.topk + own : own) * a.d;
-      left &= left - 1;
-    }
-  }
+  for (int i = 1; i < TT; ++i) hrow = (lane >> 2) % TT == i && i < tokens ? hrows[i] : hrow;
   const int plane = min((lane >> 2) / TT, kPlanes - 1);
 
   const WindowWeight& W = shared ? a.s2 : a.w2;
-  const int64_t e0 = (int64_t)(entry & 0xffffu) * a.d;  // the expert's first column
+  const int64_t e0 = (int64_t)expert * a.d;  // the expert's first column
   const uint32_t cbytes = (uint32_t)(WQ == kWFull ? k * 2 : k >> 1);
   const uint32_t coff = (uint32_t)(lane >> 2) * cbytes + 16 * (lane & 3);
   const uint16_t* hbase = a.h + (shared ? shared_h(a) : 0);
@@ -527,12 +551,12 @@ __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_down_kernel(MoeArgs a) 
       tot[c][q] = __builtin_fmaf(down, rest, fbits(lo[0])) * (1.0f / inner_scale<PK>());
     }
   if (wave % KS == 0 && set < sets && lane < 16) {
-    float* y = a.y + (int64_t)set * (16 * CT) + row;
+    float* y = a.y + (shared ? (int64_t)a.m * a.topk * a.d : 0) + (int64_t)set * (16 * CT) + row;
 #pragma unroll
     for (int q = 0; q < TT; ++q)
-      if (yrow[q] >= 0) {
+      if (q < tokens) {
 #pragma unroll
-        for (int c = 0; c < CT; ++c) y[yrow[q] + 16 * c] = tot[c][q];
+        for (int c = 0; c < CT; ++c) y[(int64_t)hrows[q] * a.d + 16 * c] = tot[c][q];
       }
   }
 }
@@ -608,7 +632,8 @@ moe_fn pick(int kind, int group, bool zeros, bool up, bool wide) {
 
 int moe_planes() { return kPlanes; }
 
-hipError_t launch_moe(const MoeArgs& a, int kind, int group, hipStream_t stream) {
+hipError_t launch_moe(const MoeArgs& args, int kind, int group, hipStream_t stream) {
+  MoeArgs a = args;
   if (a.m < 1 || a.m > kGemvMaxM || a.experts < 1 || a.experts > kMoeMaxExperts || a.topk < 1 ||
       a.topk > SKINNY_TOPK_MAX || a.topk > a.experts || a.d % 32 != 0 || a.inter % 32 != 0 || a.shared_inter % 32 != 0 ||
       (group != 0 && group != 32 && group != 64 && group != 128) ||
@@ -617,6 +642,9 @@ hipError_t launch_moe(const MoeArgs& a, int kind, int group, hipStream_t stream)
     return hipErrorInvalidValue;
   const int64_t slots = (int64_t)a.m * a.topk < a.experts ? (int64_t)a.m * a.topk : a.experts;
   if (slots > a.max_slots || a.max_slots > kGemvMaxM * SKINNY_TOPK_MAX) return hipErrorInvalidValue;
+  // An expert of n tokens has (n + 3) / 4 <= (n + 3 slots) / 4 parts; one for n <= 4
+  static_assert(kMoeDownTokens == 4, "");
+  a.max_parts = (int32_t)(a.m <= 4 ? slots : ((int64_t)a.m * a.topk + 3 * slots) / 4);
   // Two column tiles of h per workgroup where that still leaves many workgroups:
   // the loads of x serve twice the columns (a column's arithmetic does not depend
   // on it).  Measured (us, one / two tiles; sets of 32 columns): 4480 (16 of 256
@@ -632,8 +660,8 @@ hipError_t launch_moe(const MoeArgs& a, int kind, int group, hipStream_t stream)
     const int per = kMoeWaves / down_waves((int)((inter + unit - 1) / unit), a.d, a.topk);
     return (sets + per - 1) / per;
   };
-  const int64_t down_blocks = slots * blocks(a.inter) + (a.shared_inter > 0 ? blocks(a.shared_inter) : 0);
-  const int tokens = kMoeDownTokens;
+  const int64_t shared_parts = a.shared_inter > 0 ? (a.m + kMoeDownTokens - 1) / kMoeDownTokens : 0;
+  const int64_t down_blocks = a.max_parts * blocks(a.inter) + (shared_parts > 0 ? shared_parts * blocks(a.shared_inter) : 0);
   if (up_blocks > 0x7fffffff || down_blocks > 0x7fffffff) return hipErrorInvalidValue;
   const bool zeros = a.w13.zeros != nullptr;
   const bool f16 = kind == CK_F16;
@@ -645,8 +673,7 @@ hipError_t launch_moe(const MoeArgs& a, int kind, int group, hipStream_t stream)
                      stream, a);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(pick(kind, group, zeros, false, false), dim3((unsigned)down_blocks, (unsigned)((a.m + tokens - 1) / tokens)), dim3(64 * kMoeWaves), 0,
-                     stream, a);
+  hipLaunchKernelGGL(pick(kind, group, zeros, false, false), dim3((unsigned)down_blocks), dim3(64 * kMoeWaves), 0, stream, a);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(moe_sum_kernel, dim3((unsigned)((a.d + 255) / 256), (unsigned)a.m), dim3(64), 0, stream, a);

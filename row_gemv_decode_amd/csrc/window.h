@@ -57,6 +57,7 @@ struct MoeArgs {
   const float* logits;     // [m][experts]
   uint32_t* slots;         // distinct experts, ascending: expert | token mask << 16
   int32_t* slot_rank;      // [max_slots][16]: each slot's place among the experts of a token it serves
+  uint32_t* parts;         // [max_parts][4]: expert | tokens << 16, their rows of h (16 bits each)
   float* weights;          // [m][topk + 1]: routing weights, the shared expert's gate last
   uint16_t* h;             // [m][topk][planes][inter], then [m][planes][shared_inter]
   float* y;                // the experts' outputs, [m][topk][d], then the shared expert's, [m][d]
@@ -65,6 +66,7 @@ struct MoeArgs {
   void* out;               // [m][ldo]
   int64_t ldo;
   int32_t m, experts, topk, renorm, max_slots, out_kind;
+  int32_t max_parts;       // (set by the launch)
 };
 
 int moe_planes();  // 16-bit planes that hold one inner value
