@@ -48,7 +48,8 @@ typedef struct skinny_w4 {
 } skinny_w4;
 
 /* C[0:m, 0:n] = A[0:m, :] . W for a decode window's rows and a 4-bit grouped
- * weight, in one launch that reads W once for all rows.  Products are exact
+ * weight, in one launch that reads W once for all rows (past 2^27 columns, one
+ * launch for each 2^27).  Products are exact
  * and summed in fp32, the group's scale is applied to its sum; row i of C at
  * any m equals the m = 1 call on that row bit for bit.
  *   m        1 <= m <= SKINNY_GEMV_MAX_M
@@ -90,7 +91,10 @@ SKINNY_API skinny_status skinny_w4_mm_run(int64_t m, int64_t n, int64_t k, int32
  *   out_dtype     SKINNY_F32, SKINNY_F16 or SKINNY_BF16
  *   max_m         1 .. SKINNY_GEMV_MAX_M
  *   d, inter, shared_inter   multiples of 32 (and of group), up to 2^20;
- *                 shared_inter 0: no shared expert
+ *                 shared_inter 0: no shared expert.  Together with max_m, topk and
+ *                 experts not so large that a launch would need more than 2^31
+ *                 threads, 8 for each inner value of a window's experts and 16
+ *                 for each of their outputs (else SKINNY_ERR_UNSUPPORTED)
  *   experts       topk .. SKINNY_MOE_MAX_EXPERTS; topk 1 .. SKINNY_TOPK_MAX
  *   ldx, ldo      row strides of x and out in elements, 0: d; ldx a multiple of 8
  *   flags         SKINNY_MOE_RENORM or 0
@@ -183,7 +187,7 @@ SKINNY_API skinny_status skinny_moe_run(const skinny_moe_plan* plan, int64_t m, 
  *                (may be NULL when that is 0); a completed run leaves it ready
  *                for the next, of any size it suffices for.  Two runs in
  *                flight at once must not share one.
- * All device pointers.  One launch. */
+ * All device pointers.  One launch (past 2^22 rows, one for each 2^22). */
 SKINNY_API skinny_status skinny_token_logprobs_workspace_size(int64_t m, int64_t vocab, int32_t topk, size_t* bytes);
 SKINNY_API skinny_status skinny_token_logprobs_run(int64_t m, int64_t vocab, const void* logits, int64_t ld,
                                                    int32_t dtype, const void* tokens, int32_t tokens64,

@@ -140,6 +140,15 @@ skinny_status skinny_moe_plan_create(const skinny_moe_desc* desc, skinny_moe_pla
     return SKINNY_ERR_SHAPE;
   if (d.ldx % 8 != 0) return SKINNY_ERR_ALIGNMENT;
 
+  MoeArgs sizes{};
+  sizes.m = (int32_t)d.max_m;
+  sizes.topk = d.topk;
+  sizes.experts = (int32_t)d.experts;
+  sizes.d = d.d;
+  sizes.inter = d.inter;
+  sizes.shared_inter = d.shared_inter;
+  if (!moe_fits(sizes, d.group)) return SKINNY_ERR_UNSUPPORTED;
+
   skinny_mm_desc r{};
   r.struct_size = sizeof(r);
   r.a_dtype = d.dtype;

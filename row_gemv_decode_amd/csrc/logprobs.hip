@@ -622,6 +622,26 @@ hipError_t launch_logprobs(const LogprobArgs& a, int x_kind, hipStream_t stream)
       a.m * a.segments > 0x7fffffff)
     return hipErrorInvalidValue;
   if (a.waves != 4 && a.waves != 8) return hipErrorInvalidValue;
+  constexpr int64_t most = kMaxLaunchThreads / (64 * 8);  // rows of a launch
+  if (a.m > most) {
+    if (a.segments != 1) return hipErrorInvalidValue;
+    LogprobArgs part = a;
+    for (int64_t r = 0; r < a.m; r += most) {
+      part.m = a.m - r < most ? a.m - r : most;
+      part.logits = (const char*)a.logits + r * a.ld * (x_kind == CK_F32 ? 4 : 2);
+      part.tokens = (const char*)a.tokens + r * (a.tokens64 ? 8 : 4);
+      part.logprob = a.logprob + r;
+      part.entropy = a.entropy + r;
+      part.rank = a.rank + r;
+      if (a.topk > 0) {
+        part.top_ids = a.top_ids + r * a.topk;
+        part.top_logprobs = a.top_logprobs + r * a.topk;
+      }
+      const hipError_t e = launch_logprobs(part, x_kind, stream);
+      if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+  }
   const bool eight = a.waves == 8;
   const auto fn = x_kind == CK_F32   ? (eight ? logprobs_kernel<CK_F32, 8> : logprobs_kernel<CK_F32, 4>)
                   : x_kind == CK_F16 ? (eight ? logprobs_kernel<CK_F16, 8> : logprobs_kernel<CK_F16, 4>)

@@ -632,6 +632,48 @@ moe_fn pick(int kind, int group, bool zeros, bool up, bool wide) {
 
 int moe_planes() { return kPlanes; }
 
+namespace {
+
+// workgroups of a layer's launches, and how many slots and parts they cover
+struct MoeGrid {
+  int64_t slots, parts, up, down;
+  bool wide;
+};
+
+MoeGrid moe_grid(const MoeArgs& a, int group) {
+  MoeGrid g;
+  const int64_t pairs = (int64_t)a.m * a.topk;
+  g.slots = pairs < a.experts ? pairs : a.experts;
+  // An expert of n tokens has (n + 3) / 4 parts: one for n <= 4, (n + 3 slots) / 4 in all at most
+  static_assert(kMoeDownTokens == 4, "");
+  g.parts = a.m <= 4 ? g.slots : (pairs + 3 * g.slots) / 4;
+  // Two column tiles of h per workgroup where that still leaves many workgroups:
+  // the loads of x serve twice the columns (a column's arithmetic does not depend
+  // on it).  Measured (us, one / two tiles; sets of 32 columns): 4480 (16 of 256
+  // experts) 154 / 146, 2048 (16 of 8, inter = 8192) 78 / 74, 1050 (5 of 512) 36 / 40,
+  // 280 (1 of 256 bf16) 42 / 49
+  g.wide = g.slots * (a.inter / 32) >= 2048;
+  const int64_t tile = g.wide ? 32 : 16;
+  g.up = g.slots * (a.inter / tile) + a.shared_inter / tile;
+  // the down product: as in its kernel
+  const int unit = group == 0 ? unit_len<kWFull>() : unit_len<128>();
+  const int64_t sets = a.d / 16 / (group == 0 ? down_tiles<kWFull>() : down_tiles<128>());
+  auto blocks = [&](int64_t inter) {
+    const int per = kMoeWaves / down_waves((int)((inter + unit - 1) / unit), a.d, a.topk);
+    return (sets + per - 1) / per;
+  };
+  g.down = g.parts * blocks(a.inter);
+  if (a.shared_inter > 0) g.down += (a.m + kMoeDownTokens - 1) / kMoeDownTokens * blocks(a.shared_inter);
+  return g;
+}
+
+}  // namespace
+
+bool moe_fits(const MoeArgs& args, int group) {
+  const MoeGrid g = moe_grid(args, group);
+  return (g.up > g.down ? g.up : g.down) * (64 * kMoeWaves) <= kMaxLaunchThreads;
+}
+
 hipError_t launch_moe(const MoeArgs& args, int kind, int group, hipStream_t stream) {
   MoeArgs a = args;
   if (a.m < 1 || a.m > kGemvMaxM || a.experts < 1 || a.experts > kMoeMaxExperts || a.topk < 1 ||
@@ -640,40 +682,19 @@ hipError_t launch_moe(const MoeArgs& args, int kind, int group, hipStream_t stre
       (group != 0 && (a.d % group != 0 || a.inter % group != 0 || a.shared_inter % group != 0)) ||
       (kind != CK_F16 && kind != CK_BF16))
     return hipErrorInvalidValue;
-  const int64_t slots = (int64_t)a.m * a.topk < a.experts ? (int64_t)a.m * a.topk : a.experts;
-  if (slots > a.max_slots || a.max_slots > kGemvMaxM * SKINNY_TOPK_MAX) return hipErrorInvalidValue;
-  // An expert of n tokens has (n + 3) / 4 <= (n + 3 slots) / 4 parts; one for n <= 4
-  static_assert(kMoeDownTokens == 4, "");
-  a.max_parts = (int32_t)(a.m <= 4 ? slots : ((int64_t)a.m * a.topk + 3 * slots) / 4);
-  // Two column tiles of h per workgroup where that still leaves many workgroups:
-  // the loads of x serve twice the columns (a column's arithmetic does not depend
-  // on it).  Measured (us, one / two tiles; sets of 32 columns): 4480 (16 of 256
-  // experts) 154 / 146, 2048 (16 of 8, inter = 8192) 78 / 74, 1050 (5 of 512) 36 / 40,
-  // 280 (1 of 256 bf16) 42 / 49
-  const bool wide = slots * (a.inter / 32) >= 2048;
-  const int64_t tile = wide ? 32 : 16;
-  const int64_t up_blocks = slots * (a.inter / tile) + a.shared_inter / tile;
-  // the down product: as in its kernel
-  const int unit = group == 0 ? unit_len<kWFull>() : unit_len<128>();
-  const int64_t sets = a.d / 16 / (group == 0 ? down_tiles<kWFull>() : down_tiles<128>());
-  auto blocks = [&](int64_t inter) {
-    const int per = kMoeWaves / down_waves((int)((inter + unit - 1) / unit), a.d, a.topk);
-    return (sets + per - 1) / per;
-  };
-  const int64_t shared_parts = a.shared_inter > 0 ? (a.m + kMoeDownTokens - 1) / kMoeDownTokens : 0;
-  const int64_t down_blocks = a.max_parts * blocks(a.inter) + (shared_parts > 0 ? shared_parts * blocks(a.shared_inter) : 0);
-  if (up_blocks > 0x7fffffff || down_blocks > 0x7fffffff) return hipErrorInvalidValue;
+  const MoeGrid g = moe_grid(a, group);
+  if (g.slots > a.max_slots || a.max_slots > kGemvMaxM * SKINNY_TOPK_MAX || !moe_fits(a, group)) return hipErrorInvalidValue;
+  a.max_parts = (int32_t)g.parts;
   const bool zeros = a.w13.zeros != nullptr;
   const bool f16 = kind == CK_F16;
   hipLaunchKernelGGL(f16 ? pick_route<CK_F16>(a.experts) : pick_route<CK_BF16>(a.experts),
                      dim3(a.shared_inter > 0 ? 2 : 1), dim3(64 * a.m), 0, stream, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(pick(kind, group, zeros, true, wide), dim3((unsigned)up_blocks), dim3(64 * kMoeWaves), 0,
-                     stream, a);
+  hipLaunchKernelGGL(pick(kind, group, zeros, true, g.wide), dim3((unsigned)g.up), dim3(64 * kMoeWaves), 0, stream, a);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(pick(kind, group, zeros, false, false), dim3((unsigned)down_blocks), dim3(64 * kMoeWaves), 0, stream, a);
+  hipLaunchKernelGGL(pick(kind, group, zeros, false, false), dim3((unsigned)g.down), dim3(64 * kMoeWaves), 0, stream, a);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(moe_sum_kernel, dim3((unsigned)((a.d + 255) / 256), (unsigned)a.m), dim3(64), 0, stream, a);

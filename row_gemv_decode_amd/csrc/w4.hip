@@ -75,6 +75,20 @@ hipError_t launch_w4_mm(const W4Args& args, int a_kind, int group, hipStream_t s
   if (args.m < 1 || args.m > kGemvMaxM || args.n < 1 || args.k < 32 || args.k % group != 0 || args.k > kW4MaxK ||
       (group != 32 && group != 64 && group != 128) || (a_kind != CK_F16 && a_kind != CK_BF16))
     return hipErrorInvalidValue;
+  constexpr int64_t most = kMaxLaunchThreads / (64 * kW4Waves) * 16;  // columns of a launch, by any rule below
+  if (args.n > most) {
+    W4Args part = args;
+    for (int64_t j = 0; j < args.n; j += most) {
+      part.n = args.n - j < most ? args.n - j : most;
+      part.w.codes = (const char*)args.w.codes + j * (args.k / 2);
+      part.w.scales = (const char*)args.w.scales + j * (args.k / group) * 2;
+      if (args.w.zeros != nullptr) part.w.zeros = (const char*)args.w.zeros + j * (args.k / group);
+      part.C = (char*)args.C + j * (args.c_kind == CK_F32 ? 4 : 2);
+      const hipError_t e = launch_w4_mm(part, a_kind, group, stream);
+      if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+  }
   const int64_t tiles = (args.n + 15) / 16;
   // Column tiles per wave: more tiles share the loads of A, fewer make more
   // workgroups.  Measured (us, 1 / 2 / 4 tiles): n x k = 512 x 2560 (m = 4, groups

@@ -15,6 +15,10 @@ namespace skinny {
 // kk/2, the low nibble for even kk), scales [n][k/group] in the rows' type,
 // zero points uint8 [n][k/group] or null (8): W = s * (q - z)
 // ---------------------------------------------------------------------------
+// A launch's grid counts its threads in 32 bits, and a larger one is cut off
+// without an error: larger work goes in several launches, or is refused.
+constexpr int64_t kMaxLaunchThreads = 1LL << 31;
+
 struct WindowWeight {     // 16-bit weights in `codes`, or a 4-bit grouped weight
   const void* codes;
   const void* scales;
@@ -70,6 +74,8 @@ struct MoeArgs {
 };
 
 int moe_planes();  // 16-bit planes that hold one inner value
+// whether the layer's launches fit a grid (for args.m, topk, experts, d, inter, shared_inter)
+bool moe_fits(const MoeArgs& args, int group);
 
 // kind: CK_F16 or CK_BF16; group: 0 (16-bit weights), 32, 64 or 128
 hipError_t launch_moe(const MoeArgs& args, int kind, int group, hipStream_t stream);

@@ -307,3 +307,23 @@ def test_lp_graph_outlives_the_streams_workspace():
         assert all(torch.equal(a, b) for a, b in zip(out, want))
         assert all(torch.equal(a, b) for e in eager for a, b in zip(e, bwant))
         assert all(bool((n == 1 + n.numel() % 100).all()) for n in near)
+
+
+def test_lp_more_rows_than_a_launch():
+    """Row counts at, past and far past a launch's 2^22 (2^24 rows of four waves
+    are 2^32 threads, which a grid does not hold): rows of one and of three
+    logits, the results by the formula."""
+    for m, V, kind in (((1 << 22) + 1, 3, "f16"), ((1 << 24) + 65, 1, "bf16"), ((1 << 23) + 3, 3, "f32")):
+        print(f"logprobs m={m} V={V} {kind}", flush=True)
+        g = torch.Generator(device="cuda").manual_seed(m)
+        x = torch.randint(-2, 3, (m, V), device="cuda", generator=g).to(DT[kind])
+        tok = torch.randint(0, V, (m,), device="cuda", generator=g, dtype=torch.int32)
+        got = sk.token_logprobs(x, tok, topk=1)
+        t = tok.long()[:, None]
+        lp = torch.log_softmax(x.double(), dim=1)
+        mine, before = x.gather(1, t), torch.arange(V, device="cuda")[None] < t
+        assert torch.equal(got.rank, (1 + ((x > mine) | ((x == mine) & before)).sum(1)).int())
+        assert torch.equal(got.top_ids[:, 0].long(), (x == x.amax(1, keepdim=True)).int().argmax(1))
+        # at most three terms: a few roundings of values below 6
+        assert float((got.logprob.double() - lp.gather(1, t)[:, 0]).abs().max()) <= 64 * 2.0 ** -24
+        assert float((got.entropy.double() + (lp.exp() * lp).sum(1)).abs().max()) <= 64 * 2.0 ** -24

@@ -200,3 +200,22 @@ def test_w4_rows_that_share_memory():
         sk.mm_w4(one, W, out=torch.zeros(300, device="cuda").expand(1, -1)[:, :299])
     with pytest.raises(ValueError):
         sk.mm_w4(one.expand(3, -1), W, out=torch.zeros(300, device="cuda").expand(3, -1))
+
+
+@pytest.mark.parametrize("n,zeros", [((1 << 27) + 5, True), ((1 << 28) + 1, False), ((1 << 30) + 65, False)])
+def test_w4_more_columns_than_a_launch(n, zeros):
+    """Column counts past a launch's 2^27, and past 2^32 threads in all.  One-hot
+    rows pick exact values, which are compared column by column."""
+    print(f"w4 n={n} zeros={zeros}", flush=True)
+    g = torch.Generator(device="cuda").manual_seed(n)
+    codes = torch.randint(0, 256, (n, 16), dtype=torch.uint8, device="cuda", generator=g)
+    scales = torch.randint(1, 9, (n, 1), dtype=torch.uint8, device="cuda", generator=g).to(torch.float16)
+    z = torch.randint(0, 16, (n, 1), dtype=torch.uint8, device="cuda", generator=g) if zeros else None
+    W = sk.W4(codes, scales, z)
+    A = torch.zeros((1, 32), dtype=torch.float16, device="cuda")
+    A[0, 21] = 1.0
+    got = sk.mm_w4(A, W, out_dtype=torch.float16)
+    for j in range(0, n, 1 << 26):
+        q = (codes[j:j + (1 << 26), 10] >> 4).to(torch.float16)
+        zz = 8.0 if z is None else z[j:j + (1 << 26), 0].to(torch.float16)
+        assert torch.equal(got[0, j:j + (1 << 26)], scales[j:j + (1 << 26), 0] * (q - zz))

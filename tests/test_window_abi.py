@@ -186,3 +186,18 @@ def test_moe_workspace_holds_a_row_per_tokens_expert(topk, experts, shared_inter
     rows = m * (topk * (inter * 6 + d * 4) + (shared_inter * 6 + d * 4 if shared_inter else 0))
     lists = m * experts * 4 + m * topk * 128  # logits, routing
     assert rows <= n.value <= rows + lists + (1 << 14)
+
+
+@pytest.mark.parametrize("kw,status", [
+    # 512 slots of 2^20 inner values: 2^29 / 32 workgroups of 256 threads
+    (dict(topk=32, experts=1024, d=32, inter=1 << 20, shared_inter=0), sk.ERR_UNSUPPORTED),
+    # 512 parts of 2^20 / 16 sets of columns, two sets per workgroup
+    (dict(topk=32, experts=1024, d=1 << 20, inter=576, shared_inter=0), sk.ERR_UNSUPPORTED),
+    (dict(topk=32, experts=256, d=32, inter=1 << 20, shared_inter=0), sk.OK),
+    (dict(topk=32, experts=1024, d=32, inter=1 << 20, shared_inter=0, max_m=8), sk.OK),
+])
+def test_moe_plan_refuses_launches_past_a_grid(kw, status):
+    """A grid counts threads in 32 bits; a larger launch would be cut off silently."""
+    st, h = moe_create(**kw)
+    assert st == status
+    lib.skinny_moe_plan_destroy(h)
