@@ -489,18 +489,7 @@ __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_down_kernel(MoeArgs a) 
     f32x4 sv[CT], zv[CT];
     q.s.template get<TK>(sv, zv, groups - u * GU);
     turn_unit<WQ, CT>(q.w, q.a, turn, lane);
-    if constexpr (WQ == kWFull) {
-      // (the matrix core's results are read in the straight line of code that
-      // forms them: for a read behind a branch the compiler has left out the wait)
-      f32x4 acc[CT];
-#pragma unroll
-      for (int c = 0; c < CT; ++c) acc[c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-      mul_unit<PK, WQ, CT, true, false>(q.w, sv, zv, q.a, acc, 0, 0);
-#pragma unroll
-      for (int c = 0; c < CT; ++c) tot[c] += acc[c];
-    } else {
-      mul_unit<PK, WQ, CT, true, false>(q.w, sv, zv, q.a, tot, 0, 0);
-    }
+    mul_unit<PK, WQ, CT, true, false>(q.w, sv, zv, q.a, tot, 0, 0);
     __builtin_amdgcn_sched_barrier(0);  // used up before it is loaded again: same registers, no copies
   };
   {

@@ -260,19 +260,28 @@ __device__ __forceinline__ void turn_unit(WUnit<WQ, CT>& w, u32x4 (&a)[unit_bloc
   for (int i = 0; i < NB; ++i)
     a[i] = group_len<WQ>() == 128 ? as[(lane >> 4) * 64 + Turn::entry(lane & 15, i)] : as[i * 64 + t.get];
 }
+
 // tot[c] += A(unit) . W(unit) for CT column tiles (kOrdered: A's elements are in
 // pair order already).  sv[c][g], zv[c][g]: the unit's group g's scale and
 // -(16 + zero point).
+//
+// The matrix core's sums are read (and added to tot by vector instructions) in the
+// straight line of code that forms them, with no branch between: a read behind a
+// branch or a loop's end needs a wait that a listing of an earlier form of these
+// kernels did not have on every path.
 template <int TK, int WQ, int CT, bool kOrdered, bool kPart>
 __device__ __forceinline__ void mul_unit(const WUnit<WQ, CT>& w, const f32x4 (&sv)[CT], const f32x4 (&zv)[CT],
                                          const u32x4 (&a)[unit_blocks<WQ>()], f32x4 (&tot)[CT], int u, int k) {
   if constexpr (WQ == kWFull) {
+    f32x4 acc[CT];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      if (kPart && u * 64 + 32 * i >= k) break;
+    for (int c = 0; c < CT; ++c) acc[c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int c = 0; c < CT; ++c) tot[c] = mfma16<TK>(a[i], w.v[c][i], tot[c]);
-    }
+    for (int i = 0; i < (kPart ? 1 : 2); ++i)  // (k is a multiple of 32: a partial unit is one block)
+#pragma unroll
+      for (int c = 0; c < CT; ++c) acc[c] = mfma16<TK>(a[i], w.v[c][i], acc[c]);
+#pragma unroll
+    for (int c = 0; c < CT; ++c) tot[c] += acc[c];
   } else {
     constexpr int NB = group_len<WQ>() / 32;  // blocks per group
     const CodeBits bits = code_bits<TK>();
