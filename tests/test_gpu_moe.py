@@ -354,3 +354,9 @@ def test_moe_small_inputs(scale, kind):
     ref, _, _, _ = R.moe(c.x, c.router, c.w13, c.w2, 6, False, c.sh, kind, "f32")
     off = np.sqrt(((got - ref) ** 2).mean() / (ref ** 2).mean())
     assert off <= (2 * np.sqrt(768) + np.sqrt(256) + 16) * 2.0 ** -24
+
+
+@pytest.mark.parametrize("d,inter,group", [(2592, 64, 32), (5184, 64, 64), (10496, 128, 128), (64, 5152, 32)])
+def test_moe_several_spans_of_scales(d, inter, group):
+    """Lengths of more than 80 groups: the up product stages its scales in spans."""
+    Case(5, 6, 2, d, inter, shared=group, group=group, zeros=True, kind="f16", seed=9600 + d).check()

@@ -219,3 +219,21 @@ def test_w4_more_columns_than_a_launch(n, zeros):
         q = (codes[j:j + (1 << 26), 10] >> 4).to(torch.float16)
         zz = 8.0 if z is None else z[j:j + (1 << 26), 0].to(torch.float16)
         assert torch.equal(got[0, j:j + (1 << 26)], scales[j:j + (1 << 26), 0] * (q - zz))
+
+
+@pytest.mark.parametrize("k,group", [(2592, 32), (4096, 32), (8192, 32), (5184, 64), (7680, 64), (10368, 128), (16384, 128)])
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+def test_w4_several_spans_of_scales(k, group, kind):
+    """A k of more than 80 groups, whose scales are staged in several spans (the
+    last of them short, the last unit partial): parity and row invariance at a
+    column tail, and the same bits in wide weights, whose waves take two and
+    four tiles of columns."""
+    A, W, got = check(16, 50, k, group, kind, "f32", True, 7900 + k)
+    check(3, 50, k, group, kind, "f32", False, 7901 + k)
+    for m in (1, 5):
+        assert torch.equal(sk.mm_w4(A[:m], W), got[:m])
+    for n in (5011, 24603):
+        reps = n // 50 + 1
+        wide = sk.W4(*(t.repeat(reps, 1)[:n].contiguous() for t in (W.codes, W.scales, W.zeros)))
+        full = sk.mm_w4(A[:3], wide)
+        assert torch.equal(full, got[:3].repeat(1, reps)[:, :n])
