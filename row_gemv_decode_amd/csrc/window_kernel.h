@@ -468,11 +468,14 @@ __device__ __forceinline__ void block_product(f32x4 (&tot)[CT], ScaleLds<WQ, CT>
   w_tiles<WQ, CT>(t, weight, j, k, cols, lane);
   const int groups = WQ == kWFull ? 0 : k / (WQ == kWFull ? 1 : group_len<WQ>());
   int span = k;
-  if constexpr (WQ != kWFull) {  // as few spans as hold k, of about one length, each for all waves
+  if constexpr (WQ != kWFull) {
+    // as few spans as hold k, of about one length, each for all waves and (but
+    // for the last) of whole pieces of 8 groups
     constexpr int most = kSpanGroups * group_len<WQ>() / UL;
-    static_assert(most % NW == 0, "");
+    constexpr int step = NW * GU % 8 == 0 ? NW : 8 / GU;
+    static_assert(most % step == 0 && step % NW == 0, "");
     const int units = (k + UL - 1) / UL, spans = (units + most - 1) / most;
-    span = (((units + spans - 1) / spans + NW - 1) / NW * NW) * UL;
+    span = (((units + spans - 1) / spans + step - 1) / step * step) * UL;
   }
 #pragma unroll 1
   for (int k0 = 0; k0 < k; k0 += span) {
@@ -482,7 +485,7 @@ __device__ __forceinline__ void block_product(f32x4 (&tot)[CT], ScaleLds<WQ, CT>
     const int first = min(u0 + wave * per, full);
     const int n = min(u0 + wave * per + per, full) - first;
     const bool part = end % UL != 0 && (full - u0) / per == wave;
-    const int g0 = u0 * GU, ng = min(kSpanGroups, groups - g0);
+    const int g0 = u0 * GU, ng = min(span / UL * GU, groups - g0);  // the span's own groups
     const int row = min(lane & 15, cols - 1) * scale_stride(ng) - g0;
 
     WUnit<WQ, CT> w0, w1;
