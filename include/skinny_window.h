@@ -52,6 +52,11 @@ typedef struct skinny_w4 {
  * launch for each 2^27).  Products are exact
  * and summed in fp32, the group's scale is applied to its sum; row i of C at
  * any m equals the m = 1 call on that row bit for bit.
+ *   A group's sum is the difference of sum (16 + code) a and (16 + zero) sum a,
+ * so C is off by at most (group + k/group + 10) 2^-24 times the sum over k of
+ * |scale| (32 + code + zero) |a|.  In root mean square that is 0.3 to 1.5 times
+ * the error of an fp32 product of the same numbers (k = 2560; rows of mean 0,
+ * of mean 4, and with one element of 1000).
  *   m        1 <= m <= SKINNY_GEMV_MAX_M
  *   n, k     1 <= n < 2^31; k a multiple of group, up to 2^24
  *   A        [m][lda] SKINNY_F16 or SKINNY_BF16 (a_dtype); lda >= k a multiple

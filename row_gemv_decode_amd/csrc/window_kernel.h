@@ -26,6 +26,9 @@
 //     constant 1 as weight, sa = sum a, both exact products added in fp32; the
 //     group's contribution is s * (acc - (16 + z) * sa) in fp32.  So no weight
 //     is rounded, and the correction costs one MFMA per block for all columns.
+//     Both parts are some 5 times the difference for rows of mean 0, and more for
+//     rows with a mean, which costs their sums' roundings no more than 1.5 times
+//     the error of an fp32 product (the entry point states the bound).
 //     Against subtracting the zero point from every code this takes one VALU
 //     instruction per weight instead of two or more.
 #pragma once

@@ -237,3 +237,37 @@ def test_w4_several_spans_of_scales(k, group, kind):
         wide = sk.W4(*(t.repeat(reps, 1)[:n].contiguous() for t in (W.codes, W.scales, W.zeros)))
         full = sk.mm_w4(A[:3], wide)
         assert torch.equal(full, got[:3].repeat(1, reps)[:, :n])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("group", [32, 128])
+@pytest.mark.parametrize("rows", ["centred", "offset", "outlier"])
+@pytest.mark.parametrize("zeros", [True, False])
+def test_w4_cancellation(zeros, rows, group, kind):
+    """A group's sum is a difference: sum (16 + q) a - (16 + z) sum a, whose
+    parts are some 5 times the result for centred rows and more for rows with a
+    mean.  At most `group` additions form each part; an addition rounds by at
+    most 2^-24 of what it has added up, 1/sqrt(3) of that in root mean square,
+    and the sum so far is 1/sqrt(3) of the last one where it grows evenly.  So
+    the error's root mean square is at most sqrt(2 group) * 2^-24 / 3 * the
+    part's magnitudes, squared and added over the groups, next to the adding up
+    of the groups: as much again."""
+    m, n, k = 4, 300, 2560
+    rng = np.random.default_rng(8000)
+    v = rng.normal(0.0, 1.0, size=(m, k))
+    if rows == "offset":
+        v += 4.0
+    if rows == "outlier":
+        v[:, 1234] = 1000.0
+    a, w = WL.to_bits(v, kind), R.gen_w4((n, k), group, kind, zeros, 8001)
+    got = sk.mm_w4(to_dev(a, kind), dev_w4(w, kind)).double().cpu().numpy()
+    q, s, z = R.w4_parts(w, kind)
+    A = R.f64(a, kind)
+    ref = A @ (s * (q - z)).T
+    part = (np.abs(A)[:, None, :] * (np.abs(s) * (16.0 + np.maximum(q, z)))[None]).reshape(m, n, k // group, group).sum(-1)
+    most = np.sqrt(2 * group) * 2.0 ** -24 / 3 * np.sqrt((part ** 2).sum(-1))
+    off = np.sqrt(((got - ref) ** 2).mean())
+    plain = (torch.from_numpy(A).float() @ torch.from_numpy(s * (q - z)).float().T).double().numpy()
+    off32 = np.sqrt(((plain - ref) ** 2).mean())
+    print(f"w4 {rows} group={group} zeros={zeros} {kind}: off {off:.2e}, in fp32 {off32:.2e}, outputs {np.sqrt((ref ** 2).mean()):.2e}", flush=True)
+    assert off <= 2 * np.sqrt((most ** 2).mean())
