@@ -105,32 +105,10 @@ __device__ __forceinline__ void rebase(Soft& a, float to) {
   a.m = to;
 }
 
-__device__ __forceinline__ float wave_max_f32(float v) {
-  v = fmaxf(v, dpp_mov<kDppXor1>(v));
-  v = fmaxf(v, dpp_mov<kDppXor2>(v));
-  v = fmaxf(v, dpp_mov<kDppRowHalfMirror>(v));
-  v = fmaxf(v, dpp_mov<kDppRowMirror>(v));
-  auto r16 = __builtin_amdgcn_permlane16_swap(ubits(v), ubits(v), false, false);
-  v = fmaxf(fbits(r16[0]), fbits(r16[1]));
-  auto r32 = __builtin_amdgcn_permlane32_swap(ubits(v), ubits(v), false, false);
-  return fmaxf(fbits(r32[0]), fbits(r32[1]));
-}
-
-__device__ __forceinline__ float wave_sum(float v) {
-  v += dpp_mov<kDppXor1>(v);
-  v += dpp_mov<kDppXor2>(v);
-  v += dpp_mov<kDppRowHalfMirror>(v);
-  v += dpp_mov<kDppRowMirror>(v);
-  auto r16 = __builtin_amdgcn_permlane16_swap(ubits(v), ubits(v), false, false);
-  v = fbits(r16[0]) + fbits(r16[1]);
-  auto r32 = __builtin_amdgcn_permlane32_swap(ubits(v), ubits(v), false, false);
-  return fbits(r32[0]) + fbits(r32[1]);
-}
-
 __device__ __forceinline__ Soft wave_join(Soft a) {
   rebase(a, wave_max_f32(a.m));
-  a.s = wave_sum(a.s);
-  a.u = wave_sum(a.u);
+  a.s = wave_sum_f32(a.s);
+  a.u = wave_sum_f32(a.u);
   return a;
 }
 
@@ -241,11 +219,6 @@ struct Pending {
   uint64_t* e;
   int n;
 };
-
-__device__ __forceinline__ void wave_lds_order() {  // LDS writes of the wave before its later reads, and the reverse
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-}
 
 __device__ __forceinline__ void list_flush(List& l, Pending& p, int topk, int lane) {
   wave_lds_order();

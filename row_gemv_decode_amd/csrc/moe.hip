@@ -46,17 +46,6 @@ namespace {
 constexpr int kMoeWaves = 4;
 constexpr int kMoeDownTokens = 4;  // of a workgroup of the down product: 16 rows hold their planes
 
-__device__ __forceinline__ float wave_sum_f32(float v) {
-  v += dpp_mov<kDppXor1>(v);
-  v += dpp_mov<kDppXor2>(v);
-  v += dpp_mov<kDppRowHalfMirror>(v);
-  v += dpp_mov<kDppRowMirror>(v);
-  auto r16 = __builtin_amdgcn_permlane16_swap(ubits(v), ubits(v), false, false);
-  v = fbits(r16[0]) + fbits(r16[1]);
-  auto r32 = __builtin_amdgcn_permlane32_swap(ubits(v), ubits(v), false, false);
-  return fbits(r32[0]) + fbits(r32[1]);
-}
-
 // Workgroup 0, one wave per token: each round of the top-k takes the largest
 // remaining order key of the row (ties: the lowest column); lane i keeps the
 // i-th winner.  The softmax sums in a fixed order: over the winners lane by

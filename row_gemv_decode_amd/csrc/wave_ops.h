@@ -69,6 +69,35 @@ __device__ __forceinline__ int wave_min_i32(int v) {
   return v;
 }
 
+__device__ __forceinline__ float wave_max_f32(float v) {
+  v = fmaxf(v, dpp_mov<kDppXor1>(v));
+  v = fmaxf(v, dpp_mov<kDppXor2>(v));
+  v = fmaxf(v, dpp_mov<kDppRowHalfMirror>(v));
+  v = fmaxf(v, dpp_mov<kDppRowMirror>(v));
+  auto r16 = __builtin_amdgcn_permlane16_swap(ubits(v), ubits(v), false, false);
+  v = fmaxf(fbits(r16[0]), fbits(r16[1]));
+  auto r32 = __builtin_amdgcn_permlane32_swap(ubits(v), ubits(v), false, false);
+  return fmaxf(fbits(r32[0]), fbits(r32[1]));
+}
+
+__device__ __forceinline__ float wave_sum_f32(float v) {
+  v += dpp_mov<kDppXor1>(v);
+  v += dpp_mov<kDppXor2>(v);
+  v += dpp_mov<kDppRowHalfMirror>(v);
+  v += dpp_mov<kDppRowMirror>(v);
+  auto r16 = __builtin_amdgcn_permlane16_swap(ubits(v), ubits(v), false, false);
+  v = fbits(r16[0]) + fbits(r16[1]);
+  auto r32 = __builtin_amdgcn_permlane32_swap(ubits(v), ubits(v), false, false);
+  return fbits(r32[0]) + fbits(r32[1]);
+}
+
+// order of a wave's LDS writes and its later reads by other lanes (the LDS
+// works in order; this keeps the compiler from moving them)
+__device__ __forceinline__ void wave_lds_order() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
 }  // namespace
 
 }  // namespace skinny

@@ -34,6 +34,7 @@
 #pragma once
 
 #include "device_common.h"
+#include "wave_ops.h"
 #include "window.h"
 
 namespace skinny {
@@ -160,13 +161,6 @@ __device__ __forceinline__ void lds_barrier() {
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
   __builtin_amdgcn_s_barrier();
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
-}
-
-// order of a wave's LDS writes and its later reads by other lanes (the LDS
-// works in order; this keeps the compiler from moving them)
-__device__ __forceinline__ void wave_lds_order() {
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  __builtin_amdgcn_wave_barrier();
 }
 
 // A weight matrix as a wave sees it: CT tiles of 16 consecutive columns, each
