@@ -1,8 +1,9 @@
 // gemv.hip -- the per-row top-k launch, the standalone block dequants and the
 // GEMV launch dispatch, for gfx950 (MI355X).  The GEMV kernel itself is in
 // gemv_kernel.h.
-#include "gemv_kernel.h"
+#include "internal.h"
 #include "skinny.h"
+#include "wave_ops.h"
 
 namespace skinny {
 
@@ -38,41 +39,6 @@ namespace {
 // the t-th winner, so the results leave in one coalesced store.
 // Generic path (larger n): each round rescans the row.
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ int order_key(float x) {
-  uint32_t b = ubits(x);
-  if (b == 0x80000000u) b = 0u;  // -0 ranks with +0
-  return (int)(b ^ ((uint32_t)((int)b >> 31) & 0x7fffffffu));
-}
-
-template <int CTRL>
-__device__ __forceinline__ int dpp_mov_i(int x) {
-  return (int)__builtin_amdgcn_update_dpp(0u, (uint32_t)x, CTRL, 0xF, 0xF, false);
-}
-
-__device__ __forceinline__ int wave_max_i32(int v) {
-  v = max(v, dpp_mov_i<kDppXor1>(v));
-  v = max(v, dpp_mov_i<kDppXor2>(v));
-  v = max(v, dpp_mov_i<kDppRowHalfMirror>(v));
-  v = max(v, dpp_mov_i<kDppRowMirror>(v));
-  auto r16 = __builtin_amdgcn_permlane16_swap((uint32_t)v, (uint32_t)v, false, false);
-  v = max((int)r16[0], (int)r16[1]);
-  auto r32 = __builtin_amdgcn_permlane32_swap((uint32_t)v, (uint32_t)v, false, false);
-  v = max((int)r32[0], (int)r32[1]);
-  return v;
-}
-
-__device__ __forceinline__ int wave_min_i32(int v) {
-  v = min(v, dpp_mov_i<kDppXor1>(v));
-  v = min(v, dpp_mov_i<kDppXor2>(v));
-  v = min(v, dpp_mov_i<kDppRowHalfMirror>(v));
-  v = min(v, dpp_mov_i<kDppRowMirror>(v));
-  auto r16 = __builtin_amdgcn_permlane16_swap((uint32_t)v, (uint32_t)v, false, false);
-  v = min((int)r16[0], (int)r16[1]);
-  auto r32 = __builtin_amdgcn_permlane32_swap((uint32_t)v, (uint32_t)v, false, false);
-  v = min((int)r32[0], (int)r32[1]);
-  return v;
-}
-
 // (key, j) comes after (pkey, pj) in the order above
 __device__ __forceinline__ bool after(int key, int j, int pkey, int pj) {
   return key < pkey || (key == pkey && j > pj);
@@ -80,11 +46,6 @@ __device__ __forceinline__ bool after(int key, int j, int pkey, int pj) {
 
 constexpr int kNoColumn = 0x7fffffff;
 constexpr int kNoKey = (int)0x80000000;  // below every non-NaN value's key
-
-// the float whose order key is `key` (-0 comes back as +0)
-__device__ __forceinline__ float key_value(int key) {
-  return fbits((uint32_t)key ^ ((uint32_t)(key >> 31) & 0x7fffffffu));
-}
 
 // TK > 0: topk is TK, known at compile time (the fast pass unrolls); 0: runtime
 template <int NC, int TK>

@@ -1,7 +1,6 @@
 // gemv_kernel.h -- the multi-row GEMV kernel for gfx950 (MI355X), included by
 // gemv_inst.hip (compiled once per weight kind, A kind and T, so the
-// instantiations build in parallel) and by gemv.hip for the shared wave
-// helpers.
+// instantiations build in parallel).
 //
 // What is computed (the pages print no code for any of it):
 //   C[r][j] = sum_kk A[r][kk] * W[j][kk] for r < m <= 16, W stored [n][k]
@@ -34,6 +33,7 @@
 
 #include "device_common.h"
 #include "internal.h"
+#include "wave_ops.h"
 
 namespace skinny {
 
@@ -53,21 +53,6 @@ struct GemvShape {
   static constexpr int P2 = next_pow2(P);
   static constexpr int LV = ctz_pow2(P2);  // transposed levels (<= 6)
 };
-
-__device__ __forceinline__ float fbits(uint32_t u) { return __builtin_bit_cast(float, u); }
-__device__ __forceinline__ uint32_t ubits(float f) { return __builtin_bit_cast(uint32_t, f); }
-
-template <int CTRL>
-__device__ __forceinline__ float dpp_mov(float x) {
-  return fbits(__builtin_amdgcn_update_dpp(0u, ubits(x), CTRL, 0xF, 0xF, false));
-}
-
-// DPP controls: row_mirror (l ^ 15 in a row of 16), row_half_mirror (l ^ 7),
-// quad_perm [2,3,0,1] (l ^ 2), quad_perm [1,0,3,2] (l ^ 1)
-constexpr int kDppRowMirror = 0x140;
-constexpr int kDppRowHalfMirror = 0x141;
-constexpr int kDppXor2 = 0x4E;
-constexpr int kDppXor1 = 0xB1;
 
 // level L of the fixed tree: partner lane and the lane bit that picks the kept half
 template <int L>

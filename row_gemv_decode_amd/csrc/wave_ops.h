@@ -1,8 +1,6 @@
 // wave_ops.h -- reductions over the 64 lanes of a wavefront by DPP and
-// permlane exchanges, and the order keys of a top-k, for the decode window's
-// operators (gfx950).  The router GEMV and its top-k have their own in
-// gemv_kernel.h and gemv.hip: the measured traffic of that kernel names its
-// sources by their hash, so they stay as they are.
+// permlane exchanges, and the order keys of a top-k, shared by the library's
+// kernels (gfx950).
 #pragma once
 
 #include "device_common.h"
