@@ -91,11 +91,25 @@ hipError_t launch_w4_mm(const W4Args& args, int a_kind, int group, hipStream_t s
   }
   const int64_t tiles = (args.n + 15) / 16;
   // Column tiles per wave: more tiles share the loads of A, fewer make more
-  // workgroups.  Measured (us, 1 / 2 / 4 tiles): n x k = 512 x 2560 (m = 4, groups
-  // of 64) 5.7 / 6.8 / 9.3; 4864 x 896 (m = 1, 32) 4.8 / 5.1 / 6.6; 5120 x 5120 (m = 1,
-  // 128) 10.5 / 10.1 / 14.2; 7680 x 2560 (m = 16, 128) 8.5 / 8.5 / 10.8; 32000 x 4096
-  // (m = 16, 32) 33 / 31 / 29; 100003 x 5120 (m = 16, 128) 107 / 84 / 80
-  const int ct = tiles >= 1536 ? 4 : tiles >= 312 ? 2 : 1;
+  // workgroups.  About three workgroups of one tile are resident per CU, three of
+  // two and two of four, so: four tiles where their workgroups make one nearly full
+  // round; two where one-tile workgroups would need a second round, or, for groups
+  // of 128 (the least work per unit), where the two-tile ones are one per CU at
+  // most.  Measured (us on the device, 1 / 2 / 4 tiles):
+  //   tiles 304   k 5120 g 128 m 16  12.3 / 11.3 / 15.0   k 4096 g 32 m 4  11.3 / 11.7 / 17.2
+  //         480                      12.4 / 11.4 / 14.6                    11.8 / 12.3 / 17.3
+  //         768                      17.1 / 16.5 / 16.0                    14.2 / 15.8 / 17.9
+  //         1024                     23.9 / 17.6 / 17.1                    16.7 / 16.4 / 19.0
+  //         1536                     30.1 / 22.9 / 24.7                    24.2 / 20.0 / 24.8
+  //         1664                     33.5 / 28.5 / 25.3  (m 16, as below)  28.2 / 27.1 / 25.4
+  //         2000                     37.9 / 29.7 / 26.1                    32.6 / 28.2 / 26.1
+  //         2250                     42.3 / 33.7 / 34.8                    36.2 / 31.8 / 38.0
+  //         6250                     107 / 79.9 / 76.7                     89.7 / 74.2 / 78.3
+  //   k 896 g 32 m 1: 304 4.8 / 5.1 / 6.6, 1536 9.2 / 8.2 / 10.1, 2000 10.5 / 10.2 / 10.8
+  // Over 148 random shapes the rule loses 0.3 % to the best of the three.
+  const int ct = args.k >= 2048 && tiles >= 1640 && tiles <= 2048            ? 4
+                 : tiles > 768 || (group == 128 && tiles > 256 && tiles <= 512) ? 2
+                                                                               : 1;
   const w4_fn fn = args.w.zeros == nullptr
                        ? (a_kind == CK_F16 ? w4_pick<CK_F16, 0>(group, ct) : w4_pick<CK_BF16, 0>(group, ct))
                        : (a_kind == CK_F16 ? w4_pick<CK_F16, kZeros>(group, ct) : w4_pick<CK_BF16, kZeros>(group, ct));

@@ -271,3 +271,15 @@ def test_w4_cancellation(zeros, rows, group, kind):
     off32 = np.sqrt(((plain - ref) ** 2).mean())
     print(f"w4 {rows} group={group} zeros={zeros} {kind}: off {off:.2e}, in fp32 {off32:.2e}, outputs {np.sqrt((ref ** 2).mean()):.2e}", flush=True)
     assert off <= 2 * np.sqrt((most ** 2).mean())
+
+
+@pytest.mark.parametrize("k,group", [(2048, 128), (2080, 32), (2112, 64), (5152, 32)])
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+def test_w4_bits_do_not_depend_on_the_tiles(k, group, kind):
+    """Column counts on both sides of every step of the tile choice, ends inside
+    a workgroup's tiles among them: the columns' bits are those of a narrow call."""
+    A, W, got = check(7, 50, k, group, kind, "f32", True, 8100 + k)
+    for n in (16 * 256, 16 * 256 + 1, 16 * 512 + 1, 16 * 768, 16 * 768 + 9, 16 * 1639, 16 * 1639 + 1, 26297, 32765, 16 * 2048 + 1):
+        reps = n // 50 + 1
+        wide = sk.W4(*(t.repeat(reps, 1)[:n].contiguous() for t in (W.codes, W.scales, W.zeros)))
+        assert torch.equal(sk.mm_w4(A, wide), got.repeat(1, reps)[:, :n])
