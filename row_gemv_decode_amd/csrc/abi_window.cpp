@@ -39,23 +39,33 @@ int64_t round256(int64_t b) { return (b + 255) / 256 * 256; }
 
 // Workgroups per row of the log probabilities: as many as give four workgroups of
 // four waves per CU of 256, but at most 16 (which cuts a window's rows alike at
-// every m), each of at least 4096 logits; from 256 rows on a row is one
-// workgroup's, of eight waves up to 1023 rows and four from there on.  Measured
-// (us): at most 16 / 32 segments, 16 x 131071 bf16, top 20, 15.1 / 17.9, 1 x 151000
-// bf16 11.3 / 13.0; segments of at least 4096 / 8192, 1 x 32000 fp32 9.3 / 10.7,
-// 4 x 50000 10.6 / 11.9; 512 x 50021 f16 with four / eight waves 26.6 / 22.0, 2048 x
-// 32000 bf16 45 / 54; two segments of four waves for 512 x 50021 25.6.
+// every m), each of at least 4096 logits.  From 256 rows on a row is one
+// workgroup's, of eight waves up to 1023 rows and four from there on, but for long
+// rows that leave the CUs unevenly filled: fewer than 512 of at least 98304 logits
+// are cut in three, of four waves each.  Measured (us): at most 16 / 32 segments,
+// 16 x 131071 bf16, top 20, 15.1 / 17.9, 1 x 151000 bf16 11.3 / 13.0; segments of at
+// least 4096 / 8192, 1 x 32000 fp32 9.3 / 10.7, 4 x 50000 10.6 / 11.9.  Top 5, one
+// workgroup of four waves / one of eight / two, three, four of four:
+//   256 x 50021 f16     25.2 / 18.1 / 21.0, 19.4, 19.3
+//   256 x 100003 fp32   39.0 / 28.4 / 31.1, 27.7, 28.3
+//   300 x 100003 bf16   40.5 / 33.9 / 33.4, 29.4, 28.0
+//   300 x 100003 fp32   41.8 / 35.9 / 34.6, 32.7, 34.0
+//   400 x 151936 bf16   54.2 / 44.8 / 47.2, 42.0, 44.7
+//   512 x 100003 bf16   41.5 / 35.7 / 38.0, 36.4, 41.9
+//   512 x 151936 fp32   57.4 / 55.3 / 58.1, 63.4, 64.1
+//   1023 x 151936 bf16  74.4 / 74.5 / 83.0, 81.4, 85.2   (2048 x 32000 bf16  45 / 54)
 struct RowSegments {
   int64_t count, len;
   int waves;
 };
 RowSegments row_segments(int64_t m, int64_t vocab) {
-  int64_t want = m < 256 ? (1024 + m - 1) / m : 1;
+  const bool thirds = m >= 256 && m < 512 && vocab >= 98304;
+  int64_t want = m < 256 ? (1024 + m - 1) / m : thirds ? 3 : 1;
   if (want > kLogprobMaxSegments) want = kLogprobMaxSegments;
   const int64_t most = (vocab + 4095) / 4096;
   if (want > most) want = most;
   const int64_t len = ((vocab + want - 1) / want + 7) / 8 * 8;
-  return {(vocab + len - 1) / len, len, m >= 256 && m < 1024 ? 8 : 4};
+  return {(vocab + len - 1) / len, len, m >= 256 && m < 1024 && !thirds ? 8 : 4};
 }
 // workspace: the rows' arrival counters, then the segments' partial results.
 // The counters' region has one fixed size, so that one workspace serves runs

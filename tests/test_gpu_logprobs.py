@@ -327,3 +327,14 @@ def test_lp_more_rows_than_a_launch():
         # at most three terms: a few roundings of values below 6
         assert float((got.logprob.double() - lp.gather(1, t)[:, 0]).abs().max()) <= 64 * 2.0 ** -24
         assert float((got.entropy.double() + (lp.exp() * lp).sum(1)).abs().max()) <= 64 * 2.0 ** -24
+
+
+@pytest.mark.parametrize("m,V", [(255, 98304), (256, 98303), (256, 98304), (300, 100003), (511, 98305), (512, 98305)])
+def test_lp_hundreds_of_long_rows(m, V):
+    """On both sides of the steps at which a row is cut in three."""
+    x, t = normal(m, V, 10600 + m)
+    x[3] = -np.inf
+    x[4, :] = np.linspace(-5.0, 5.0, V)
+    check(x, t, 7, "bf16")
+    rows = slice(0, 8)
+    check(x[rows], t[rows], 20, "f16")
