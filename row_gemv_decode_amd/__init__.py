@@ -576,15 +576,20 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _capturing(handle, stream):
-    """Whether the stream that a call runs on is being captured (the default
-    stream, handle 0, cannot be)."""
+# (from the HIP runtime that the library is linked with)
+_is_capturing = _lib.hipStreamIsCapturing
+_is_capturing.argtypes = [_vp, ctypes.POINTER(ctypes.c_int)]
+_is_capturing.restype = ctypes.c_int
+
+
+def _capturing(handle):
+    """Whether a stream is being captured (the default stream, handle 0, cannot be)."""
     if handle == 0:
         return False
-    if stream is None:
-        return torch.cuda.is_current_stream_capturing()
-    with torch.cuda.stream(stream):
-        return torch.cuda.is_current_stream_capturing()
+    status = ctypes.c_int()
+    if _is_capturing(handle, ctypes.byref(status)) != 0:
+        raise SkinnyError(ERR_HIP, "hipStreamIsCapturing")
+    return status.value != 0
 
 
 def _stream_workspace(cache, key, nbytes, counters, device, handle, stream):
@@ -593,7 +598,7 @@ def _stream_workspace(cache, key, nbytes, counters, device, handle, stream):
     always gets one of its own, from the graph's memory, whose first `counters`
     bytes the graph zeroes at every replay: the stream's may be replaced by a
     larger one, and eager runs may use it, while the graph lives."""
-    capturing = _capturing(handle, stream)
+    capturing = _capturing(handle)
     ws = None if capturing else cache.get(key)
     if ws is None or ws.numel() < nbytes:
         with torch.cuda.stream(torch.cuda.current_stream(device) if stream is None else stream):

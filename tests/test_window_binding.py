@@ -132,7 +132,7 @@ def test_a_capture_never_takes_the_streams_workspace(lib, monkeypatch, stream):
     monkeypatch.setattr(sk, "_handle", lambda index, stream: 5)
     monkeypatch.setattr(torch.cuda, "stream", lambda s: contextlib.nullcontext())
     monkeypatch.setattr(torch.cuda, "current_stream", lambda d=None: None)
-    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: capturing[0])
+    monkeypatch.setattr(sk, "_capturing", lambda handle, *stream: handle == 5 and capturing[0])
     used = []
 
     def during(name, args):
