@@ -535,15 +535,18 @@ def _input_rows(where, name, t, stream):
     to several, windows that overlap) are copied apart on the stream that reads
     them: the library takes no row stride below the rows' length."""
     shape = t.shape
-    if len(shape) == 2 and shape[0] > 1 and t.stride(1) == 1:
-        ld = t.stride(0)
-        if ld >= shape[1]:
-            return t, ld
-        if stream is None:
-            t = t.contiguous()
-        else:
-            with torch.cuda.stream(stream):
+    if len(shape) == 2:
+        ld, step = t.stride()
+        if step == 1:
+            if shape[0] < 2:
+                return t, 0
+            if ld >= shape[1]:
+                return t, ld
+            if stream is None:
                 t = t.contiguous()
+            else:
+                with torch.cuda.stream(stream):
+                    t = t.contiguous()
     return t, _rows(where, name, t)
 
 
