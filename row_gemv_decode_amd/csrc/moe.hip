@@ -198,12 +198,18 @@ __host__ __device__ __forceinline__ int down_waves(int units, int64_t d, int top
   return n;
 }
 
-// column tiles of a wave in the down product.  Measured (us, 1 / 2 / 4 tiles):
-// 16-bit weights, 1 of 256 experts (d = 5120, inter = 896) 21.1 / 22.9 / 25.0;
-// 4 bits, 16 of 256 110 / 83 / 82, 3 of 256 33 / 27 / 29, 5 of 512 (d = 2560,
-// inter = 672) 31 / 27 / 26, 1 of 8 (d = 4096, inter = 8192) 16.4 / 15.5 / 19.5
-template <int WQ>
-constexpr int down_tiles() { return WQ == kWFull ? 1 : 2; }
+// Column tiles of a wave in the down product (a column's arithmetic does not depend
+// on them): one for 16-bit weights; for 4-bit ones two, or, where that leaves at
+// least 3072 waves of work, four (not for groups of 32, whose waves then take too
+// many registers).  Measured (us, 1 / 2 / 4 tiles; waves of 4): 16 bits, 1 of 256
+// experts (d = 5120, inter = 896) 20.7 / 22.0 / 23.9, 16 of 64 (d = 2560) 55.3 / 55.6 /
+// 59.2; groups of 128, 16 of 256 103 / 82 / 75 (12800), 16 of 8 (d = 4096, inter = 8192)
+// 73 / 59 / 51 (3584), 1 of 8 15.4 / 14.7 / 18.6 (512); of 64, 3 of 256 28.7 / 26.0 / 28.5
+// (2480); of 32, 5 of 512 (d = 2560, inter = 672) 28.4 / 26.1 / 25.1 (2000), 16 of 512 the
+// whole layer - / 162 / 166 (6400)
+int down_tiles(int group, int64_t d, int64_t waves_of_4) {
+  return group == 0 ? 1 : group > 32 && d % 64 == 0 && waves_of_4 >= 3072 ? 4 : 2;
+}
 
 __device__ const u32x4 kZeroLine = {0u, 0u, 0u, 0u};
 
@@ -369,10 +375,9 @@ struct UnitScales<kWFull, CT> {
 // 16 of 256 experts 20 us more.
 // Bound by what a wave does per byte, not by memory alone: with the planes in
 // turn, h for 16 tokens and the waves splitting k, 16 of 256 experts (d = 5120,
-// inter = 896, 4 bits) took 130 to 170 us; so, 83 (3.5 TB/s).
-template <int TK, int WQ>
+// inter = 896, 4 bits) took 130 to 170 us; so, 75 (3.9 TB/s).
+template <int TK, int WQ, int CT>
 __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_down_kernel(MoeArgs a) {
-  constexpr int CT = down_tiles<WQ>();
   constexpr int NB = unit_blocks<WQ>();
   constexpr int UL = unit_len<WQ>();
   constexpr int TT = kMoeDownTokens;
@@ -585,25 +590,37 @@ moe_fn pick_route(int experts) {
 }
 
 template <int TK, int WQ>
-moe_fn pick_stage(bool up, bool wide) {
-  return !up ? moe_down_kernel<TK, WQ> : wide ? moe_up_kernel<TK, WQ, 2> : moe_up_kernel<TK, WQ, 1>;
-}
+moe_fn pick_up(bool wide) { return wide ? moe_up_kernel<TK, WQ, 2> : moe_up_kernel<TK, WQ, 1>; }
 
-template <int TK>
-moe_fn pick_weight(int group, bool zeros, bool up, bool wide) {
-  switch (group + (zeros ? kZeros : 0)) {
-    case 0: return pick_stage<TK, kWFull>(up, wide);
-    case 32: return pick_stage<TK, 32>(up, wide);
-    case 64: return pick_stage<TK, 64>(up, wide);
-    case 128: return pick_stage<TK, 128>(up, wide);
-    case 32 + kZeros: return pick_stage<TK, 32 + kZeros>(up, wide);
-    case 64 + kZeros: return pick_stage<TK, 64 + kZeros>(up, wide);
-    default: return pick_stage<TK, 128 + kZeros>(up, wide);
+template <int TK, int WQ>
+moe_fn pick_down(int tiles) {
+  if constexpr (WQ == kWFull) {
+    return moe_down_kernel<TK, WQ, 1>;
+  } else {
+    if constexpr (group_len<WQ>() > 32)
+      if (tiles == 4) return moe_down_kernel<TK, WQ, 4>;
+    return moe_down_kernel<TK, WQ, 2>;
   }
 }
 
-moe_fn pick(int kind, int group, bool zeros, bool up, bool wide) {
-  return kind == CK_F16 ? pick_weight<CK_F16>(group, zeros, up, wide) : pick_weight<CK_BF16>(group, zeros, up, wide);
+// the up kernel (tiles 0), or the down kernel of that many column tiles
+template <int TK>
+moe_fn pick_weight(int group, bool zeros, int tiles, bool wide) {
+#define SKINNY_MOE_PICK(wq) return tiles == 0 ? pick_up<TK, wq>(wide) : pick_down<TK, wq>(tiles)
+  switch (group + (zeros ? kZeros : 0)) {
+    case 0: SKINNY_MOE_PICK(kWFull);
+    case 32: SKINNY_MOE_PICK(32);
+    case 64: SKINNY_MOE_PICK(64);
+    case 128: SKINNY_MOE_PICK(128);
+    case 32 + kZeros: SKINNY_MOE_PICK(32 + kZeros);
+    case 64 + kZeros: SKINNY_MOE_PICK(64 + kZeros);
+    default: SKINNY_MOE_PICK(128 + kZeros);
+  }
+#undef SKINNY_MOE_PICK
+}
+
+moe_fn pick(int kind, int group, bool zeros, int tiles, bool wide) {
+  return kind == CK_F16 ? pick_weight<CK_F16>(group, zeros, tiles, wide) : pick_weight<CK_BF16>(group, zeros, tiles, wide);
 }
 
 }  // namespace
@@ -615,6 +632,7 @@ namespace {
 // workgroups of a layer's launches, and how many slots and parts they cover
 struct MoeGrid {
   int64_t slots, parts, up, down;
+  int down_tiles;
   bool wide;
 };
 
@@ -635,13 +653,13 @@ MoeGrid moe_grid(const MoeArgs& a, int group) {
   g.up = g.slots * (a.inter / tile) + a.shared_inter / tile;
   // the down product: as in its kernel
   const int unit = group == 0 ? unit_len<kWFull>() : unit_len<128>();
-  const int64_t sets = a.d / 16 / (group == 0 ? down_tiles<kWFull>() : down_tiles<128>());
-  auto blocks = [&](int64_t inter) {
-    const int per = kMoeWaves / down_waves((int)((inter + unit - 1) / unit), a.d, a.topk);
-    return (sets + per - 1) / per;
-  };
-  g.down = g.parts * blocks(a.inter);
-  if (a.shared_inter > 0) g.down += (a.m + kMoeDownTokens - 1) / kMoeDownTokens * blocks(a.shared_inter);
+  const int64_t shared_parts = a.shared_inter > 0 ? (a.m + kMoeDownTokens - 1) / kMoeDownTokens : 0;
+  auto waves = [&](int64_t inter) { return down_waves((int)((inter + unit - 1) / unit), a.d, a.topk); };
+  const int64_t ks = waves(a.inter), ks0 = shared_parts > 0 ? waves(a.shared_inter) : 1;
+  g.down_tiles = down_tiles(group, a.d, (g.parts * ks + shared_parts * ks0) * (a.d / 64));
+  const int64_t sets = a.d / 16 / g.down_tiles;
+  auto blocks = [&](int64_t k) { return (sets + kMoeWaves / k - 1) / (kMoeWaves / k); };
+  g.down = g.parts * blocks(ks) + shared_parts * blocks(ks0);
   return g;
 }
 
@@ -669,10 +687,10 @@ hipError_t launch_moe(const MoeArgs& args, int kind, int group, hipStream_t stre
                      dim3(a.shared_inter > 0 ? 2 : 1), dim3(64 * a.m), 0, stream, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(pick(kind, group, zeros, true, g.wide), dim3((unsigned)g.up), dim3(64 * kMoeWaves), 0, stream, a);
+  hipLaunchKernelGGL(pick(kind, group, zeros, 0, g.wide), dim3((unsigned)g.up), dim3(64 * kMoeWaves), 0, stream, a);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(pick(kind, group, zeros, false, false), dim3((unsigned)g.down), dim3(64 * kMoeWaves), 0, stream, a);
+  hipLaunchKernelGGL(pick(kind, group, zeros, g.down_tiles, false), dim3((unsigned)g.down), dim3(64 * kMoeWaves), 0, stream, a);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(moe_sum_kernel, dim3((unsigned)((a.d + 255) / 256), (unsigned)a.m), dim3(64), 0, stream, a);

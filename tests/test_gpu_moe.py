@@ -360,3 +360,16 @@ def test_moe_small_inputs(scale, kind):
 def test_moe_several_spans_of_scales(d, inter, group):
     """Lengths of more than 80 groups: the up product stages its scales in spans."""
     Case(5, 6, 2, d, inter, shared=group, group=group, zeros=True, kind="f16", seed=9600 + d).check()
+
+
+@pytest.mark.parametrize("group,kind,d,inter", [(32, "f16", 4096, 160), (64, "bf16", 4160, 192), (128, "f16", 4096, 384),
+                                                (128, "bf16", 4224, 128)])
+def test_moe_bits_do_not_depend_on_the_launch(group, kind, d, inter):
+    """Windows that fill the chip, whose down product takes four column tiles per
+    wave, against one-token calls, whose takes two."""
+    c = Case(16, 24, 12, d, inter, shared=2 * group, group=group, zeros=True, kind=kind, seed=9700)
+    layer, x, got = c.check()
+    for i in (0, 7, 15):
+        assert torch.equal(layer(x[i:i + 1].contiguous())[0], got[i])
+    for m in (4, 5, 9):
+        assert torch.equal(layer(x[:m].contiguous()), got[:m])

@@ -126,7 +126,7 @@ def listings(tmp_path_factory):
         return dict(zip(("moe.hip", "w4.hip"), ex.map(listing, ("moe.hip", "w4.hip"))))
 
 
-@pytest.mark.parametrize("source,kernels", [("moe.hip", 42), ("w4.hip", 36)])
+@pytest.mark.parametrize("source,kernels", [("moe.hip", 50), ("w4.hip", 36)])
 def test_no_kernel_reads_the_matrix_core_early(listings, source, kernels):
     parts = re.split(r"\n(_Z\w+):", listings[source])
     with_mfma = 0
