@@ -375,7 +375,7 @@ struct UnitScales<kWFull, CT> {
 // 16 of 256 experts 20 us more.
 // Bound by what a wave does per byte, not by memory alone: with the planes in
 // turn, h for 16 tokens and the waves splitting k, 16 of 256 experts (d = 5120,
-// inter = 896, 4 bits) took 130 to 170 us; so, 75 (3.9 TB/s).
+// inter = 896, 4 bits) took 130 to 170 us; so, 77 (3.8 TB/s).
 template <int TK, int WQ, int CT>
 __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_down_kernel(MoeArgs a) {
   constexpr int NB = unit_blocks<WQ>();
@@ -547,8 +547,9 @@ __global__ __launch_bounds__(64 * kMoeWaves, 2) void moe_down_kernel(MoeArgs a) 
 // out[t] = the sum of token t's experts' rows, largest logit first, then the
 // shared expert's, each times its weight; a thread adds four columns.  Twelve rows are fetched before
 // the first is added (loads past the last row repeat it), so the kernel waits
-// for memory once for up to twelve (1 of 64 experts, top 4: 2.4 us, and 2.7 row by
-// row; of the 4.6 us of 5 of 512 most is reading rows that other XCDs wrote).
+// for memory once for up to twelve (1 of 64 experts, top 4, as a plain sum: 2.4 us,
+// and 2.7 row by row; 2.7 with the weights.  Of the 4.6 us of 5 of 512 most is
+// reading rows that other XCDs wrote).
 __global__ __launch_bounds__(64) void moe_sum_kernel(MoeArgs a) {
   constexpr int R = 12;
   const int64_t j = 4 * (int64_t)(blockIdx.x * 64 + threadIdx.x);

@@ -4,7 +4,7 @@
 //   C[r][j] = sum over groups g of  s[j][g] * sum over kk in g of (q[j][kk] - z[j][g]) * A[r][kk]
 //
 // for r < m <= 16.  HBM-bound: the codes and scales are read once per call for
-// all rows (3 x 100003 x 5120, groups of 128, 265 MB: 71 us, 3.7 TB/s, where a
+// all rows (3 x 100003 x 5120, groups of 128, 265 MB: 66 us, 4.0 TB/s, where a
 // large copy moves 4.9 TB/s; below about 10 MB the launch and one round trip to
 // HBM are the time).  A workgroup of four waves owns CT tiles of 16 columns; each
 // wave takes a quarter of k (a run of units of 128) and streams it with two units
@@ -91,7 +91,7 @@ hipError_t launch_w4_mm(const W4Args& args, int a_kind, int group, hipStream_t s
   }
   const int64_t tiles = (args.n + 15) / 16;
   // Column tiles per wave: more tiles share the loads of A, fewer make more
-  // workgroups.  About three workgroups of one tile are resident per CU, three of
+  // workgroups.  Three or four workgroups of one tile are resident per CU, three of
   // two and two of four, so: four tiles where their workgroups make one nearly full
   // round; two where one-tile workgroups would need a second round, or, for groups
   // of 128 (the least work per unit), where the two-tile ones are one per CU at
