@@ -207,11 +207,27 @@ def prepare(case, seed):
     g = torch.Generator(device="cuda").manual_seed(int(seed))
     s = {"case": case}
     {"norm": _prepare_norm, "adapt": _prepare_adapt, "adjust": _prepare_adjust}[case["op"]](case, g, s)
-    if own and case["op"] == "adapt":
-        import row_gemv_decode_amd as sk
-
-        s["adapters"] = sk.Adapters(s["A"], s["B"], scaling=s["scaling"], ranks=s["ranks"])
+    if own:
+        _handles(s)
     return s
+
+
+def _handles(s):
+    """What a program that uses the library keeps beside its tensors: the pool of
+    adapters, the rules' tensors that it fills from step to step."""
+    import row_gemv_decode_amd as sk
+
+    if s["case"]["op"] == "adapt":
+        s["adapters"] = sk.Adapters(s["A"], s["B"], scaling=s["scaling"], ranks=s["ranks"])
+    elif s["case"]["op"] == "adjust":
+        more = {}
+        if s["history"] is not None:
+            more = {k: s[k] for k in ("history", "lengths", "prompt_lengths", "repetition", "frequency", "presence")}
+        if s["bias_ids"] is not None:
+            more |= {"bias_ids": s["bias_ids"], "bias_values": s["bias_values"]}
+        if s["mask"] is not None:
+            more |= {"mask": s["mask"], "mask_rows": s["mask_rows"]}
+        s["rules"] = sk.LogitRules(s["case"]["m"], s["case"]["vocab"], **more)
 
 
 # --- the plain form ----------------------------------------------------------
@@ -290,14 +306,7 @@ def run(state):
             return {k: v for k, v in r._asdict().items() if v is not None}
         if op == "adapt":
             return sk.add_adapters(s["x"], s["adapters"], s["ids"], s["base"], out=s["out"])
-        more = {}
-        if s["history"] is not None:
-            more = {k: s[k] for k in ("history", "lengths", "prompt_lengths", "repetition", "frequency", "presence")}
-        if s["bias_ids"] is not None:
-            more |= {"bias_ids": s["bias_ids"], "bias_values": s["bias_values"]}
-        if s["mask"] is not None:
-            more |= {"mask": s["mask"], "mask_rows": s["mask_rows"]}
-        return sk.adjust_logits(s["logits"], out=s["logits"] if s["out"] is None else s["out"], **more)
+        return sk.adjust_logits(s["logits"], s["rules"], out=s["logits"] if s["out"] is None else s["out"])
     return {"norm": _plain_norm, "adapt": _plain_adapt, "adjust": _plain_adjust}[op](s)
 
 
