@@ -64,6 +64,14 @@ WINDOW_EXPORTS = (
     "skinny_moe_plan_create", "skinny_moe_plan_destroy", "skinny_moe_workspace_size", "skinny_moe_run",
     "skinny_token_logprobs_workspace_size", "skinny_token_logprobs_run",
 )
+# the entry points of include/skinny_requests.h
+REQUEST_EXPORTS = (
+    "skinny_rms_norm_run",
+    "skinny_adapters_workspace_size", "skinny_adapters_run",
+    "skinny_adjust_logits_run",
+)
+ADAPTERS_MAX = 8192
+ADAPTER_RANK_MAX = 256
 STATIC_SCRATCH_BYTES = 32 << 20
 STATIC_COUNTER_BYTES = 1 << 20
 
@@ -114,6 +122,43 @@ class MoEWeightsDesc(ctypes.Structure):
                 ("shared2", W4Desc), ("shared_gate", ctypes.c_void_p)]
 
 
+class AdaptersDesc(ctypes.Structure):
+    _fields_ = [
+        ("struct_size", ctypes.c_uint32),
+        ("dtype", ctypes.c_int32),
+        ("count", ctypes.c_int64),
+        ("rank", ctypes.c_int64),
+        ("k", ctypes.c_int64),
+        ("n", ctypes.c_int64),
+        ("A", ctypes.c_void_p),
+        ("B", ctypes.c_void_p),
+        ("ranks", ctypes.c_void_p),
+        ("scaling", ctypes.c_void_p),
+    ]
+
+
+class LogitRulesDesc(ctypes.Structure):
+    _fields_ = [
+        ("struct_size", ctypes.c_uint32),
+        ("tokens64", ctypes.c_int32),
+        ("history", ctypes.c_void_p),
+        ("ldh", ctypes.c_int64),
+        ("history_len", ctypes.c_int64),
+        ("lengths", ctypes.c_void_p),
+        ("prompt_lengths", ctypes.c_void_p),
+        ("repetition", ctypes.c_void_p),
+        ("frequency", ctypes.c_void_p),
+        ("presence", ctypes.c_void_p),
+        ("bias_ids", ctypes.c_void_p),
+        ("bias_values", ctypes.c_void_p),
+        ("biases", ctypes.c_int64),
+        ("mask", ctypes.c_void_p),
+        ("ldm", ctypes.c_int64),
+        ("masks", ctypes.c_int64),
+        ("mask_rows", ctypes.c_void_p),
+    ]
+
+
 _vp, _i64, _i32, _sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
 _lib.skinny_mm_plan.argtypes = [ctypes.POINTER(MMDesc), ctypes.POINTER(_vp)]
 _lib.skinny_mm_plan.restype = ctypes.c_int
@@ -152,6 +197,15 @@ _lib.skinny_token_logprobs_workspace_size.restype = ctypes.c_int
 _lib.skinny_token_logprobs_run.argtypes = [_i64, _i64, _vp, _i64, _i32, _vp, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _sz,
                                            _vp]
 _lib.skinny_token_logprobs_run.restype = ctypes.c_int
+_lib.skinny_rms_norm_run.argtypes = [_i64, _i64, _vp, _i64, _i32, _vp, _i64, _i32, _vp, _i32, ctypes.c_float, _vp, _i64, _vp,
+                                     _i64, _i32, _vp, _i64, _vp, _i32, _vp]
+_lib.skinny_rms_norm_run.restype = ctypes.c_int
+_lib.skinny_adapters_workspace_size.argtypes = [_vp, _i64, ctypes.POINTER(_sz)]
+_lib.skinny_adapters_workspace_size.restype = ctypes.c_int
+_lib.skinny_adapters_run.argtypes = [_vp, _i64, _vp, _i64, _vp, _i32, _vp, _i64, _i32, _vp, _i64, _i32, _vp, _sz, _vp]
+_lib.skinny_adapters_run.restype = ctypes.c_int
+_lib.skinny_adjust_logits_run.argtypes = [_i64, _i64, _vp, _i64, _i32, _vp, _vp, _i64, _i32, _vp]
+_lib.skinny_adjust_logits_run.restype = ctypes.c_int
 _lib.skinny_mm_plan_info.argtypes = [_vp, _i64, ctypes.c_char_p, _sz]
 _lib.skinny_mm_plan_info.restype = ctypes.c_int
 _lib.skinny_gemm_tile_count.argtypes = []
@@ -828,3 +882,285 @@ def token_logprobs(logits, tokens, topk=0, stream=None):
                                           p_rank, p_rank + 4 * m, p + 8 * m, None if ws is None else ws.data_ptr(), need, handle),
            "skinny_token_logprobs_run")
     return TokenLogprobs(lp, ent, rank.view(torch.int32), ids.view(torch.int32).view(m, topk), top.view(m, topk))
+
+
+# --- operators of a batch of requests (include/skinny_requests.h) ------------
+class RMSNorm(NamedTuple):
+    """What rms_norm gives; None for what was not asked for."""
+    out: "torch.Tensor"       # [m][d]
+    residual: "torch.Tensor"  # [m][d], the sum that the next layer's residual starts from
+    q: "torch.Tensor"         # float8_e4m3fn [m][d]
+    scales: "torch.Tensor"    # float32 [m][groups]
+
+
+def _output(where, name, t, index, shape, dtype):
+    """Row stride of a given output of that shape (and type, unless it is None)."""
+    if t.shape != shape or (dtype is not None and t.dtype is not dtype):
+        raise ValueError(f"{where}: {name} must be {list(shape)}" + (f" of type {dtype}" if dtype else ""))
+    if t.get_device() != index:
+        raise ValueError(f"{where}: {name} must be on the GPU of the other tensors")
+    return _rows(where, name, t)
+
+
+def rms_norm(x, weight=None, eps=1e-6, residual=None, residual_out=None, out=None, out_dtype=None, quant=None, q=None,
+             scales=None, stream=None):
+    """The residual's addition and a root-mean-square norm, in one launch:
+    h = x + residual, y = h / sqrt(mean(h^2) + eps) * weight, in fp32.
+
+    x [m][d], residual [m][d] and weight [d] (or None) float32, float16 or
+    bfloat16, each its own.  Gives RMSNorm(out, residual, q, scales):
+    residual is h in the residual's type (residual_out, which may be `residual`
+    itself, or a new tensor), out is y in out_dtype (x's type by default; `out`
+    may be x).  With quant = 0 or a group length of 32, 64 or 128, q is y in 8 bits
+    (float8_e4m3fn) and scales holds what to multiply them by, one per row or per
+    group of columns; then there is an `out` only if it or out_dtype is given.
+    Rows of any stride; input rows that share memory are copied apart first."""
+    x, ldx = _input_rows("rms_norm", "x", x, stream)
+    shape, dtype = x.shape, x.dtype
+    m, d = shape
+    code = _CODES.get(dtype)
+    if code is None:
+        raise TypeError(f"rms_norm: unsupported dtype {dtype}")
+    index = _gpu("rms_norm", x)
+    if _current_device() != index:
+        with torch.cuda.device(index):
+            return rms_norm(x, weight, eps, residual, residual_out, out, out_dtype, quant, q, scales, stream)
+    w_ptr, w_code = None, code
+    if weight is not None:
+        if weight.shape != (d,) or not weight.is_contiguous() or weight.get_device() != index:
+            raise ValueError(f"rms_norm: weight must be contiguous [{d}], on x's GPU")
+        w_ptr, w_code = weight.data_ptr(), _CODES.get(weight.dtype, 0)
+    r_ptr, ldr, r_code, ro_ptr, ldro = None, 0, code, None, 0
+    if residual is not None:
+        residual, ldr = _input_rows("rms_norm", "residual", residual, stream)
+        if residual.shape != shape or residual.get_device() != index:
+            raise ValueError(f"rms_norm: residual must be {list(shape)}, on x's GPU")
+        r_ptr, r_code = residual.data_ptr(), _CODES.get(residual.dtype, 0)
+        if residual_out is None:
+            residual_out = _empty(shape, residual.dtype, x.device, stream)
+        else:
+            ldro = _output("rms_norm", "residual_out", residual_out, index, shape, residual.dtype)
+        ro_ptr = residual_out.data_ptr()
+    elif residual_out is not None:
+        raise ValueError("rms_norm: residual_out without a residual")
+    o_ptr, ldo, o_code = None, 0, code
+    if out is not None:
+        ldo = _output("rms_norm", "out", out, index, shape, out_dtype)
+    elif quant is None or out_dtype is not None:
+        out = _empty(shape, out_dtype or dtype, x.device, stream)
+    if out is not None:
+        o_ptr, o_code = out.data_ptr(), _CODES.get(out.dtype, 0)
+    q_ptr, ldq, s_ptr = None, 0, None
+    if quant is not None:
+        groups = -(-d // quant) if quant > 0 else 1
+        if q is None:
+            q = _empty(shape, torch.float8_e4m3fn, x.device, stream)
+        else:
+            ldq = _output("rms_norm", "q", q, index, shape, torch.float8_e4m3fn)
+        if scales is None:
+            scales = _empty((m, groups), torch.float32, x.device, stream)
+        else:
+            _output("rms_norm", "scales", scales, index, (m, groups), torch.float32)
+            if not scales.is_contiguous():
+                raise ValueError("rms_norm: scales must be contiguous")
+        q_ptr, s_ptr = q.data_ptr(), scales.data_ptr()
+    elif q is not None or scales is not None:
+        raise ValueError("rms_norm: q and scales go with quant")
+    _check(_lib.skinny_rms_norm_run(m, d, x.data_ptr(), ldx, code, r_ptr, ldr, r_code, w_ptr, w_code, eps, ro_ptr, ldro, o_ptr,
+                                    ldo, o_code, q_ptr, ldq, s_ptr, quant or 0, _handle(index, stream)), "skinny_rms_norm_run")
+    return RMSNorm(out, residual_out, q, scales)
+
+
+class Adapters:
+    """A pool of low-rank adapters for one projection [n][k]: A [count][rank][k]
+    and B [count][n][rank], float16 or bfloat16, scaling float32 [count] (None: 1)
+    and ranks int32 [count], each adapter's own rank (None: rank; what A and B
+    hold past it is not used).  rank and k are multiples of 8, rank up to 256.
+    Checked once, here; the tensors are kept alive and read at every call, so
+    an adapter is exchanged by writing into them."""
+
+    def __init__(self, A, B, scaling=None, ranks=None):
+        if A.dim() != 3 or B.dim() != 3 or A.dtype not in (torch.float16, torch.bfloat16) or B.dtype != A.dtype:
+            raise TypeError("Adapters: A [count][rank][k] and B [count][n][rank], both float16 or bfloat16")
+        count, rank, k = A.shape
+        if B.shape[0] != count or B.shape[2] != rank:
+            raise ValueError(f"Adapters: B {tuple(B.shape)} does not fit A {tuple(A.shape)}")
+        for name, t, dt in (("scaling", scaling, torch.float32), ("ranks", ranks, torch.int32)):
+            if t is not None and (t.dtype != dt or tuple(t.shape) != (count,)):
+                raise ValueError(f"Adapters: {name} must be {dt} [{count}]")
+        _dense("Adapters", A=A, B=B, scaling=scaling, ranks=ranks)
+        _on("Adapters", A.device, B, scaling, ranks)
+        self.A, self.B, self.scaling, self.ranks = A, B, scaling, ranks
+        self.count, self.rank, self.k, self.n = count, rank, k, B.shape[1]
+        self.dtype, self.device, self._index = A.dtype, A.device, _gpu("Adapters", A)
+        self._code = _dtype_code(A.dtype, "A")
+        self._desc = AdaptersDesc(ctypes.sizeof(AdaptersDesc), self._code, count, rank, k, self.n, A.data_ptr(), B.data_ptr(),
+                                  0 if ranks is None else ranks.data_ptr(), 0 if scaling is None else scaling.data_ptr())
+        self._addr = ctypes.addressof(self._desc)
+        self._need = {}  # rows -> workspace bytes
+        self.workspace_bytes(1)  # (refuses sizes that the library does not take)
+
+    def workspace_bytes(self, m):
+        need = self._need.get(m)
+        if need is None:
+            sz = ctypes.c_size_t()
+            _check(_lib.skinny_adapters_workspace_size(self._addr, m, ctypes.byref(sz)), "skinny_adapters_workspace_size")
+            if len(self._need) > 4096:
+                self._need.clear()
+            need = self._need[m] = int(sz.value)
+        return need
+
+
+_adapter_ws = {}
+# a run is several launches over its stream's workspace: two threads on one
+# stream must not interleave theirs
+_adapter_lock = threading.Lock()
+
+
+def add_adapters(x, adapters, ids, base=None, out=None, out_dtype=None, stream=None):
+    """out[t] = base[t] + scaling[a] * B[a] (A[a] x[t]) with a = ids[t], for the rows
+    of many requests beside their shared projection: x [m][k] of the adapters'
+    type, ids [m] int32 or int64 (outside 0 .. count - 1: no adapter), base [m][n]
+    of the adapters' type or float32, the shared projection's output (None: 0).
+    out has base's type (the adapters' without one) unless `out` or `out_dtype`
+    says otherwise, and may be base itself.  Sums are held in fp32 and rounded
+    once.  Rows of any stride (x's a multiple of 8); input rows that share memory
+    are copied apart first."""
+    x, ldx = _input_rows("add_adapters", "x", x, stream)
+    m, k = x.shape
+    if not isinstance(adapters, Adapters) or x.dtype is not adapters.dtype:
+        raise TypeError("add_adapters: takes Adapters of x's type")
+    if k != adapters.k:
+        raise ValueError(f"add_adapters: adapters for k = {adapters.k} do not fit x {tuple(x.shape)}")
+    index, n = adapters._index, adapters.n
+    ids64 = ids.dtype is torch.int64
+    if ids.shape != (m,) or not (ids64 or ids.dtype is torch.int32) or not ids.is_contiguous():
+        raise ValueError(f"add_adapters: ids must be contiguous int64 or int32 [{m}]")
+    if _gpu("add_adapters", x) != index or ids.get_device() != index:
+        raise ValueError(f"add_adapters: x and ids must be on {adapters.device}")
+    if _current_device() != index:
+        with torch.cuda.device(index):
+            return add_adapters(x, adapters, ids, base, out, out_dtype, stream)
+    b_ptr, ldb, b_code = None, 0, F32
+    if base is not None:
+        base, ldb = _input_rows("add_adapters", "base", base, stream)
+        if base.shape != (m, n) or base.get_device() != index:
+            raise ValueError(f"add_adapters: base must be [{m}][{n}] on {adapters.device}")
+        b_ptr, b_code = base.data_ptr(), _CODES.get(base.dtype, 0)
+    if out is None:
+        out = _empty((m, n), out_dtype or (adapters.dtype if base is None else base.dtype), x.device, stream)
+        ldo = 0
+    else:
+        ldo = _output("add_adapters", "out", out, index, (m, n), out_dtype)
+    need = adapters._need.get(m) or adapters.workspace_bytes(m)
+    handle = _handle(index, stream)
+    with _adapter_lock:
+        ws = _stream_workspace(_adapter_ws, (index, handle), need, 0, x.device, handle, stream)
+        _check(_lib.skinny_adapters_run(adapters._addr, m, x.data_ptr(), ldx, ids.data_ptr(), ids64, b_ptr, ldb, b_code,
+                                        out.data_ptr(), ldo, _CODES.get(out.dtype, 0), ws.data_ptr(), need, handle),
+               "skinny_adapters_run")
+    return out
+
+
+class LogitRules:
+    """What adjust_logits does to rows of logits [m][vocab].  Every tensor is
+    optional, kept alive and read at every call, so a program fills them in place
+    from step to step:
+
+    history [m][room] int32 or int64, the rows' token ids so far, of which row i
+    has lengths[i] (int32 [m]; None: all), the first prompt_lengths[i] (int32 [m];
+    None: 0) of the prompt, the others generated.  With the history: repetition
+    (> 0), frequency and presence, float32 [m].  bias_ids [m][biases] of the
+    history's type with bias_values float32 [m][biases]; ids outside the
+    vocabulary fill a list up.  mask int32 [masks][>= ceil(vocab / 32)], bit j % 32
+    of word j / 32 set where token j is allowed, and mask_rows int32 [m], the mask
+    of each row (negative: none; None: row i has mask i)."""
+
+    def __init__(self, m, vocab, history=None, lengths=None, prompt_lengths=None, repetition=None, frequency=None,
+                 presence=None, bias_ids=None, bias_values=None, mask=None, mask_rows=None):
+        tensors = dict(history=history, lengths=lengths, prompt_lengths=prompt_lengths, repetition=repetition,
+                       frequency=frequency, presence=presence, bias_ids=bias_ids, bias_values=bias_values, mask=mask,
+                       mask_rows=mask_rows)
+        if m < 1 or vocab < 1:
+            raise ValueError("LogitRules: m and vocab must be at least 1")
+        if history is None and any(tensors[k] is not None for k in list(tensors)[1:6]):
+            raise ValueError("LogitRules: lengths and penalties go with a history")
+        if (bias_ids is None) != (bias_values is None):
+            raise ValueError("LogitRules: bias_ids and bias_values go together")
+        if mask is None and mask_rows is not None:
+            raise ValueError("LogitRules: mask_rows goes with a mask")
+        for names, dt in ((("lengths", "prompt_lengths", "mask_rows"), torch.int32),
+                          (("repetition", "frequency", "presence"), torch.float32)):
+            for name in names:
+                t = tensors[name]
+                if t is not None and (t.dtype != dt or tuple(t.shape) != (m,) or not t.is_contiguous()):
+                    raise ValueError(f"LogitRules: {name} must be contiguous {dt} [{m}]")
+        tokens = [t for t in (history, bias_ids) if t is not None]
+        for t in tokens:
+            if t.dtype not in (torch.int32, torch.int64) or t.dtype != tokens[0].dtype or t.dim() != 2 or t.shape[0] != m:
+                raise ValueError(f"LogitRules: history and bias_ids must be int32 or int64 (both the same) [{m}][..]")
+        ldh = ldm = 0
+        if history is not None:
+            ldh = _rows("LogitRules", "history", history)
+        biases = 0
+        if bias_ids is not None:
+            biases = bias_ids.shape[1]
+            if bias_values.dtype != torch.float32 or bias_values.shape != bias_ids.shape:
+                raise ValueError("LogitRules: bias_values must be float32, of bias_ids' shape")
+            _dense("LogitRules", bias_ids=bias_ids, bias_values=bias_values)
+        masks = 0
+        if mask is not None:
+            words = (vocab + 31) // 32
+            if mask.dtype != torch.int32 or mask.dim() != 2 or mask.shape[1] < words or mask.shape[0] < 1:
+                raise ValueError(f"LogitRules: mask must be int32 [masks][{words} or more]")
+            if mask_rows is None and mask.shape[0] < m:
+                raise ValueError(f"LogitRules: {mask.shape[0]} masks for {m} rows")
+            ldm, masks = _rows("LogitRules", "mask", mask), mask.shape[0]
+        used = [t for t in tensors.values() if t is not None]
+        self.m, self.vocab, self.device = m, vocab, used[0].device if used else None
+        _on("LogitRules", self.device, *used)
+        self._index = _gpu("LogitRules", used[0]) if used else None
+        self._keep = tensors
+        ptr = {k: 0 if t is None or t.numel() == 0 else t.data_ptr() for k, t in tensors.items()}
+        room = history.shape[1] if ptr["history"] else 0
+        if not ptr["history"]:  # (a history without room is none, and nothing repeats)
+            for name in list(tensors)[1:6]:
+                ptr[name] = 0
+        self._desc = LogitRulesDesc(ctypes.sizeof(LogitRulesDesc), bool(tokens) and tokens[0].dtype == torch.int64,
+                                    ptr["history"], ldh if room else 0, room, ptr["lengths"], ptr["prompt_lengths"],
+                                    ptr["repetition"], ptr["frequency"], ptr["presence"], ptr["bias_ids"],
+                                    ptr["bias_values"], biases, ptr["mask"], ldm, masks, ptr["mask_rows"])
+        self._addr = ctypes.addressof(self._desc)
+
+
+def adjust_logits(logits, rules, out=None, out_dtype=None, stream=None):
+    """The logits [m][vocab] (float32, float16 or bfloat16) with the rules' penalties,
+    biases and masks applied, in this order, in fp32, in one launch (see LogitRules):
+    seen tokens' logits are divided (> 0) or multiplied (else) by repetition; generated
+    ones lose frequency * count + presence; biases are added; what the mask does not
+    allow becomes -inf.  The result has the logits' type or is float32 (out_dtype,
+    `out`); out may be the logits themselves, of which then only those that change
+    are written.  Rows of any stride; input rows that share memory are copied apart."""
+    given = logits
+    logits, ld = _input_rows("adjust_logits", "logits", logits, stream)
+    shape = logits.shape
+    m, vocab = shape
+    if not isinstance(rules, LogitRules) or rules.m != m or rules.vocab != vocab:
+        raise ValueError(f"adjust_logits: takes LogitRules for {m} rows of {vocab} logits")
+    code = _CODES.get(logits.dtype)
+    if code is None:
+        raise TypeError(f"adjust_logits: unsupported dtype {logits.dtype}")
+    index = _gpu("adjust_logits", logits)
+    if rules._index is not None and rules._index != index:
+        raise ValueError(f"adjust_logits: the rules' tensors are on {rules.device}, the logits on {logits.device}")
+    if _current_device() != index:
+        with torch.cuda.device(index):
+            return adjust_logits(given, rules, out, out_dtype, stream)
+    if out is None:
+        out = _empty(shape, out_dtype or logits.dtype, logits.device, stream)
+        ldo = 0
+    else:
+        ldo = _output("adjust_logits", "out", out, index, shape, out_dtype)
+    _check(_lib.skinny_adjust_logits_run(m, vocab, logits.data_ptr(), ld, code, rules._addr, out.data_ptr(), ldo,
+                                         _CODES.get(out.dtype, 0), _handle(index, stream)), "skinny_adjust_logits_run")
+    return out

@@ -16,7 +16,7 @@ OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libskinny.so")
 ARCH = "gfx950"
 SOURCES = ["abi.cpp", "abi_window.cpp", "gemv.hip", "gemm.hip", "combine.hip", "w4.hip", "moe.hip", "logprobs.hip",
-           "static_scratch.hip"]
+           "abi_requests.cpp", "norm.hip", "adapters.hip", "adjust.hip", "static_scratch.hip"]
 # sources compiled once per kernel family member: (source, object name, defines)
 INSTANCES = [
     ("gemv_inst.hip", f"gemv_{w}{'_a32' if a == 'kAF32' else ''}_t{t}",

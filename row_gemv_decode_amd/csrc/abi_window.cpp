@@ -6,6 +6,7 @@
 
 #include <new>
 
+#include "abi_checks.h"
 #include "skinny_window.h"
 #include "window.h"
 
@@ -13,27 +14,7 @@ using namespace skinny;
 
 namespace {
 
-bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
-
-int kind_of(int32_t dt) { return dt == SKINNY_F32 ? CK_F32 : dt == SKINNY_F16 ? CK_F16 : CK_BF16; }
-bool half_type(int32_t dt) { return dt == SKINNY_F16 || dt == SKINNY_BF16; }
-bool float_type(int32_t dt) { return half_type(dt) || dt == SKINNY_F32; }
-int64_t size_of(int32_t dt) { return dt == SKINNY_F32 ? 4 : 2; }
-
-// two byte ranges share a byte (a null pointer shares none)
-bool overlap(const void* a, int64_t abytes, const void* b, int64_t bbytes) {
-  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
-  return a != nullptr && b != nullptr && a0 < b0 + (uintptr_t)bbytes && b0 < a0 + (uintptr_t)abytes;
-}
-
-skinny_status hip_status(hipError_t e) { return e == hipSuccess ? SKINNY_OK : SKINNY_ERR_HIP; }
-
-constexpr int64_t kMaxDim = (1LL << 31) - 1;
-
 bool group_ok(int32_t group) { return group == 32 || group == 64 || group == 128; }
-
-// bytes from the first element of row 0 to the last of row rows - 1
-int64_t span(int64_t rows, int64_t ld, int64_t len, int64_t size) { return ((rows - 1) * ld + len) * size; }
 
 int64_t round256(int64_t b) { return (b + 255) / 256 * 256; }
 

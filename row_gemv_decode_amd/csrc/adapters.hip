@@ -1,0 +1,497 @@
+// adapters.hip -- low-rank adapters of many requests beside a shared projection,
+// for gfx950 (MI355X).
+//
+//   out_t = base_t + scaling[a] B[a] (A[a] x_t),   a = ids[t]
+//
+// Two launches.  The first ("down") gives the inner values A x of every row, the
+// second ("up") multiplies them by B and adds the base.  Rows of one adapter are
+// gathered into tiles, so that 16 rows share one read of the adapter's weights
+// (64 in batches of more than kAdaptDirectRows rows) and a matrix-core step has
+// rows to multiply.  For few rows each workgroup finds its tile in the list of
+// ids by itself, which costs no more than reading its own id would: a wave
+// compares 64 ids per ballot.  For many, one more launch before the two sorts
+// the rows by adapter.
+//
+// Down: v_mfma_f32_16x16x32 over k, which is split over the workgroup's waves and
+// over workgroups; the workgroups' parts go to memory in fp32 and the up launch
+// adds them in order.  Up: the inner values keep 24 bits as three bf16 planes
+// (each the rounded remainder of the last), so that the result is that of fp32
+// products; bf16 weights then take three matrix-core steps, and f16 weights,
+// which are the exact sum of two bf16 numbers, five (the two products of the
+// lowest planes lie below 2^-24).  Planes in f16 would lose small inner values.
+// The work of both is bound by memory: by latency for a few rows, for many by x
+// in the one and base and out in the other.
+#include "requests.h"
+#include "vector_io.h"
+#include "window_kernel.h"
+
+namespace skinny {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWaves = 4;
+constexpr int kNoBase = -1;
+
+__device__ __forceinline__ int id_at(const AdaptArgs& g, int t) {  // -1: no adapter
+  const int64_t a = g.ids64 != 0 ? ((const int64_t*)g.ids)[t] : (int64_t)((const int32_t*)g.ids)[t];
+  return a >= 0 && a < g.count ? (int)a : -1;
+}
+
+__device__ __forceinline__ int rank_of(const AdaptArgs& g, int a) {
+  if (a < 0) return 0;
+  if (g.ranks == nullptr) return g.rank;
+  const int r = g.ranks[a];
+  return r >= 1 && r <= g.rank ? r : 0;
+}
+
+// The rows of tile `index`, in rows_s, after the next barrier; false if there is no
+// such tile (the same in every thread).
+struct Tile {
+  int adapter, rows;
+};
+template <bool LIST>
+__device__ __forceinline__ bool find_tile(const AdaptArgs& g, int index, int* rows_s, Tile& tile) {
+  const int tid = threadIdx.x;
+  if constexpr (LIST) {
+    if (index >= (int)g.tiles[0]) return false;
+    const uint32_t* t = g.tiles + 4 + 4 * index;
+    tile.adapter = (int)t[0];
+    tile.rows = (int)t[2];
+    if (tid < tile.rows) rows_s[tid] = (int)g.order[t[1] + tid];
+    return true;
+  } else {
+    // The tile of row `index`, if that row is the first of 16 of its adapter.
+    constexpr int kChunks = kAdaptDirectRows / 64;
+    const int lane = tid & 63;
+    int a[kChunks];
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) a[c] = c * 64 + lane < g.m ? id_at(g, c * 64 + lane) : -2;
+    const int mine = __builtin_amdgcn_readfirstlane(id_at(g, index));
+    uint64_t same[kChunks];
+    int before = 0, all = 0;
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+      same[c] = __builtin_amdgcn_ballot_w64(a[c] == mine);
+      const int below = index - c * 64;  // rows of this chunk that come first
+      const uint64_t low = below <= 0 ? 0 : below >= 64 ? ~0ull : (1ull << below) - 1;
+      before += __builtin_popcountll(same[c] & low);
+    }
+    if ((before & 15) != 0) return false;
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+      const int place = all + __builtin_popcountll(same[c] & ((1ull << lane) - 1)) - before;
+      if (tid < 64 && (same[c] >> lane & 1) != 0 && place >= 0 && place < 16) rows_s[place] = c * 64 + lane;
+      all += __builtin_popcountll(same[c]);
+    }
+    tile.adapter = mine;
+    tile.rows = min(16, all - before);
+    return true;
+  }
+}
+
+// --- sorting the rows of a large batch ---------------------------------------
+// One workgroup counts the rows of each adapter (those without one last), places
+// the tiles and the rows behind one another.  The order of the rows within an
+// adapter is that of the atomics; no row's result depends on it.
+constexpr int kSortThreads = 1024;
+constexpr int kSortEach = (kAdaptersMax + 1 + kSortThreads - 1) / kSortThreads;
+
+// adds `v` at counts[a] for every active lane and gives the lane its place; a
+// wave of one adapter's rows adds once
+__device__ __forceinline__ uint32_t take_places(uint32_t* counts, int a, bool active) {
+  const uint64_t on = __builtin_amdgcn_ballot_w64(active);
+  if (on == 0) return 0;
+  const int lane = threadIdx.x & 63;
+  const int leader = __builtin_ctzll(on);
+  const int first = __builtin_amdgcn_readlane(a, leader);
+  if (__builtin_amdgcn_ballot_w64(active && a == first) == on) {
+    uint32_t at = 0;
+    if (lane == leader) at = atomicAdd(&counts[first], (uint32_t)__builtin_popcountll(on));
+    at = (uint32_t)__builtin_amdgcn_readlane((int)at, leader);
+    return at + (uint32_t)__builtin_popcountll(on & ((1ull << lane) - 1));
+  }
+  return active ? atomicAdd(&counts[a], 1u) : 0;
+}
+
+__global__ __launch_bounds__(kSortThreads) void adapter_sort_kernel(AdaptArgs g) {
+  __shared__ uint32_t counts_s[kSortEach * kSortThreads];
+  __shared__ uint32_t rows_s[kSortThreads / 64], tiles_s[kSortThreads / 64];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+#pragma unroll
+  for (int i = 0; i < kSortEach; ++i) counts_s[i * kSortThreads + tid] = 0;
+  __syncthreads();
+  for (int t0 = 0; t0 < g.m; t0 += kSortThreads) {
+    const int t = t0 + tid;
+    const int a = t < g.m ? id_at(g, t) : 0;
+    take_places(counts_s, a < 0 ? g.count : a, t < g.m);
+  }
+  __syncthreads();
+  // each thread's consecutive adapters, then the sums of the threads before it
+  uint32_t rows = 0, tiles = 0, count[kSortEach];
+#pragma unroll
+  for (int i = 0; i < kSortEach; ++i) {
+    count[i] = counts_s[tid * kSortEach + i];
+    rows += count[i];
+    tiles += (count[i] + kAdaptTileRows - 1) / kAdaptTileRows;
+  }
+  uint32_t row_at = rows, tile_at = tiles;  // inclusive sums over the wave
+#pragma unroll
+  for (int s = 1; s < 64; s *= 2) {
+    const uint32_t r = (uint32_t)__shfl_up((int)row_at, s), t = (uint32_t)__shfl_up((int)tile_at, s);
+    if (lane >= s) row_at += r, tile_at += t;
+  }
+  if (lane == 63) rows_s[wave] = row_at, tiles_s[wave] = tile_at;
+  __syncthreads();
+  row_at -= rows, tile_at -= tiles;
+  for (int i = 0; i < wave; ++i) row_at += rows_s[i], tile_at += tiles_s[i];
+  if (tid == kSortThreads - 1) g.tiles[0] = tile_at + tiles;
+#pragma unroll
+  for (int i = 0; i < kSortEach; ++i) {
+    const int a = tid * kSortEach + i;
+    counts_s[a] = row_at;
+    for (uint32_t done = 0; done < count[i]; done += kAdaptTileRows) {
+      uint32_t* t = g.tiles + 4 + 4 * tile_at++;
+      t[0] = a < g.count ? (uint32_t)a : ~0u;
+      t[1] = row_at + done;
+      t[2] = min(count[i] - done, (uint32_t)kAdaptTileRows);
+    }
+    row_at += count[i];
+  }
+  __syncthreads();
+  for (int t0 = 0; t0 < g.m; t0 += kSortThreads) {
+    const int t = t0 + tid;
+    const int a = t < g.m ? id_at(g, t) : 0;
+    const uint32_t at = take_places(counts_s, a < 0 ? g.count : a, t < g.m);
+    if (t < g.m) g.order[at] = (uint32_t)t;
+  }
+}
+
+// --- down: the inner values --------------------------------------------------
+// A workgroup: 16 TR rows, 16 NR ranks, one split of k.  Its waves take every
+// fourth 64 elements of the split (128 bytes of a row), UN of them at once.
+template <int TR, int NR>
+constexpr int down_units() { return TR == 1 ? (NR == 1 ? 4 : 2) : (NR == 4 ? 1 : 2); }
+
+template <int TK, int TR, int NR>
+__global__ __launch_bounds__(kThreads) void adapter_down_kernel(AdaptArgs g) {
+  constexpr bool LIST = TR > 1;
+  constexpr int UN = down_units<TR, NR>();
+  extern __shared__ f32x4 sums_s[];  // [waves][TR][NR][64]
+  __shared__ int rows_s[16 * TR];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int split = (int)blockIdx.x % g.splits;
+  const int rank0 = (int)blockIdx.x / g.splits * (16 * NR);
+  Tile tile;
+  if (!find_tile<LIST>(g, blockIdx.y, rows_s, tile)) return;
+  const int rank = rank_of(g, tile.adapter);
+  if (rank0 >= rank) return;
+  __syncthreads();
+
+  const int low = lane & 15, h = lane >> 4;
+  const uint16_t* x[TR];
+#pragma unroll
+  for (int t = 0; t < TR; ++t) {
+    const int i = t * 16 + low;
+    x[t] = (const uint16_t*)g.x + rows_s[i < tile.rows ? i : 0] * g.ldx + 8 * h;
+  }
+  const uint16_t* w[NR];
+#pragma unroll
+  for (int n = 0; n < NR; ++n) {
+    const int j = rank0 + n * 16 + low;
+    w[n] = (const uint16_t*)g.A + ((int64_t)tile.adapter * g.rank + (j < rank ? j : 0)) * g.k + 8 * h;
+  }
+  const int begin = split * g.split_len;
+  const int len = min(g.split_len, g.k - begin);
+  const int units = (len + 63) / 64;
+  f32x4 acc[TR][NR];
+#pragma unroll
+  for (int t = 0; t < TR; ++t)
+#pragma unroll
+    for (int n = 0; n < NR; ++n) acc[t][n] = f32x4{0, 0, 0, 0};
+  for (int u0 = wave; u0 < units; u0 += kWaves * UN) {
+    u32x4 xf[UN][2][TR], wf[UN][2][NR];
+#pragma unroll
+    for (int u = 0; u < UN; ++u)
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        // past the split: any elements of the row, which count as 0
+        const int at = (u0 + u * kWaves) * 64 + b * 32;
+        const bool in = at + 8 * h < len;
+        const int k0 = in ? begin + at : -8 * h;
+#pragma unroll
+        for (int t = 0; t < TR; ++t) {
+          const u32x4 v = *(const u32x4*)(x[t] + k0);
+          xf[u][b][t] = in ? v : u32x4{0, 0, 0, 0};
+        }
+#pragma unroll
+        for (int n = 0; n < NR; ++n) wf[u][b][n] = *(const u32x4*)(w[n] + k0);
+      }
+#pragma unroll
+    for (int u = 0; u < UN; ++u)
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int t = 0; t < TR; ++t)
+#pragma unroll
+          for (int n = 0; n < NR; ++n) acc[t][n] = mfma16<TK>(wf[u][b][n], xf[u][b][t], acc[t][n]);
+  }
+  // a lane holds ranks 4 h .. 4 h + 3 of row low: the waves' parts are added in
+  // the order of the waves
+#pragma unroll
+  for (int t = 0; t < TR; ++t)
+#pragma unroll
+    for (int n = 0; n < NR; ++n) sums_s[((wave * TR + t) * NR + n) * 64 + lane] = acc[t][n];
+  __syncthreads();
+#pragma unroll
+  for (int i0 = 0; i0 < TR * NR; i0 += kWaves) {
+    const int i = i0 + wave;
+    if (TR * NR < kWaves && i >= TR * NR) break;
+    f32x4 s = sums_s[i * 64 + lane];
+#pragma unroll
+    for (int v = 1; v < kWaves; ++v) s += sums_s[(v * TR * NR + i) * 64 + lane];
+    const int row = i / NR * 16 + low, j = rank0 + i % NR * 16 + 4 * h;
+    if (row < tile.rows && j < rank)
+      *(f32x4*)(g.h + ((int64_t)split * g.m + rows_s[row]) * g.rank + j) = s;
+  }
+}
+
+// --- up: B's product and the sum ---------------------------------------------
+constexpr int kPlanes = 3;
+constexpr int kColTiles = 4;               // 16 columns each, per wave
+constexpr int kWaveCols = 16 * kColTiles;  // a lane holds kColTiles consecutive columns of its rows
+constexpr int kBlockCols = kWaveCols * kWaves;
+
+// the remainder of v past its rounding to bf16, which is left in `bits`
+__device__ __forceinline__ float bf16_plane(float v, uint16_t& bits) {
+  bits = f32_half<CK_BF16>(v);
+  return v - f32_from_bits((uint32_t)bits << 16);
+}
+
+// eight f16 weights as the sum of two bf16 numbers each
+__device__ __forceinline__ void f16_planes(u32x4 w, u32x4& hi, u32x4& lo) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const uint32_t u = w[q];
+    const h2_t v = as_h2(u);
+    const float a = (float)v[0], b = (float)v[1];
+    const uint32_t top = pack2<CK_BF16>(a, b);
+    hi[q] = top;
+    lo[q] = pack2<CK_BF16>(a - f32_from_bits(top << 16), b - f32_from_bits(top & 0xffff0000u));
+  }
+}
+
+template <int TK, int TR, int BK>
+__global__ __launch_bounds__(kThreads) void adapter_up_kernel(AdaptArgs g, int col_blocks) {
+  constexpr bool LIST = TR > 1;
+  extern __shared__ uint16_t planes_s[];  // [planes][16 TR][pitch]
+  __shared__ int rows_s[16 * TR];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  Tile tile;
+  if (!find_tile<LIST>(g, blockIdx.y, rows_s, tile)) return;
+  const int rank = rank_of(g, tile.adapter);
+  if (rank == 0 && g.out == g.base) return;  // nothing to add
+  const float scale = rank == 0 || g.scaling == nullptr ? 1.0f : g.scaling[tile.adapter];
+  const int steps = (rank + 31) / 32;
+  const int pitch = (g.rank + 31) / 32 * 32 + 8;
+  __syncthreads();
+
+  // the rows' inner values: the splits' parts in order, four ranks per thread
+  for (int e = tid; e < tile.rows * steps * 8; e += kThreads) {
+    const int row = e / (steps * 8), j = e % (steps * 8) * 4;
+    f32x4 v = f32x4{0, 0, 0, 0};
+    if (j < rank) {
+      const float* part = g.h + (int64_t)rows_s[row] * g.rank + j;
+      for (int s = 0; s < g.splits; ++s) v += *(const f32x4*)(part + (int64_t)s * g.m * g.rank);
+    }
+    uint16_t bits[kPlanes][4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      float rest = j + q < rank ? v[q] : 0.0f;
+#pragma unroll
+      for (int p = 0; p < kPlanes; ++p) rest = bf16_plane(rest, bits[p][q]);
+    }
+#pragma unroll
+    for (int p = 0; p < kPlanes; ++p)
+      *(u32x2*)&planes_s[(p * 16 * TR + row) * pitch + j] =
+          u32x2{bits[p][0] | (uint32_t)bits[p][1] << 16, bits[p][2] | (uint32_t)bits[p][3] << 16};
+  }
+  __syncthreads();
+
+  const int low = lane & 15, h = lane >> 4;
+  const uint16_t* wb = (const uint16_t*)g.B + (int64_t)max(tile.adapter, 0) * g.n * g.rank;
+  int row_of[TR][4];  // the lane's rows, -1 past the tile
+#pragma unroll
+  for (int t = 0; t < TR; ++t)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int i = t * 16 + 4 * h + q;
+      row_of[t][q] = i < tile.rows ? rows_s[i] : -1;
+    }
+  for (int cb = 0; cb < col_blocks; ++cb) {
+    const int col = ((int)blockIdx.x * col_blocks + cb) * kBlockCols + wave * kWaveCols;
+    if (col >= g.n) break;
+    const int c0 = col + low * kColTiles;
+    const bool whole = c0 + kColTiles <= g.n;
+    Raw<BK == kNoBase ? CK_F32 : BK, kColTiles> base[TR][4];
+    if constexpr (BK != kNoBase) {
+#pragma unroll
+      for (int t = 0; t < TR; ++t)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (g.n >= kColTiles)
+            base[t][q] = load_raw<BK, kColTiles>(g.base, max(row_of[t][q], 0) * g.ldb + (whole ? c0 : 0));
+    }
+    f32x4 acc[TR][kColTiles];
+#pragma unroll
+    for (int t = 0; t < TR; ++t)
+#pragma unroll
+      for (int s = 0; s < kColTiles; ++s) acc[t][s] = f32x4{0, 0, 0, 0};
+    for (int b = 0; b < steps; ++b) {
+      const int k0 = b * 32 + 8 * h;
+      const int valid = rank - k0;  // elements of this lane's eight that count
+      u32x4 w[kColTiles];
+#pragma unroll
+      for (int s = 0; s < kColTiles; ++s) {
+        const int64_t c = min(c0 + s, g.n - 1);
+        w[s] = *(const u32x4*)(wb + c * g.rank + (valid > 0 ? k0 : 0));
+      }
+      u32x4 keep;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) keep[q] = valid >= 2 * q + 2 ? ~0u : valid == 2 * q + 1 ? 0xffffu : 0u;
+      u32x4 lo[kColTiles];
+#pragma unroll
+      for (int s = 0; s < kColTiles; ++s) {
+        w[s] &= keep;
+        if constexpr (TK == CK_F16) f16_planes(w[s], w[s], lo[s]);
+      }
+#pragma unroll
+      for (int t = 0; t < TR; ++t) {
+        if (t * 16 >= tile.rows) break;
+        u32x4 v[kPlanes];
+#pragma unroll
+        for (int p = 0; p < kPlanes; ++p) v[p] = *(const u32x4*)&planes_s[((p * TR + t) * 16 + low) * pitch + k0];
+#pragma unroll
+        for (int p = kPlanes - 1; p >= 0; --p)
+#pragma unroll
+          for (int s = 0; s < kColTiles; ++s) {
+            if constexpr (TK == CK_F16) {
+              if (p < kPlanes - 1) acc[t][s] = mfma16<CK_BF16>(v[p], lo[s], acc[t][s]);
+            }
+            acc[t][s] = mfma16<CK_BF16>(v[p], w[s], acc[t][s]);
+          }
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < TR; ++t)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int row = row_of[t][q];
+        if (row < 0) continue;
+        float v[kColTiles];
+        if (whole) {
+          if constexpr (BK != kNoBase) {
+            unpack_raw<BK, kColTiles>(base[t][q], v);
+          } else {
+#pragma unroll
+            for (int s = 0; s < kColTiles; ++s) v[s] = 0.0f;
+          }
+        } else {
+#pragma unroll
+          for (int s = 0; s < kColTiles; ++s) {
+            v[s] = 0.0f;
+            if constexpr (BK != kNoBase) {
+              if (c0 + s < g.n) v[s] = value_at<BK>(g.base, row * g.ldb + c0 + s);
+            }
+          }
+        }
+        if (rank != 0) {
+#pragma unroll
+          for (int s = 0; s < kColTiles; ++s) v[s] = __builtin_fmaf(scale, acc[t][s][q], v[s]);
+        }
+        const int64_t at = row * g.ldo + c0;
+        if (whole) {
+          if (g.out_kind == CK_F32) {
+            store_vec<CK_F32, kColTiles>(g.out, at, v);
+          } else {
+            store_vec<TK, kColTiles>(g.out, at, v);
+          }
+        } else {
+#pragma unroll
+          for (int s = 0; s < kColTiles; ++s)
+            if (c0 + s < g.n) {
+              if (g.out_kind == CK_F32) {
+                store_out<CK_F32>(g.out, at + s, v[s]);
+              } else {
+                store_out<TK>(g.out, at + s, v[s]);
+              }
+            }
+        }
+      }
+  }
+}
+
+template <int TK, int TR>
+hipError_t launch_tiles(const AdaptArgs& a, hipStream_t stream) {
+  const unsigned tiles = (unsigned)(TR == 1 ? a.m : a.max_tiles);
+  const int nr = a.rank > 32 ? 4 : a.rank > 16 ? 2 : 1;
+  const unsigned blocks = (unsigned)((a.rank + 16 * nr - 1) / (16 * nr) * a.splits);
+  const size_t lds = (size_t)kWaves * TR * nr * 64 * sizeof(f32x4);
+  const auto down = nr == 1   ? adapter_down_kernel<TK, TR, 1>
+                    : nr == 2 ? adapter_down_kernel<TK, TR, 2> : adapter_down_kernel<TK, TR, 4>;
+  hipLaunchKernelGGL(down, dim3(blocks, tiles), dim3(kThreads), lds, stream, a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const int col_blocks = TR == 1 ? 1 : 4;
+  const unsigned cols = (unsigned)((a.n + kBlockCols * col_blocks - 1) / (kBlockCols * col_blocks));
+  const size_t planes = (size_t)kPlanes * 16 * TR * ((a.rank + 31) / 32 * 32 + 8) * 2;
+  const auto up = a.base == nullptr          ? adapter_up_kernel<TK, TR, kNoBase>
+                  : a.base_kind == CK_F32 ? adapter_up_kernel<TK, TR, CK_F32> : adapter_up_kernel<TK, TR, TK>;
+  if (planes > 65536) {
+    e = hipFuncSetAttribute((const void*)up, hipFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024 - 1024);
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL(up, dim3(cols, tiles), dim3(kThreads), planes, stream, a, col_blocks);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+int adapt_splits(int64_t m, int64_t k, int64_t rank, int64_t* split_len) {
+  // 16 rows and fewer: a wave takes 64 elements of k (the same at every m, and so
+  // the same bits)
+  int64_t len = m <= kGemvMaxM ? 256 : m <= 64 ? 512 : 1024;
+  if (m > kAdaptDirectRows) {
+    const int64_t nr = rank > 32 ? 4 : rank > 16 ? 2 : 1;
+    const int64_t groups = (m + kAdaptTileRows - 1) / kAdaptTileRows * ((rank + 16 * nr - 1) / (16 * nr));
+    const int64_t want = (256 + groups - 1) / groups;
+    len = (k + want - 1) / want;
+    len = (len + 255) / 256 * 256;
+  }
+  while ((k + len - 1) / len > 32) len *= 2;
+  *split_len = len;
+  return (int)((k + len - 1) / len);
+}
+
+int64_t adapt_max_tiles(int64_t m, int64_t count) {
+  if (m <= kAdaptDirectRows) return 0;
+  const int64_t groups = count + 1 < m ? count + 1 : m;
+  return m / kAdaptTileRows + groups;
+}
+
+hipError_t launch_adapters(const AdaptArgs& a, int kind, hipStream_t stream) {
+  if (a.m < 1 || a.rank < 8 || a.rank % 8 != 0 || a.rank > kAdapterRankMax || a.count < 1 || a.count > kAdaptersMax ||
+      a.k % 8 != 0 || a.splits < 1 || (int64_t)a.splits * a.split_len < a.k || a.split_len % 256 != 0 ||
+      a.max_tiles > 65535)
+    return hipErrorInvalidValue;
+  if (a.m <= kAdaptDirectRows)
+    return kind == CK_F16 ? launch_tiles<CK_F16, 1>(a, stream) : launch_tiles<CK_BF16, 1>(a, stream);
+  hipLaunchKernelGGL(adapter_sort_kernel, dim3(1), dim3(kSortThreads), 0, stream, a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  return kind == CK_F16 ? launch_tiles<CK_F16, 4>(a, stream) : launch_tiles<CK_BF16, 4>(a, stream);
+}
+
+}  // namespace skinny

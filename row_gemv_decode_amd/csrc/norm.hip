@@ -1,0 +1,383 @@
+// norm.hip -- the residual's addition and a root-mean-square norm, with a 16-
+// or 32-bit output and / or one in 8 bits (e4m3) with scales, for gfx950
+// (MI355X).
+//
+//   h = x + r,  y = h / sqrt(mean(h^2) + eps) * w,  s_g = max|y| / 448,  q = e4m3(y / s_g)
+//
+// One pass over the data: a row's h stays in registers between the sum of its
+// squares and its outputs, and every load of a row (the weight's too) is issued
+// before the first arithmetic.  HBM-bound for many rows; for few, one launch
+// and one memory round trip.
+//
+// A lane holds CH chunks of eight consecutive values.  A row of up to 1024
+// values belongs to 8 to 64 lanes of one wave, so that no barrier is needed and
+// short rows fill a wave together; a longer one to a workgroup of its own.
+// Rows past 32768 values do not stay in registers and are read two or three
+// times (norm_long_kernel).
+//
+// q is y times the reciprocal of its scale: the quotient rounded once more,
+// 2^-23 off at the most before it is rounded to 8 bits.  |y / s| is at most
+// 448 (1 + 2^-22), which rounds to 448, so nothing has to be clamped and a NaN
+// stays one.
+#include "requests.h"
+#include "vector_io.h"
+#include "wave_ops.h"
+
+namespace skinny {
+
+namespace {
+
+constexpr int kNone = -1;  // RK: no residual
+constexpr float kTop8 = 448.0f;  // largest e4m3 value
+constexpr float kLeastScale = 1.17549435e-38f;  // 2^-126: a group of zeros has codes 0, not NaN
+
+// sum or maximum over `lanes` (8 .. 64) consecutive lanes, in all of them; the
+// steps past 8 lanes are uniform branches
+template <bool MAX>
+__device__ __forceinline__ float lanes_reduce(float v, int lanes) {
+  auto join = [](float a, float b) { return MAX ? fmaxf(a, b) : a + b; };
+  v = join(v, dpp_mov<kDppXor1>(v));
+  v = join(v, dpp_mov<kDppXor2>(v));
+  if (lanes > 4) v = join(v, dpp_mov<kDppRowHalfMirror>(v));
+  if (lanes > 8) v = join(v, dpp_mov<kDppRowMirror>(v));
+  if (lanes > 16) {
+    auto r = __builtin_amdgcn_permlane16_swap(ubits(v), ubits(v), false, false);
+    v = join(fbits(r[0]), fbits(r[1]));
+  }
+  if (lanes > 32) {
+    auto r = __builtin_amdgcn_permlane32_swap(ubits(v), ubits(v), false, false);
+    v = join(fbits(r[0]), fbits(r[1]));
+  }
+  return v;
+}
+
+// the same over the waves of a workgroup, in the order of the waves
+template <bool MAX>
+__device__ __forceinline__ float block_reduce(float v, float* parts, int waves) {
+  v = lanes_reduce<MAX>(v, 64);
+  if (waves > 1) {
+    if ((threadIdx.x & 63) == 0) parts[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = parts[0];
+    for (int i = 1; i < waves; ++i) v = MAX ? fmaxf(v, parts[i]) : v + parts[i];
+  }
+  return v;
+}
+
+// values e0 .. e0 + 7 of a row, 0 from d on.  In a vector where all lie in the
+// row (else any eight of it, where it has eight, so that no load is behind a
+// branch), and one by one at the row's end.
+template <int K>
+__device__ __forceinline__ void load8(const void* row, int e0, int d, float (&x)[8]) {
+  Raw<K, 8> raw;
+  const bool whole = e0 + 8 <= d;
+  if (d >= 8) raw = load_raw<K, 8>(row, whole ? e0 : 0);
+  if (whole) {
+    unpack_raw<K, 8>(raw, x);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = 0.0f;
+    if (d % 8 != 0 && e0 < d) {
+#pragma unroll
+      for (int e = 0; e < 7; ++e)
+        if (e0 + e < d) x[e] = value_at<K>(row, e0 + e);
+    }
+  }
+}
+
+template <int K>
+__device__ __forceinline__ void store8(void* row, int e0, int d, const float (&x)[8]) {
+  if (e0 + 8 <= d) {
+    store_vec<K, 8>(row, e0, x);
+  } else if (d % 8 != 0) {
+#pragma unroll
+    for (int e = 0; e < 7; ++e)
+      if (e0 + e < d) store_out<K>(row, e0 + e, x[e]);
+  }
+}
+
+__device__ __forceinline__ void store8_kind(void* row, int kind, int e0, int d, const float (&x)[8]) {
+  if (kind == CK_F32) {
+    store8<CK_F32>(row, e0, d, x);
+  } else if (kind == CK_F16) {
+    store8<CK_F16>(row, e0, d, x);
+  } else {
+    store8<CK_BF16>(row, e0, d, x);
+  }
+}
+
+__device__ __forceinline__ void load_weight8(const NormArgs& g, int e0, float (&w)[8]) {
+  if (g.weight == nullptr) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e] = 1.0f;
+  } else if (g.w_kind == CK_F32) {
+    load8<CK_F32>(g.weight, e0, g.d, w);
+  } else if (g.w_kind == CK_F16) {
+    load8<CK_F16>(g.weight, e0, g.d, w);
+  } else {
+    load8<CK_BF16>(g.weight, e0, g.d, w);
+  }
+}
+
+__device__ __forceinline__ float max8(const float (&y)[8]) {
+  float m = 0.0f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(y[e]));
+  return m;
+}
+
+__device__ __forceinline__ float scale_of(float top) { return fmaxf(top / kTop8, kLeastScale); }
+
+__device__ __forceinline__ void store8_q(uint8_t* row, int e0, int d, const float (&y)[8], float inv) {
+  uint32_t w[2];
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    int v = 0;
+    v = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * q] * inv, y[4 * q + 1] * inv, v, false);
+    v = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * q + 2] * inv, y[4 * q + 3] * inv, v, true);
+    w[q] = (uint32_t)v;
+  }
+  if (e0 + 8 <= d) {
+    *(u32x2_align1*)(row + e0) = u32x2{w[0], w[1]};
+  } else if (d % 8 != 0) {
+#pragma unroll
+    for (int e = 0; e < 7; ++e)
+      if (e0 + e < d) row[e0 + e] = (uint8_t)(w[e / 4] >> (8 * (e % 4)));
+  }
+}
+
+struct RowPtrs {
+  const char *x, *r;
+  char *ro, *out;
+  uint8_t* q;
+  float* scales;
+};
+template <int XK, int RK>
+__device__ __forceinline__ RowPtrs row_ptrs(const NormArgs& g, int64_t row) {
+  RowPtrs p;
+  p.x = (const char*)g.x + row * g.ldx * kind_size<XK>();
+  p.r = RK == kNone ? nullptr : (const char*)g.residual + row * g.ldr * kind_size<RK>();
+  p.ro = RK == kNone || g.residual_out == nullptr ? nullptr : (char*)g.residual_out + row * g.ldro * kind_size<RK>();
+  p.out = g.out == nullptr ? nullptr : (char*)g.out + row * g.ldo * kind_bytes(g.out_kind);
+  p.q = g.q == nullptr ? nullptr : g.q + row * g.ldq;
+  p.scales = g.q == nullptr ? nullptr : g.scales + row * g.groups;
+  return p;
+}
+
+// A row of at most 8 CH lanes values.  BLOCK: the lanes of a workgroup, else
+// 2^lanes_log2 of a wave's.
+template <int XK, int RK, int CH, bool BLOCK>
+__global__ __launch_bounds__(BLOCK ? 1024 : 256) void norm_kernel(NormArgs g) {
+  __shared__ float parts_s[2][16];
+  const int tid = threadIdx.x;
+  const int lanes = BLOCK ? 64 : 1 << g.lanes_log2;
+  const int step = BLOCK ? (int)blockDim.x : lanes;
+  const int place = BLOCK ? tid : tid & (lanes - 1);
+  const int waves = BLOCK ? (int)blockDim.x >> 6 : 1;
+  const int64_t r = BLOCK ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * (256 >> g.lanes_log2) + (tid >> g.lanes_log2);
+  const bool active = BLOCK || r < g.m;
+  const int d = g.d;
+  const RowPtrs p = row_ptrs<XK, RK>(g, active ? r : 0);
+
+  float h[CH][8], w[CH][8];
+#pragma unroll
+  for (int c = 0; c < CH; ++c) load8<XK>(p.x, (c * step + place) * 8, d, h[c]);
+  if constexpr (RK != kNone) {
+    float res[CH][8];
+#pragma unroll
+    for (int c = 0; c < CH; ++c) load8<RK>(p.r, (c * step + place) * 8, d, res[c]);
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) h[c][e] += res[c][e];
+  }
+#pragma unroll
+  for (int c = 0; c < CH; ++c) load_weight8(g, (c * step + place) * 8, w[c]);
+
+  float sum = 0.0f;
+#pragma unroll
+  for (int c = 0; c < CH; ++c)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum = __builtin_fmaf(h[c][e], h[c][e], sum);
+  if constexpr (BLOCK) {
+    sum = block_reduce<false>(sum, parts_s[0], waves);
+  } else {
+    sum = lanes_reduce<false>(sum, lanes);
+  }
+  const float inv = 1.0f / sqrtf(sum / (float)d + g.eps);
+
+  // (every load of the row has arrived: its rows may be written in place)
+  if constexpr (RK != kNone) {
+    if (active && p.ro != nullptr) {
+#pragma unroll
+      for (int c = 0; c < CH; ++c) store8<RK>(p.ro, (c * step + place) * 8, d, h[c]);
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < CH; ++c)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) h[c][e] = h[c][e] * inv * w[c][e];
+  if (active && p.out != nullptr) {
+#pragma unroll
+    for (int c = 0; c < CH; ++c) store8_kind(p.out, g.out_kind, (c * step + place) * 8, d, h[c]);
+  }
+  if (p.q == nullptr) return;
+
+  float top[CH];
+#pragma unroll
+  for (int c = 0; c < CH; ++c) top[c] = max8(h[c]);
+  if (g.group == 0) {
+#pragma unroll
+    for (int c = 1; c < CH; ++c) top[0] = fmaxf(top[0], top[c]);
+    if constexpr (BLOCK) {
+      top[0] = block_reduce<true>(top[0], parts_s[1], waves);
+    } else {
+      top[0] = lanes_reduce<true>(top[0], lanes);
+    }
+    const float s = scale_of(top[0]), si = 1.0f / s;
+    if (active) {
+#pragma unroll
+      for (int c = 0; c < CH; ++c) store8_q(p.q, (c * step + place) * 8, d, h[c], si);
+      if (place == 0) p.scales[0] = s;
+    }
+  } else {
+    // a group is group / 8 lanes of one chunk (fewer where the row has fewer)
+    const int mine = min(g.group >> 3, lanes);
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int e0 = (c * step + place) * 8;
+      const float s = scale_of(lanes_reduce<true>(top[c], mine));
+      if (active) {
+        store8_q(p.q, e0, d, h[c], 1.0f / s);
+        if ((place & (mine - 1)) == 0 && e0 < d) p.scales[e0 / g.group] = s;
+      }
+    }
+  }
+}
+
+// Rows that do not fit the registers: one workgroup of 1024 per row, which reads
+// the row for the sum, once more for a scale of the whole row, and for the outputs.
+template <int XK, int RK>
+__global__ __launch_bounds__(1024) void norm_long_kernel(NormArgs g) {
+  __shared__ float parts_s[2][16];
+  constexpr int kStep = 8 * 1024;
+  const int d = g.d;
+  const RowPtrs p = row_ptrs<XK, RK>(g, blockIdx.x);
+  auto sum_at = [&](int e0, float(&h)[8]) {
+    load8<XK>(p.x, e0, d, h);
+    if constexpr (RK != kNone) {
+      float res[8];
+      load8<RK>(p.r, e0, d, res);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) h[e] += res[e];
+    }
+  };
+  auto norm_at = [&](int e0, float inv, float(&h)[8]) {
+    float w[8];
+    load_weight8(g, e0, w);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) h[e] = h[e] * inv * w[e];
+  };
+  const int first = (int)threadIdx.x * 8;
+  float sum = 0.0f;
+  for (int e0 = first; e0 < d; e0 += kStep) {
+    float h[8];
+    sum_at(e0, h);
+    float s = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s = __builtin_fmaf(h[e], h[e], s);
+    sum += s;
+  }
+  sum = block_reduce<false>(sum, parts_s[0], 16);
+  const float inv = 1.0f / sqrtf(sum / (float)d + g.eps);
+  float s = 0.0f;
+  if (p.q != nullptr && g.group == 0) {
+    float top = 0.0f;
+    for (int e0 = first; e0 < d; e0 += kStep) {
+      float h[8];
+      sum_at(e0, h);
+      norm_at(e0, inv, h);
+      top = fmaxf(top, max8(h));
+    }
+    s = scale_of(block_reduce<true>(top, parts_s[1], 16));
+    if (threadIdx.x == 0) p.scales[0] = s;
+  }
+  // (all lanes of a wave, so that groups are whole; a value is read and written
+  // by one thread, so rows may be written in place)
+  for (int e0 = first; e0 - first < d; e0 += kStep) {
+    float h[8];
+    sum_at(e0, h);
+    if constexpr (RK != kNone) {
+      if (p.ro != nullptr) store8<RK>(p.ro, e0, d, h);
+    }
+    norm_at(e0, inv, h);
+    if (p.out != nullptr) store8_kind(p.out, g.out_kind, e0, d, h);
+    if (p.q != nullptr) {
+      if (g.group != 0) {
+        s = scale_of(lanes_reduce<true>(max8(h), g.group >> 3));
+        if ((e0 & (g.group - 1)) == 0 && e0 < d) p.scales[e0 / g.group] = s;
+      }
+      store8_q(p.q, e0, d, h, 1.0f / s);
+    }
+  }
+}
+
+template <int XK, int RK>
+hipError_t launch_kinds(NormArgs a, hipStream_t stream) {
+  const int chunks = (a.d + 7) / 8;
+  const bool block = chunks > 128;
+  int threads = 256;
+  int64_t rows = 1;  // of a workgroup
+  void (*fn)(NormArgs) = nullptr;
+  if (!block) {
+    a.lanes_log2 = 3;
+    while (a.lanes_log2 < 6 && (1 << a.lanes_log2) < chunks) ++a.lanes_log2;
+    rows = 256 >> a.lanes_log2;
+    fn = chunks > 64 ? norm_kernel<XK, RK, 2, false> : norm_kernel<XK, RK, 1, false>;
+  } else if (chunks <= 4 * 1024) {
+    const int ch = chunks <= 1024 ? 1 : chunks <= 2 * 1024 ? 2 : 4;
+    threads = ((chunks + ch - 1) / ch + 63) / 64 * 64;
+    fn = ch == 1 ? norm_kernel<XK, RK, 1, true> : ch == 2 ? norm_kernel<XK, RK, 2, true> : norm_kernel<XK, RK, 4, true>;
+  } else {
+    threads = 1024;
+    fn = norm_long_kernel<XK, RK>;
+  }
+  const int64_t most = kMaxLaunchThreads / threads / 2 * rows;  // rows of a launch
+  for (int64_t r = 0; r < a.m; r += most) {
+    NormArgs part = a;
+    part.m = a.m - r < most ? a.m - r : most;
+    part.x = (const char*)a.x + r * a.ldx * kind_size<XK>();
+    if (RK != kNone) {
+      part.residual = (const char*)a.residual + r * a.ldr * kind_size<RK>();
+      if (a.residual_out != nullptr) part.residual_out = (char*)a.residual_out + r * a.ldro * kind_size<RK>();
+    }
+    if (a.out != nullptr) part.out = (char*)a.out + r * a.ldo * (a.out_kind == CK_F32 ? 4 : 2);
+    if (a.q != nullptr) {
+      part.q = a.q + r * a.ldq;
+      part.scales = a.scales + r * a.groups;
+    }
+    hipLaunchKernelGGL(fn, dim3((unsigned)((part.m + rows - 1) / rows)), dim3(threads), 0, stream, part);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+template <int XK>
+hipError_t launch_residual(const NormArgs& a, int r_kind, hipStream_t stream) {
+  return a.residual == nullptr ? launch_kinds<XK, kNone>(a, stream)
+         : r_kind == CK_F32    ? launch_kinds<XK, CK_F32>(a, stream)
+         : r_kind == CK_F16    ? launch_kinds<XK, CK_F16>(a, stream)
+                               : launch_kinds<XK, CK_BF16>(a, stream);
+}
+
+}  // namespace
+
+hipError_t launch_norm(const NormArgs& a, int x_kind, int r_kind, hipStream_t stream) {
+  if (a.m < 1 || a.d < 1 || (a.group != 0 && a.group != 32 && a.group != 64 && a.group != 128)) return hipErrorInvalidValue;
+  return x_kind == CK_F32   ? launch_residual<CK_F32>(a, r_kind, stream)
+         : x_kind == CK_F16 ? launch_residual<CK_F16>(a, r_kind, stream)
+                            : launch_residual<CK_BF16>(a, r_kind, stream);
+}
+
+}  // namespace skinny
