@@ -45,25 +45,27 @@ __device__ __forceinline__ int rank_of(const AdaptArgs& g, int a) {
   return r >= 1 && r <= g.rank ? r : 0;
 }
 
-// The rows of tile `index`, in rows_s, after the next barrier; false if there is no
-// such tile (the same in every thread).
+// The rows of tile `index` in rows_s; false if there is no such tile (the same in
+// every thread).  A tile of the list is read by the workgroup, and there once it
+// has met; in the direct form each wave finds it and has rows_s to itself.
 struct Tile {
   int adapter, rows;
 };
 template <bool LIST>
 __device__ __forceinline__ bool find_tile(const AdaptArgs& g, int index, int* rows_s, Tile& tile) {
-  const int tid = threadIdx.x;
   if constexpr (LIST) {
+    const int tid = threadIdx.x;
     if (index >= (int)g.tiles[0]) return false;
     const uint32_t* t = g.tiles + 4 + 4 * index;
     tile.adapter = (int)t[0];
     tile.rows = (int)t[2];
     if (tid < tile.rows) rows_s[tid] = (int)g.order[t[1] + tid];
+    __syncthreads();
     return true;
   } else {
     // The tile of row `index`, if that row is the first of 16 of its adapter.
     constexpr int kChunks = kAdaptDirectRows / 64;
-    const int lane = tid & 63;
+    const int lane = threadIdx.x & 63;
     int a[kChunks];
 #pragma unroll
     for (int c = 0; c < kChunks; ++c) a[c] = c * 64 + lane < g.m ? id_at(g, c * 64 + lane) : -2;
@@ -81,9 +83,10 @@ __device__ __forceinline__ bool find_tile(const AdaptArgs& g, int index, int* ro
 #pragma unroll
     for (int c = 0; c < kChunks; ++c) {
       const int place = all + __builtin_popcountll(same[c] & ((1ull << lane) - 1)) - before;
-      if (tid < 64 && (same[c] >> lane & 1) != 0 && place >= 0 && place < 16) rows_s[place] = c * 64 + lane;
+      if ((same[c] >> lane & 1) != 0 && place >= 0 && place < 16) rows_s[place] = c * 64 + lane;
       all += __builtin_popcountll(same[c]);
     }
+    wave_lds_order();
     tile.adapter = mine;
     tile.rows = min(16, all - before);
     return true;
@@ -95,9 +98,9 @@ __device__ __forceinline__ bool find_tile(const AdaptArgs& g, int index, int* ro
 // the tiles and the rows behind one another.  The order of the rows within an
 // adapter is that of the atomics; no row's result depends on it.
 constexpr int kSortThreads = 1024;
-constexpr int kSortEach = (kAdaptersMax + 1 + kSortThreads - 1) / kSortThreads;
+constexpr int kSortIds = 4;  // ids of a thread that are read once and kept
 
-// adds `v` at counts[a] for every active lane and gives the lane its place; a
+// adds 1 at counts[a] for every active lane and gives the lane its place; a
 // wave of one adapter's rows adds once
 __device__ __forceinline__ uint32_t take_places(uint32_t* counts, int a, bool active) {
   const uint64_t on = __builtin_amdgcn_ballot_w64(active);
@@ -115,25 +118,31 @@ __device__ __forceinline__ uint32_t take_places(uint32_t* counts, int a, bool ac
 }
 
 __global__ __launch_bounds__(kSortThreads) void adapter_sort_kernel(AdaptArgs g) {
-  __shared__ uint32_t counts_s[kSortEach * kSortThreads];
+  extern __shared__ uint32_t counts_s[];  // count + 1
   __shared__ uint32_t rows_s[kSortThreads / 64], tiles_s[kSortThreads / 64];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int places = g.count + 1;
+  auto place_of = [&](int t) {
+    const int a = id_at(g, min(t, g.m - 1));
+    return a < 0 ? g.count : a;
+  };
+  int kept[kSortIds];
 #pragma unroll
-  for (int i = 0; i < kSortEach; ++i) counts_s[i * kSortThreads + tid] = 0;
+  for (int i = 0; i < kSortIds; ++i) kept[i] = place_of(i * kSortThreads + tid);
+  for (int i = tid; i < places; i += kSortThreads) counts_s[i] = 0;
   __syncthreads();
-  for (int t0 = 0; t0 < g.m; t0 += kSortThreads) {
-    const int t = t0 + tid;
-    const int a = t < g.m ? id_at(g, t) : 0;
-    take_places(counts_s, a < 0 ? g.count : a, t < g.m);
-  }
+#pragma unroll
+  for (int i = 0; i < kSortIds; ++i) take_places(counts_s, kept[i], i * kSortThreads + tid < g.m);
+  for (int t0 = kSortIds * kSortThreads; t0 < g.m; t0 += kSortThreads)
+    take_places(counts_s, place_of(t0 + tid), t0 + tid < g.m);
   __syncthreads();
   // each thread's consecutive adapters, then the sums of the threads before it
-  uint32_t rows = 0, tiles = 0, count[kSortEach];
-#pragma unroll
-  for (int i = 0; i < kSortEach; ++i) {
-    count[i] = counts_s[tid * kSortEach + i];
-    rows += count[i];
-    tiles += (count[i] + kAdaptTileRows - 1) / kAdaptTileRows;
+  const int each = (places + kSortThreads - 1) / kSortThreads;
+  const int a0 = tid * each, a1 = min(a0 + each, places);
+  uint32_t rows = 0, tiles = 0;
+  for (int a = a0; a < a1; ++a) {
+    rows += counts_s[a];
+    tiles += (counts_s[a] + kAdaptTileRows - 1) / kAdaptTileRows;
   }
   uint32_t row_at = rows, tile_at = tiles;  // inclusive sums over the wave
 #pragma unroll
@@ -146,25 +155,25 @@ __global__ __launch_bounds__(kSortThreads) void adapter_sort_kernel(AdaptArgs g)
   row_at -= rows, tile_at -= tiles;
   for (int i = 0; i < wave; ++i) row_at += rows_s[i], tile_at += tiles_s[i];
   if (tid == kSortThreads - 1) g.tiles[0] = tile_at + tiles;
-#pragma unroll
-  for (int i = 0; i < kSortEach; ++i) {
-    const int a = tid * kSortEach + i;
+  for (int a = a0; a < a1; ++a) {
+    const uint32_t count = counts_s[a];
     counts_s[a] = row_at;
-    for (uint32_t done = 0; done < count[i]; done += kAdaptTileRows) {
+    for (uint32_t done = 0; done < count; done += kAdaptTileRows) {
       uint32_t* t = g.tiles + 4 + 4 * tile_at++;
       t[0] = a < g.count ? (uint32_t)a : ~0u;
       t[1] = row_at + done;
-      t[2] = min(count[i] - done, (uint32_t)kAdaptTileRows);
+      t[2] = min(count - done, (uint32_t)kAdaptTileRows);
     }
-    row_at += count[i];
+    row_at += count;
   }
   __syncthreads();
-  for (int t0 = 0; t0 < g.m; t0 += kSortThreads) {
-    const int t = t0 + tid;
-    const int a = t < g.m ? id_at(g, t) : 0;
-    const uint32_t at = take_places(counts_s, a < 0 ? g.count : a, t < g.m);
+  auto put = [&](int t, int a) {
+    const uint32_t at = take_places(counts_s, a, t < g.m);
     if (t < g.m) g.order[at] = (uint32_t)t;
-  }
+  };
+#pragma unroll
+  for (int i = 0; i < kSortIds; ++i) put(i * kSortThreads + tid, kept[i]);
+  for (int t0 = kSortIds * kSortThreads; t0 < g.m; t0 += kSortThreads) put(t0 + tid, place_of(t0 + tid));
 }
 
 // --- down: the inner values --------------------------------------------------
@@ -178,16 +187,16 @@ __global__ __launch_bounds__(kThreads) void adapter_down_kernel(AdaptArgs g) {
   constexpr bool LIST = TR > 1;
   constexpr int UN = down_units<TR, NR>();
   extern __shared__ f32x4 sums_s[];  // [waves][TR][NR][64]
-  __shared__ int rows_s[16 * TR];
+  __shared__ int lists_s[LIST ? 16 * TR : 16 * kWaves];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int split = (int)blockIdx.x % g.splits;
   const int rank0 = (int)blockIdx.x / g.splits * (16 * NR);
+  int* rows_s = lists_s + (LIST ? 0 : 16 * wave);
   Tile tile;
   if (!find_tile<LIST>(g, blockIdx.y, rows_s, tile)) return;
   const int rank = rank_of(g, tile.adapter);
   if (rank0 >= rank) return;
-  __syncthreads();
 
   const int low = lane & 15, h = lane >> 4;
   const uint16_t* x[TR];
@@ -282,13 +291,47 @@ __device__ __forceinline__ void f16_planes(u32x4 w, u32x4& hi, u32x4& lo) {
   }
 }
 
-template <int TK, int TR, int BK>
+// B's fragments of 16 kColTiles columns for one step of 32 ranks: lane (low, h) has
+// ranks 32 b + 8 h .. + 7 of columns c0 + s; what lies past the adapter's rank is 0
+template <int TK>
+struct WeightFrags {
+  u32x4 hi[kColTiles], lo[TK == CK_F16 ? kColTiles : 1];
+};
+template <int TK>
+__device__ __forceinline__ void load_frags(const AdaptArgs& g, const uint16_t* wb, int c0, int k0, WeightFrags<TK>& w) {
+#pragma unroll
+  for (int s = 0; s < kColTiles; ++s)
+    w.hi[s] = *(const u32x4*)(wb + (int64_t)min(c0 + s, g.n - 1) * g.rank + (k0 < g.rank ? k0 : 0));
+}
+template <int TK>
+__device__ __forceinline__ void finish_frags(int rank, int k0, WeightFrags<TK>& w) {
+  const int valid = rank - k0;  // elements of this lane's eight that count
+  u32x4 keep;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) keep[q] = valid >= 2 * q + 2 ? ~0u : valid == 2 * q + 1 ? 0xffffu : 0u;
+#pragma unroll
+  for (int s = 0; s < kColTiles; ++s) {
+    w.hi[s] &= keep;
+    if constexpr (TK == CK_F16) f16_planes(w.hi[s], w.hi[s], w.lo[s]);
+  }
+}
+
+// A workgroup: the rows of a tile, col_blocks times kBlockCols columns, 64 of them
+// per wave.  HELD: steps of 32 ranks whose fragments of B stay in registers over the
+// tile's rows (0: they are read for every 16 rows).  The matrix core's sums are read
+// in the straight line of code that forms them (the hardware does not hold back a
+// read that comes too early, and the compiler has missed some behind branches): all
+// HELD steps are multiplied, with zeros past the adapter's rank, and the others one
+// by one into running totals.
+template <int TK, int TR, int BK, int HELD>
 __global__ __launch_bounds__(kThreads) void adapter_up_kernel(AdaptArgs g, int col_blocks) {
   constexpr bool LIST = TR > 1;
   extern __shared__ uint16_t planes_s[];  // [planes][16 TR][pitch]
-  __shared__ int rows_s[16 * TR];
+  __shared__ int lists_s[LIST ? 16 * TR : 16 * kWaves];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int low = lane & 15, h = lane >> 4;
+  int* rows_s = lists_s + (LIST ? 0 : 16 * wave);
   Tile tile;
   if (!find_tile<LIST>(g, blockIdx.y, rows_s, tile)) return;
   const int rank = rank_of(g, tile.adapter);
@@ -296,15 +339,47 @@ __global__ __launch_bounds__(kThreads) void adapter_up_kernel(AdaptArgs g, int c
   const float scale = rank == 0 || g.scaling == nullptr ? 1.0f : g.scaling[tile.adapter];
   const int steps = (rank + 31) / 32;
   const int pitch = (g.rank + 31) / 32 * 32 + 8;
-  __syncthreads();
+  const uint16_t* wb = (const uint16_t*)g.B + (int64_t)max(tile.adapter, 0) * g.n * g.rank;
+
+  // The base of rows 4 h .. 4 h + 3 of 16, at the lane's columns.  Vectors that
+  // pass n are read at column 0 and not used.
+  typedef Raw<BK == kNoBase ? CK_F32 : BK, kColTiles> BaseVec;
+  auto load_base = [&](int t, int c0, BaseVec(&v)[4]) {
+    if constexpr (BK != kNoBase) {
+      if (g.n < kColTiles) return;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int i = t * 16 + 4 * h + q;
+        v[q] = load_raw<BK, kColTiles>(g.base, rows_s[i < tile.rows ? i : 0] * g.ldb + (c0 + kColTiles <= g.n ? c0 : 0));
+      }
+    }
+  };
+  const int first = (int)blockIdx.x * col_blocks * kBlockCols + wave * kWaveCols + low * kColTiles;
+  BaseVec base[4];
+  WeightFrags<TK> w[HELD > 0 ? HELD : 1];
+  // (in flight while the inner values are added up)
+  load_base(0, first, base);
+  if (rank != 0) {
+#pragma unroll
+    for (int b = 0; b < HELD; ++b) load_frags<TK>(g, wb, first, b * 32 + 8 * h, w[b]);
+  }
 
   // the rows' inner values: the splits' parts in order, four ranks per thread
-  for (int e = tid; e < tile.rows * steps * 8; e += kThreads) {
-    const int row = e / (steps * 8), j = e % (steps * 8) * 4;
+  const int quads = (HELD > 0 ? HELD : steps) * 8;
+  for (int e = tid; e < tile.rows * quads; e += kThreads) {
+    const int row = e / quads, j = e % quads * 4;
     f32x4 v = f32x4{0, 0, 0, 0};
     if (j < rank) {
       const float* part = g.h + (int64_t)rows_s[row] * g.rank + j;
-      for (int s = 0; s < g.splits; ++s) v += *(const f32x4*)(part + (int64_t)s * g.m * g.rank);
+      const int64_t stride = (int64_t)g.m * g.rank;
+      for (int s0 = 0; s0 < g.splits; s0 += 8) {
+        f32x4 p[8];
+#pragma unroll
+        for (int s = 0; s < 8; ++s) p[s] = *(const f32x4*)(part + min(s0 + s, g.splits - 1) * stride);
+#pragma unroll
+        for (int s = 0; s < 8; ++s)
+          if (s0 + s < g.splits) v += p[s];
+      }
     }
     uint16_t bits[kPlanes][4];
 #pragma unroll
@@ -320,96 +395,89 @@ __global__ __launch_bounds__(kThreads) void adapter_up_kernel(AdaptArgs g, int c
   }
   __syncthreads();
 
-  const int low = lane & 15, h = lane >> 4;
-  const uint16_t* wb = (const uint16_t*)g.B + (int64_t)max(tile.adapter, 0) * g.n * g.rank;
-  int row_of[TR][4];  // the lane's rows, -1 past the tile
-#pragma unroll
-  for (int t = 0; t < TR; ++t)
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int i = t * 16 + 4 * h + q;
-      row_of[t][q] = i < tile.rows ? rows_s[i] : -1;
-    }
   for (int cb = 0; cb < col_blocks; ++cb) {
-    const int col = ((int)blockIdx.x * col_blocks + cb) * kBlockCols + wave * kWaveCols;
-    if (col >= g.n) break;
-    const int c0 = col + low * kColTiles;
+    const int c0 = first + cb * kBlockCols;
+    if (c0 - low * kColTiles >= g.n) break;
     const bool whole = c0 + kColTiles <= g.n;
-    Raw<BK == kNoBase ? CK_F32 : BK, kColTiles> base[TR][4];
-    if constexpr (BK != kNoBase) {
+    if (cb > 0) {
+      load_base(0, c0, base);
+      if (rank != 0) {
 #pragma unroll
-      for (int t = 0; t < TR; ++t)
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          if (g.n >= kColTiles)
-            base[t][q] = load_raw<BK, kColTiles>(g.base, max(row_of[t][q], 0) * g.ldb + (whole ? c0 : 0));
+        for (int b = 0; b < HELD; ++b) load_frags<TK>(g, wb, c0, b * 32 + 8 * h, w[b]);
+      }
     }
-    f32x4 acc[TR][kColTiles];
 #pragma unroll
-    for (int t = 0; t < TR; ++t)
-#pragma unroll
-      for (int s = 0; s < kColTiles; ++s) acc[t][s] = f32x4{0, 0, 0, 0};
-    for (int b = 0; b < steps; ++b) {
-      const int k0 = b * 32 + 8 * h;
-      const int valid = rank - k0;  // elements of this lane's eight that count
-      u32x4 w[kColTiles];
-#pragma unroll
-      for (int s = 0; s < kColTiles; ++s) {
-        const int64_t c = min(c0 + s, g.n - 1);
-        w[s] = *(const u32x4*)(wb + c * g.rank + (valid > 0 ? k0 : 0));
-      }
-      u32x4 keep;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) keep[q] = valid >= 2 * q + 2 ? ~0u : valid == 2 * q + 1 ? 0xffffu : 0u;
-      u32x4 lo[kColTiles];
-#pragma unroll
-      for (int s = 0; s < kColTiles; ++s) {
-        w[s] &= keep;
-        if constexpr (TK == CK_F16) f16_planes(w[s], w[s], lo[s]);
-      }
-#pragma unroll
-      for (int t = 0; t < TR; ++t) {
-        if (t * 16 >= tile.rows) break;
+    for (int b = 0; b < HELD; ++b) finish_frags<TK>(rank, b * 32 + 8 * h, w[b]);
+#pragma unroll 1
+    for (int t = 0; t * 16 < tile.rows; ++t) {
+      BaseVec next[4];
+      if (TR > 1 && (t + 1) * 16 < tile.rows) load_base(t + 1, c0, next);
+      float sum[kColTiles][4];
+      auto multiply = [&](int b, const WeightFrags<TK>& f, f32x4(&acc)[kColTiles]) {
         u32x4 v[kPlanes];
 #pragma unroll
-        for (int p = 0; p < kPlanes; ++p) v[p] = *(const u32x4*)&planes_s[((p * TR + t) * 16 + low) * pitch + k0];
+        for (int p = 0; p < kPlanes; ++p)
+          v[p] = *(const u32x4*)&planes_s[((p * TR + t) * 16 + low) * pitch + b * 32 + 8 * h];
 #pragma unroll
-        for (int p = kPlanes - 1; p >= 0; --p)
+        for (int p = kPlanes - 1; p >= 0; --p) {
+          if constexpr (TK == CK_F16) {
+            if (p < kPlanes - 1) {
 #pragma unroll
-          for (int s = 0; s < kColTiles; ++s) {
-            if constexpr (TK == CK_F16) {
-              if (p < kPlanes - 1) acc[t][s] = mfma16<CK_BF16>(v[p], lo[s], acc[t][s]);
+              for (int s = 0; s < kColTiles; ++s) acc[s] = mfma16<CK_BF16>(v[p], f.lo[s], acc[s]);
             }
-            acc[t][s] = mfma16<CK_BF16>(v[p], w[s], acc[t][s]);
           }
-      }
-    }
 #pragma unroll
-    for (int t = 0; t < TR; ++t)
+          for (int s = 0; s < kColTiles; ++s) acc[s] = mfma16<CK_BF16>(v[p], f.hi[s], acc[s]);
+        }
+      };
+      if constexpr (HELD > 0) {
+        f32x4 acc[kColTiles];
+#pragma unroll
+        for (int s = 0; s < kColTiles; ++s) acc[s] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int b = 0; b < HELD; ++b) multiply(b, w[b], acc);
+#pragma unroll
+        for (int s = 0; s < kColTiles; ++s)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) sum[s][q] = scale * acc[s][q];
+      } else {
+#pragma unroll
+        for (int s = 0; s < kColTiles; ++s)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) sum[s][q] = 0.0f;
+        for (int b = 0; b < steps; ++b) {
+          load_frags<TK>(g, wb, c0, b * 32 + 8 * h, w[0]);
+          finish_frags<TK>(rank, b * 32 + 8 * h, w[0]);
+          f32x4 acc[kColTiles];
+#pragma unroll
+          for (int s = 0; s < kColTiles; ++s) acc[s] = f32x4{0, 0, 0, 0};
+          multiply(b, w[0], acc);
+#pragma unroll
+          for (int s = 0; s < kColTiles; ++s)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) sum[s][q] = __builtin_fmaf(scale, acc[s][q], sum[s][q]);
+        }
+      }
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const int row = row_of[t][q];
-        if (row < 0) continue;
+        const int i = t * 16 + 4 * h + q;
+        if (i >= tile.rows) continue;
+        const int row = rows_s[i];
         float v[kColTiles];
-        if (whole) {
-          if constexpr (BK != kNoBase) {
-            unpack_raw<BK, kColTiles>(base[t][q], v);
+#pragma unroll
+        for (int s = 0; s < kColTiles; ++s) v[s] = 0.0f;
+        if constexpr (BK != kNoBase) {
+          if (whole) {
+            unpack_raw<BK, kColTiles>(base[q], v);
           } else {
 #pragma unroll
-            for (int s = 0; s < kColTiles; ++s) v[s] = 0.0f;
-          }
-        } else {
-#pragma unroll
-          for (int s = 0; s < kColTiles; ++s) {
-            v[s] = 0.0f;
-            if constexpr (BK != kNoBase) {
+            for (int s = 0; s < kColTiles; ++s)
               if (c0 + s < g.n) v[s] = value_at<BK>(g.base, row * g.ldb + c0 + s);
-            }
           }
         }
         if (rank != 0) {
 #pragma unroll
-          for (int s = 0; s < kColTiles; ++s) v[s] = __builtin_fmaf(scale, acc[t][s][q], v[s]);
+          for (int s = 0; s < kColTiles; ++s) v[s] += sum[s][q];
         }
         const int64_t at = row * g.ldo + c0;
         if (whole) {
@@ -430,7 +498,18 @@ __global__ __launch_bounds__(kThreads) void adapter_up_kernel(AdaptArgs g, int c
             }
         }
       }
+      if constexpr (TR > 1) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) base[q] = next[q];
+      }
+    }
   }
+}
+
+template <int TK, int TR, int BK>
+auto up_kernel(int rank) {
+  return rank <= 32   ? adapter_up_kernel<TK, TR, BK, 1>
+         : rank <= 64 ? adapter_up_kernel<TK, TR, BK, 2> : adapter_up_kernel<TK, TR, BK, 0>;
 }
 
 template <int TK, int TR>
@@ -444,11 +523,11 @@ hipError_t launch_tiles(const AdaptArgs& a, hipStream_t stream) {
   hipLaunchKernelGGL(down, dim3(blocks, tiles), dim3(kThreads), lds, stream, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int col_blocks = TR == 1 ? 1 : 4;
+  const int col_blocks = TR == 1 ? 1 : 2;
   const unsigned cols = (unsigned)((a.n + kBlockCols * col_blocks - 1) / (kBlockCols * col_blocks));
   const size_t planes = (size_t)kPlanes * 16 * TR * ((a.rank + 31) / 32 * 32 + 8) * 2;
-  const auto up = a.base == nullptr          ? adapter_up_kernel<TK, TR, kNoBase>
-                  : a.base_kind == CK_F32 ? adapter_up_kernel<TK, TR, CK_F32> : adapter_up_kernel<TK, TR, TK>;
+  const auto up = a.base == nullptr       ? up_kernel<TK, TR, kNoBase>((int)a.rank)
+                  : a.base_kind == CK_F32 ? up_kernel<TK, TR, CK_F32>((int)a.rank) : up_kernel<TK, TR, TK>((int)a.rank);
   if (planes > 65536) {
     e = hipFuncSetAttribute((const void*)up, hipFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024 - 1024);
     if (e != hipSuccess) return e;
@@ -488,7 +567,7 @@ hipError_t launch_adapters(const AdaptArgs& a, int kind, hipStream_t stream) {
     return hipErrorInvalidValue;
   if (a.m <= kAdaptDirectRows)
     return kind == CK_F16 ? launch_tiles<CK_F16, 1>(a, stream) : launch_tiles<CK_BF16, 1>(a, stream);
-  hipLaunchKernelGGL(adapter_sort_kernel, dim3(1), dim3(kSortThreads), 0, stream, a);
+  hipLaunchKernelGGL(adapter_sort_kernel, dim3(1), dim3(kSortThreads), (size_t)(a.count + 1) * 4, stream, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   return kind == CK_F16 ? launch_tiles<CK_F16, 4>(a, stream) : launch_tiles<CK_BF16, 4>(a, stream);
