@@ -27,18 +27,18 @@ struct Rows {
 
 bool meet(const Rows& a, const Rows& b) { return overlap(a.p, a.bytes(), b.p, b.bytes()); }
 
-// workspace of the adapters: the inner values, then the sorted rows
+// workspace of the adapters: the inner values, then the tiles and their rows
 struct AdaptSizes {
   int splits;
-  int64_t split_len, tiles, order, max_tiles, bytes;
+  int64_t split_len, max_tiles, tiles, order, bytes;
 };
 AdaptSizes adapt_sizes(const skinny_adapters& a, int64_t m) {
   AdaptSizes s;
   s.splits = adapt_splits(m, a.k, a.rank, &s.split_len);
   s.max_tiles = adapt_max_tiles(m, a.count);
-  s.tiles = round16((int64_t)s.splits * m * a.rank * 4);
-  s.order = s.tiles + (s.max_tiles > 0 ? (4 + 4 * s.max_tiles) * 4 : 0);
-  s.bytes = s.order + (s.max_tiles > 0 ? round16(m * 4) : 0);
+  s.tiles = round16((int64_t)s.splits * m * a.rank * 4) + 16;  // (the tile count is before them)
+  s.order = s.tiles + s.max_tiles * 16;
+  s.bytes = s.order + s.max_tiles * adapt_tile_rows(m) * 4;
   return s;
 }
 
@@ -181,6 +181,7 @@ skinny_status skinny_adapters_run(const skinny_adapters* adapters, int64_t m, co
   a.splits = s.splits;
   a.split_len = (int32_t)s.split_len;
   a.h = (float*)workspace;
+  a.tile_count = (uint32_t*)((char*)workspace + s.tiles - 16);
   a.tiles = (uint32_t*)((char*)workspace + s.tiles);
   a.order = (uint32_t*)((char*)workspace + s.order);
   a.max_tiles = (int32_t)s.max_tiles;

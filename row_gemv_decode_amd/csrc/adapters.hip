@@ -45,39 +45,102 @@ __device__ __forceinline__ int rank_of(const AdaptArgs& g, int a) {
   return r >= 1 && r <= g.rank ? r : 0;
 }
 
-// The rows of tile `index` in rows_s; false if there is no such tile (the same in
-// every thread).  A tile of the list is read by the workgroup, and there once it
-// has met; in the direct form each wave finds it and has rows_s to itself.
+// Tile `later` of those past an adapter's first 16 rows, in the order of the
+// adapters (rows without one last), for at most 256 rows whose ids the lanes
+// hold: a wave counts them in LDS of its own.
+__device__ __forceinline__ bool later_tile(const AdaptArgs& g, int later, const int (&a)[kAdaptDirectRows / 64], int& adapter,
+                                           int& before) {
+  __shared__ uint32_t counts_s[kWaves][kAdaptDirectRows];
+  const int lane = threadIdx.x & 63;
+  uint32_t* counts = counts_s[threadIdx.x >> 6];
+#pragma unroll
+  for (int c = 0; c < kAdaptDirectRows / 64; ++c) counts[c * 64 + lane] = 0;
+  wave_lds_order();
+#pragma unroll
+  for (int c = 0; c < kAdaptDirectRows / 64; ++c)
+    if (a[c] >= -1) atomicAdd(&counts[a[c] < 0 ? g.count : a[c]], 1u);
+  wave_lds_order();
+  const u32x4 mine = *(const u32x4*)&counts[4 * lane];
+  int tiles[4], sum = 0;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    tiles[q] = mine[q] > 16 ? ((int)mine[q] - 1) / 16 : 0;
+    sum += tiles[q];
+  }
+  int upto = sum;
+#pragma unroll
+  for (int s = 1; s < 64; s *= 2) {
+    const int o = __shfl_up(upto, s);
+    if (lane >= s) upto += o;
+  }
+  const uint64_t past = __builtin_amdgcn_ballot_w64(upto > later);
+  if (past == 0) return false;
+  const int owner = __builtin_ctzll(past);
+  int at = later - __builtin_amdgcn_readlane(upto - sum, owner);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int n = __builtin_amdgcn_readlane(tiles[q], owner);
+    if (at >= 0 && at < n) {
+      adapter = 4 * owner + q < g.count ? 4 * owner + q : -1;
+      before = 16 * (at + 1);
+    }
+    at -= n;
+  }
+  return true;
+}
+
+// A tile as the launches hand it on: its entry of g.tiles, and its rows in
+// g.order from `index` times the tile's size on.
 struct Tile {
-  int adapter, rows;
+  int adapter, rows, rank;
+  float scale;
 };
+__device__ __forceinline__ u32x4 tile_entry(const AdaptArgs& g, int adapter, int rows) {
+  const int rank = rank_of(g, adapter);
+  const float scale = rank == 0 || g.scaling == nullptr ? 1.0f : g.scaling[adapter];
+  return u32x4{(uint32_t)adapter, (uint32_t)rows, (uint32_t)rank, ubits(scale)};
+}
+__device__ __forceinline__ Tile tile_of(u32x4 e) {
+  const uint32_t scale = e[3];
+  return Tile{(int)e[0], (int)e[1], (int)e[2], fbits(scale)};
+}
+
+// Tile `index` and its rows in rows_s; false if there is no such tile (the same in
+// every thread).  A tile of the sorted list is read by the workgroup; in the direct
+// form each wave finds it, and has rows_s to itself.
 template <bool LIST>
 __device__ __forceinline__ bool find_tile(const AdaptArgs& g, int index, int* rows_s, Tile& tile) {
   if constexpr (LIST) {
     const int tid = threadIdx.x;
-    if (index >= (int)g.tiles[0]) return false;
-    const uint32_t* t = g.tiles + 4 + 4 * index;
-    tile.adapter = (int)t[0];
-    tile.rows = (int)t[2];
-    if (tid < tile.rows) rows_s[tid] = (int)g.order[t[1] + tid];
+    const int tiles = (int)g.tile_count[0];
+    const u32x4 entry = ((const u32x4*)g.tiles)[index];
+    if (tid < kAdaptTileRows) rows_s[tid] = (int)g.order[index * kAdaptTileRows + tid];
+    tile = tile_of(entry);
     __syncthreads();
-    return true;
+    return index < tiles;
   } else {
-    // The tile of row `index`, if that row is the first of 16 of its adapter.
     constexpr int kChunks = kAdaptDirectRows / 64;
     const int lane = threadIdx.x & 63;
     int a[kChunks];
 #pragma unroll
     for (int c = 0; c < kChunks; ++c) a[c] = c * 64 + lane < g.m ? id_at(g, c * 64 + lane) : -2;
-    const int mine = __builtin_amdgcn_readfirstlane(id_at(g, index));
+    int mine, before = 0, all = 0;  // the tile's adapter, how many of its rows come before the tile
+    if (g.by_adapter == 0) {
+      // the tile of row `index`, if that row is the first of 16 of its adapter
+      mine = __builtin_amdgcn_readfirstlane(id_at(g, index));
+    } else if (index <= g.count) {
+      mine = index < g.count ? index : -1;
+    } else if (!later_tile(g, index - g.count - 1, a, mine, before)) {
+      return false;
+    }
     uint64_t same[kChunks];
-    int before = 0, all = 0;
 #pragma unroll
     for (int c = 0; c < kChunks; ++c) {
       same[c] = __builtin_amdgcn_ballot_w64(a[c] == mine);
-      const int below = index - c * 64;  // rows of this chunk that come first
-      const uint64_t low = below <= 0 ? 0 : below >= 64 ? ~0ull : (1ull << below) - 1;
-      before += __builtin_popcountll(same[c] & low);
+      if (g.by_adapter == 0) {
+        const int below = index - c * 64;  // rows of this chunk that come first
+        before += __builtin_popcountll(same[c] & (below <= 0 ? 0 : below >= 64 ? ~0ull : (1ull << below) - 1));
+      }
     }
     if ((before & 15) != 0) return false;
 #pragma unroll
@@ -86,16 +149,16 @@ __device__ __forceinline__ bool find_tile(const AdaptArgs& g, int index, int* ro
       if ((same[c] >> lane & 1) != 0 && place >= 0 && place < 16) rows_s[place] = c * 64 + lane;
       all += __builtin_popcountll(same[c]);
     }
+    if (all <= before) return false;
     wave_lds_order();
-    tile.adapter = mine;
-    tile.rows = min(16, all - before);
+    tile = tile_of(tile_entry(g, mine, min(16, all - before)));
     return true;
   }
 }
 
 // --- sorting the rows of a large batch ---------------------------------------
-// One workgroup counts the rows of each adapter (those without one last), places
-// the tiles and the rows behind one another.  The order of the rows within an
+// One workgroup counts the rows of each adapter (those without one last) and gives
+// each as many tiles as it needs, one behind the other.  The order of the rows within an
 // adapter is that of the atomics; no row's result depends on it.
 constexpr int kSortThreads = 1024;
 constexpr int kSortIds = 4;  // ids of a thread that are read once and kept
@@ -119,74 +182,78 @@ __device__ __forceinline__ uint32_t take_places(uint32_t* counts, int a, bool ac
 
 __global__ __launch_bounds__(kSortThreads) void adapter_sort_kernel(AdaptArgs g) {
   extern __shared__ uint32_t counts_s[];  // count + 1
-  __shared__ uint32_t rows_s[kSortThreads / 64], tiles_s[kSortThreads / 64];
+  __shared__ uint32_t tiles_s[kSortThreads / 64];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int places = g.count + 1;
   auto place_of = [&](int t) {
     const int a = id_at(g, min(t, g.m - 1));
     return a < 0 ? g.count : a;
   };
+  // (a batch whose ids are kept takes its places while it is counted)
+  const bool once = g.m <= kSortIds * kSortThreads;
   int kept[kSortIds];
+  uint32_t place[kSortIds];
+  if (once) {
 #pragma unroll
-  for (int i = 0; i < kSortIds; ++i) kept[i] = place_of(i * kSortThreads + tid);
+    for (int i = 0; i < kSortIds; ++i) kept[i] = place_of(i * kSortThreads + tid);
+  }
   for (int i = tid; i < places; i += kSortThreads) counts_s[i] = 0;
   __syncthreads();
+  if (once) {
 #pragma unroll
-  for (int i = 0; i < kSortIds; ++i) take_places(counts_s, kept[i], i * kSortThreads + tid < g.m);
-  for (int t0 = kSortIds * kSortThreads; t0 < g.m; t0 += kSortThreads)
-    take_places(counts_s, place_of(t0 + tid), t0 + tid < g.m);
+    for (int i = 0; i < kSortIds; ++i) place[i] = take_places(counts_s, kept[i], i * kSortThreads + tid < g.m);
+  } else {
+    for (int t0 = 0; t0 < g.m; t0 += kSortThreads) take_places(counts_s, place_of(t0 + tid), t0 + tid < g.m);
+  }
   __syncthreads();
   // each thread's consecutive adapters, then the sums of the threads before it
   const int each = (places + kSortThreads - 1) / kSortThreads;
   const int a0 = tid * each, a1 = min(a0 + each, places);
-  uint32_t rows = 0, tiles = 0;
-  for (int a = a0; a < a1; ++a) {
-    rows += counts_s[a];
-    tiles += (counts_s[a] + kAdaptTileRows - 1) / kAdaptTileRows;
-  }
-  uint32_t row_at = rows, tile_at = tiles;  // inclusive sums over the wave
+  uint32_t tiles = 0;
+  for (int a = a0; a < a1; ++a) tiles += (counts_s[a] + kAdaptTileRows - 1) / kAdaptTileRows;
+  uint32_t tile_at = tiles;  // inclusive sum over the wave
 #pragma unroll
   for (int s = 1; s < 64; s *= 2) {
-    const uint32_t r = (uint32_t)__shfl_up((int)row_at, s), t = (uint32_t)__shfl_up((int)tile_at, s);
-    if (lane >= s) row_at += r, tile_at += t;
+    const uint32_t t = (uint32_t)__shfl_up((int)tile_at, s);
+    if (lane >= s) tile_at += t;
   }
-  if (lane == 63) rows_s[wave] = row_at, tiles_s[wave] = tile_at;
+  if (lane == 63) tiles_s[wave] = tile_at;
   __syncthreads();
-  row_at -= rows, tile_at -= tiles;
-  for (int i = 0; i < wave; ++i) row_at += rows_s[i], tile_at += tiles_s[i];
-  if (tid == kSortThreads - 1) g.tiles[0] = tile_at + tiles;
+  tile_at -= tiles;
+  for (int i = 0; i < wave; ++i) tile_at += tiles_s[i];
+  if (tid == kSortThreads - 1) g.tile_count[0] = tile_at + tiles;
   for (int a = a0; a < a1; ++a) {
     const uint32_t count = counts_s[a];
-    counts_s[a] = row_at;
-    for (uint32_t done = 0; done < count; done += kAdaptTileRows) {
-      uint32_t* t = g.tiles + 4 + 4 * tile_at++;
-      t[0] = a < g.count ? (uint32_t)a : ~0u;
-      t[1] = row_at + done;
-      t[2] = min(count - done, (uint32_t)kAdaptTileRows);
-    }
-    row_at += count;
+    counts_s[a] = tile_at * kAdaptTileRows;  // where the adapter's rows start
+    for (uint32_t done = 0; done < count; done += kAdaptTileRows)
+      ((u32x4*)g.tiles)[tile_at++] =
+          tile_entry(g, a < g.count ? a : -1, (int)min(count - done, (uint32_t)kAdaptTileRows));
   }
   __syncthreads();
-  auto put = [&](int t, int a) {
-    const uint32_t at = take_places(counts_s, a, t < g.m);
-    if (t < g.m) g.order[at] = (uint32_t)t;
-  };
+  if (once) {
 #pragma unroll
-  for (int i = 0; i < kSortIds; ++i) put(i * kSortThreads + tid, kept[i]);
-  for (int t0 = kSortIds * kSortThreads; t0 < g.m; t0 += kSortThreads) put(t0 + tid, place_of(t0 + tid));
+    for (int i = 0; i < kSortIds; ++i)
+      if (i * kSortThreads + tid < g.m) g.order[counts_s[kept[i]] + place[i]] = (uint32_t)(i * kSortThreads + tid);
+  } else {
+    for (int t0 = 0; t0 < g.m; t0 += kSortThreads) {
+      const bool on = t0 + tid < g.m;
+      const uint32_t at = take_places(counts_s, place_of(t0 + tid), on);
+      if (on) g.order[at] = (uint32_t)(t0 + tid);
+    }
+  }
 }
 
 // --- down: the inner values --------------------------------------------------
 // A workgroup: 16 TR rows, 16 NR ranks, one split of k.  Its waves take every
 // fourth 64 elements of the split (128 bytes of a row), UN of them at once.
 template <int TR, int NR>
-constexpr int down_units() { return TR == 1 ? (NR == 1 ? 4 : 2) : (NR == 4 ? 1 : 2); }
+constexpr int down_units() { return TR == 1 ? (NR == 1 ? 4 : 2) : (NR == 1 ? 2 : 1); }
 
 template <int TK, int TR, int NR>
 __global__ __launch_bounds__(kThreads) void adapter_down_kernel(AdaptArgs g) {
   constexpr bool LIST = TR > 1;
   constexpr int UN = down_units<TR, NR>();
-  extern __shared__ f32x4 sums_s[];  // [waves][TR][NR][64]
+  extern __shared__ f32x4 sums_s[];  // the waves' slots, then [waves][TR][NR][64]
   __shared__ int lists_s[LIST ? 16 * TR : 16 * kWaves];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -194,26 +261,35 @@ __global__ __launch_bounds__(kThreads) void adapter_down_kernel(AdaptArgs g) {
   const int rank0 = (int)blockIdx.x / g.splits * (16 * NR);
   int* rows_s = lists_s + (LIST ? 0 : 16 * wave);
   Tile tile;
-  if (!find_tile<LIST>(g, blockIdx.y, rows_s, tile)) return;
-  const int rank = rank_of(g, tile.adapter);
-  if (rank0 >= rank) return;
+  const bool found = find_tile<LIST>(g, blockIdx.y, rows_s, tile);
+  if (!LIST && blockIdx.x == 0 && wave == 0) {  // for the up launch
+    if (lane < 16 && found) g.order[blockIdx.y * 16 + lane] = (uint32_t)rows_s[lane];
+    if (lane == 0)
+      ((u32x4*)g.tiles)[blockIdx.y] =
+          found ? u32x4{(uint32_t)tile.adapter, (uint32_t)tile.rows, (uint32_t)tile.rank, ubits(tile.scale)} : u32x4{0, 0, 0, 0};
+  }
+  if (!found || rank0 >= tile.rank) return;
+  const int rank = tile.rank;
 
-  const int low = lane & 15, h = lane >> 4;
+  // a load gives four consecutive lanes 64 bytes of a row, which pass through the
+  // wave's slots of LDS to the lanes that multiply them (see Turn)
+  const int row4 = lane >> 2, piece = lane & 3;
   const uint16_t* x[TR];
 #pragma unroll
   for (int t = 0; t < TR; ++t) {
-    const int i = t * 16 + low;
-    x[t] = (const uint16_t*)g.x + rows_s[i < tile.rows ? i : 0] * g.ldx + 8 * h;
+    const int i = t * 16 + row4;
+    x[t] = (const uint16_t*)g.x + rows_s[i < tile.rows ? i : 0] * g.ldx + 8 * piece;
   }
   const uint16_t* w[NR];
 #pragma unroll
   for (int n = 0; n < NR; ++n) {
-    const int j = rank0 + n * 16 + low;
-    w[n] = (const uint16_t*)g.A + ((int64_t)tile.adapter * g.rank + (j < rank ? j : 0)) * g.k + 8 * h;
+    const int j = rank0 + n * 16 + row4;
+    w[n] = (const uint16_t*)g.A + ((int64_t)tile.adapter * g.rank + (j < rank ? j : 0)) * g.k + 8 * piece;
   }
   const int begin = split * g.split_len;
   const int len = min(g.split_len, g.k - begin);
   const int units = (len + 63) / 64;
+  const Turn turn((u32x4*)sums_s + wave * (2 * (TR + NR) * 64), lane);
   f32x4 acc[TR][NR];
 #pragma unroll
   for (int t = 0; t < TR; ++t)
@@ -227,8 +303,8 @@ __global__ __launch_bounds__(kThreads) void adapter_down_kernel(AdaptArgs g) {
       for (int b = 0; b < 2; ++b) {
         // past the split: any elements of the row, which count as 0
         const int at = (u0 + u * kWaves) * 64 + b * 32;
-        const bool in = at + 8 * h < len;
-        const int k0 = in ? begin + at : -8 * h;
+        const bool in = at + 8 * piece < len;
+        const int k0 = in ? begin + at : -8 * piece;
 #pragma unroll
         for (int t = 0; t < TR; ++t) {
           const u32x4 v = *(const u32x4*)(x[t] + k0);
@@ -238,14 +314,33 @@ __global__ __launch_bounds__(kThreads) void adapter_down_kernel(AdaptArgs g) {
         for (int n = 0; n < NR; ++n) wf[u][b][n] = *(const u32x4*)(w[n] + k0);
       }
 #pragma unroll
-    for (int u = 0; u < UN; ++u)
+    for (int u = 0; u < UN; ++u) {
+      wave_lds_order();
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+#pragma unroll
+        for (int t = 0; t < TR; ++t) turn.slots[(b * (TR + NR) + t) * 64 + turn.put] = xf[u][b][t];
+#pragma unroll
+        for (int n = 0; n < NR; ++n) turn.slots[(b * (TR + NR) + TR + n) * 64 + turn.put] = wf[u][b][n];
+      }
+      wave_lds_order();
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+#pragma unroll
+        for (int t = 0; t < TR; ++t) xf[u][b][t] = turn.slots[(b * (TR + NR) + t) * 64 + turn.get];
+#pragma unroll
+        for (int n = 0; n < NR; ++n) wf[u][b][n] = turn.slots[(b * (TR + NR) + TR + n) * 64 + turn.get];
+      }
 #pragma unroll
       for (int b = 0; b < 2; ++b)
 #pragma unroll
         for (int t = 0; t < TR; ++t)
 #pragma unroll
           for (int n = 0; n < NR; ++n) acc[t][n] = mfma16<TK>(wf[u][b][n], xf[u][b][t], acc[t][n]);
+    }
   }
+  const int low = lane & 15, h = lane >> 4;
+  __syncthreads();  // (the slots are the sums' place too)
   // a lane holds ranks 4 h .. 4 h + 3 of row low: the waves' parts are added in
   // the order of the waves
 #pragma unroll
@@ -291,27 +386,51 @@ __device__ __forceinline__ void f16_planes(u32x4 w, u32x4& hi, u32x4& lo) {
   }
 }
 
-// B's fragments of 16 kColTiles columns for one step of 32 ranks: lane (low, h) has
-// ranks 32 b + 8 h .. + 7 of columns c0 + s; what lies past the adapter's rank is 0
+// B's fragments of a wave's 64 columns for one step of 32 ranks.  As loaded: the
+// adapter's ranks of the step are `parts` pieces of 16 bytes of each column, and
+// consecutive lanes take a column's pieces one after another (so a load of an
+// adapter of rank 16 covers 32 columns).  They then pass through the wave's slots of
+// LDS (see Turn): lane (low, h) takes piece h of columns 4 low .. 4 low + 3.
 template <int TK>
 struct WeightFrags {
   u32x4 hi[kColTiles], lo[TK == CK_F16 ? kColTiles : 1];
 };
-template <int TK>
-__device__ __forceinline__ void load_frags(const AdaptArgs& g, const uint16_t* wb, int c0, int k0, WeightFrags<TK>& w) {
-#pragma unroll
-  for (int s = 0; s < kColTiles; ++s)
-    w.hi[s] = *(const u32x4*)(wb + (int64_t)min(c0 + s, g.n - 1) * g.rank + (k0 < g.rank ? k0 : 0));
+__device__ __forceinline__ int step_parts_log2(int rank, int step) {
+  const int left = rank - 32 * step;
+  return left > 16 ? 2 : left > 8 ? 1 : 0;
 }
 template <int TK>
-__device__ __forceinline__ void finish_frags(int rank, int k0, WeightFrags<TK>& w) {
-  const int valid = rank - k0;  // elements of this lane's eight that count
+__device__ __forceinline__ void load_frags(const AdaptArgs& g, const uint16_t* wb, int rank, int step, int col, int lane,
+                                           WeightFrags<TK>& w) {
+  const int log2 = step_parts_log2(rank, step);
+  const int piece = 32 * step + 8 * (lane & ((1 << log2) - 1));
+  const uint16_t* at = wb + (piece < rank ? piece : 32 * step);
+#pragma unroll
+  for (int i = 0; i < kColTiles; ++i)
+    if (i < 1 << log2) {
+      const int c = col + ((i * 64 + lane) >> log2);
+      w.hi[i] = *(const u32x4*)(at + (int64_t)min(c, g.n - 1) * g.rank);
+    }
+}
+template <int TK>
+__device__ __forceinline__ void finish_frags(int rank, int step, int lane, u32x4* slots, WeightFrags<TK>& w) {
+  const int log2 = step_parts_log2(rank, step);
+  const int low = lane & 15, h = lane >> 4;
+  wave_lds_order();
+#pragma unroll
+  for (int i = 0; i < kColTiles; ++i)
+    if (i < 1 << log2) {
+      const int c = (i * 64 + lane) >> log2;
+      slots[(c & 3) * 64 + Turn::entry(c >> 2, lane & ((1 << log2) - 1))] = w.hi[i];
+    }
+  wave_lds_order();
+  const int valid = rank - 32 * step - 8 * h;  // elements of this lane's eight that count
   u32x4 keep;
 #pragma unroll
   for (int q = 0; q < 4; ++q) keep[q] = valid >= 2 * q + 2 ? ~0u : valid == 2 * q + 1 ? 0xffffu : 0u;
 #pragma unroll
   for (int s = 0; s < kColTiles; ++s) {
-    w.hi[s] &= keep;
+    w.hi[s] = slots[s * 64 + Turn::entry(low, h)] & keep;
     if constexpr (TK == CK_F16) f16_planes(w.hi[s], w.hi[s], w.lo[s]);
   }
 }
@@ -325,21 +444,23 @@ __device__ __forceinline__ void finish_frags(int rank, int k0, WeightFrags<TK>& 
 // by one into running totals.
 template <int TK, int TR, int BK, int HELD>
 __global__ __launch_bounds__(kThreads) void adapter_up_kernel(AdaptArgs g, int col_blocks) {
-  constexpr bool LIST = TR > 1;
   extern __shared__ uint16_t planes_s[];  // [planes][16 TR][pitch]
-  __shared__ int lists_s[LIST ? 16 * TR : 16 * kWaves];
+  __shared__ uint32_t rows_s[16 * TR];
+  __shared__ u32x4 slots_s[kWaves][64 * kColTiles];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int low = lane & 15, h = lane >> 4;
-  int* rows_s = lists_s + (LIST ? 0 : 16 * wave);
-  Tile tile;
-  if (!find_tile<LIST>(g, blockIdx.y, rows_s, tile)) return;
-  const int rank = rank_of(g, tile.adapter);
+  const uint32_t tiles = TR > 1 ? g.tile_count[0] : gridDim.y;
+  const Tile tile = tile_of(((const u32x4*)g.tiles)[blockIdx.y]);
+  if (tid < 16 * TR) rows_s[tid] = g.order[blockIdx.y * (16 * TR) + tid];
+  if (blockIdx.y >= tiles || tile.rows == 0) return;
+  const int rank = tile.rank;
   if (rank == 0 && g.out == g.base) return;  // nothing to add
-  const float scale = rank == 0 || g.scaling == nullptr ? 1.0f : g.scaling[tile.adapter];
+  const float scale = tile.scale;
   const int steps = (rank + 31) / 32;
   const int pitch = (g.rank + 31) / 32 * 32 + 8;
   const uint16_t* wb = (const uint16_t*)g.B + (int64_t)max(tile.adapter, 0) * g.n * g.rank;
+  __syncthreads();
 
   // The base of rows 4 h .. 4 h + 3 of 16, at the lane's columns.  Vectors that
   // pass n are read at column 0 and not used.
@@ -350,19 +471,19 @@ __global__ __launch_bounds__(kThreads) void adapter_up_kernel(AdaptArgs g, int c
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const int i = t * 16 + 4 * h + q;
-        v[q] = load_raw<BK, kColTiles>(g.base, rows_s[i < tile.rows ? i : 0] * g.ldb + (c0 + kColTiles <= g.n ? c0 : 0));
+        v[q] = load_raw<BK, kColTiles>(g.base, (int64_t)rows_s[i < tile.rows ? i : 0] * g.ldb + (c0 + kColTiles <= g.n ? c0 : 0));
       }
     }
   };
-  const int first = (int)blockIdx.x * col_blocks * kBlockCols + wave * kWaveCols + low * kColTiles;
+  const int wave_col = (int)blockIdx.x * col_blocks * kBlockCols + wave * kWaveCols;
+  const int first = wave_col + low * kColTiles;
   BaseVec base[4];
   WeightFrags<TK> w[HELD > 0 ? HELD : 1];
   // (in flight while the inner values are added up)
   load_base(0, first, base);
-  if (rank != 0) {
 #pragma unroll
-    for (int b = 0; b < HELD; ++b) load_frags<TK>(g, wb, first, b * 32 + 8 * h, w[b]);
-  }
+  for (int b = 0; b < HELD; ++b)
+    if (b < steps) load_frags<TK>(g, wb, rank, b, wave_col, lane, w[b]);
 
   // the rows' inner values: the splits' parts in order, four ranks per thread
   const int quads = (HELD > 0 ? HELD : steps) * 8;
@@ -396,22 +517,25 @@ __global__ __launch_bounds__(kThreads) void adapter_up_kernel(AdaptArgs g, int c
   __syncthreads();
 
   for (int cb = 0; cb < col_blocks; ++cb) {
-    const int c0 = first + cb * kBlockCols;
-    if (c0 - low * kColTiles >= g.n) break;
+    const int col = wave_col + cb * kBlockCols, c0 = col + low * kColTiles;
+    if (col >= g.n) break;
     const bool whole = c0 + kColTiles <= g.n;
-    if (cb > 0) {
-      load_base(0, c0, base);
-      if (rank != 0) {
+    WeightFrags<TK> next_w[HELD > 0 ? HELD : 1];  // the next columns'
+    if (cb + 1 < col_blocks) {
 #pragma unroll
-        for (int b = 0; b < HELD; ++b) load_frags<TK>(g, wb, c0, b * 32 + 8 * h, w[b]);
-      }
+      for (int b = 0; b < HELD; ++b)
+        if (b < steps) load_frags<TK>(g, wb, rank, b, col + kBlockCols, lane, next_w[b]);
     }
 #pragma unroll
-    for (int b = 0; b < HELD; ++b) finish_frags<TK>(rank, b * 32 + 8 * h, w[b]);
-#pragma unroll 1
-    for (int t = 0; t * 16 < tile.rows; ++t) {
+    for (int b = 0; b < HELD; ++b) finish_frags<TK>(rank, b, lane, slots_s[wave], w[b]);
+    auto sixteen_rows = [&](int t) __attribute__((always_inline)) {
+      // the next rows' base, or that of the next columns' first rows
       BaseVec next[4];
-      if (TR > 1 && (t + 1) * 16 < tile.rows) load_base(t + 1, c0, next);
+      if (TR > 1 && (t + 1) * 16 < tile.rows) {
+        load_base(t + 1, c0, next);
+      } else if (cb + 1 < col_blocks) {
+        load_base(0, c0 + kBlockCols, next);
+      }
       float sum[kColTiles][4];
       auto multiply = [&](int b, const WeightFrags<TK>& f, f32x4(&acc)[kColTiles]) {
         u32x4 v[kPlanes];
@@ -446,8 +570,8 @@ __global__ __launch_bounds__(kThreads) void adapter_up_kernel(AdaptArgs g, int c
 #pragma unroll
           for (int q = 0; q < 4; ++q) sum[s][q] = 0.0f;
         for (int b = 0; b < steps; ++b) {
-          load_frags<TK>(g, wb, c0, b * 32 + 8 * h, w[0]);
-          finish_frags<TK>(rank, b * 32 + 8 * h, w[0]);
+          load_frags<TK>(g, wb, rank, b, col, lane, w[0]);
+          finish_frags<TK>(rank, b, lane, slots_s[wave], w[0]);
           f32x4 acc[kColTiles];
 #pragma unroll
           for (int s = 0; s < kColTiles; ++s) acc[s] = f32x4{0, 0, 0, 0};
@@ -462,7 +586,7 @@ __global__ __launch_bounds__(kThreads) void adapter_up_kernel(AdaptArgs g, int c
       for (int q = 0; q < 4; ++q) {
         const int i = t * 16 + 4 * h + q;
         if (i >= tile.rows) continue;
-        const int row = rows_s[i];
+        const int64_t row = rows_s[i];
         float v[kColTiles];
 #pragma unroll
         for (int s = 0; s < kColTiles; ++s) v[s] = 0.0f;
@@ -498,10 +622,22 @@ __global__ __launch_bounds__(kThreads) void adapter_up_kernel(AdaptArgs g, int c
             }
         }
       }
-      if constexpr (TR > 1) {
+      if (TR > 1 || cb + 1 < col_blocks) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) base[q] = next[q];
       }
+    };
+    if constexpr (TR == 1) {
+      sixteen_rows(0);
+    } else {
+#pragma unroll 1
+      for (int t = 0; t * 16 < tile.rows; ++t) sixteen_rows(t);
+    }
+    if (cb + 1 < col_blocks) {
+#pragma unroll
+      for (int b = 0; b < HELD; ++b)
+#pragma unroll
+        for (int s = 0; s < kColTiles; ++s) w[b].hi[s] = next_w[b].hi[s];
     }
   }
 }
@@ -514,27 +650,34 @@ auto up_kernel(int rank) {
 
 template <int TK, int TR>
 hipError_t launch_tiles(const AdaptArgs& a, hipStream_t stream) {
-  const unsigned tiles = (unsigned)(TR == 1 ? a.m : a.max_tiles);
+  const unsigned tiles = (unsigned)a.max_tiles;
   const int nr = a.rank > 32 ? 4 : a.rank > 16 ? 2 : 1;
   const unsigned blocks = (unsigned)((a.rank + 16 * nr - 1) / (16 * nr) * a.splits);
-  const size_t lds = (size_t)kWaves * TR * nr * 64 * sizeof(f32x4);
+  const int entries = TR * nr > 2 * (TR + nr) ? TR * nr : 2 * (TR + nr);  // of 1 KiB, per wave
+  const size_t lds = (size_t)kWaves * entries * 64 * sizeof(f32x4);
   const auto down = nr == 1   ? adapter_down_kernel<TK, TR, 1>
                     : nr == 2 ? adapter_down_kernel<TK, TR, 2> : adapter_down_kernel<TK, TR, 4>;
   hipLaunchKernelGGL(down, dim3(blocks, tiles), dim3(kThreads), lds, stream, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int col_blocks = TR == 1 ? 1 : 2;
+  // columns of a workgroup: as many as leave about four workgroups for each CU
+  const int64_t all = (int64_t)tiles * ((a.n + kBlockCols - 1) / kBlockCols);
+  const int col_blocks = TR > 1 ? 2 : all >= 4096 ? 4 : all >= 1536 ? 2 : 1;
   const unsigned cols = (unsigned)((a.n + kBlockCols * col_blocks - 1) / (kBlockCols * col_blocks));
   const size_t planes = (size_t)kPlanes * 16 * TR * ((a.rank + 31) / 32 * 32 + 8) * 2;
   const auto up = a.base == nullptr       ? up_kernel<TK, TR, kNoBase>((int)a.rank)
                   : a.base_kind == CK_F32 ? up_kernel<TK, TR, CK_F32>((int)a.rank) : up_kernel<TK, TR, TK>((int)a.rank);
-  if (planes > 65536) {
-    e = hipFuncSetAttribute((const void*)up, hipFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024 - 1024);
+  if (planes > 40 * 1024) {  // (with the static part past the 64 KiB that need no asking)
+    e = hipFuncSetAttribute((const void*)up, hipFuncAttributeMaxDynamicSharedMemorySize, 128 * 1024);
     if (e != hipSuccess) return e;
   }
   hipLaunchKernelGGL(up, dim3(cols, tiles), dim3(kThreads), planes, stream, a, col_blocks);
   return hipGetLastError();
 }
+
+// Up to kAdaptDirectRows rows: a place of the grid for each adapter and for each 16
+// rows that one may have more, if those are fewer than the rows.
+bool adapt_by_adapter(int64_t m, int64_t count) { return count + 1 + m / 16 < m; }
 
 }  // namespace
 
@@ -555,7 +698,7 @@ int adapt_splits(int64_t m, int64_t k, int64_t rank, int64_t* split_len) {
 }
 
 int64_t adapt_max_tiles(int64_t m, int64_t count) {
-  if (m <= kAdaptDirectRows) return 0;
+  if (m <= kAdaptDirectRows) return adapt_by_adapter(m, count) ? count + 1 + m / 16 : m;
   const int64_t groups = count + 1 < m ? count + 1 : m;
   return m / kAdaptTileRows + groups;
 }
@@ -565,8 +708,11 @@ hipError_t launch_adapters(const AdaptArgs& a, int kind, hipStream_t stream) {
       a.k % 8 != 0 || a.splits < 1 || (int64_t)a.splits * a.split_len < a.k || a.split_len % 256 != 0 ||
       a.max_tiles > 65535)
     return hipErrorInvalidValue;
-  if (a.m <= kAdaptDirectRows)
-    return kind == CK_F16 ? launch_tiles<CK_F16, 1>(a, stream) : launch_tiles<CK_BF16, 1>(a, stream);
+  if (a.m <= kAdaptDirectRows) {
+    AdaptArgs d = a;
+    d.by_adapter = adapt_by_adapter(a.m, a.count);
+    return kind == CK_F16 ? launch_tiles<CK_F16, 1>(d, stream) : launch_tiles<CK_BF16, 1>(d, stream);
+  }
   hipLaunchKernelGGL(adapter_sort_kernel, dim3(1), dim3(kSortThreads), (size_t)(a.count + 1) * 4, stream, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;

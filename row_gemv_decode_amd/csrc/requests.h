@@ -62,16 +62,19 @@ struct AdaptArgs {
   int32_t splits;        // of k over workgroups
   int32_t split_len;     // elements of a split, a multiple of 32
   float* h;              // [splits][m][rank] partial inner values
-  uint32_t* tiles;       // batches past kAdaptDirectRows: tile count, then (adapter, first, rows) each
-  uint32_t* order;       // and the rows, by adapter
+  uint32_t* tile_count;  // batches past kAdaptDirectRows: how many tiles there are
+  uint32_t* tiles;       // [max_tiles][4]: adapter, rows (0: no tile), rank, scaling
+  uint32_t* order;       // the tiles' rows, room for adapt_tile_rows each
   int32_t max_tiles;
+  int32_t by_adapter;    // (set by the launch) up to kAdaptDirectRows: tiles in the order of the adapters
 };
 
 // rows up to which every workgroup finds its adapter's rows by itself
 constexpr int kAdaptDirectRows = 256;
 constexpr int kAdaptTileRows = 64;  // rows of a tile in larger batches
 int adapt_splits(int64_t m, int64_t k, int64_t rank, int64_t* split_len);
-int64_t adapt_max_tiles(int64_t m, int64_t count);  // 0: no tile list
+constexpr int64_t adapt_tile_rows(int64_t m) { return m <= kAdaptDirectRows ? 16 : kAdaptTileRows; }
+int64_t adapt_max_tiles(int64_t m, int64_t count);
 
 hipError_t launch_adapters(const AdaptArgs& args, int kind, hipStream_t stream);
 

@@ -32,11 +32,12 @@ __device__ __forceinline__ float value_at(const void* p, int64_t i) {
   }
 }
 
-// the stored bits of N values (4 or 8): dwords in memory order
+// the stored bits of N values (4 or 8): dwords in memory order.  (A vector, not an
+// array: arrays of these that are copied as a whole ended up in scratch memory.)
 template <int K, int N>
 struct Raw {
   static constexpr int kWords = N * kind_size<K>() / 4;
-  uint32_t w[kWords];
+  uint32_t w __attribute__((ext_vector_type(kWords)));
 };
 
 template <int K, int N>
