@@ -893,13 +893,22 @@ class RMSNorm(NamedTuple):
     scales: "torch.Tensor"    # float32 [m][groups]
 
 
-def _output(where, name, t, index, shape, dtype):
-    """Row stride of a given output of that shape (and type, unless it is None)."""
+_new_norm = tuple.__new__  # (a named tuple's own constructor takes twice as long)
+
+
+def _input_stride(where, name, t, stream):
+    """_input_rows, with 0 for the stride of rows that lie one behind the other (the
+    library's word for dense rows), which costs the host less."""
+    return (t, 0) if t.is_contiguous() else _input_rows(where, name, t, stream)
+
+
+def _output_stride(where, name, t, index, shape, dtype):
+    """Row stride (0: dense) of a given output of that shape and type (None: any)."""
     if t.shape != shape or (dtype is not None and t.dtype is not dtype):
         raise ValueError(f"{where}: {name} must be {list(shape)}" + (f" of type {dtype}" if dtype else ""))
     if t.get_device() != index:
         raise ValueError(f"{where}: {name} must be on the GPU of the other tensors")
-    return _rows(where, name, t)
+    return 0 if t.is_contiguous() else _rows(where, name, t)
 
 
 def rms_norm(x, weight=None, eps=1e-6, residual=None, residual_out=None, out=None, out_dtype=None, quant=None, q=None,
@@ -915,7 +924,7 @@ def rms_norm(x, weight=None, eps=1e-6, residual=None, residual_out=None, out=Non
     (float8_e4m3fn) and scales holds what to multiply them by, one per row or per
     group of columns; then there is an `out` only if it or out_dtype is given.
     Rows of any stride; input rows that share memory are copied apart first."""
-    x, ldx = _input_rows("rms_norm", "x", x, stream)
+    x, ldx = _input_stride("rms_norm", "x", x, stream)
     shape, dtype = x.shape, x.dtype
     m, d = shape
     code = _CODES.get(dtype)
@@ -932,20 +941,20 @@ def rms_norm(x, weight=None, eps=1e-6, residual=None, residual_out=None, out=Non
         w_ptr, w_code = weight.data_ptr(), _CODES.get(weight.dtype, 0)
     r_ptr, ldr, r_code, ro_ptr, ldro = None, 0, code, None, 0
     if residual is not None:
-        residual, ldr = _input_rows("rms_norm", "residual", residual, stream)
+        residual, ldr = _input_stride("rms_norm", "residual", residual, stream)
         if residual.shape != shape or residual.get_device() != index:
             raise ValueError(f"rms_norm: residual must be {list(shape)}, on x's GPU")
         r_ptr, r_code = residual.data_ptr(), _CODES.get(residual.dtype, 0)
         if residual_out is None:
             residual_out = _empty(shape, residual.dtype, x.device, stream)
         else:
-            ldro = _output("rms_norm", "residual_out", residual_out, index, shape, residual.dtype)
+            ldro = _output_stride("rms_norm", "residual_out", residual_out, index, shape, residual.dtype)
         ro_ptr = residual_out.data_ptr()
     elif residual_out is not None:
         raise ValueError("rms_norm: residual_out without a residual")
     o_ptr, ldo, o_code = None, 0, code
     if out is not None:
-        ldo = _output("rms_norm", "out", out, index, shape, out_dtype)
+        ldo = _output_stride("rms_norm", "out", out, index, shape, out_dtype)
     elif quant is None or out_dtype is not None:
         out = _empty(shape, out_dtype or dtype, x.device, stream)
     if out is not None:
@@ -956,11 +965,11 @@ def rms_norm(x, weight=None, eps=1e-6, residual=None, residual_out=None, out=Non
         if q is None:
             q = _empty(shape, torch.float8_e4m3fn, x.device, stream)
         else:
-            ldq = _output("rms_norm", "q", q, index, shape, torch.float8_e4m3fn)
+            ldq = _output_stride("rms_norm", "q", q, index, shape, torch.float8_e4m3fn)
         if scales is None:
             scales = _empty((m, groups), torch.float32, x.device, stream)
         else:
-            _output("rms_norm", "scales", scales, index, (m, groups), torch.float32)
+            _output_stride("rms_norm", "scales", scales, index, (m, groups), torch.float32)
             if not scales.is_contiguous():
                 raise ValueError("rms_norm: scales must be contiguous")
         q_ptr, s_ptr = q.data_ptr(), scales.data_ptr()
@@ -968,7 +977,7 @@ def rms_norm(x, weight=None, eps=1e-6, residual=None, residual_out=None, out=Non
         raise ValueError("rms_norm: q and scales go with quant")
     _check(_lib.skinny_rms_norm_run(m, d, x.data_ptr(), ldx, code, r_ptr, ldr, r_code, w_ptr, w_code, eps, ro_ptr, ldro, o_ptr,
                                     ldo, o_code, q_ptr, ldq, s_ptr, quant or 0, _handle(index, stream)), "skinny_rms_norm_run")
-    return RMSNorm(out, residual_out, q, scales)
+    return _new_norm(RMSNorm, (out, residual_out, q, scales))
 
 
 class Adapters:
@@ -1026,7 +1035,7 @@ def add_adapters(x, adapters, ids, base=None, out=None, out_dtype=None, stream=N
     says otherwise, and may be base itself.  Sums are held in fp32 and rounded
     once.  Rows of any stride (x's a multiple of 8); input rows that share memory
     are copied apart first."""
-    x, ldx = _input_rows("add_adapters", "x", x, stream)
+    x, ldx = _input_stride("add_adapters", "x", x, stream)
     m, k = x.shape
     if not isinstance(adapters, Adapters) or x.dtype is not adapters.dtype:
         raise TypeError("add_adapters: takes Adapters of x's type")
@@ -1043,7 +1052,7 @@ def add_adapters(x, adapters, ids, base=None, out=None, out_dtype=None, stream=N
             return add_adapters(x, adapters, ids, base, out, out_dtype, stream)
     b_ptr, ldb, b_code = None, 0, F32
     if base is not None:
-        base, ldb = _input_rows("add_adapters", "base", base, stream)
+        base, ldb = _input_stride("add_adapters", "base", base, stream)
         if base.shape != (m, n) or base.get_device() != index:
             raise ValueError(f"add_adapters: base must be [{m}][{n}] on {adapters.device}")
         b_ptr, b_code = base.data_ptr(), _CODES.get(base.dtype, 0)
@@ -1051,7 +1060,7 @@ def add_adapters(x, adapters, ids, base=None, out=None, out_dtype=None, stream=N
         out = _empty((m, n), out_dtype or (adapters.dtype if base is None else base.dtype), x.device, stream)
         ldo = 0
     else:
-        ldo = _output("add_adapters", "out", out, index, (m, n), out_dtype)
+        ldo = _output_stride("add_adapters", "out", out, index, (m, n), out_dtype)
     need = adapters._need.get(m) or adapters.workspace_bytes(m)
     handle = _handle(index, stream)
     with _adapter_lock:
@@ -1142,7 +1151,7 @@ def adjust_logits(logits, rules, out=None, out_dtype=None, stream=None):
     `out`); out may be the logits themselves, of which then only those that change
     are written.  Rows of any stride; input rows that share memory are copied apart."""
     given = logits
-    logits, ld = _input_rows("adjust_logits", "logits", logits, stream)
+    logits, ld = _input_stride("adjust_logits", "logits", logits, stream)
     shape = logits.shape
     m, vocab = shape
     if not isinstance(rules, LogitRules) or rules.m != m or rules.vocab != vocab:
@@ -1160,7 +1169,7 @@ def adjust_logits(logits, rules, out=None, out_dtype=None, stream=None):
         out = _empty(shape, out_dtype or logits.dtype, logits.device, stream)
         ldo = 0
     else:
-        ldo = _output("adjust_logits", "out", out, index, shape, out_dtype)
+        ldo = _output_stride("adjust_logits", "out", out, index, shape, out_dtype)
     _check(_lib.skinny_adjust_logits_run(m, vocab, logits.data_ptr(), ld, code, rules._addr, out.data_ptr(), ldo,
                                          _CODES.get(out.dtype, 0), _handle(index, stream)), "skinny_adjust_logits_run")
     return out

@@ -197,6 +197,10 @@ __global__ __launch_bounds__(kSortThreads) void adapter_sort_kernel(AdaptArgs g)
 #pragma unroll
     for (int i = 0; i < kSortIds; ++i) kept[i] = place_of(i * kSortThreads + tid);
   }
+  // each thread's consecutive adapters; the first one's rank and scaling are in flight
+  const int each = (places + kSortThreads - 1) / kSortThreads;
+  const int a0 = tid * each, a1 = min(a0 + each, places);
+  const u32x4 entry0 = tile_entry(g, a0 < g.count ? a0 : -1, 0);
   for (int i = tid; i < places; i += kSortThreads) counts_s[i] = 0;
   __syncthreads();
   if (once) {
@@ -206,9 +210,7 @@ __global__ __launch_bounds__(kSortThreads) void adapter_sort_kernel(AdaptArgs g)
     for (int t0 = 0; t0 < g.m; t0 += kSortThreads) take_places(counts_s, place_of(t0 + tid), t0 + tid < g.m);
   }
   __syncthreads();
-  // each thread's consecutive adapters, then the sums of the threads before it
-  const int each = (places + kSortThreads - 1) / kSortThreads;
-  const int a0 = tid * each, a1 = min(a0 + each, places);
+  // their tiles, then the sums of the threads before it
   uint32_t tiles = 0;
   for (int a = a0; a < a1; ++a) tiles += (counts_s[a] + kAdaptTileRows - 1) / kAdaptTileRows;
   uint32_t tile_at = tiles;  // inclusive sum over the wave
@@ -225,9 +227,12 @@ __global__ __launch_bounds__(kSortThreads) void adapter_sort_kernel(AdaptArgs g)
   for (int a = a0; a < a1; ++a) {
     const uint32_t count = counts_s[a];
     counts_s[a] = tile_at * kAdaptTileRows;  // where the adapter's rows start
-    for (uint32_t done = 0; done < count; done += kAdaptTileRows)
-      ((u32x4*)g.tiles)[tile_at++] =
-          tile_entry(g, a < g.count ? a : -1, (int)min(count - done, (uint32_t)kAdaptTileRows));
+    if (count == 0) continue;
+    u32x4 entry = a == a0 ? entry0 : tile_entry(g, a < g.count ? a : -1, 0);
+    for (uint32_t done = 0; done < count; done += kAdaptTileRows) {
+      entry[1] = min(count - done, (uint32_t)kAdaptTileRows);
+      ((u32x4*)g.tiles)[tile_at++] = entry;
+    }
   }
   __syncthreads();
   if (once) {

@@ -5,30 +5,27 @@
 //   x_j = x_j - (frequency c_j + presence [c_j > 0])          c_j: times j was generated
 //   x_j = x_j + bias_j;   x_j = -inf where the mask does not allow j
 //
-// Few of a row's logits are penalised or biased, so the work is a stream and a
-// few corrections.  A workgroup owns a segment of a row:
-//   * it counts the row's tokens that fall into the segment in a table in LDS
-//     (one entry per token of the vocabulary: times generated, whether in the
-//     prompt, whether biased) and lists those that occur, each once, by the
-//     first count of its entry;
-//   * it copies the segment, converted to the output's type, with -inf where the
-//     mask says so (in place: it writes only what the mask takes away);
-//   * it then computes each listed token's logit from the input and the
-//     table and overwrites the copy.
-// The stream needs no table, and the corrections cost a gather of a few logits.
-// Counts are integers and each logit has one writer after the stream, so the
-// order of the atomics changes nothing.  HBM-bound for many rows: the logits
-// are read and written once; a row's tokens are read once per segment, from L2.
+// A workgroup owns a segment of a row.  It counts the row's tokens that fall into
+// the segment in a table in LDS (an entry per token of the vocabulary: times
+// generated, whether in the prompt, whether biased), then streams the segment
+// from input to output with each vector's entries and mask bits at hand; in place it
+// touches only the vectors that change.  Counts are integers, so the order of the
+// atomics changes nothing.  Biased tokens are few: the stream leaves their logits as
+// they are, and where a segment has any, one thread each computes them afterwards,
+// adding a token's biases in the order of the list.
+// HBM-bound for many rows: the logits are read and written once; a row's tokens
+// are read once per segment, from L2.  For few rows the chain of memory latencies
+// counts: what the first steps need is all in flight before the table is cleared.
 #include <math.h>
 
 #include "requests.h"
 #include "vector_io.h"
+#include "wave_ops.h"
 
 namespace skinny {
 
 namespace {
 
-constexpr int kThreads = 256;
 constexpr int kSegmentMax = 16384;  // tokens of a segment with a table
 // table entries: 16 bits, or 32 for histories that could count further than 14 bits
 constexpr uint32_t kInPrompt = 1, kBiased = 2, kOnce = 4;
@@ -62,23 +59,35 @@ __device__ __forceinline__ float penalised(float x, uint32_t entry, const Penalt
   return x;
 }
 
-// four token ids from position i of a list of `room` on (-1 past it)
-__device__ __forceinline__ void load_tokens4(const void* list, int64_t at, int i, int room, int tokens64, int64_t (&t)[4]) {
+// four token ids of a list of `room`, from position i on (any past it): 16 bytes, or
+// 32 for 64-bit ids, as loaded
+struct Tokens4 {
+  Raw<CK_F32, 8> w;
+};
+__device__ __forceinline__ void load_tokens4(const void* list, int64_t at, int i, int room, int tokens64, Tokens4& t) {
   if (i + 4 <= room) {
     if (tokens64 != 0) {
-      const Raw<CK_F32, 8> w = load_raw<CK_F32, 8>(list, 2 * (at + i));
-#pragma unroll
-      for (int e = 0; e < 4; ++e) t[e] = (int64_t)((uint64_t)w.w[2 * e + 1] << 32 | w.w[2 * e]);
+      t.w = load_raw<CK_F32, 8>(list, 2 * (at + i));
     } else {
       const Raw<CK_F32, 4> w = load_raw<CK_F32, 4>(list, at + i);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) t[e] = (int32_t)w.w[e];
+      for (int e = 0; e < 4; ++e) t.w.w[e] = w.w[e];
     }
   } else {
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      t[e] = i + e >= room ? -1 : tokens64 != 0 ? ((const int64_t*)list)[at + i + e] : (int64_t)((const int32_t*)list)[at + i + e];
+    for (int e = 0; e < 4; ++e) {
+      if (i + e >= room) break;
+      if (tokens64 != 0) {
+        const u32x2 v = *(const u32x2_align4*)((const int64_t*)list + at + i + e);
+        t.w.w[2 * e] = v[0], t.w.w[2 * e + 1] = v[1];
+      } else {
+        t.w.w[e] = ((const uint32_t*)list)[at + i + e];
+      }
+    }
   }
+}
+__device__ __forceinline__ int64_t token_of(const Tokens4& t, int e, int tokens64) {
+  return tokens64 != 0 ? (int64_t)((uint64_t)t.w.w[2 * e + 1] << 32 | t.w.w[2 * e]) : (int64_t)(int32_t)t.w.w[e];
 }
 
 __device__ __forceinline__ int64_t token_at(const void* list, int64_t i, int tokens64) {
@@ -91,12 +100,12 @@ constexpr int stream_elems() { return XK == CK_F32 || OK == CK_F32 ? 4 : 8; }
 
 // TABLE: 0 (mask only), or an entry's bits
 template <int XK, int OK, bool IN_PLACE, int TABLE>
-__global__ __launch_bounds__(kThreads) void adjust_kernel(AdjustArgs g) {
+__global__ __launch_bounds__(512) void adjust_kernel(AdjustArgs g) {
   extern __shared__ uint32_t table_s[];
-  __shared__ int listed_s, twice_s;
+  __shared__ int biased_s, twice_s;
   constexpr int CW = TABLE == 0 ? 16 : TABLE;
   using At = Entry<CW>;
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, threads = blockDim.x;
   const uint32_t row_index = blockIdx.x / (uint32_t)g.segments;
   const int64_t r = row_index;
   const int first = (int)(blockIdx.x - row_index * (uint32_t)g.segments) * g.seg_len;  // a multiple of 32
@@ -108,125 +117,158 @@ __global__ __launch_bounds__(kThreads) void adjust_kernel(AdjustArgs g) {
     const int which = g.mask_rows != nullptr ? g.mask_rows[r] : (int)r;
     if (which >= 0 && which < g.masks) mask = (const uint8_t*)(g.mask + which * g.ldm) + (first >> 3);
   }
-  uint16_t* list_s = (uint16_t*)(table_s + (g.seg_len * CW / 32));
+
+  // what the first steps of both loops need is in flight before either begins
+  constexpr int H = 4;  // history loads of a thread in flight, four ids each
+  Tokens4 ids[TABLE != 0 ? H : 1];
+  int held = 0, prompt = 0;
+  Penalties pen = {1.0f, 0.0f, 0.0f};
+  const int64_t bias_row = r * g.biases;
+  auto bias_off = [&](int i) -> int64_t {  // -1: not in the segment
+    const int64_t off = token_at(g.bias_ids, bias_row + i, g.tokens64) - first;
+    return off < len ? off : -1;
+  };
+  int64_t my_bias = -1;
+  if constexpr (TABLE != 0) {
+    if (g.history != nullptr) {
+#pragma unroll
+      for (int u = 0; u < H; ++u)
+        load_tokens4(g.history, r * g.ldh, (u * threads + tid) * 4, g.history_len, g.tokens64, ids[u]);
+      held = g.lengths != nullptr ? max(0, min(g.lengths[r], g.history_len)) : g.history_len;
+      prompt = g.prompt_lengths != nullptr ? max(0, min(g.prompt_lengths[r], held)) : 0;
+      if (g.repetition != nullptr) pen.theta = g.repetition[r];
+      if (g.frequency != nullptr) pen.frequency = g.frequency[r];
+      if (g.presence != nullptr) pen.presence = g.presence[r];
+    }
+    if (tid < g.biases) my_bias = bias_off(tid);
+  }
+  constexpr int VE = stream_elems<XK, OK>();
+  constexpr int U = 4;  // vectors of a thread in flight
+  constexpr uint32_t kAll = (1u << VE) - 1;
+  const int vectors = len / VE;
+  auto mask_bits = [&](int v) -> uint32_t {  // bits of vector v's tokens
+    if (mask == nullptr) return kAll;
+    return VE == 8 ? mask[v] : (uint32_t)mask[v >> 1] >> (4 * (v & 1)) & kAll;
+  };
+  Raw<XK, VE> raw[U];
+  uint32_t bits[U];
+  auto load_step = [&](int v0) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int v = min(v0 + u * threads, vectors - 1);
+      bits[u] = mask_bits(v);
+      if (!IN_PLACE) raw[u] = load_raw<XK, VE>(x_row, (int64_t)v * VE);
+    }
+  };
+  if (vectors > 0) load_step(tid);
 
   if constexpr (TABLE != 0) {
-    for (int i = tid; i < g.seg_len * CW / 32; i += kThreads) table_s[i] = 0;
-    if (tid == 0) listed_s = twice_s = 0;
-    __syncthreads();
-    if (g.history != nullptr) {
-      const int held = g.lengths != nullptr ? max(0, min(g.lengths[r], g.history_len)) : g.history_len;
-      const int prompt = g.prompt_lengths != nullptr ? max(0, min(g.prompt_lengths[r], held)) : 0;
-      for (int i = tid * 4; i < held; i += kThreads * 4) {
-        int64_t t[4];
-        load_tokens4(g.history, r * g.ldh, i, g.history_len, g.tokens64, t);
+    for (int i = tid; i < g.seg_len * CW / 32; i += threads) table_s[i] = 0;
+    if (tid == 0) biased_s = twice_s = 0;
+    lds_barrier();
+    for (int i0 = 0; i0 < held; i0 += H * threads * 4) {
+      if (i0 > 0) {
+#pragma unroll
+        for (int u = 0; u < H; ++u)
+          load_tokens4(g.history, r * g.ldh, i0 + (u * threads + tid) * 4, held, g.tokens64, ids[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < H; ++u) {
+        const int i = i0 + (u * threads + tid) * 4;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int64_t off = t[e] - first;
+          const int64_t off = token_of(ids[u], e, g.tokens64) - first;
           if (i + e < held && off >= 0 && off < len) {
             const At at((int)off);
-            const uint32_t old = i + e < prompt ? atomicOr(&table_s[at.word], kInPrompt << at.shift)
-                                                : atomicAdd(&table_s[at.word], kOnce << at.shift);
-            if (at.of(old) == 0) list_s[atomicAdd(&listed_s, 1)] = (uint16_t)off;
+            if (i + e < prompt) {
+              atomicOr(&table_s[at.word], kInPrompt << at.shift);
+            } else {
+              atomicAdd(&table_s[at.word], kOnce << at.shift);
+            }
           }
         }
       }
     }
+    for (int i = tid; i < g.biases; i += threads) {
+      const int64_t off = i == tid ? my_bias : bias_off(i);
+      if (off >= 0) {
+        const At at((int)off);
+        biased_s = 1;
+        if ((at.of(atomicOr(&table_s[at.word], kBiased << at.shift)) & kBiased) != 0) twice_s = 1;
+      }
+    }
+    lds_barrier();
   }
 
-  // the stream
-  constexpr int VE = stream_elems<XK, OK>();
-  const int vectors = len / VE;
-  auto mask_bits = [&](int v) -> uint32_t {  // bits of vector v's tokens
-    if (mask == nullptr) return 0xffu;
-    return VE == 8 ? mask[v] : (uint32_t)mask[v >> 1] >> (4 * (v & 1)) & 15u;
+  // the entries of vector v, and whether any of them is not 0
+  auto entries = [&](int v, uint32_t(&e)[VE]) -> bool {
+    constexpr int W = VE * CW / 32;
+    uint32_t w[W], some = 0;
+#pragma unroll
+    for (int i = 0; i < W; ++i) some |= w[i] = table_s[v * W + i];
+#pragma unroll
+    for (int i = 0; i < VE; ++i) e[i] = CW == 16 ? (w[i / 2] >> (16 * (i & 1))) & 0xffffu : w[i];
+    return some != 0;
   };
-  constexpr uint32_t kAll = (1u << VE) - 1;
-  if constexpr (IN_PLACE) {
-    if (mask != nullptr) {
-      for (int v = tid; v < vectors; v += kThreads) {
-        const uint32_t b = mask_bits(v) & kAll;
-        if (b == kAll) continue;
-        float x[VE];
-        if (b != 0) unpack_raw<XK, VE>(load_raw<XK, VE>(x_row, (int64_t)v * VE), x);
+  auto adjusted = [&](float x, uint32_t entry) { return (entry & kBiased) != 0 ? x : penalised(x, entry, pen); };
+  for (int v0 = tid; v0 < vectors; v0 += U * threads) {
+    if (v0 != tid) load_step(v0);
+    uint32_t e[U][VE];
+    bool some[U];  // whether a vector has entries
 #pragma unroll
-        for (int e = 0; e < VE; ++e) x[e] = (b >> e & 1) != 0 ? x[e] : -INFINITY;
-        store_vec<OK, VE>(o_row, (int64_t)v * VE, x);
-      }
-      for (int j = vectors * VE + tid; j < len; j += kThreads)
-        if (!allowed_at(mask, j)) store_out<OK>(o_row, j, -INFINITY);
-    }
-  } else {
-    constexpr int U = 4;  // vectors of a thread in flight
-    for (int v0 = tid; v0 < vectors; v0 += U * kThreads) {
-      Raw<XK, VE> raw[U];
-      uint32_t bits[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int v = min(v0 + u * kThreads, vectors - 1);
-        raw[u] = load_raw<XK, VE>(x_row, (int64_t)v * VE);
-        bits[u] = mask_bits(v);
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        float x[VE];
-        unpack_raw<XK, VE>(raw[u], x);
-#pragma unroll
-        for (int e = 0; e < VE; ++e) x[e] = (bits[u] >> e & 1) != 0 ? x[e] : -INFINITY;
-        if (v0 + u * kThreads < vectors) store_vec<OK, VE>(o_row, (int64_t)(v0 + u * kThreads) * VE, x);
+    for (int u = 0; u < U; ++u) {
+      const int v = v0 + u * threads;
+      some[u] = TABLE != 0 && entries(min(v, vectors - 1), e[u]);
+      if (IN_PLACE) {
+        if (v >= vectors) some[u] = false, bits[u] = kAll;
+        if (bits[u] != 0 && (bits[u] != kAll || some[u])) raw[u] = load_raw<XK, VE>(x_row, (int64_t)v * VE);
       }
     }
-    for (int j = vectors * VE + tid; j < len; j += kThreads)
-      store_out<OK>(o_row, j, allowed_at(mask, j) ? value_at<XK>(x_row, j) : -INFINITY);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int v = v0 + u * threads;
+      float x[VE];
+      unpack_raw<XK, VE>(raw[u], x);
+      if (TABLE != 0 && some[u]) {
+#pragma unroll
+        for (int i = 0; i < VE; ++i) x[i] = adjusted(x[i], e[u][i]);
+      }
+#pragma unroll
+      for (int i = 0; i < VE; ++i) x[i] = (bits[u] >> i & 1) != 0 ? x[i] : -INFINITY;
+      if (IN_PLACE ? bits[u] != kAll || some[u] : v < vectors) store_vec<OK, VE>(o_row, (int64_t)v * VE, x);
+    }
+  }
+  for (int j = vectors * VE + tid; j < len; j += threads) {
+    const At at(j);
+    const uint32_t entry = TABLE != 0 ? at.of(table_s[at.word]) : 0;
+    if (!allowed_at(mask, j)) {
+      store_out<OK>(o_row, j, -INFINITY);
+    } else if (!IN_PLACE || entry != 0) {
+      store_out<OK>(o_row, j, adjusted(value_at<XK>(x_row, j), entry));
+    }
   }
 
   if constexpr (TABLE != 0) {
-    // the biased tokens' flags; which are listed twice matters later
-    const int64_t bias_row = r * g.biases;
-    if (g.biases > 0) {
-      for (int i = tid; i < g.biases; i += kThreads) {
-        const int64_t off = token_at(g.bias_ids, bias_row + i, g.tokens64) - first;
-        if (off >= 0 && off < len) {
-          const At at((int)off);
-          if ((at.of(atomicOr(&table_s[at.word], kBiased << at.shift)) & kBiased) != 0) twice_s = 1;
-        }
-      }
-    }
-    wait_mem();  // the stream's stores come before the corrections
+    if (biased_s == 0) return;  // (the same in every thread)
+    wait_mem();                 // the stream's stores come before the biased tokens'
     __syncthreads();
-    Penalties p;
-    p.theta = g.repetition != nullptr ? g.repetition[r] : 1.0f;
-    p.frequency = g.frequency != nullptr ? g.frequency[r] : 0.0f;
-    p.presence = g.presence != nullptr ? g.presence[r] : 0.0f;
-    const int listed = listed_s;
-    for (int i = tid; i < listed; i += kThreads) {
-      const int off = list_s[i];
+    const bool twice = twice_s != 0;
+    for (int i = tid; i < g.biases; i += threads) {
+      const int64_t o = i == tid ? my_bias : bias_off(i);
+      if (o < 0) continue;
+      const int off = (int)o;
       const At at(off);
-      const uint32_t entry = at.of(table_s[at.word]);
-      if ((entry & kBiased) != 0) continue;
-      const float x = penalised(value_at<XK>(x_row, off), entry, p);
-      store_out<OK>(o_row, off, allowed_at(mask, off) ? x : -INFINITY);
-    }
-    if (g.biases > 0) {
-      __syncthreads();
-      const bool twice = twice_s != 0;
-      for (int i = tid; i < g.biases; i += kThreads) {
-        const int64_t token = token_at(g.bias_ids, bias_row + i, g.tokens64), o = token - first;
-        if (o < 0 || o >= len) continue;
-        const int off = (int)o;
-        const At at(off);
-        // the first to take the flag away writes the token's logit
-        const uint32_t entry = at.of(atomicAnd(&table_s[at.word], ~(kBiased << at.shift)));
-        if ((entry & kBiased) == 0) continue;
-        float b = g.bias_values[bias_row + i];
-        if (twice) {
-          b = 0.0f;
-          for (int k = 0; k < g.biases; ++k)
-            if (token_at(g.bias_ids, bias_row + k, g.tokens64) == token) b += g.bias_values[bias_row + k];
-        }
-        const float x = penalised(value_at<XK>(x_row, off), entry, p) + b;
-        store_out<OK>(o_row, off, allowed_at(mask, off) ? x : -INFINITY);
+      // the first to take the flag away writes the token's logit
+      const uint32_t entry = at.of(atomicAnd(&table_s[at.word], ~(kBiased << at.shift)));
+      if ((entry & kBiased) == 0) continue;
+      float b = g.bias_values[bias_row + i];
+      if (twice) {
+        b = 0.0f;
+        for (int k = 0; k < g.biases; ++k)
+          if (bias_off(k) == o) b += g.bias_values[bias_row + k];
       }
+      const float x = penalised(value_at<XK>(x_row, off), entry, pen) + b;
+      store_out<OK>(o_row, off, allowed_at(mask, off) ? x : -INFINITY);
     }
   }
 }
@@ -243,15 +285,11 @@ hipError_t launch_kinds(AdjustArgs a, hipStream_t stream) {
   if (seg > a.vocab) seg = a.vocab;
   a.seg_len = (int32_t)((seg + 31) / 32 * 32);
   a.segments = (a.vocab + a.seg_len - 1) / a.seg_len;
-  a.list_len = a.history == nullptr ? 0 : a.history_len < a.seg_len ? a.history_len : a.seg_len;
-  const size_t lds = rules ? (size_t)a.seg_len * bits / 8 + (size_t)(a.list_len + 1) / 2 * 4 : 0;
+  const int threads = a.seg_len > 4096 ? 512 : 256;
+  const size_t lds = rules ? (size_t)a.seg_len * bits / 8 : 0;
   const auto fn = !rules ? adjust_kernel<XK, OK, IN_PLACE, 0>
                   : bits == 16 ? adjust_kernel<XK, OK, IN_PLACE, 16> : adjust_kernel<XK, OK, IN_PLACE, 32>;
-  if (lds > 65536) {
-    const hipError_t e = hipFuncSetAttribute((const void*)fn, hipFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024 - 256);
-    if (e != hipSuccess) return e;
-  }
-  const int64_t most = kMaxLaunchThreads / 2 / kThreads / a.segments;  // rows of a launch
+  const int64_t most = kMaxLaunchThreads / 2 / threads / a.segments;  // rows of a launch
   if (most < 1) return hipErrorInvalidValue;
   for (int64_t r = 0; r < a.m; r += most) {
     AdjustArgs part = a;
@@ -275,7 +313,7 @@ hipError_t launch_kinds(AdjustArgs a, hipStream_t stream) {
       part.mask = a.mask + r * a.ldm;
       part.masks = (int32_t)(a.masks - r);
     }
-    hipLaunchKernelGGL(fn, dim3((unsigned)(part.m * a.segments)), dim3(kThreads), lds, stream, part);
+    hipLaunchKernelGGL(fn, dim3((unsigned)(part.m * a.segments)), dim3(threads), lds, stream, part);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }

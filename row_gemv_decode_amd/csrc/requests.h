@@ -106,7 +106,6 @@ struct AdjustArgs {
   const int32_t* mask_rows;
   int32_t segments;      // (set by the launch) workgroups per row, seg_len tokens each
   int32_t seg_len;
-  int32_t list_len;      // (set by the launch) room for tokens that occur in a segment
 };
 
 hipError_t launch_adjust(const AdjustArgs& args, int x_kind, int out_kind, hipStream_t stream);

@@ -92,8 +92,8 @@ def test_norm_arguments(lib):
     x, r = torch.zeros((3, 40), dtype=half)[:, :32], torch.zeros((3, 32))
     got = sk.rms_norm(x, torch.ones(32), 1e-5, residual=r, residual_out=r, quant=0)
     (_, a), = lib.calls
-    assert a[:5] == (3, 32, x.data_ptr(), 40, sk.BF16) and a[5:8] == (r.data_ptr(), 32, sk.F32) and a[9:13] == (
-        sk.F32, 1e-5, r.data_ptr(), 32)
+    assert a[:5] == (3, 32, x.data_ptr(), 40, sk.BF16) and a[5:8] == (r.data_ptr(), 0, sk.F32) and a[9:13] == (
+        sk.F32, 1e-5, r.data_ptr(), 0)
     assert a[13] is None and got.out is None and got.residual is r          # 8 bits only
     assert got.q.dtype is torch.float8_e4m3fn and tuple(got.scales.shape) == (3, 1) and a[19] == 0
     got = sk.rms_norm(x, out_dtype=torch.float16, quant=32)
