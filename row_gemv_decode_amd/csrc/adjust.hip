@@ -18,6 +18,8 @@
 // counts: what the first steps need is all in flight before the table is cleared.
 #include <math.h>
 
+#include <type_traits>
+
 #include "requests.h"
 #include "vector_io.h"
 #include "wave_ops.h"
@@ -26,7 +28,8 @@ namespace skinny {
 
 namespace {
 
-constexpr int kSegmentMax = 16384;  // tokens of a segment with a table
+constexpr int kSegmentMax = 16384;     // tokens of a segment with a table
+constexpr int kMaskSegmentMax = 4096;  // and without one
 // table entries: 16 bits, or 32 for histories that could count further than 14 bits
 constexpr uint32_t kInPrompt = 1, kBiased = 2, kOnce = 4;
 
@@ -59,35 +62,34 @@ __device__ __forceinline__ float penalised(float x, uint32_t entry, const Penalt
   return x;
 }
 
-// four token ids of a list of `room`, from position i on (any past it): 16 bytes, or
-// 32 for 64-bit ids, as loaded
-struct Tokens4 {
-  Raw<CK_F32, 8> w;
-};
-__device__ __forceinline__ void load_tokens4(const void* list, int64_t at, int i, int room, int tokens64, Tokens4& t) {
-  if (i + 4 <= room) {
-    if (tokens64 != 0) {
-      t.w = load_raw<CK_F32, 8>(list, 2 * (at + i));
-    } else {
-      const Raw<CK_F32, 4> w = load_raw<CK_F32, 4>(list, at + i);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) t.w.w[e] = w.w[e];
+// 16 bytes of a list of `room` token ids, from position i on (any past the list): four
+// ids of 32 bits, two of 64
+__device__ __forceinline__ u32x4 load_tokens(const void* list, int64_t at, int i, int room, int tokens64) {
+  u32x4 w = {0, 0, 0, 0};
+  if (tokens64 != 0) {
+    const uint32_t* p = (const uint32_t*)list + 2 * (at + i);
+    if (i + 2 <= room) {
+      w = *(const u32x4_align4*)p;
+    } else if (i < room) {
+      w[0] = p[0], w[1] = p[1];
     }
   } else {
+    const uint32_t* p = (const uint32_t*)list + at + i;
+    if (i + 4 <= room) {
+      w = *(const u32x4_align4*)p;
+    } else {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if (i + e >= room) break;
-      if (tokens64 != 0) {
-        const u32x2 v = *(const u32x2_align4*)((const int64_t*)list + at + i + e);
-        t.w.w[2 * e] = v[0], t.w.w[2 * e + 1] = v[1];
-      } else {
-        t.w.w[e] = ((const uint32_t*)list)[at + i + e];
-      }
+      for (int e = 0; e < 3; ++e)
+        if (i + e < room) w[e] = p[e];
     }
   }
+  return w;
 }
-__device__ __forceinline__ int64_t token_of(const Tokens4& t, int e, int tokens64) {
-  return tokens64 != 0 ? (int64_t)((uint64_t)t.w.w[2 * e + 1] << 32 | t.w.w[2 * e]) : (int64_t)(int32_t)t.w.w[e];
+// id e's place in a segment that starts at token `first`; not below its length (which
+// is at most 2^30) where the id lies elsewhere
+__device__ __forceinline__ uint32_t token_off(const u32x4& w, int e, int tokens64, int first) {
+  const uint32_t low32 = w[e], low64 = w[2 * (e & 1)], high64 = w[2 * (e & 1) + 1];
+  return tokens64 == 0 ? low32 - (uint32_t)first : e < 2 && high64 == 0 ? low64 - (uint32_t)first : ~0u;
 }
 
 __device__ __forceinline__ int64_t token_at(const void* list, int64_t i, int tokens64) {
@@ -119,8 +121,9 @@ __global__ __launch_bounds__(512) void adjust_kernel(AdjustArgs g) {
   }
 
   // what the first steps of both loops need is in flight before either begins
-  constexpr int H = 4;  // history loads of a thread in flight, four ids each
-  Tokens4 ids[TABLE != 0 ? H : 1];
+  constexpr int H = 2;  // history loads of a thread in flight
+  const int per = g.tokens64 != 0 ? 2 : 4;  // ids of a load
+  u32x4 ids[TABLE != 0 ? H : 1];
   int held = 0, prompt = 0;
   Penalties pen = {1.0f, 0.0f, 0.0f};
   const int64_t bias_row = r * g.biases;
@@ -133,7 +136,8 @@ __global__ __launch_bounds__(512) void adjust_kernel(AdjustArgs g) {
     if (g.history != nullptr) {
 #pragma unroll
       for (int u = 0; u < H; ++u)
-        load_tokens4(g.history, r * g.ldh, (u * threads + tid) * 4, g.history_len, g.tokens64, ids[u]);
+        if (u * threads * per < g.history_len)
+          ids[u] = load_tokens(g.history, r * g.ldh, (u * threads + tid) * per, g.history_len, g.tokens64);
       held = g.lengths != nullptr ? max(0, min(g.lengths[r], g.history_len)) : g.history_len;
       prompt = g.prompt_lengths != nullptr ? max(0, min(g.prompt_lengths[r], held)) : 0;
       if (g.repetition != nullptr) pen.theta = g.repetition[r];
@@ -150,35 +154,48 @@ __global__ __launch_bounds__(512) void adjust_kernel(AdjustArgs g) {
     if (mask == nullptr) return kAll;
     return VE == 8 ? mask[v] : (uint32_t)mask[v >> 1] >> (4 * (v & 1)) & kAll;
   };
+  // A step is U vectors of each thread.  The last one has fewer and skips those that
+  // no thread has; the others run straight through (with a branch at each vector 512
+  // rows of 100003 took 92.8 us for 85.3).
   Raw<XK, VE> raw[U];
   uint32_t bits[U];
-  auto load_step = [&](int v0) {
+  auto whole = [&](int v0) { return v0 - tid + U * threads <= vectors; };
+  auto load_step = [&](auto full, int v0) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
+      if (!full.value && v0 - tid + u * threads >= vectors) break;
       const int v = min(v0 + u * threads, vectors - 1);
       bits[u] = mask_bits(v);
       if (!IN_PLACE) raw[u] = load_raw<XK, VE>(x_row, (int64_t)v * VE);
     }
   };
-  if (vectors > 0) load_step(tid);
+  auto load_vectors = [&](int v0) {
+    if (whole(v0)) {
+      load_step(std::true_type{}, v0);
+    } else {
+      load_step(std::false_type{}, v0);
+    }
+  };
+  if (vectors > 0) load_vectors(tid);
 
   if constexpr (TABLE != 0) {
     for (int i = tid; i < g.seg_len * CW / 32; i += threads) table_s[i] = 0;
     if (tid == 0) biased_s = twice_s = 0;
     lds_barrier();
-    for (int i0 = 0; i0 < held; i0 += H * threads * 4) {
+    for (int i0 = 0; i0 < held; i0 += H * threads * per) {
       if (i0 > 0) {
 #pragma unroll
         for (int u = 0; u < H; ++u)
-          load_tokens4(g.history, r * g.ldh, i0 + (u * threads + tid) * 4, held, g.tokens64, ids[u]);
+          ids[u] = load_tokens(g.history, r * g.ldh, i0 + (u * threads + tid) * per, held, g.tokens64);
       }
 #pragma unroll
       for (int u = 0; u < H; ++u) {
-        const int i = i0 + (u * threads + tid) * 4;
+        if (i0 + u * threads * per >= held) break;
+        const int i = i0 + (u * threads + tid) * per;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int64_t off = token_of(ids[u], e, g.tokens64) - first;
-          if (i + e < held && off >= 0 && off < len) {
+          const uint32_t off = token_off(ids[u], e, g.tokens64, first);
+          if (i + e < held && off < (uint32_t)len) {  // (a 64-bit load's ids 2 and 3 lie nowhere)
             const At at((int)off);
             if (i + e < prompt) {
               atomicOr(&table_s[at.word], kInPrompt << at.shift);
@@ -211,21 +228,22 @@ __global__ __launch_bounds__(512) void adjust_kernel(AdjustArgs g) {
     return some != 0;
   };
   auto adjusted = [&](float x, uint32_t entry) { return (entry & kBiased) != 0 ? x : penalised(x, entry, pen); };
-  for (int v0 = tid; v0 < vectors; v0 += U * threads) {
-    if (v0 != tid) load_step(v0);
+  auto stream_step = [&](auto full, int v0) {
     uint32_t e[U][VE];
     bool some[U];  // whether a vector has entries
 #pragma unroll
     for (int u = 0; u < U; ++u) {
+      if (!full.value && v0 - tid + u * threads >= vectors) break;
       const int v = v0 + u * threads;
       some[u] = TABLE != 0 && entries(min(v, vectors - 1), e[u]);
       if (IN_PLACE) {
         if (v >= vectors) some[u] = false, bits[u] = kAll;
-        if (bits[u] != 0 && (bits[u] != kAll || some[u])) raw[u] = load_raw<XK, VE>(x_row, (int64_t)v * VE);
+        if (bits[u] != 0 && some[u]) raw[u] = load_raw<XK, VE>(x_row, (int64_t)v * VE);
       }
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
+      if (!full.value && v0 - tid + u * threads >= vectors) break;
       const int v = v0 + u * threads;
       float x[VE];
       unpack_raw<XK, VE>(raw[u], x);
@@ -235,7 +253,23 @@ __global__ __launch_bounds__(512) void adjust_kernel(AdjustArgs g) {
       }
 #pragma unroll
       for (int i = 0; i < VE; ++i) x[i] = (bits[u] >> i & 1) != 0 ? x[i] : -INFINITY;
-      if (IN_PLACE ? bits[u] != kAll || some[u] : v < vectors) store_vec<OK, VE>(o_row, (int64_t)v * VE, x);
+      if (IN_PLACE ? bits[u] == 0 : full.value || v < vectors) {
+        store_vec<OK, VE>(o_row, (int64_t)v * VE, x);
+      } else if (IN_PLACE && (bits[u] != kAll || some[u])) {
+        // one by one: without reading what stays (256 masks of 50021 in f16 took 10.5 us
+        // with whole vectors read and written again, 9.0 so; 512 of 50000 in fp32 47 and 35)
+#pragma unroll
+        for (int i = 0; i < VE; ++i)
+          if ((bits[u] >> i & 1) == 0 || (TABLE != 0 && e[u][i] != 0)) store_out<OK>(o_row, (int64_t)v * VE + i, x[i]);
+      }
+    }
+  };
+  for (int v0 = tid; v0 - tid < vectors; v0 += U * threads) {
+    if (v0 != tid) load_vectors(v0);
+    if (whole(v0)) {
+      stream_step(std::true_type{}, v0);
+    } else {
+      stream_step(std::false_type{}, v0);
     }
   }
   for (int j = vectors * VE + tid; j < len; j += threads) {
@@ -277,11 +311,21 @@ template <int XK, int OK, bool IN_PLACE>
 hipError_t launch_kinds(AdjustArgs a, hipStream_t stream) {
   const bool rules = a.history != nullptr || a.biases > 0;
   const int bits = a.history_len < 1 << 14 ? 16 : 32;
-  // segments: as many as give eight workgroups per CU, of at least 2048 tokens
-  int64_t want = (2048 + a.m - 1) / a.m;
+  // Segments: as many as give four workgroups per CU, of at least 1024 tokens, and at
+  // most as long as the table stays small beside the workgroups that share a CU's LDS
+  // (without one, short segments).  Measured (us):
+  //   four / eight workgroups per CU  16 x 131071 bf16, 4096 ids  8.8 / 12.1, 64 x 32000 6.6 / 8.6
+  //   at least 1024 / 2048 / 4096     1 x 32000 fp32  3.9 / 4.5 / 5.6
+  //   at most 8192 / 16384 / 32768    512 x 100003 fp32, 1024 ids  84.6 / 85.3 / 107,
+  //                                   256 x 100003 bf16, 8192 ids  53.0 / 48.0 / 52.5
+  //   masks alone, at most 2048 / 4096 / 8192 / 16384   512 x 50000 fp32 in place
+  //                                   27.7 / 26.1 / 27.2 / 34.4, bf16 to fp32 35.9 / 35.0 / 35.0 / 40.7
+  // and 512 threads for segments past 4096 (512 x 100003: 85.3, with 256 92.9).
+  int64_t want = (1024 + a.m - 1) / a.m;
   int64_t seg = (a.vocab + want - 1) / want;
-  if (seg < 2048) seg = 2048;
-  if (seg > kSegmentMax) seg = kSegmentMax;
+  if (seg < 1024) seg = 1024;
+  const int64_t longest = rules ? kSegmentMax : kMaskSegmentMax;
+  if (seg > longest) seg = longest;
   if (seg > a.vocab) seg = a.vocab;
   a.seg_len = (int32_t)((seg + 31) / 32 * 32);
   a.segments = (a.vocab + a.seg_len - 1) / a.seg_len;
