@@ -31,7 +31,7 @@ extern "C" {
 /* For each row x of m rows of d values, with the residual r (or 0 without one):
  *   h            = x + r                                    in fp32
  *   residual_out = h, rounded to the residual's type
- *   y            = h / sqrt(mean(h^2) + eps) * weight       in fp32
+ *   y            = h * weight / sqrt(mean(h^2) + eps)       in fp32
  *   out          = y, rounded to its type (nearest even)
  *   scales_g     = max(max |y_j| over group g / 448, 2^-126)
  *   q_j          = y_j / scales_g, rounded to 8 bits (e4m3, nearest even): q_j *

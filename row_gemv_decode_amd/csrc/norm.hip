@@ -2,7 +2,7 @@
 // or 32-bit output and / or one in 8 bits (e4m3) with scales, for gfx950
 // (MI355X).
 //
-//   h = x + r,  y = h / sqrt(mean(h^2) + eps) * w,  s_g = max|y| / 448,  q = e4m3(y / s_g)
+//   h = x + r,  y = h w / sqrt(mean(h^2) + eps),  s_g = max|y| / 448,  q = e4m3(y / s_g)
 //
 // One pass over the data: a row's h stays in registers between the sum of its
 // squares and its outputs, and every load of a row (the weight's too) is issued
@@ -11,7 +11,10 @@
 //
 // A lane holds CH chunks of eight consecutive values.  A row of up to 1024
 // values belongs to 8 to 64 lanes of one wave, so that no barrier is needed and
-// short rows fill a wave together; a longer one to a workgroup of its own.
+// short rows fill a wave together; a longer one to a workgroup of its own.  The
+// largest |h w| of a row or group is found beside the sum of squares: rounding keeps
+// order, so its product with 1 / sqrt(..) is the largest |y| exactly, and a row's
+// waves meet once.
 // Rows past 32768 values do not stay in registers and are read two or three
 // times (norm_long_kernel).
 //
@@ -51,17 +54,21 @@ __device__ __forceinline__ float lanes_reduce(float v, int lanes) {
   return v;
 }
 
-// the same over the waves of a workgroup, in the order of the waves
-template <bool MAX>
-__device__ __forceinline__ float block_reduce(float v, float* parts, int waves) {
-  v = lanes_reduce<MAX>(v, 64);
-  if (waves > 1) {
-    if ((threadIdx.x & 63) == 0) parts[threadIdx.x >> 6] = v;
-    __syncthreads();
-    v = parts[0];
-    for (int i = 1; i < waves; ++i) v = MAX ? fmaxf(v, parts[i]) : v + parts[i];
+// a row's sum and largest value over the waves of a workgroup, in the order of the waves
+__device__ __forceinline__ void block_reduce(float& sum, float& top, bool both, float (&parts)[2][16], int waves) {
+  sum = lanes_reduce<false>(sum, 64);
+  if (both) top = lanes_reduce<true>(top, 64);
+  if (waves == 1) return;
+  if ((threadIdx.x & 63) == 0) {
+    parts[0][threadIdx.x >> 6] = sum;
+    parts[1][threadIdx.x >> 6] = top;
   }
-  return v;
+  __syncthreads();
+  sum = parts[0][0], top = parts[1][0];
+  for (int i = 1; i < waves; ++i) {
+    sum += parts[0][i];
+    top = fmaxf(top, parts[1][i]);
+  }
 }
 
 // values e0 .. e0 + 7 of a row, 0 from d on.  In a vector where all lie in the
@@ -88,7 +95,7 @@ __device__ __forceinline__ void load8(const void* row, int e0, int d, float (&x)
 template <int K>
 __device__ __forceinline__ void store8(void* row, int e0, int d, const float (&x)[8]) {
   if (e0 + 8 <= d) {
-    store_vec<K, 8>(row, e0, x);
+    store_vec<K, 8, true>(row, e0, x);
   } else if (d % 8 != 0) {
 #pragma unroll
     for (int e = 0; e < 7; ++e)
@@ -138,7 +145,7 @@ __device__ __forceinline__ void store8_q(uint8_t* row, int e0, int d, const floa
     w[q] = (uint32_t)v;
   }
   if (e0 + 8 <= d) {
-    *(u32x2_align1*)(row + e0) = u32x2{w[0], w[1]};
+    put_vec<true>(u32x2{w[0], w[1]}, (u32x2_align1*)(row + e0));
   } else if (d % 8 != 0) {
 #pragma unroll
     for (int e = 0; e < 7; ++e)
@@ -194,15 +201,26 @@ __global__ __launch_bounds__(BLOCK ? 1024 : 256) void norm_kernel(NormArgs g) {
 #pragma unroll
   for (int c = 0; c < CH; ++c) load_weight8(g, (c * step + place) * 8, w[c]);
 
-  float sum = 0.0f;
+  // w becomes h w
+  float sum = 0.0f, top[CH];
 #pragma unroll
-  for (int c = 0; c < CH; ++c)
+  for (int c = 0; c < CH; ++c) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sum = __builtin_fmaf(h[c][e], h[c][e], sum);
+    for (int e = 0; e < 8; ++e) {
+      sum = __builtin_fmaf(h[c][e], h[c][e], sum);
+      w[c][e] *= h[c][e];
+    }
+    top[c] = max8(w[c]);
+  }
+  const bool row_scale = p.q != nullptr && g.group == 0;
+  float row_top = top[0];
+#pragma unroll
+  for (int c = 1; c < CH; ++c) row_top = fmaxf(row_top, top[c]);
   if constexpr (BLOCK) {
-    sum = block_reduce<false>(sum, parts_s[0], waves);
+    block_reduce(sum, row_top, row_scale, parts_s, waves);
   } else {
     sum = lanes_reduce<false>(sum, lanes);
+    if (row_scale) row_top = lanes_reduce<true>(row_top, lanes);
   }
   const float inv = 1.0f / sqrtf(sum / (float)d + g.eps);
 
@@ -216,25 +234,14 @@ __global__ __launch_bounds__(BLOCK ? 1024 : 256) void norm_kernel(NormArgs g) {
 #pragma unroll
   for (int c = 0; c < CH; ++c)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) h[c][e] = h[c][e] * inv * w[c][e];
+    for (int e = 0; e < 8; ++e) h[c][e] = w[c][e] * inv;
   if (active && p.out != nullptr) {
 #pragma unroll
     for (int c = 0; c < CH; ++c) store8_kind(p.out, g.out_kind, (c * step + place) * 8, d, h[c]);
   }
   if (p.q == nullptr) return;
-
-  float top[CH];
-#pragma unroll
-  for (int c = 0; c < CH; ++c) top[c] = max8(h[c]);
-  if (g.group == 0) {
-#pragma unroll
-    for (int c = 1; c < CH; ++c) top[0] = fmaxf(top[0], top[c]);
-    if constexpr (BLOCK) {
-      top[0] = block_reduce<true>(top[0], parts_s[1], waves);
-    } else {
-      top[0] = lanes_reduce<true>(top[0], lanes);
-    }
-    const float s = scale_of(top[0]), si = 1.0f / s;
+  if (row_scale) {
+    const float s = scale_of(row_top * inv), si = 1.0f / s;
     if (active) {
 #pragma unroll
       for (int c = 0; c < CH; ++c) store8_q(p.q, (c * step + place) * 8, d, h[c], si);
@@ -246,7 +253,7 @@ __global__ __launch_bounds__(BLOCK ? 1024 : 256) void norm_kernel(NormArgs g) {
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const int e0 = (c * step + place) * 8;
-      const float s = scale_of(lanes_reduce<true>(top[c], mine));
+      const float s = scale_of(lanes_reduce<true>(top[c], mine) * inv);
       if (active) {
         store8_q(p.q, e0, d, h[c], 1.0f / s);
         if ((place & (mine - 1)) == 0 && e0 < d) p.scales[e0 / g.group] = s;
@@ -256,14 +263,14 @@ __global__ __launch_bounds__(BLOCK ? 1024 : 256) void norm_kernel(NormArgs g) {
 }
 
 // Rows that do not fit the registers: one workgroup of 1024 per row, which reads
-// the row for the sum, once more for a scale of the whole row, and for the outputs.
+// the row twice.
 template <int XK, int RK>
 __global__ __launch_bounds__(1024) void norm_long_kernel(NormArgs g) {
   __shared__ float parts_s[2][16];
   constexpr int kStep = 8 * 1024;
   const int d = g.d;
   const RowPtrs p = row_ptrs<XK, RK>(g, blockIdx.x);
-  auto sum_at = [&](int e0, float(&h)[8]) {
+  auto load_both = [&](int e0, float(&h)[8], float(&hw)[8]) {
     load8<XK>(p.x, e0, d, h);
     if constexpr (RK != kNone) {
       float res[8];
@@ -271,53 +278,44 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(NormArgs g) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) h[e] += res[e];
     }
-  };
-  auto norm_at = [&](int e0, float inv, float(&h)[8]) {
-    float w[8];
-    load_weight8(g, e0, w);
+    load_weight8(g, e0, hw);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) h[e] = h[e] * inv * w[e];
+    for (int e = 0; e < 8; ++e) hw[e] *= h[e];
   };
   const int first = (int)threadIdx.x * 8;
-  float sum = 0.0f;
+  const bool row_scale = p.q != nullptr && g.group == 0;
+  float sum = 0.0f, top = 0.0f;
   for (int e0 = first; e0 < d; e0 += kStep) {
-    float h[8];
-    sum_at(e0, h);
+    float h[8], hw[8];
+    load_both(e0, h, hw);
     float s = 0.0f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) s = __builtin_fmaf(h[e], h[e], s);
     sum += s;
+    top = fmaxf(top, max8(hw));
   }
-  sum = block_reduce<false>(sum, parts_s[0], 16);
+  block_reduce(sum, top, row_scale, parts_s, 16);
   const float inv = 1.0f / sqrtf(sum / (float)d + g.eps);
-  float s = 0.0f;
-  if (p.q != nullptr && g.group == 0) {
-    float top = 0.0f;
-    for (int e0 = first; e0 < d; e0 += kStep) {
-      float h[8];
-      sum_at(e0, h);
-      norm_at(e0, inv, h);
-      top = fmaxf(top, max8(h));
-    }
-    s = scale_of(block_reduce<true>(top, parts_s[1], 16));
-    if (threadIdx.x == 0) p.scales[0] = s;
-  }
+  float s = scale_of(top * inv);
+  if (row_scale && threadIdx.x == 0) p.scales[0] = s;
   // (all lanes of a wave, so that groups are whole; a value is read and written
   // by one thread, so rows may be written in place)
   for (int e0 = first; e0 - first < d; e0 += kStep) {
-    float h[8];
-    sum_at(e0, h);
+    float h[8], y[8];
+    load_both(e0, h, y);
     if constexpr (RK != kNone) {
       if (p.ro != nullptr) store8<RK>(p.ro, e0, d, h);
     }
-    norm_at(e0, inv, h);
-    if (p.out != nullptr) store8_kind(p.out, g.out_kind, e0, d, h);
+    const float group_top = max8(y);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] *= inv;
+    if (p.out != nullptr) store8_kind(p.out, g.out_kind, e0, d, y);
     if (p.q != nullptr) {
       if (g.group != 0) {
-        s = scale_of(lanes_reduce<true>(max8(h), g.group >> 3));
+        s = scale_of(lanes_reduce<true>(group_top, g.group >> 3) * inv);
         if ((e0 & (g.group - 1)) == 0 && e0 < d) p.scales[e0 / g.group] = s;
       }
-      store8_q(p.q, e0, d, h, 1.0f / s);
+      store8_q(p.q, e0, d, y, 1.0f / s);
     }
   }
 }
@@ -335,7 +333,10 @@ hipError_t launch_kinds(NormArgs a, hipStream_t stream) {
     rows = 256 >> a.lanes_log2;
     fn = chunks > 64 ? norm_kernel<XK, RK, 2, false> : norm_kernel<XK, RK, 1, false>;
   } else if (chunks <= 4 * 1024) {
-    const int ch = chunks <= 1024 ? 1 : chunks <= 2 * 1024 ? 2 : 4;
+    // one chunk per lane; two for many long rows, which makes more rows share a CU:
+    // 16384 x 5120 to 8 bits 123 -> 113 us, 8192 x 5120 64.7 -> 62.8, but 1 x 5120
+    // 2.9 -> 3.3, 256 x 5120 3.6 -> 3.8 and 4096 x 2560 fp32 36.2 -> 39.5
+    const int ch = chunks > 2 * 1024 ? 4 : chunks > 1024 || (chunks > 512 && a.m >= 512) ? 2 : 1;
     threads = ((chunks + ch - 1) / ch + 63) / 64 * 64;
     fn = ch == 1 ? norm_kernel<XK, RK, 1, true> : ch == 2 ? norm_kernel<XK, RK, 2, true> : norm_kernel<XK, RK, 4, true>;
   } else {
