@@ -34,7 +34,7 @@ struct AdaptSizes {
 };
 AdaptSizes adapt_sizes(const skinny_adapters& a, int64_t m) {
   AdaptSizes s;
-  s.splits = adapt_splits(m, a.k, a.rank, &s.split_len);
+  s.splits = adapt_splits(m, a.k, a.rank, a.count, &s.split_len);
   s.max_tiles = adapt_max_tiles(m, a.count);
   s.tiles = round16((int64_t)s.splits * m * a.rank * 4) + 16;  // (the tile count is before them)
   s.order = s.tiles + s.max_tiles * 16;

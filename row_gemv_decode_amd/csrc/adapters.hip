@@ -442,11 +442,10 @@ __device__ __forceinline__ void finish_frags(int rank, int step, int lane, u32x4
 
 // A workgroup: the rows of a tile, col_blocks times kBlockCols columns, 64 of them
 // per wave.  HELD: steps of 32 ranks whose fragments of B stay in registers over the
-// tile's rows (0: they are read for every 16 rows).  The matrix core's sums are read
+// tile's rows (0: the steps follow one another, with running totals of all rows).  The matrix core's sums are read
 // in the straight line of code that forms them (the hardware does not hold back a
 // read that comes too early, and the compiler has missed some behind branches): all
-// HELD steps are multiplied, with zeros past the adapter's rank, and the others one
-// by one into running totals.
+// HELD steps are multiplied, with zeros past the adapter's rank.
 template <int TK, int TR, int BK, int HELD>
 __global__ __launch_bounds__(kThreads) void adapter_up_kernel(AdaptArgs g, int col_blocks) {
   extern __shared__ uint16_t planes_s[];  // [planes][16 TR][pitch]
@@ -531,8 +530,53 @@ __global__ __launch_bounds__(kThreads) void adapter_up_kernel(AdaptArgs g, int c
       for (int b = 0; b < HELD; ++b)
         if (b < steps) load_frags<TK>(g, wb, rank, b, col + kBlockCols, lane, next_w[b]);
     }
+    auto multiply = [&](int t, int b, const WeightFrags<TK>& f, f32x4(&acc)[kColTiles]) __attribute__((always_inline)) {
+      u32x4 v[kPlanes];
 #pragma unroll
-    for (int b = 0; b < HELD; ++b) finish_frags<TK>(rank, b, lane, slots_s[wave], w[b]);
+      for (int p = 0; p < kPlanes; ++p)
+        v[p] = *(const u32x4*)&planes_s[((p * TR + t) * 16 + low) * pitch + b * 32 + 8 * h];
+#pragma unroll
+      for (int p = kPlanes - 1; p >= 0; --p) {
+        if constexpr (TK == CK_F16) {
+          if (p < kPlanes - 1) {
+#pragma unroll
+            for (int s = 0; s < kColTiles; ++s) acc[s] = mfma16<CK_BF16>(v[p], f.lo[s], acc[s]);
+          }
+        }
+#pragma unroll
+        for (int s = 0; s < kColTiles; ++s) acc[s] = mfma16<CK_BF16>(v[p], f.hi[s], acc[s]);
+      }
+    };
+    float total[HELD > 0 ? 1 : TR][kColTiles][4];
+    if constexpr (HELD > 0) {
+#pragma unroll
+      for (int b = 0; b < HELD; ++b) finish_frags<TK>(rank, b, lane, slots_s[wave], w[b]);
+    } else {
+#pragma unroll
+      for (int t = 0; t < TR; ++t)
+#pragma unroll
+        for (int s = 0; s < kColTiles; ++s)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) total[t][s][q] = 0.0f;
+      if (steps > 0) load_frags<TK>(g, wb, rank, 0, col, lane, w[0]);
+      for (int b = 0; b < steps; ++b) {
+        if (b + 1 < steps) load_frags<TK>(g, wb, rank, b + 1, col, lane, next_w[0]);
+        finish_frags<TK>(rank, b, lane, slots_s[wave], w[0]);
+#pragma unroll
+        for (int t = 0; t < TR; ++t) {
+          f32x4 acc[kColTiles];
+#pragma unroll
+          for (int s = 0; s < kColTiles; ++s) acc[s] = f32x4{0, 0, 0, 0};
+          multiply(t, b, w[0], acc);
+#pragma unroll
+          for (int s = 0; s < kColTiles; ++s)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) total[t][s][q] = __builtin_fmaf(scale, acc[s][q], total[t][s][q]);
+        }
+#pragma unroll
+        for (int s = 0; s < kColTiles; ++s) w[0].hi[s] = next_w[0].hi[s];
+      }
+    }
     auto sixteen_rows = [&](int t) __attribute__((always_inline)) {
       // the next rows' base, or that of the next columns' first rows
       BaseVec next[4];
@@ -542,29 +586,12 @@ __global__ __launch_bounds__(kThreads) void adapter_up_kernel(AdaptArgs g, int c
         load_base(0, c0 + kBlockCols, next);
       }
       float sum[kColTiles][4];
-      auto multiply = [&](int b, const WeightFrags<TK>& f, f32x4(&acc)[kColTiles]) {
-        u32x4 v[kPlanes];
-#pragma unroll
-        for (int p = 0; p < kPlanes; ++p)
-          v[p] = *(const u32x4*)&planes_s[((p * TR + t) * 16 + low) * pitch + b * 32 + 8 * h];
-#pragma unroll
-        for (int p = kPlanes - 1; p >= 0; --p) {
-          if constexpr (TK == CK_F16) {
-            if (p < kPlanes - 1) {
-#pragma unroll
-              for (int s = 0; s < kColTiles; ++s) acc[s] = mfma16<CK_BF16>(v[p], f.lo[s], acc[s]);
-            }
-          }
-#pragma unroll
-          for (int s = 0; s < kColTiles; ++s) acc[s] = mfma16<CK_BF16>(v[p], f.hi[s], acc[s]);
-        }
-      };
       if constexpr (HELD > 0) {
         f32x4 acc[kColTiles];
 #pragma unroll
         for (int s = 0; s < kColTiles; ++s) acc[s] = f32x4{0, 0, 0, 0};
 #pragma unroll
-        for (int b = 0; b < HELD; ++b) multiply(b, w[b], acc);
+        for (int b = 0; b < HELD; ++b) multiply(t, b, w[b], acc);
 #pragma unroll
         for (int s = 0; s < kColTiles; ++s)
 #pragma unroll
@@ -573,19 +600,7 @@ __global__ __launch_bounds__(kThreads) void adapter_up_kernel(AdaptArgs g, int c
 #pragma unroll
         for (int s = 0; s < kColTiles; ++s)
 #pragma unroll
-          for (int q = 0; q < 4; ++q) sum[s][q] = 0.0f;
-        for (int b = 0; b < steps; ++b) {
-          load_frags<TK>(g, wb, rank, b, col, lane, w[0]);
-          finish_frags<TK>(rank, b, lane, slots_s[wave], w[0]);
-          f32x4 acc[kColTiles];
-#pragma unroll
-          for (int s = 0; s < kColTiles; ++s) acc[s] = f32x4{0, 0, 0, 0};
-          multiply(b, w[0], acc);
-#pragma unroll
-          for (int s = 0; s < kColTiles; ++s)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) sum[s][q] = __builtin_fmaf(scale, acc[s][q], sum[s][q]);
-        }
+          for (int q = 0; q < 4; ++q) sum[s][q] = total[t][s][q];
       }
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
@@ -611,9 +626,9 @@ __global__ __launch_bounds__(kThreads) void adapter_up_kernel(AdaptArgs g, int c
         const int64_t at = row * g.ldo + c0;
         if (whole) {
           if (g.out_kind == CK_F32) {
-            store_vec<CK_F32, kColTiles>(g.out, at, v);
+            store_vec<CK_F32, kColTiles, true>(g.out, at, v);
           } else {
-            store_vec<TK, kColTiles>(g.out, at, v);
+            store_vec<TK, kColTiles, true>(g.out, at, v);
           }
         } else {
 #pragma unroll
@@ -634,6 +649,10 @@ __global__ __launch_bounds__(kThreads) void adapter_up_kernel(AdaptArgs g, int c
     };
     if constexpr (TR == 1) {
       sixteen_rows(0);
+    } else if constexpr (HELD == 0) {
+#pragma unroll
+      for (int t = 0; t < TR; ++t)
+        if (t * 16 < tile.rows) sixteen_rows(t);
     } else {
 #pragma unroll 1
       for (int t = 0; t * 16 < tile.rows; ++t) sixteen_rows(t);
@@ -665,9 +684,11 @@ hipError_t launch_tiles(const AdaptArgs& a, hipStream_t stream) {
   hipLaunchKernelGGL(down, dim3(blocks, tiles), dim3(kThreads), lds, stream, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  // columns of a workgroup: as many as leave about four workgroups for each CU
+  // Columns of a workgroup: 256 times what leaves about four workgroups for each CU.
+  // 4096 rows x 7680 (2190 pieces of 256 columns) once / twice / three times 49.8 / 48.6 /
+  // 50.4 us, 2000 x 2560 (350 pieces) 22.2 / 25.7 / 30.5, 1 x 7680 8.1, four times 10.7.
   const int64_t all = (int64_t)tiles * ((a.n + kBlockCols - 1) / kBlockCols);
-  const int col_blocks = TR > 1 ? 2 : all >= 4096 ? 4 : all >= 1536 ? 2 : 1;
+  const int col_blocks = TR == 1 && all >= 4096 ? 4 : all >= 1536 ? 2 : 1;
   const unsigned cols = (unsigned)((a.n + kBlockCols * col_blocks - 1) / (kBlockCols * col_blocks));
   const size_t planes = (size_t)kPlanes * 16 * TR * ((a.rank + 31) / 32 * 32 + 8) * 2;
   const auto up = a.base == nullptr       ? up_kernel<TK, TR, kNoBase>((int)a.rank)
@@ -686,13 +707,16 @@ bool adapt_by_adapter(int64_t m, int64_t count) { return count + 1 + m / 16 < m;
 
 }  // namespace
 
-int adapt_splits(int64_t m, int64_t k, int64_t rank, int64_t* split_len) {
-  // 16 rows and fewer: a wave takes 64 elements of k (the same at every m, and so
-  // the same bits)
-  int64_t len = m <= kGemvMaxM ? 256 : m <= 64 ? 512 : 1024;
+// Splits of k over workgroups.  The up launch adds their parts again in each of its
+// workgroups, so splits are longer where the rank or the rows give workgroups enough.
+// For up to 16 rows they depend on k and the rank alone, as a row's bits do.
+int adapt_splits(int64_t m, int64_t k, int64_t rank, int64_t count, int64_t* split_len) {
+  int64_t len = m <= kGemvMaxM ? (rank <= 16 ? 256 : rank <= 64 ? 512 : 1024) : m <= 64 && rank <= 64 ? 512 : 1024;
   if (m > kAdaptDirectRows) {
+    // about one workgroup per CU, if one in eight rows begins an adapter's at the most
     const int64_t nr = rank > 32 ? 4 : rank > 16 ? 2 : 1;
-    const int64_t groups = (m + kAdaptTileRows - 1) / kAdaptTileRows * ((rank + 16 * nr - 1) / (16 * nr));
+    const int64_t starts = count + 1 < m / 8 ? count + 1 : m / 8;
+    const int64_t groups = (m / kAdaptTileRows + starts) * ((rank + 16 * nr - 1) / (16 * nr));
     const int64_t want = (256 + groups - 1) / groups;
     len = (k + want - 1) / want;
     len = (len + 255) / 256 * 256;

@@ -72,7 +72,7 @@ struct AdaptArgs {
 // rows up to which every workgroup finds its adapter's rows by itself
 constexpr int kAdaptDirectRows = 256;
 constexpr int kAdaptTileRows = 64;  // rows of a tile in larger batches
-int adapt_splits(int64_t m, int64_t k, int64_t rank, int64_t* split_len);
+int adapt_splits(int64_t m, int64_t k, int64_t rank, int64_t count, int64_t* split_len);
 constexpr int64_t adapt_tile_rows(int64_t m) { return m <= kAdaptDirectRows ? 16 : kAdaptTileRows; }
 int64_t adapt_max_tiles(int64_t m, int64_t count);
 
