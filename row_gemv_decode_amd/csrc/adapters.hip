@@ -442,10 +442,11 @@ __device__ __forceinline__ void finish_frags(int rank, int step, int lane, u32x4
 
 // A workgroup: the rows of a tile, col_blocks times kBlockCols columns, 64 of them
 // per wave.  HELD: steps of 32 ranks whose fragments of B stay in registers over the
-// tile's rows (0: the steps follow one another, with running totals of all rows).  The matrix core's sums are read
-// in the straight line of code that forms them (the hardware does not hold back a
-// read that comes too early, and the compiler has missed some behind branches): all
-// HELD steps are multiplied, with zeros past the adapter's rank.
+// tile's rows (0: the steps follow one another, with running totals of all rows).
+// The matrix core's sums are read in the straight line of code that forms them (the
+// hardware does not hold back a read that comes too early, and the compiler has
+// missed some behind branches): all HELD steps are multiplied, with zeros past the
+// adapter's rank.
 template <int TK, int TR, int BK, int HELD>
 __global__ __launch_bounds__(kThreads) void adapter_up_kernel(AdaptArgs g, int col_blocks) {
   extern __shared__ uint16_t planes_s[];  // [planes][16 TR][pitch]
@@ -709,9 +710,12 @@ bool adapt_by_adapter(int64_t m, int64_t count) { return count + 1 + m / 16 < m;
 
 // Splits of k over workgroups.  The up launch adds their parts again in each of its
 // workgroups, so splits are longer where the rank or the rows give workgroups enough.
-// For up to 16 rows they depend on k and the rank alone, as a row's bits do.
+// For up to 16 rows they depend on k and the rank alone, as a row's bits do.  Measured
+// (us): 1 row, rank 16, k 2560 in splits of 256 / 512 / 1024 8.2 / 7.6 / 7.6, 16 rows, k 5120
+// 10.1 / 9.0 / 8.5; 8 rows, rank 32, k 8192 512 / 768 8.2 / 9.0; 16 rows, rank 256, k 5120
+// 512 / 1024 / 2048 22.2 / 18.9 / 21.9.
 int adapt_splits(int64_t m, int64_t k, int64_t rank, int64_t count, int64_t* split_len) {
-  int64_t len = m <= kGemvMaxM ? (rank <= 16 ? 256 : rank <= 64 ? 512 : 1024) : m <= 64 && rank <= 64 ? 512 : 1024;
+  int64_t len = m <= 64 && rank > 16 && rank <= 64 ? 512 : 1024;
   if (m > kAdaptDirectRows) {
     // about one workgroup per CU, if one in eight rows begins an adapter's at the most
     const int64_t nr = rank > 32 ? 4 : rank > 16 ? 2 : 1;

@@ -145,7 +145,7 @@ __device__ __forceinline__ void store8_q(uint8_t* row, int e0, int d, const floa
     w[q] = (uint32_t)v;
   }
   if (e0 + 8 <= d) {
-    put_vec<true>(u32x2{w[0], w[1]}, (u32x2_align1*)(row + e0));
+    put8<true>(u32x2{w[0], w[1]}, (char*)row + e0);
   } else if (d % 8 != 0) {
 #pragma unroll
     for (int e = 0; e < 7; ++e)

@@ -97,12 +97,20 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 // STREAM: past the caches' replacement order.  What a launch writes, the next one
 // mostly reads on another XCD, so nothing is gained by keeping it; rows that start in
 // the middle of a cache line gain most (2000 x 7681 norm 33.1 -> 24.1 us).
-template <bool STREAM, typename V, typename P>
-__device__ __forceinline__ void put_vec(V v, P* at) {
+template <bool STREAM>
+__device__ __forceinline__ void put8(u32x2 v, char* at) {
   if constexpr (STREAM) {
-    __builtin_nontemporal_store(v, at);
+    __builtin_nontemporal_store(v, (u32x2_align1*)at);
   } else {
-    *at = v;
+    *(u32x2_align1*)at = v;
+  }
+}
+template <bool STREAM>
+__device__ __forceinline__ void put16(u32x4 v, char* at) {
+  if constexpr (STREAM) {
+    __builtin_nontemporal_store(v, (u32x4_align2*)at);
+  } else {
+    *(u32x4_align2*)at = v;
   }
 }
 
@@ -112,17 +120,17 @@ __device__ __forceinline__ void store_vec(void* p, int64_t i, const float (&x)[N
   if constexpr (K == CK_F32) {
 #pragma unroll
     for (int q = 0; q < N / 4; ++q)
-      put_vec<STREAM>(u32x4{__builtin_bit_cast(uint32_t, x[4 * q]), __builtin_bit_cast(uint32_t, x[4 * q + 1]),
-                            __builtin_bit_cast(uint32_t, x[4 * q + 2]), __builtin_bit_cast(uint32_t, x[4 * q + 3])},
-                      (u32x4_align4*)(at + 16 * q));
+      put16<STREAM>(u32x4{__builtin_bit_cast(uint32_t, x[4 * q]), __builtin_bit_cast(uint32_t, x[4 * q + 1]),
+                          __builtin_bit_cast(uint32_t, x[4 * q + 2]), __builtin_bit_cast(uint32_t, x[4 * q + 3])},
+                    at + 16 * q);
   } else if constexpr (N == 4) {
-    put_vec<STREAM>(u32x2{pack2<K>(x[0], x[1]), pack2<K>(x[2], x[3])}, (u32x2_align2*)at);
+    put8<STREAM>(u32x2{pack2<K>(x[0], x[1]), pack2<K>(x[2], x[3])}, at);
   } else {
 #pragma unroll
     for (int q = 0; q < N / 8; ++q)
-      put_vec<STREAM>(u32x4{pack2<K>(x[8 * q], x[8 * q + 1]), pack2<K>(x[8 * q + 2], x[8 * q + 3]),
-                            pack2<K>(x[8 * q + 4], x[8 * q + 5]), pack2<K>(x[8 * q + 6], x[8 * q + 7])},
-                      (u32x4_align2*)(at + 16 * q));
+      put16<STREAM>(u32x4{pack2<K>(x[8 * q], x[8 * q + 1]), pack2<K>(x[8 * q + 2], x[8 * q + 3]),
+                          pack2<K>(x[8 * q + 4], x[8 * q + 5]), pack2<K>(x[8 * q + 6], x[8 * q + 7])},
+                    at + 16 * q);
   }
 }
 
