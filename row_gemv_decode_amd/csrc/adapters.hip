@@ -440,6 +440,103 @@ __device__ __forceinline__ void finish_frags(int rank, int step, int lane, u32x4
   }
 }
 
+// acc[s] += the inner values' planes times one step of column tile s; `planes` is the
+// lane's piece of its row's first plane.  The smallest products come first.
+template <int TK>
+__device__ __forceinline__ void multiply_step(const uint16_t* planes, int plane, const WeightFrags<TK>& f,
+                                              f32x4 (&acc)[kColTiles]) {
+  u32x4 v[kPlanes];
+#pragma unroll
+  for (int p = 0; p < kPlanes; ++p) v[p] = *(const u32x4*)(planes + p * plane);
+#pragma unroll
+  for (int p = kPlanes - 1; p >= 0; --p) {
+    if constexpr (TK == CK_F16) {
+      if (p < kPlanes - 1) {
+#pragma unroll
+        for (int s = 0; s < kColTiles; ++s) acc[s] = mfma16<CK_BF16>(v[p], f.lo[s], acc[s]);
+      }
+    }
+#pragma unroll
+    for (int s = 0; s < kColTiles; ++s) acc[s] = mfma16<CK_BF16>(v[p], f.hi[s], acc[s]);
+  }
+}
+
+// four inner values in their planes, at one place of each
+__device__ __forceinline__ void store_planes(uint16_t* at, int plane, const float (&v)[4]) {
+  uint16_t bits[kPlanes][4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    float rest = v[q];
+#pragma unroll
+    for (int p = 0; p < kPlanes; ++p) rest = bf16_plane(rest, bits[p][q]);
+  }
+#pragma unroll
+  for (int p = 0; p < kPlanes; ++p)
+    *(u32x2*)(at + p * plane) = u32x2{bits[p][0] | (uint32_t)bits[p][1] << 16, bits[p][2] | (uint32_t)bits[p][3] << 16};
+}
+
+// The base of rows 4 h .. 4 h + 3 of the 16 from rows_s on, at columns c0 .. c0 + 3.
+// Vectors that pass n are read at column 0 and not used, and so are rows past `rows`.
+template <int BK>
+using BaseVec = Raw<BK == kNoBase ? CK_F32 : BK, kColTiles>;
+template <int BK, typename R>
+__device__ __forceinline__ void load_base(const AdaptArgs& g, const R* rows_s, int rows, int h, int c0, BaseVec<BK> (&v)[4]) {
+  if constexpr (BK != kNoBase) {
+    if (g.n < kColTiles) return;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int64_t row = rows_s[4 * h + q < rows ? 4 * h + q : 0];
+      v[q] = load_raw<BK, kColTiles>(g.base, row * g.ldb + (c0 + kColTiles <= g.n ? c0 : 0));
+    }
+  }
+}
+
+// the lane's rows and columns of the output: the base plus sum[column][row]
+template <int TK, int BK, typename R>
+__device__ __forceinline__ void store_rows(const AdaptArgs& g, const R* rows_s, int rows, int h, int c0, bool add,
+                                           const BaseVec<BK> (&base)[4], const float (&sum)[kColTiles][4]) {
+  const bool whole = c0 + kColTiles <= g.n;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    if (4 * h + q >= rows) continue;
+    const int64_t row = rows_s[4 * h + q];
+    float v[kColTiles];
+#pragma unroll
+    for (int s = 0; s < kColTiles; ++s) v[s] = 0.0f;
+    if constexpr (BK != kNoBase) {
+      if (whole) {
+        unpack_raw<BK, kColTiles>(base[q], v);
+      } else {
+#pragma unroll
+        for (int s = 0; s < kColTiles; ++s)
+          if (c0 + s < g.n) v[s] = value_at<BK>(g.base, row * g.ldb + c0 + s);
+      }
+    }
+    if (add) {
+#pragma unroll
+      for (int s = 0; s < kColTiles; ++s) v[s] += sum[s][q];
+    }
+    const int64_t at = row * g.ldo + c0;
+    if (whole) {
+      if (g.out_kind == CK_F32) {
+        store_vec<CK_F32, kColTiles, true>(g.out, at, v);
+      } else {
+        store_vec<TK, kColTiles, true>(g.out, at, v);
+      }
+    } else {
+#pragma unroll
+      for (int s = 0; s < kColTiles; ++s)
+        if (c0 + s < g.n) {
+          if (g.out_kind == CK_F32) {
+            store_out<CK_F32>(g.out, at + s, v[s]);
+          } else {
+            store_out<TK>(g.out, at + s, v[s]);
+          }
+        }
+    }
+  }
+}
+
 // A workgroup: the rows of a tile, col_blocks times kBlockCols columns, 64 of them
 // per wave.  HELD: steps of 32 ranks whose fragments of B stay in registers over the
 // tile's rows (0: the steps follow one another, with running totals of all rows).
@@ -467,25 +564,12 @@ __global__ __launch_bounds__(kThreads) void adapter_up_kernel(AdaptArgs g, int c
   const uint16_t* wb = (const uint16_t*)g.B + (int64_t)max(tile.adapter, 0) * g.n * g.rank;
   __syncthreads();
 
-  // The base of rows 4 h .. 4 h + 3 of 16, at the lane's columns.  Vectors that
-  // pass n are read at column 0 and not used.
-  typedef Raw<BK == kNoBase ? CK_F32 : BK, kColTiles> BaseVec;
-  auto load_base = [&](int t, int c0, BaseVec(&v)[4]) {
-    if constexpr (BK != kNoBase) {
-      if (g.n < kColTiles) return;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int i = t * 16 + 4 * h + q;
-        v[q] = load_raw<BK, kColTiles>(g.base, (int64_t)rows_s[i < tile.rows ? i : 0] * g.ldb + (c0 + kColTiles <= g.n ? c0 : 0));
-      }
-    }
-  };
   const int wave_col = (int)blockIdx.x * col_blocks * kBlockCols + wave * kWaveCols;
   const int first = wave_col + low * kColTiles;
-  BaseVec base[4];
+  BaseVec<BK> base[4];
   WeightFrags<TK> w[HELD > 0 ? HELD : 1];
   // (in flight while the inner values are added up)
-  load_base(0, first, base);
+  load_base<BK>(g, rows_s, tile.rows, h, first, base);
 #pragma unroll
   for (int b = 0; b < HELD; ++b)
     if (b < steps) load_frags<TK>(g, wb, rank, b, wave_col, lane, w[b]);
@@ -507,24 +591,16 @@ __global__ __launch_bounds__(kThreads) void adapter_up_kernel(AdaptArgs g, int c
           if (s0 + s < g.splits) v += p[s];
       }
     }
-    uint16_t bits[kPlanes][4];
+    float kept[4];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      float rest = j + q < rank ? v[q] : 0.0f;
-#pragma unroll
-      for (int p = 0; p < kPlanes; ++p) rest = bf16_plane(rest, bits[p][q]);
-    }
-#pragma unroll
-    for (int p = 0; p < kPlanes; ++p)
-      *(u32x2*)&planes_s[(p * 16 * TR + row) * pitch + j] =
-          u32x2{bits[p][0] | (uint32_t)bits[p][1] << 16, bits[p][2] | (uint32_t)bits[p][3] << 16};
+    for (int q = 0; q < 4; ++q) kept[q] = j + q < rank ? v[q] : 0.0f;
+    store_planes(planes_s + row * pitch + j, 16 * TR * pitch, kept);
   }
   __syncthreads();
 
   for (int cb = 0; cb < col_blocks; ++cb) {
     const int col = wave_col + cb * kBlockCols, c0 = col + low * kColTiles;
     if (col >= g.n) break;
-    const bool whole = c0 + kColTiles <= g.n;
     WeightFrags<TK> next_w[HELD > 0 ? HELD : 1];  // the next columns'
     if (cb + 1 < col_blocks) {
 #pragma unroll
@@ -532,21 +608,7 @@ __global__ __launch_bounds__(kThreads) void adapter_up_kernel(AdaptArgs g, int c
         if (b < steps) load_frags<TK>(g, wb, rank, b, col + kBlockCols, lane, next_w[b]);
     }
     auto multiply = [&](int t, int b, const WeightFrags<TK>& f, f32x4(&acc)[kColTiles]) __attribute__((always_inline)) {
-      u32x4 v[kPlanes];
-#pragma unroll
-      for (int p = 0; p < kPlanes; ++p)
-        v[p] = *(const u32x4*)&planes_s[((p * TR + t) * 16 + low) * pitch + b * 32 + 8 * h];
-#pragma unroll
-      for (int p = kPlanes - 1; p >= 0; --p) {
-        if constexpr (TK == CK_F16) {
-          if (p < kPlanes - 1) {
-#pragma unroll
-            for (int s = 0; s < kColTiles; ++s) acc[s] = mfma16<CK_BF16>(v[p], f.lo[s], acc[s]);
-          }
-        }
-#pragma unroll
-        for (int s = 0; s < kColTiles; ++s) acc[s] = mfma16<CK_BF16>(v[p], f.hi[s], acc[s]);
-      }
+      multiply_step<TK>(planes_s + (t * 16 + low) * pitch + b * 32 + 8 * h, 16 * TR * pitch, f, acc);
     };
     float total[HELD > 0 ? 1 : TR][kColTiles][4];
     if constexpr (HELD > 0) {
@@ -580,11 +642,11 @@ __global__ __launch_bounds__(kThreads) void adapter_up_kernel(AdaptArgs g, int c
     }
     auto sixteen_rows = [&](int t) __attribute__((always_inline)) {
       // the next rows' base, or that of the next columns' first rows
-      BaseVec next[4];
+      BaseVec<BK> next[4];
       if (TR > 1 && (t + 1) * 16 < tile.rows) {
-        load_base(t + 1, c0, next);
+        load_base<BK>(g, rows_s + (t + 1) * 16, tile.rows - (t + 1) * 16, h, c0, next);
       } else if (cb + 1 < col_blocks) {
-        load_base(0, c0 + kBlockCols, next);
+        load_base<BK>(g, rows_s, tile.rows, h, c0 + kBlockCols, next);
       }
       float sum[kColTiles][4];
       if constexpr (HELD > 0) {
@@ -603,46 +665,7 @@ __global__ __launch_bounds__(kThreads) void adapter_up_kernel(AdaptArgs g, int c
 #pragma unroll
           for (int q = 0; q < 4; ++q) sum[s][q] = total[t][s][q];
       }
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int i = t * 16 + 4 * h + q;
-        if (i >= tile.rows) continue;
-        const int64_t row = rows_s[i];
-        float v[kColTiles];
-#pragma unroll
-        for (int s = 0; s < kColTiles; ++s) v[s] = 0.0f;
-        if constexpr (BK != kNoBase) {
-          if (whole) {
-            unpack_raw<BK, kColTiles>(base[q], v);
-          } else {
-#pragma unroll
-            for (int s = 0; s < kColTiles; ++s)
-              if (c0 + s < g.n) v[s] = value_at<BK>(g.base, row * g.ldb + c0 + s);
-          }
-        }
-        if (rank != 0) {
-#pragma unroll
-          for (int s = 0; s < kColTiles; ++s) v[s] += sum[s][q];
-        }
-        const int64_t at = row * g.ldo + c0;
-        if (whole) {
-          if (g.out_kind == CK_F32) {
-            store_vec<CK_F32, kColTiles, true>(g.out, at, v);
-          } else {
-            store_vec<TK, kColTiles, true>(g.out, at, v);
-          }
-        } else {
-#pragma unroll
-          for (int s = 0; s < kColTiles; ++s)
-            if (c0 + s < g.n) {
-              if (g.out_kind == CK_F32) {
-                store_out<CK_F32>(g.out, at + s, v[s]);
-              } else {
-                store_out<TK>(g.out, at + s, v[s]);
-              }
-            }
-        }
-      }
+      store_rows<TK, BK>(g, rows_s + t * 16, tile.rows - t * 16, h, c0, rank != 0, base, sum);
       if (TR > 1 || cb + 1 < col_blocks) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) base[q] = next[q];
@@ -665,6 +688,153 @@ __global__ __launch_bounds__(kThreads) void adapter_up_kernel(AdaptArgs g, int c
         for (int s = 0; s < kColTiles; ++s) w[b].hi[s] = next_w[b].hi[s];
     }
   }
+}
+
+// --- both in one launch --------------------------------------------------------
+// For a few rows and a small A: each workgroup of the up product computes its tile's
+// inner values by itself, which costs a read of the adapter's A from L2 and saves
+// the other launch and the way through memory.  The loads of all splits of k, of B
+// and of the base are in flight together.  Waves, splits and additions are those of
+// the two launches, and so are the bits, so the choice may depend on the rows.
+constexpr int kOneSplits = 4;
+constexpr int kOnePitch = 32 + 8;
+constexpr int64_t kOneReads = 10 << 20;  // elements of A
+
+template <int TK, int BK, int NR>
+__global__ __launch_bounds__(kThreads) void adapter_one_kernel(AdaptArgs g) {
+  constexpr int UN = NR == 1 ? 4 : 2;  // units of a wave in a split: 1024 or 512 elements
+  constexpr int kSlots = 2 * (1 + NR) > kColTiles ? 2 * (1 + NR) : kColTiles;
+  __shared__ u32x4 slots_s[kWaves][64 * kSlots];
+  __shared__ f32x4 sums_s[kOneSplits][kWaves][NR][64];
+  __shared__ uint16_t planes_s[kPlanes * 16 * kOnePitch] __attribute__((aligned(16)));
+  __shared__ int lists_s[16 * kWaves];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int low = lane & 15, h = lane >> 4;
+  int* rows_s = lists_s + 16 * wave;
+  Tile tile;
+  if (!find_tile<false>(g, blockIdx.y, rows_s, tile)) return;
+  const int rank = tile.rank;
+  if (rank == 0 && g.out == g.base) return;  // nothing to add
+  const int col = ((int)blockIdx.x * kWaves + wave) * kWaveCols, c0 = col + low * kColTiles;
+  BaseVec<BK> base[4];
+  WeightFrags<TK> f;
+
+  if (rank > 0) {
+    const int row4 = lane >> 2, piece = lane & 3;
+    const uint16_t* x = (const uint16_t*)g.x + rows_s[row4 < tile.rows ? row4 : 0] * g.ldx + 8 * piece;
+    const uint16_t* w[NR];
+#pragma unroll
+    for (int n = 0; n < NR; ++n) {
+      const int j = n * 16 + row4;
+      w[n] = (const uint16_t*)g.A + ((int64_t)tile.adapter * g.rank + (j < rank ? j : 0)) * g.k + 8 * piece;
+    }
+    const Turn turn(slots_s[wave], lane);
+    u32x4 xf[kOneSplits][UN][2], wf[kOneSplits][UN][2][NR];
+#pragma unroll
+    for (int p = 0; p < kOneSplits; ++p)
+#pragma unroll
+      for (int u = 0; u < UN; ++u) {
+        const int unit = p * g.split_len + (wave + u * kWaves) * 64;
+        if (unit >= g.k) break;
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          // past the row: any elements of it, which count as 0
+          const int at = unit + b * 32;
+          const int k0 = at + 8 * piece < g.k ? at : -8 * piece;
+          xf[p][u][b] = *(const u32x4*)(x + k0);
+#pragma unroll
+          for (int n = 0; n < NR; ++n) wf[p][u][b][n] = *(const u32x4*)(w[n] + k0);
+        }
+      }
+    load_base<BK>(g, rows_s, tile.rows, h, c0, base);
+    load_frags<TK>(g, (const uint16_t*)g.B + (int64_t)tile.adapter * g.n * g.rank, rank, 0, col, lane, f);
+#pragma unroll
+    for (int p = 0; p < kOneSplits; ++p) {
+      if (p >= g.splits) break;
+      f32x4 acc[NR];
+#pragma unroll
+      for (int n = 0; n < NR; ++n) acc[n] = f32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int u = 0; u < UN; ++u) {
+        const int unit = p * g.split_len + (wave + u * kWaves) * 64;
+        wave_lds_order();
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          const bool in = unit + b * 32 + 8 * piece < g.k;
+          turn.slots[b * (1 + NR) * 64 + turn.put] = in ? xf[p][u][b] : u32x4{0, 0, 0, 0};
+#pragma unroll
+          for (int n = 0; n < NR; ++n)
+            turn.slots[(b * (1 + NR) + 1 + n) * 64 + turn.put] = unit < g.k ? wf[p][u][b][n] : u32x4{0, 0, 0, 0};
+        }
+        wave_lds_order();
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          const u32x4 a = turn.slots[b * (1 + NR) * 64 + turn.get];
+#pragma unroll
+          for (int n = 0; n < NR; ++n) acc[n] = mfma16<TK>(turn.slots[(b * (1 + NR) + 1 + n) * 64 + turn.get], a, acc[n]);
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < NR; ++n) sums_s[p][wave][n][lane] = acc[n];
+    }
+  } else {
+    load_base<BK>(g, rows_s, tile.rows, h, c0, base);
+  }
+  __syncthreads();
+  // a wave for each 16 ranks of the step: the waves' parts of a split, then the splits
+  if (rank > 0 && wave < 2) {
+    f32x4 v = {0, 0, 0, 0};
+    if (wave < NR) {
+      for (int p = 0; p < g.splits; ++p) {
+        f32x4 s = sums_s[p][0][wave < NR ? wave : 0][lane];
+#pragma unroll
+        for (int i = 1; i < kWaves; ++i) s += sums_s[p][i][wave < NR ? wave : 0][lane];
+        v += s;
+      }
+    }
+    float kept[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) kept[q] = 16 * wave + 4 * h + q < rank ? v[q] : 0.0f;
+    store_planes(planes_s + low * kOnePitch + 16 * wave + 4 * h, 16 * kOnePitch, kept);
+  }
+  __syncthreads();
+  if (col >= g.n) return;
+  finish_frags<TK>(rank, 0, lane, slots_s[wave], f);
+  f32x4 acc[kColTiles];
+#pragma unroll
+  for (int s = 0; s < kColTiles; ++s) acc[s] = f32x4{0, 0, 0, 0};
+  multiply_step<TK>(planes_s + low * kOnePitch + 8 * h, 16 * kOnePitch, f, acc);
+  float sum[kColTiles][4];
+#pragma unroll
+  for (int s = 0; s < kColTiles; ++s)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) sum[s][q] = tile.scale * acc[s][q];
+  store_rows<TK, BK>(g, rows_s, tile.rows, h, c0, rank != 0, base, sum);
+}
+
+template <int TK, int NR>
+auto one_kernel(const AdaptArgs& a) {
+  return a.base == nullptr ? adapter_one_kernel<TK, kNoBase, NR>
+         : a.base_kind == CK_F32 ? adapter_one_kernel<TK, CK_F32, NR> : adapter_one_kernel<TK, TK, NR>;
+}
+// Whether the one launch takes a call: its splits are the two launches', and its
+// workgroups together read less than 20 MB of A.  Measured (us in a graph, and called
+// back to back, where the second launch costs the host 2.8 us; one launch / two):
+//   1 x 2560 x 7680, rank 16   7.0, 7.2 / 7.6, 8.9      8 x 2560 x 7680  7.4, 7.5 / 7.9, 9.4
+//   8 x 4096 x 4096, rank 16   8.6, 8.7 / 8.0, 9.4     16 x 4096 x 4096  9.2, 9.2 / 7.9, 9.4 (34 MB)
+//   16 x 2048 x 2048, rank 32  8.1, 8.2 / 8.0, 9.3      1 x 1024 x 1024, rank 8  4.6 / 6.9 in a graph
+bool takes_one(const AdaptArgs& a) {
+  const int64_t blocks = (int64_t)a.m * ((a.n + kBlockCols - 1) / kBlockCols);
+  return a.m <= kGemvMaxM && a.rank <= 32 && a.splits <= kOneSplits && a.split_len == (a.rank <= 16 ? 1024 : 512) &&
+         blocks * a.rank * a.k <= kOneReads;
+}
+
+template <int TK>
+hipError_t launch_one(const AdaptArgs& a, hipStream_t stream) {
+  const auto fn = a.rank <= 16 ? one_kernel<TK, 1>(a) : one_kernel<TK, 2>(a);
+  hipLaunchKernelGGL(fn, dim3((unsigned)((a.n + kBlockCols - 1) / kBlockCols), (unsigned)a.m), dim3(kThreads), 0, stream, a);
+  return hipGetLastError();
 }
 
 template <int TK, int TR, int BK>
@@ -741,6 +911,8 @@ hipError_t launch_adapters(const AdaptArgs& a, int kind, hipStream_t stream) {
       a.k % 8 != 0 || a.splits < 1 || (int64_t)a.splits * a.split_len < a.k || a.split_len % 256 != 0 ||
       a.max_tiles > 65535)
     return hipErrorInvalidValue;
+  if (takes_one(a))
+    return kind == CK_F16 ? launch_one<CK_F16>(a, stream) : launch_one<CK_BF16>(a, stream);
   if (a.m <= kAdaptDirectRows) {
     AdaptArgs d = a;
     d.by_adapter = adapt_by_adapter(a.m, a.count);

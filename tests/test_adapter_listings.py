@@ -47,4 +47,5 @@ def test_no_adapter_kernel_reads_the_matrix_core_early(tmp_path):
         body = body.split(".Lfunc_end")[0]
         with_mfma += "v_mfma" in body
         assert early_reads(one_file(body).splitlines()) == [], name
+        assert "scratch_" not in body, name  # (arrays that the compiler did not keep in registers)
     assert with_mfma >= 20

@@ -120,6 +120,22 @@ def test_adapters_many_and_large():
     Case(5000, 72, 80, 3, 16, "f16", "f16", ids=ids).check()
 
 
+@pytest.mark.parametrize("rank", [8, 16, 24, 32])
+@pytest.mark.parametrize("kind,base", [("bf16", "bf16"), ("f16", "f32"), ("bf16", None)])
+def test_adapters_bits_are_those_of_the_one_row_call(kind, base, rank):
+    """Across the sizes at which a window's rows are one launch's or two's, for k of a
+    part of a split, one, several, and an odd end."""
+    for k, n in ((72, 5003), (512, 40), (1096, 5003), (2040, 4100), (4096, 2570), (4104, 700)):
+        c = Case(16, k, n, 4, rank, kind, base, ids=[0, 1, -1, 3, 3, 2])
+        want = c.check()
+        for m in (1, 3, 6, 7, 9, 12, 13, 15):
+            got = sk.add_adapters(c.x[0][:m], c.pool, c.dev_ids[:m], None if base is None else c.base[0][:m])
+            assert torch.equal(got, want[:m])
+        for i in (2, 5, 15):
+            got = sk.add_adapters(c.x[0][i:i + 1], c.pool, c.dev_ids[i:i + 1], None if base is None else c.base[0][i:i + 1])
+            assert torch.equal(got[0], want[i])
+
+
 @pytest.mark.parametrize("kind", ["bf16", "f16"])
 def test_adapters_rows_do_not_depend_on_the_batch(kind):
     """Row i of up to 16 rows is the one-row call's, bit for bit, whichever adapters the
@@ -198,8 +214,8 @@ def test_adapters_large_offsets():
 def test_adapters_streams_graphs_and_threads():
     """Each stream has its own workspace and a capture one of its own; threads on one
     stream do not interleave their launches."""
-    for m in (9, 300):
-        c, d = Case(m, 512, 120, 4, 16, "bf16"), Case(m, 512, 120, 4, 16, "bf16", seed=50)
+    for m, rank in ((9, 16), (9, 40), (300, 16), (300, 256), (100, 128)):
+        c, d = Case(m, 512, 120, 4, rank, "bf16"), Case(m, 512, 120, 4, rank, "bf16", seed=50)
         want, other = c.run(), d.run()
         s = torch.cuda.Stream()
         s.wait_stream(torch.cuda.current_stream())
