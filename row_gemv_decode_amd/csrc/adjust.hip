@@ -22,7 +22,7 @@
 
 #include "requests.h"
 #include "vector_io.h"
-#include "wave_ops.h"
+#include "window_kernel.h"
 
 namespace skinny {
 

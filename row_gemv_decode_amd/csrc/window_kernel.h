@@ -156,6 +156,13 @@ struct Turn {
   }
 };
 
+// barrier of a workgroup that shares LDS only: loads from memory stay in flight
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
 // A weight matrix as a wave sees it: CT tiles of 16 consecutive columns, each
 // from a wave-uniform address, and one 32-bit offset per lane that serves all
 // tiles.  Weight loads are plain: two units share a cache line of every column,
