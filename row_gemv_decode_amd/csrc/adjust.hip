@@ -108,9 +108,12 @@ __global__ __launch_bounds__(512) void adjust_kernel(AdjustArgs g) {
   constexpr int CW = TABLE == 0 ? 16 : TABLE;
   using At = Entry<CW>;
   const int tid = threadIdx.x, threads = blockDim.x;
-  const uint32_t row_index = blockIdx.x / (uint32_t)g.segments;
+  // (a row's segments on one XCD, so that its tokens are read into one L2: 64 x 32000 with
+  // 4096 ids 8.8 -> 7.8 us; masks alone take 3 % longer so)
+  const uint32_t index = TABLE != 0 ? xcd_place(blockIdx.x, gridDim.x) : blockIdx.x;
+  const uint32_t row_index = index / (uint32_t)g.segments;
   const int64_t r = row_index;
-  const int first = (int)(blockIdx.x - row_index * (uint32_t)g.segments) * g.seg_len;  // a multiple of 32
+  const int first = (int)(index - row_index * (uint32_t)g.segments) * g.seg_len;  // a multiple of 32
   const int len = min(g.seg_len, g.vocab - first);
   const char* x_row = (const char*)g.logits + (r * g.ld + first) * kind_size<XK>();
   char* o_row = (char*)g.out + (r * g.ldo + first) * kind_size<OK>();
@@ -320,7 +323,8 @@ hipError_t launch_kinds(AdjustArgs a, hipStream_t stream) {
   //                                   256 x 100003 bf16, 8192 ids  53.0 / 48.0 / 52.5
   //   masks alone, at most 2048 / 4096 / 8192 / 16384   512 x 50000 fp32 in place
   //                                   27.7 / 26.1 / 27.2 / 34.4, bf16 to fp32 35.9 / 35.0 / 35.0 / 40.7
-  // and 512 threads for segments past 4096 (512 x 100003: 85.3, with 256 92.9).
+  // and 512 threads for segments or histories past 4096 (512 x 100003: 85.3, with 256 92.9;
+  // 1 x 131071 with 8192 ids 4.9 and 6.5).
   int64_t want = (1024 + a.m - 1) / a.m;
   int64_t seg = (a.vocab + want - 1) / want;
   if (seg < 1024) seg = 1024;
@@ -329,7 +333,7 @@ hipError_t launch_kinds(AdjustArgs a, hipStream_t stream) {
   if (seg > a.vocab) seg = a.vocab;
   a.seg_len = (int32_t)((seg + 31) / 32 * 32);
   a.segments = (a.vocab + a.seg_len - 1) / a.seg_len;
-  const int threads = a.seg_len > 4096 ? 512 : 256;
+  const int threads = a.seg_len > 4096 || a.history_len > 4096 ? 512 : 256;
   const size_t lds = rules ? (size_t)a.seg_len * bits / 8 : 0;
   const auto fn = !rules ? adjust_kernel<XK, OK, IN_PLACE, 0>
                   : bits == 16 ? adjust_kernel<XK, OK, IN_PLACE, 16> : adjust_kernel<XK, OK, IN_PLACE, 32>;

@@ -16,6 +16,13 @@ typedef uint32_t u32x2_align4 __attribute__((ext_vector_type(2), aligned(4)));
 typedef uint32_t u32x2_align2 __attribute__((ext_vector_type(2), aligned(2)));
 typedef uint32_t u32x2_align1 __attribute__((ext_vector_type(2), aligned(1)));
 
+// Workgroup `index` of `count` in an order in which the workgroups that share an XCD
+// (every eighth one), and with it an L2, have consecutive places.
+__device__ __forceinline__ uint32_t xcd_place(uint32_t index, uint32_t count) {
+  const uint32_t xcd = index & 7, most = count >> 3, more = count & 7;
+  return xcd * most + min(xcd, more) + (index >> 3);
+}
+
 template <int K>
 constexpr int kind_size() { return K == CK_F32 ? 4 : 2; }
 
