@@ -15,8 +15,11 @@
 // largest |h w| of a row or group is found beside the sum of squares: rounding keeps
 // order, so its product with 1 / sqrt(..) is the largest |y| exactly, and a row's
 // waves meet once.
-// Rows past 32768 values do not stay in registers and are read two or three
-// times (norm_long_kernel).
+// Rows past 32768 values do not stay in registers and are read twice
+// (norm_long_kernel).
+// Measured: 16384 x 5120 bf16 to bf16 sums and 8 bits 113 us (5.2 TB/s, what a large
+// copy reaches), 2000 x 7681 bf16 23.3 (5.3), 1983 x 896 bf16 on fp32 sums 5.8,
+// 1 x 5120 2.8.
 //
 // q is y times the reciprocal of its scale: the quotient rounded once more,
 // 2^-23 off at the most before it is rounded to 8 bits.  |y / s| is at most
@@ -54,21 +57,24 @@ __device__ __forceinline__ float lanes_reduce(float v, int lanes) {
   return v;
 }
 
-// a row's sum and largest value over the waves of a workgroup, in the order of the waves
-__device__ __forceinline__ void block_reduce(float& sum, float& top, bool both, float (&parts)[2][16], int waves) {
-  sum = lanes_reduce<false>(sum, 64);
+// A row's sum and largest value over the waves of a workgroup.  The sums of 64
+// consecutive chunks are added up in the lanes of each wave, by the chunks' places, so
+// the result does not depend on how many of a row's chunks a lane has.
+template <int CH>
+__device__ __forceinline__ void block_reduce(float (&sums)[CH], float& sum, float& top, bool both, float (&parts)[16 * CH + 16],
+                                             int waves) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+  for (int c = 0; c < CH; ++c) sums[c] = lanes_reduce<false>(sums[c], 64);
   if (both) top = lanes_reduce<true>(top, 64);
-  if (waves == 1) return;
-  if ((threadIdx.x & 63) == 0) {
-    parts[0][threadIdx.x >> 6] = sum;
-    parts[1][threadIdx.x >> 6] = top;
+  if (lane == 0) {
+#pragma unroll
+    for (int c = 0; c < CH; ++c) parts[c * waves + wave] = sums[c];
+    parts[16 * CH + wave] = top;
   }
   __syncthreads();
-  sum = parts[0][0], top = parts[1][0];
-  for (int i = 1; i < waves; ++i) {
-    sum += parts[0][i];
-    top = fmaxf(top, parts[1][i]);
-  }
+  sum = lanes_reduce<false>(lane < CH * waves ? parts[lane] : 0.0f, 64);
+  if (both) top = lanes_reduce<true>(lane < waves ? parts[16 * CH + lane] : 0.0f, 64);
 }
 
 // values e0 .. e0 + 7 of a row, 0 from d on.  In a vector where all lie in the
@@ -175,7 +181,7 @@ __device__ __forceinline__ RowPtrs row_ptrs(const NormArgs& g, int64_t row) {
 // 2^lanes_log2 of a wave's.
 template <int XK, int RK, int CH, bool BLOCK>
 __global__ __launch_bounds__(BLOCK ? 1024 : 256) void norm_kernel(NormArgs g) {
-  __shared__ float parts_s[2][16];
+  __shared__ float parts_s[16 * CH + 16];
   const int tid = threadIdx.x;
   const int lanes = BLOCK ? 64 : 1 << g.lanes_log2;
   const int step = BLOCK ? (int)blockDim.x : lanes;
@@ -202,12 +208,13 @@ __global__ __launch_bounds__(BLOCK ? 1024 : 256) void norm_kernel(NormArgs g) {
   for (int c = 0; c < CH; ++c) load_weight8(g, (c * step + place) * 8, w[c]);
 
   // w becomes h w
-  float sum = 0.0f, top[CH];
+  float sum = 0.0f, sums[CH], top[CH];
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
+    sums[c] = 0.0f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      sum = __builtin_fmaf(h[c][e], h[c][e], sum);
+      sums[c] = __builtin_fmaf(h[c][e], h[c][e], sums[c]);
       w[c][e] *= h[c][e];
     }
     top[c] = max8(w[c]);
@@ -217,8 +224,10 @@ __global__ __launch_bounds__(BLOCK ? 1024 : 256) void norm_kernel(NormArgs g) {
 #pragma unroll
   for (int c = 1; c < CH; ++c) row_top = fmaxf(row_top, top[c]);
   if constexpr (BLOCK) {
-    block_reduce(sum, row_top, row_scale, parts_s, waves);
+    block_reduce<CH>(sums, sum, row_top, row_scale, parts_s, waves);
   } else {
+#pragma unroll
+    for (int c = 0; c < CH; ++c) sum += sums[c];
     sum = lanes_reduce<false>(sum, lanes);
     if (row_scale) row_top = lanes_reduce<true>(row_top, lanes);
   }
@@ -266,7 +275,7 @@ __global__ __launch_bounds__(BLOCK ? 1024 : 256) void norm_kernel(NormArgs g) {
 // the row twice.
 template <int XK, int RK>
 __global__ __launch_bounds__(1024) void norm_long_kernel(NormArgs g) {
-  __shared__ float parts_s[2][16];
+  __shared__ float parts_s[32];
   constexpr int kStep = 8 * 1024;
   const int d = g.d;
   const RowPtrs p = row_ptrs<XK, RK>(g, blockIdx.x);
@@ -284,17 +293,17 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(NormArgs g) {
   };
   const int first = (int)threadIdx.x * 8;
   const bool row_scale = p.q != nullptr && g.group == 0;
-  float sum = 0.0f, top = 0.0f;
+  float sum = 0.0f, sums[1] = {0.0f}, top = 0.0f;
   for (int e0 = first; e0 < d; e0 += kStep) {
     float h[8], hw[8];
     load_both(e0, h, hw);
     float s = 0.0f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) s = __builtin_fmaf(h[e], h[e], s);
-    sum += s;
+    sums[0] += s;
     top = fmaxf(top, max8(hw));
   }
-  block_reduce(sum, top, row_scale, parts_s, 16);
+  block_reduce<1>(sums, sum, top, row_scale, parts_s, 16);
   const float inv = 1.0f / sqrtf(sum / (float)d + g.eps);
   float s = scale_of(top * inv);
   if (row_scale && threadIdx.x == 0) p.scales[0] = s;
@@ -335,7 +344,7 @@ hipError_t launch_kinds(NormArgs a, hipStream_t stream) {
   } else if (chunks <= 4 * 1024) {
     // one chunk per lane; two for many long rows, which makes more rows share a CU:
     // 16384 x 5120 to 8 bits 123 -> 113 us, 8192 x 5120 64.7 -> 62.8, but 1 x 5120
-    // 2.9 -> 3.3, 256 x 5120 3.6 -> 3.8 and 4096 x 2560 fp32 36.2 -> 39.5
+    // 2.8 -> 3.2, 256 x 5120 3.5 -> 3.8 and 4096 x 2560 fp32 36.2 -> 39.5
     const int ch = chunks > 2 * 1024 ? 4 : chunks > 1024 || (chunks > 512 && a.m >= 512) ? 2 : 1;
     threads = ((chunks + ch - 1) / ch + 63) / 64 * 64;
     fn = ch == 1 ? norm_kernel<XK, RK, 1, true> : ch == 2 ? norm_kernel<XK, RK, 2, true> : norm_kernel<XK, RK, 4, true>;

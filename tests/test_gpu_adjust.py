@@ -112,6 +112,18 @@ def test_adjust_history_lengths(history):
     check(2, 5003, "f32", history=history, t64=history % 2 == 1)
 
 
+def test_adjust_long_histories_of_many_rows():
+    """The largest table: 32-bit entries of the longest segment."""
+    m, V = 600, 33000
+    a = rules_of(m, V, 5, history=16400)
+    x = torch.randn((m, V), generator=torch.Generator().manual_seed(1))
+    got = sk.adjust_logits(x.cuda(), sk.LogitRules(m, V, **device(a)))
+    torch.cuda.synchronize()
+    for i in (0, 1, 299, 599):
+        one = {k: v[i:i + 1] for k, v in a.items()}
+        compare(got[i:i + 1], x[i:i + 1].double().numpy(), one, "f32")
+
+
 @pytest.mark.parametrize("vocab,history", [(40000, 16383), (17, 16383), (40000, 40000), (1, 20000)])
 def test_adjust_one_token_over_and_over(vocab, history):
     """A count as long as the history."""

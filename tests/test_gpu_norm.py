@@ -112,6 +112,17 @@ def test_norm_rows_do_not_depend_on_the_others():
                     assert torch.equal(a[i].view(torch.uint8), b[0].view(torch.uint8))
 
 
+@pytest.mark.parametrize("d", [896, 4104, 5120, 7681, 8192, 9000])
+def test_norm_rows_are_the_same_bits_in_a_large_batch(d):
+    """Also where a large batch gives a row fewer threads."""
+    X, R, W = inputs(600, d, "bf16", "f32", "bf16", 6)
+    got = sk.rms_norm(X[0], W[0], residual=R[0], out_dtype=torch.float32, quant=0)
+    for m in (1, 37, 511, 512):
+        part = sk.rms_norm(X[0][:m], W[0], residual=R[0][:m], out_dtype=torch.float32, quant=0)
+        for a, b in zip(got, part):
+            assert torch.equal(a[:m].view(torch.uint8), b.view(torch.uint8))
+
+
 @pytest.mark.parametrize("offset", [0, 1, 3, 4, 7])
 @pytest.mark.parametrize("d", [40, 896, 2561])
 def test_norm_alignment_and_strides(d, offset):
