@@ -4,7 +4,8 @@
 //   out_t = base_t + scaling[a] B[a] (A[a] x_t),   a = ids[t]
 //
 // Two launches.  The first ("down") gives the inner values A x of every row, the
-// second ("up") multiplies them by B and adds the base.  Rows of one adapter are
+// second ("up") multiplies them by B and adds the base (a few rows with a small A take
+// both in one, see takes_one).  Rows of one adapter are
 // gathered into tiles, so that 16 rows share one read of the adapter's weights
 // (64 in batches of more than kAdaptDirectRows rows) and a matrix-core step has
 // rows to multiply.  For few rows each workgroup finds its tile in the list of
@@ -20,7 +21,10 @@
 // which are the exact sum of two bf16 numbers, five (the two products of the
 // lowest planes lie below 2^-24).  Planes in f16 would lose small inner values.
 // The work of both is bound by memory: by latency for a few rows, for many by x
-// in the one and base and out in the other.
+// in the one and base and out in the other.  Measured (bf16): 4096 rows of 12 prompts
+// with 8 adapters of rank 32, k 5120, n 7680: sort 5 us, down 11 (4.0 TB/s), up 27 (4.7
+// TB/s); 250 rows with 64 adapters of rank 16 to 64, k 4096, n 5003: down 8.3, up 17; 1
+// row of rank 16, k 2560, n 7680: 7.0 in one launch.
 #include "requests.h"
 #include "vector_io.h"
 #include "window_kernel.h"
