@@ -541,9 +541,9 @@ __device__ __forceinline__ void store_rows(const AdaptArgs& g, const R* rows_s, 
   }
 }
 
-// A workgroup: the rows of a tile, col_blocks times kBlockCols columns, 64 of them
+// A workgroup: 16 TR rows of a tile, col_blocks times kBlockCols columns, 64 of them
 // per wave.  HELD: steps of 32 ranks whose fragments of B stay in registers over the
-// tile's rows (0: the steps follow one another, with running totals of all rows).
+// tile's rows (0: the steps follow one another, with running totals of its 16 rows).
 // The matrix core's sums are read in the straight line of code that forms them (the
 // hardware does not hold back a read that comes too early, and the compiler has
 // missed some behind branches): all HELD steps are multiplied, with zeros past the
@@ -556,10 +556,13 @@ __global__ __launch_bounds__(kThreads) void adapter_up_kernel(AdaptArgs g, int c
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int low = lane & 15, h = lane >> 4;
-  const uint32_t tiles = TR > 1 ? g.tile_count[0] : gridDim.y;
-  const Tile tile = tile_of(((const u32x4*)g.tiles)[blockIdx.y]);
-  if (tid < 16 * TR) rows_s[tid] = g.order[blockIdx.y * (16 * TR) + tid];
-  if (blockIdx.y >= tiles || tile.rows == 0) return;
+  const bool list = TR > 1 || g.m > kAdaptDirectRows;
+  const uint32_t tiles = list ? g.tile_count[0] : gridDim.y;
+  Tile tile = tile_of(((const u32x4*)g.tiles)[blockIdx.y]);
+  const int part = (int)blockIdx.z * (16 * TR);  // of the tile's rows
+  if (tid < 16 * TR) rows_s[tid] = g.order[blockIdx.y * (list ? kAdaptTileRows : 16) + part + tid];
+  tile.rows = min(tile.rows - part, 16 * TR);
+  if (blockIdx.y >= tiles || tile.rows <= 0) return;
   const int rank = tile.rank;
   if (rank == 0 && g.out == g.base) return;  // nothing to add
   const float scale = tile.scale;
@@ -614,32 +617,28 @@ __global__ __launch_bounds__(kThreads) void adapter_up_kernel(AdaptArgs g, int c
     auto multiply = [&](int t, int b, const WeightFrags<TK>& f, f32x4(&acc)[kColTiles]) __attribute__((always_inline)) {
       multiply_step<TK>(planes_s + (t * 16 + low) * pitch + b * 32 + 8 * h, 16 * TR * pitch, f, acc);
     };
-    float total[HELD > 0 ? 1 : TR][kColTiles][4];
+    float total[kColTiles][4];
     if constexpr (HELD > 0) {
 #pragma unroll
       for (int b = 0; b < HELD; ++b) finish_frags<TK>(rank, b, lane, slots_s[wave], w[b]);
     } else {
+      static_assert(TR == 1, "running totals are those of 16 rows");
 #pragma unroll
-      for (int t = 0; t < TR; ++t)
+      for (int s = 0; s < kColTiles; ++s)
 #pragma unroll
-        for (int s = 0; s < kColTiles; ++s)
-#pragma unroll
-          for (int q = 0; q < 4; ++q) total[t][s][q] = 0.0f;
+        for (int q = 0; q < 4; ++q) total[s][q] = 0.0f;
       if (steps > 0) load_frags<TK>(g, wb, rank, 0, col, lane, w[0]);
       for (int b = 0; b < steps; ++b) {
         if (b + 1 < steps) load_frags<TK>(g, wb, rank, b + 1, col, lane, next_w[0]);
         finish_frags<TK>(rank, b, lane, slots_s[wave], w[0]);
+        f32x4 acc[kColTiles];
 #pragma unroll
-        for (int t = 0; t < TR; ++t) {
-          f32x4 acc[kColTiles];
+        for (int s = 0; s < kColTiles; ++s) acc[s] = f32x4{0, 0, 0, 0};
+        multiply(0, b, w[0], acc);
 #pragma unroll
-          for (int s = 0; s < kColTiles; ++s) acc[s] = f32x4{0, 0, 0, 0};
-          multiply(t, b, w[0], acc);
+        for (int s = 0; s < kColTiles; ++s)
 #pragma unroll
-          for (int s = 0; s < kColTiles; ++s)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) total[t][s][q] = __builtin_fmaf(scale, acc[s][q], total[t][s][q]);
-        }
+          for (int q = 0; q < 4; ++q) total[s][q] = __builtin_fmaf(scale, acc[s][q], total[s][q]);
 #pragma unroll
         for (int s = 0; s < kColTiles; ++s) w[0].hi[s] = next_w[0].hi[s];
       }
@@ -667,7 +666,7 @@ __global__ __launch_bounds__(kThreads) void adapter_up_kernel(AdaptArgs g, int c
 #pragma unroll
         for (int s = 0; s < kColTiles; ++s)
 #pragma unroll
-          for (int q = 0; q < 4; ++q) sum[s][q] = total[t][s][q];
+          for (int q = 0; q < 4; ++q) sum[s][q] = total[s][q];
       }
       store_rows<TK, BK>(g, rows_s + t * 16, tile.rows - t * 16, h, c0, rank != 0, base, sum);
       if (TR > 1 || cb + 1 < col_blocks) {
@@ -677,10 +676,6 @@ __global__ __launch_bounds__(kThreads) void adapter_up_kernel(AdaptArgs g, int c
     };
     if constexpr (TR == 1) {
       sixteen_rows(0);
-    } else if constexpr (HELD == 0) {
-#pragma unroll
-      for (int t = 0; t < TR; ++t)
-        if (t * 16 < tile.rows) sixteen_rows(t);
     } else {
 #pragma unroll 1
       for (int t = 0; t * 16 < tile.rows; ++t) sixteen_rows(t);
@@ -842,10 +837,26 @@ hipError_t launch_one(const AdaptArgs& a, hipStream_t stream) {
 }
 
 template <int TK, int TR, int BK>
-auto up_kernel(int rank) {
-  return rank <= 32   ? adapter_up_kernel<TK, TR, BK, 1>
-         : rank <= 64 ? adapter_up_kernel<TK, TR, BK, 2> : adapter_up_kernel<TK, TR, BK, 0>;
+auto up_kernel_of(int rank) {
+  if constexpr (TR == 1)
+    if (rank > 64) return adapter_up_kernel<TK, TR, BK, 0>;
+  return rank <= 32 ? adapter_up_kernel<TK, TR, BK, 1> : adapter_up_kernel<TK, TR, BK, 2>;
 }
+template <int TK, int TR>
+auto up_kernel(const AdaptArgs& a) {
+  return a.base == nullptr       ? up_kernel_of<TK, TR, kNoBase>((int)a.rank)
+         : a.base_kind == CK_F32 ? up_kernel_of<TK, TR, CK_F32>((int)a.rank) : up_kernel_of<TK, TR, TK>((int)a.rank);
+}
+
+// Workgroups of the up product that take 16 rows of a tile of 64 each: where whole tiles
+// would be too few for the chip, and for long ranks, whose totals of 64 rows leave a CU
+// too few waves.  Measured (us; whole tiles / 16 rows of each):
+//   pieces of 256 columns of a tile   48: 3002 x 74 22.1 / 15.7, 172: 2594 x 859 31.3 / 25.8,
+//   348: 849 x 1311 22.1 / 16.0, 576: 4096 x 2048 28.2 / 30.1, 924: 2683 x 5178 41.3 / 36.4,
+//   2190: 4096 x 7680 48.0 / 55.3
+//   rank 128  41: 2458 x 355 35.6 / 24.3, 1168: 4096 x 4096 86.0 / 76.2, 2190: 4096 x 7680
+//   105 / 109, 9600: 20000 x 7680 421 / 400; rank 256  4096 x 7680 221 / 180
+constexpr int64_t kPartPieces = 512;
 
 template <int TK, int TR>
 hipError_t launch_tiles(const AdaptArgs& a, hipStream_t stream) {
@@ -865,14 +876,10 @@ hipError_t launch_tiles(const AdaptArgs& a, hipStream_t stream) {
   const int64_t all = (int64_t)tiles * ((a.n + kBlockCols - 1) / kBlockCols);
   const int col_blocks = TR == 1 && all >= 4096 ? 4 : all >= 1536 ? 2 : 1;
   const unsigned cols = (unsigned)((a.n + kBlockCols * col_blocks - 1) / (kBlockCols * col_blocks));
-  const size_t planes = (size_t)kPlanes * 16 * TR * ((a.rank + 31) / 32 * 32 + 8) * 2;
-  const auto up = a.base == nullptr       ? up_kernel<TK, TR, kNoBase>((int)a.rank)
-                  : a.base_kind == CK_F32 ? up_kernel<TK, TR, CK_F32>((int)a.rank) : up_kernel<TK, TR, TK>((int)a.rank);
-  if (planes > 40 * 1024) {  // (with the static part past the 64 KiB that need no asking)
-    e = hipFuncSetAttribute((const void*)up, hipFuncAttributeMaxDynamicSharedMemorySize, 128 * 1024);
-    if (e != hipSuccess) return e;
-  }
-  hipLaunchKernelGGL(up, dim3(cols, tiles), dim3(kThreads), planes, stream, a, col_blocks);
+  const int parts = TR > 1 && (a.rank > 64 || all < kPartPieces) ? TR : 1;
+  const size_t planes = (size_t)kPlanes * 16 * (TR / parts) * ((a.rank + 31) / 32 * 32 + 8) * 2;
+  const auto up = parts > 1 ? up_kernel<TK, 1>(a) : up_kernel<TK, TR>(a);
+  hipLaunchKernelGGL(up, dim3(cols, tiles, (unsigned)parts), dim3(kThreads), planes, stream, a, col_blocks);
   return hipGetLastError();
 }
 
