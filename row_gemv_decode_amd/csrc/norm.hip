@@ -91,9 +91,12 @@ __device__ __forceinline__ void load8(const void* row, int e0, int d, float (&x)
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] = 0.0f;
     if (d % 8 != 0 && e0 < d) {
+      // (no load behind a branch of its own, where each would be waited for)
+      float v[7];
 #pragma unroll
-      for (int e = 0; e < 7; ++e)
-        if (e0 + e < d) x[e] = value_at<K>(row, e0 + e);
+      for (int e = 0; e < 7; ++e) v[e] = value_at<K>(row, min(e0 + e, d - 1));
+#pragma unroll
+      for (int e = 0; e < 7; ++e) x[e] = e0 + e < d ? v[e] : 0.0f;
     }
   }
 }
