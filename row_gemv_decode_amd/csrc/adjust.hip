@@ -12,7 +12,10 @@
 // touches only the vectors that change.  Counts are integers, so the order of the
 // atomics changes nothing.  Biased tokens are few: the stream leaves their logits as
 // they are, and where a segment has any, one thread each computes them afterwards,
-// adding a token's biases in the order of the list.
+// adding a token's biases in the order of the list, whose first 1024 entries wait in LDS
+// (read from memory again for each token that is listed twice, 64 x 50000 with 300 biases
+// took 90 us for 17).  Rules without a history or without biases have kernels of their
+// own, which are shorter (64 x 32000 with 4096 ids 7.9 -> 7.5).
 // HBM-bound for many rows: the logits are read and written once; a row's tokens
 // are read once per segment, from L2.  For few rows the chain of memory latencies
 // counts: what the first steps need is all in flight before the table is cleared.
@@ -31,8 +34,15 @@ namespace skinny {
 
 namespace {
 
-constexpr int kSegmentMax = 16384;     // tokens of a segment with a table
+constexpr int kSegmentMax = 16384;     // tokens of a segment with a table (half as many where
+                                       // 32-bit entries and a list of biases share 64 KiB)
 constexpr int kMaskSegmentMax = 4096;  // and without one
+constexpr int kThreadsMax = 512;
+constexpr int kBiasesHeld = 1024;  // a row's first biases are kept in LDS
+constexpr int kBiasStep = 16;
+constexpr int biases_held(int biases) {
+  return ((biases < kBiasesHeld ? biases : kBiasesHeld) + kBiasStep - 1) / kBiasStep * kBiasStep;
+}
 // table entries: 16 bits, or 32 for histories that could count further than 14 bits
 constexpr uint32_t kInPrompt = 1, kBiased = 2, kOnce = 4;
 
@@ -103,9 +113,9 @@ __device__ __forceinline__ int64_t token_at(const void* list, int64_t i, int tok
 template <int XK, int OK>
 constexpr int stream_elems() { return XK == CK_F32 || OK == CK_F32 ? 4 : 8; }
 
-// TABLE: 0 (mask only), or an entry's bits
-template <int XK, int OK, bool IN_PLACE, int TABLE>
-__global__ __launch_bounds__(512) void adjust_kernel(AdjustArgs g) {
+// TABLE: 0 (mask only), or an entry's bits; HISTORY, BIASES: which of the two there are
+template <int XK, int OK, bool IN_PLACE, int TABLE, bool HISTORY, bool BIASES>
+__global__ __launch_bounds__(kThreadsMax) void adjust_kernel(AdjustArgs g) {
   extern __shared__ uint32_t table_s[];
   __shared__ int biased_s, twice_s;
   constexpr int CW = TABLE == 0 ? 16 : TABLE;
@@ -129,7 +139,7 @@ __global__ __launch_bounds__(512) void adjust_kernel(AdjustArgs g) {
   // what the first steps of both loops need is in flight before either begins
   constexpr int H = 2;  // history loads of a thread in flight
   const int per = g.tokens64 != 0 ? 2 : 4;  // ids of a load
-  u32x4 ids[TABLE != 0 ? H : 1];
+  u32x4 ids[H];
   int held = 0, prompt = 0;
   Penalties pen = {1.0f, 0.0f, 0.0f};
   const int64_t bias_row = r * g.biases;
@@ -138,19 +148,23 @@ __global__ __launch_bounds__(512) void adjust_kernel(AdjustArgs g) {
     return off < len ? off : -1;
   };
   int64_t my_bias = -1;
-  if constexpr (TABLE != 0) {
-    if (g.history != nullptr) {
+  float my_value = 0.0f;
+  if constexpr (HISTORY) {
 #pragma unroll
-      for (int u = 0; u < H; ++u)
-        if (u * threads * per < g.history_len)
-          ids[u] = load_tokens(g.history, r * g.ldh, (u * threads + tid) * per, g.history_len, g.tokens64);
-      held = g.lengths != nullptr ? max(0, min(g.lengths[r], g.history_len)) : g.history_len;
-      prompt = g.prompt_lengths != nullptr ? max(0, min(g.prompt_lengths[r], held)) : 0;
-      if (g.repetition != nullptr) pen.theta = g.repetition[r];
-      if (g.frequency != nullptr) pen.frequency = g.frequency[r];
-      if (g.presence != nullptr) pen.presence = g.presence[r];
+    for (int u = 0; u < H; ++u)
+      if (u * threads * per < g.history_len)
+        ids[u] = load_tokens(g.history, r * g.ldh, (u * threads + tid) * per, g.history_len, g.tokens64);
+    held = g.lengths != nullptr ? max(0, min(g.lengths[r], g.history_len)) : g.history_len;
+    prompt = g.prompt_lengths != nullptr ? max(0, min(g.prompt_lengths[r], held)) : 0;
+    if (g.repetition != nullptr) pen.theta = g.repetition[r];
+    if (g.frequency != nullptr) pen.frequency = g.frequency[r];
+    if (g.presence != nullptr) pen.presence = g.presence[r];
+  }
+  if constexpr (BIASES) {
+    if (tid < g.biases) {
+      my_bias = bias_off(tid);
+      my_value = g.bias_values[bias_row + tid];
     }
-    if (tid < g.biases) my_bias = bias_off(tid);
   }
   constexpr int VE = stream_elems<XK, OK>();
   constexpr int U = 4;  // vectors of a thread in flight
@@ -184,11 +198,15 @@ __global__ __launch_bounds__(512) void adjust_kernel(AdjustArgs g) {
   };
   if (vectors > 0) load_vectors(tid);
 
+  // the first biases in LDS: places in the segment and values, up to a multiple of a step
+  const int held_biases = biases_held(g.biases), biases = max(g.biases, held_biases);
+  int* bias_off_s = (int*)(table_s + g.seg_len * CW / 32);
+  float* bias_s = (float*)(bias_off_s + held_biases);
   if constexpr (TABLE != 0) {
     for (int i = tid; i < g.seg_len * CW / 32; i += threads) table_s[i] = 0;
-    if (tid == 0) biased_s = twice_s = 0;
+    if (BIASES && tid == 0) biased_s = twice_s = 0;
     lds_barrier();
-    for (int i0 = 0; i0 < held; i0 += H * threads * per) {
+    for (int i0 = 0; HISTORY && i0 < held; i0 += H * threads * per) {
       if (i0 > 0) {
 #pragma unroll
         for (int u = 0; u < H; ++u)
@@ -212,8 +230,12 @@ __global__ __launch_bounds__(512) void adjust_kernel(AdjustArgs g) {
         }
       }
     }
-    for (int i = tid; i < g.biases; i += threads) {
-      const int64_t off = i == tid ? my_bias : bias_off(i);
+    for (int i = tid; BIASES && i < biases; i += threads) {
+      const int64_t off = i == tid ? my_bias : i < g.biases ? bias_off(i) : -1;
+      if (i < held_biases) {
+        bias_off_s[i] = (int)off;
+        bias_s[i] = i == tid ? my_value : i < g.biases ? g.bias_values[bias_row + i] : 0.0f;
+      }
       if (off >= 0) {
         const At at((int)off);
         biased_s = 1;
@@ -233,7 +255,7 @@ __global__ __launch_bounds__(512) void adjust_kernel(AdjustArgs g) {
     for (int i = 0; i < VE; ++i) e[i] = CW == 16 ? (w[i / 2] >> (16 * (i & 1))) & 0xffffu : w[i];
     return some != 0;
   };
-  auto adjusted = [&](float x, uint32_t entry) { return (entry & kBiased) != 0 ? x : penalised(x, entry, pen); };
+  auto adjusted = [&](float x, uint32_t entry) { return BIASES && (entry & kBiased) != 0 ? x : penalised(x, entry, pen); };
   auto stream_step = [&](auto full, int v0) {
     uint32_t e[U][VE];
     bool some[U];  // whether a vector has entries
@@ -241,7 +263,7 @@ __global__ __launch_bounds__(512) void adjust_kernel(AdjustArgs g) {
     for (int u = 0; u < U; ++u) {
       if (!full.value && v0 - tid + u * threads >= vectors) break;
       const int v = v0 + u * threads;
-      some[u] = TABLE != 0 && entries(min(v, vectors - 1), e[u]);
+      some[u] = HISTORY && entries(min(v, vectors - 1), e[u]);
       if (IN_PLACE) {
         if (v >= vectors) some[u] = false, bits[u] = kAll;
         if (bits[u] != 0 && some[u]) raw[u] = load_raw<XK, VE>(x_row, (int64_t)v * VE);
@@ -253,7 +275,7 @@ __global__ __launch_bounds__(512) void adjust_kernel(AdjustArgs g) {
       const int v = v0 + u * threads;
       float x[VE];
       unpack_raw<XK, VE>(raw[u], x);
-      if (TABLE != 0 && some[u]) {
+      if (HISTORY && some[u]) {
 #pragma unroll
         for (int i = 0; i < VE; ++i) x[i] = adjusted(x[i], e[u][i]);
       }
@@ -266,7 +288,7 @@ __global__ __launch_bounds__(512) void adjust_kernel(AdjustArgs g) {
         // with whole vectors read and written again, 9.0 so; 512 of 50000 in fp32 47 and 35)
 #pragma unroll
         for (int i = 0; i < VE; ++i)
-          if ((bits[u] >> i & 1) == 0 || (TABLE != 0 && e[u][i] != 0)) store_out<OK>(o_row, (int64_t)v * VE + i, x[i]);
+          if ((bits[u] >> i & 1) == 0 || (HISTORY && e[u][i] != 0)) store_out<OK>(o_row, (int64_t)v * VE + i, x[i]);
       }
     }
   };
@@ -280,7 +302,7 @@ __global__ __launch_bounds__(512) void adjust_kernel(AdjustArgs g) {
   }
   for (int j = vectors * VE + tid; j < len; j += threads) {
     const At at(j);
-    const uint32_t entry = TABLE != 0 ? at.of(table_s[at.word]) : 0;
+    const uint32_t entry = HISTORY ? at.of(table_s[at.word]) : 0;
     if (!allowed_at(mask, j)) {
       store_out<OK>(o_row, j, -INFINITY);
     } else if (!IN_PLACE || entry != 0) {
@@ -288,23 +310,36 @@ __global__ __launch_bounds__(512) void adjust_kernel(AdjustArgs g) {
     }
   }
 
-  if constexpr (TABLE != 0) {
+  if constexpr (BIASES) {
     if (biased_s == 0) return;  // (the same in every thread)
     wait_mem();                 // the stream's stores come before the biased tokens'
     __syncthreads();
     const bool twice = twice_s != 0;
     for (int i = tid; i < g.biases; i += threads) {
-      const int64_t o = i == tid ? my_bias : bias_off(i);
+      const int64_t o = i < held_biases ? bias_off_s[i] : bias_off(i);
       if (o < 0) continue;
       const int off = (int)o;
       const At at(off);
       // the first to take the flag away writes the token's logit
       const uint32_t entry = at.of(atomicAnd(&table_s[at.word], ~(kBiased << at.shift)));
       if ((entry & kBiased) == 0) continue;
-      float b = g.bias_values[bias_row + i];
-      if (twice) {
-        b = 0.0f;
-        for (int k = 0; k < g.biases; ++k)
+      float b = 0.0f;
+      if (!twice) {
+        b = i < held_biases ? bias_s[i] : g.bias_values[bias_row + i];
+      } else {
+        for (int k0 = 0; k0 < held_biases; k0 += kBiasStep) {
+          u32x4 offs[kBiasStep / 4];
+          f32x4 values[kBiasStep / 4];
+#pragma unroll
+          for (int q = 0; q < kBiasStep / 4; ++q) {
+            offs[q] = *(const u32x4*)(bias_off_s + k0 + 4 * q);
+            values[q] = *(const f32x4*)(bias_s + k0 + 4 * q);
+          }
+#pragma unroll
+          for (int k = 0; k < kBiasStep; ++k) b += offs[k / 4][k % 4] == (uint32_t)off ? values[k / 4][k % 4] : 0.0f;
+        }
+#pragma unroll 1
+        for (int k = held_biases; k < g.biases; ++k)
           if (bias_off(k) == o) b += g.bias_values[bias_row + k];
       }
       const float x = penalised(value_at<XK>(x_row, off), entry, pen) + b;
@@ -331,15 +366,19 @@ hipError_t launch_kinds(AdjustArgs a, hipStream_t stream) {
   int64_t want = (1024 + a.m - 1) / a.m;
   int64_t seg = (a.vocab + want - 1) / want;
   if (seg < 1024) seg = 1024;
-  const int64_t longest = rules ? kSegmentMax : kMaskSegmentMax;
+  const int64_t longest = !rules ? kMaskSegmentMax : bits == 16 || a.biases == 0 ? kSegmentMax : kSegmentMax / 2;
   if (seg > longest) seg = longest;
   if (seg > a.vocab) seg = a.vocab;
   a.seg_len = (int32_t)((seg + 31) / 32 * 32);
   a.segments = (a.vocab + a.seg_len - 1) / a.seg_len;
-  const int threads = a.seg_len > 4096 || a.history_len > 4096 ? 512 : 256;
-  const size_t lds = rules ? (size_t)a.seg_len * bits / 8 : 0;
-  const auto fn = !rules ? adjust_kernel<XK, OK, IN_PLACE, 0>
-                  : bits == 16 ? adjust_kernel<XK, OK, IN_PLACE, 16> : adjust_kernel<XK, OK, IN_PLACE, 32>;
+  const int threads = a.seg_len > 4096 || a.history_len > 4096 ? kThreadsMax : 256;
+  const size_t lds = rules ? (size_t)a.seg_len * bits / 8 + biases_held(a.biases) * 8 : 0;
+  const auto fn = !rules                ? adjust_kernel<XK, OK, IN_PLACE, 0, false, false>
+                  : a.history == nullptr ? adjust_kernel<XK, OK, IN_PLACE, 16, false, true>
+                  : a.biases == 0        ? (bits == 16 ? adjust_kernel<XK, OK, IN_PLACE, 16, true, false>
+                                                       : adjust_kernel<XK, OK, IN_PLACE, 32, true, false>)
+                  : bits == 16           ? adjust_kernel<XK, OK, IN_PLACE, 16, true, true>
+                                         : adjust_kernel<XK, OK, IN_PLACE, 32, true, true>;
   const int64_t most = kMaxLaunchThreads / 2 / threads / a.segments;  // rows of a launch
   if (most < 1) return hipErrorInvalidValue;
   for (int64_t r = 0; r < a.m; r += most) {

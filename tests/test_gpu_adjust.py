@@ -112,10 +112,11 @@ def test_adjust_history_lengths(history):
     check(2, 5003, "f32", history=history, t64=history % 2 == 1)
 
 
-def test_adjust_long_histories_of_many_rows():
-    """The largest table: 32-bit entries of the longest segment."""
+@pytest.mark.parametrize("biases", [0, 1300])
+def test_adjust_long_histories_of_many_rows(biases):
+    """The largest tables: 32-bit entries of the longest segment, without and with biases."""
     m, V = 600, 33000
-    a = rules_of(m, V, 5, history=16400)
+    a = rules_of(m, V, 5, history=16400, biases=biases)
     x = torch.randn((m, V), generator=torch.Generator().manual_seed(1))
     got = sk.adjust_logits(x.cuda(), sk.LogitRules(m, V, **device(a)))
     torch.cuda.synchronize()
@@ -135,7 +136,7 @@ def test_adjust_one_token_over_and_over(vocab, history):
     compare(sk.adjust_logits(X[0], sk.LogitRules(2, vocab, **device(a))), X[1], a, "f32")
 
 
-@pytest.mark.parametrize("biases", [1, 7, 255, 256, 300, 1000, 5000])
+@pytest.mark.parametrize("biases", [1, 7, 15, 16, 17, 255, 256, 300, 1000, 1023, 1024, 1025, 5000])
 @pytest.mark.parametrize("double", [False, True])
 def test_adjust_bias_lists(biases, double):
     """Lists longer than a workgroup; the same token several times."""
