@@ -690,7 +690,7 @@ __global__ __launch_bounds__(kThreads) void adapter_up_kernel(AdaptArgs g, int c
 }
 
 // --- both in one launch --------------------------------------------------------
-// For a few rows and a small A: each workgroup of the up product computes its tile's
+// For few rows and a small A: each workgroup of the up product computes its tile's
 // inner values by itself, which costs a read of the adapter's A from L2 and saves
 // the other launch and the way through memory.  The loads of all splits of k, of B
 // and of the base are in flight together.  Waves, splits and additions are those of
@@ -698,6 +698,7 @@ __global__ __launch_bounds__(kThreads) void adapter_up_kernel(AdaptArgs g, int c
 constexpr int kOneSplits = 4;
 constexpr int kOnePitch = 32 + 8;
 constexpr int64_t kOneReads = 10 << 20;  // elements of A
+constexpr int64_t kOneReadsMany = 2 << 20;  // and for more than 64 rows
 
 template <int TK, int BK, int NR>
 __global__ __launch_bounds__(kThreads) void adapter_one_kernel(AdaptArgs g) {
@@ -818,21 +819,26 @@ auto one_kernel(const AdaptArgs& a) {
          : a.base_kind == CK_F32 ? adapter_one_kernel<TK, CK_F32, NR> : adapter_one_kernel<TK, TK, NR>;
 }
 // Whether the one launch takes a call: its splits are the two launches', and its
-// workgroups together read less than 20 MB of A.  Measured (us in a graph, and called
+// workgroups together read less than 20 MB of A, or 4 MB past 64 rows, whose tiles take
+// longer to find.  Measured (us in a graph, and called
 // back to back, where the second launch costs the host 2.8 us; one launch / two):
 //   1 x 2560 x 7680, rank 16   7.0, 7.2 / 7.6, 8.9      8 x 2560 x 7680  7.4, 7.5 / 7.9, 9.4
 //   8 x 4096 x 4096, rank 16   8.6, 8.7 / 8.0, 9.4     16 x 4096 x 4096  9.2, 9.2 / 7.9, 9.4 (34 MB)
 //   16 x 2048 x 2048, rank 32  8.1, 8.2 / 8.0, 9.3      1 x 1024 x 1024, rank 8  4.6 / 6.9 in a graph
+// and in a graph, for rows of several adapters:
+//   64 of 8 x 1024 x 1024, rank 16  5.2 / 7.9          102 of 5 x 504 x 160, rank 8    6.1 / 9.2
+//   40 of 4 x 2560 x 7680, rank 16  7.5 / 7.8          64 of 2 x 4096 x 4096, rank 8   9.2 / 8.4
+//   256 of 64 x 1024 x 1024, rank 16  8.9 / 8.4 (11 MB)  250 of 2 x 4096 x 1024, rank 16  11.7 / 9.3 (9 MB)
 bool takes_one(const AdaptArgs& a) {
-  const int64_t blocks = (int64_t)a.m * ((a.n + kBlockCols - 1) / kBlockCols);
-  return a.m <= kGemvMaxM && a.rank <= 32 && a.splits <= kOneSplits && a.split_len == (a.rank <= 16 ? 1024 : 512) &&
-         blocks * a.rank * a.k <= kOneReads;
+  const int64_t blocks = (int64_t)a.max_tiles * ((a.n + kBlockCols - 1) / kBlockCols);
+  return a.m <= kAdaptDirectRows && a.rank <= 32 && a.splits <= kOneSplits && a.split_len == (a.rank <= 16 ? 1024 : 512) &&
+         blocks * a.rank * a.k <= (a.m <= 64 ? kOneReads : kOneReadsMany);
 }
 
 template <int TK>
 hipError_t launch_one(const AdaptArgs& a, hipStream_t stream) {
   const auto fn = a.rank <= 16 ? one_kernel<TK, 1>(a) : one_kernel<TK, 2>(a);
-  hipLaunchKernelGGL(fn, dim3((unsigned)((a.n + kBlockCols - 1) / kBlockCols), (unsigned)a.m), dim3(kThreads), 0, stream, a);
+  hipLaunchKernelGGL(fn, dim3((unsigned)((a.n + kBlockCols - 1) / kBlockCols), (unsigned)a.max_tiles), dim3(kThreads), 0, stream, a);
   return hipGetLastError();
 }
 
@@ -922,11 +928,10 @@ hipError_t launch_adapters(const AdaptArgs& a, int kind, hipStream_t stream) {
       a.k % 8 != 0 || a.splits < 1 || (int64_t)a.splits * a.split_len < a.k || a.split_len % 256 != 0 ||
       a.max_tiles > 65535)
     return hipErrorInvalidValue;
-  if (takes_one(a))
-    return kind == CK_F16 ? launch_one<CK_F16>(a, stream) : launch_one<CK_BF16>(a, stream);
   if (a.m <= kAdaptDirectRows) {
     AdaptArgs d = a;
     d.by_adapter = adapt_by_adapter(a.m, a.count);
+    if (takes_one(d)) return kind == CK_F16 ? launch_one<CK_F16>(d, stream) : launch_one<CK_BF16>(d, stream);
     return kind == CK_F16 ? launch_tiles<CK_F16, 1>(d, stream) : launch_tiles<CK_BF16, 1>(d, stream);
   }
   hipLaunchKernelGGL(adapter_sort_kernel, dim3(1), dim3(kSortThreads), (size_t)(a.count + 1) * 4, stream, a);

@@ -95,6 +95,16 @@ def test_adapters_widths(n, m):
     Case(m, 64, n, 4, 8, "bf16", "f32").check("bf16")
 
 
+@pytest.mark.parametrize("m,count", [(17, 3), (40, 3), (64, 70), (100, 2), (130, 200), (256, 20), (256, 1)])
+def test_adapters_middle_batches(m, count):
+    """In one launch and in two, by adapter and by row, with several tiles of an adapter."""
+    Case(m, 1000, 130, count, 16, "bf16").check()
+    Case(m, 4096, 1100, count, 16, "f16", "f32").check()
+    Case(m, 520, 300, count, 32, "bf16", "f32").check("bf16")
+    Case(m, 2048, 1100, count, 32, "f16", "f16").check()
+    Case(m, 1024, 300, count, 8, "f16", "f32", ids=[0]).check()
+
+
 @pytest.mark.parametrize("m", [16, 250, 600])
 def test_adapters_ids(m):
     """One adapter for all, none at all, runs, every row its own, ids out of range."""
