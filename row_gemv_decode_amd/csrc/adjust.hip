@@ -19,7 +19,7 @@
 // HBM-bound for many rows: the logits are read and written once; a row's tokens
 // are read once per segment, from L2.  For few rows the chain of memory latencies
 // counts: what the first steps need is all in flight before the table is cleared.
-// Measured: 512 x 100003 fp32 with 1024 ids, 32 biases and a mask each 85 us (4.8 TB/s),
+// Measured: 512 x 100003 fp32 with 1024 ids, 32 biases and a mask each 86 us (4.8 TB/s),
 // 16 x 131071 bf16 to fp32 with 4096 ids 7.8, 1 x 32000 fp32 3.9, 256 masks of 50021
 // f16 logits in place 8.7.
 #include <math.h>
