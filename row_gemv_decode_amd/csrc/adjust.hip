@@ -19,7 +19,7 @@
 // HBM-bound for many rows: the logits are read and written once; a row's tokens
 // are read once per segment, from L2.  For few rows the chain of memory latencies
 // counts: what the first steps need is all in flight before the table is cleared.
-// Measured: 512 x 100003 fp32 with 1024 ids, 32 biases and a mask each 86 us (4.8 TB/s),
+// Measured: 512 x 100003 fp32 with 1024 ids, 32 biases and a mask each 81 us (5.1 TB/s),
 // 16 x 131071 bf16 to fp32 with 4096 ids 7.8, 1 x 32000 fp32 3.9, 256 masks of 50021
 // f16 logits in place 8.7.
 #include <math.h>
@@ -34,9 +34,10 @@ namespace skinny {
 
 namespace {
 
-constexpr int kSegmentMax = 16384;     // tokens of a segment with a table (half as many where
-                                       // 32-bit entries and a list of biases share 64 KiB)
-constexpr int kMaskSegmentMax = 4096;  // and without one
+constexpr int kSegmentMax = 16384;      // tokens of a segment with a table (half as many where
+                                        // 32-bit entries and a list of biases share 64 KiB)
+constexpr int kShortSegmentMax = 4096;  // and where a row's tokens are few
+constexpr int kFewTokens = 4096;
 constexpr int kThreadsMax = 512;
 constexpr int kBiasesHeld = 1024;  // a row's first biases are kept in LDS
 constexpr int kBiasStep = 16;
@@ -352,26 +353,29 @@ template <int XK, int OK, bool IN_PLACE>
 hipError_t launch_kinds(AdjustArgs a, hipStream_t stream) {
   const bool rules = a.history != nullptr || a.biases > 0;
   const int bits = a.history_len < 1 << 14 ? 16 : 32;
-  // Segments: as many as give four workgroups per CU, of at least 1024 tokens, and at
-  // most as long as the table stays small beside the workgroups that share a CU's LDS
-  // (without one, short segments).  Measured (us):
+  // Segments: as many as give four workgroups per CU, of at least 1024 tokens, and short
+  // where a row has few tokens; each reads all of them, so where they are many it is as
+  // long as the table stays small beside the workgroups that share a CU's LDS.  Measured (us):
   //   four / eight workgroups per CU  16 x 131071 bf16, 4096 ids  8.8 / 12.1, 64 x 32000 6.6 / 8.6
   //   at least 1024 / 2048 / 4096     1 x 32000 fp32  3.9 / 4.5 / 5.6
-  //   at most 8192 / 16384 / 32768    512 x 100003 fp32, 1024 ids  84.6 / 85.3 / 107,
-  //                                   256 x 100003 bf16, 8192 ids  53.0 / 48.0 / 52.5
-  //   masks alone, at most 2048 / 4096 / 8192 / 16384   512 x 50000 fp32 in place
-  //                                   27.7 / 26.1 / 27.2 / 34.4, bf16 to fp32 35.9 / 35.0 / 35.0 / 40.7
-  // and 512 threads for segments or histories past 4096 (512 x 100003: 85.3, with 256 92.9;
-  // 1 x 131071 with 8192 ids 4.9 and 6.5).
+  //   at most 2048 / 4096 / 8192 / 16384   512 x 100003 fp32, 1024 ids  77.8 / 80.4 / 80.6 / 86.4,
+  //                                   4096 ids  92.1 / 82.8 / 83.2 / 88.1, 14000 ids  180 / 121 / 94.7 / 92.7
+  //                                   512 x 50021 bf16, 1024 ids  45.5 / 35.6 / 40.5 / 38.4, 8192 ids
+  //                                   96.8 / 62.5 / 48.1 / 45.3
+  //                                   masks alone, 512 x 50000 fp32 in place  27.7 / 26.1 / 27.2 / 34.4,
+  //                                   bf16 to fp32  35.9 / 35.0 / 35.0 / 40.7
+  // and 512 threads for segments or histories past 4096 (512 x 100003 in segments of 14304
+  // 85.3, with 256 92.9; 1 x 131071 with 8192 ids 4.9 and 6.5).
   int64_t want = (1024 + a.m - 1) / a.m;
   int64_t seg = (a.vocab + want - 1) / want;
   if (seg < 1024) seg = 1024;
-  const int64_t longest = !rules ? kMaskSegmentMax : bits == 16 || a.biases == 0 ? kSegmentMax : kSegmentMax / 2;
+  const int64_t longest = a.history_len <= kFewTokens   ? kShortSegmentMax
+                          : bits == 16 || a.biases == 0 ? kSegmentMax : kSegmentMax / 2;
   if (seg > longest) seg = longest;
   if (seg > a.vocab) seg = a.vocab;
   a.seg_len = (int32_t)((seg + 31) / 32 * 32);
   a.segments = (a.vocab + a.seg_len - 1) / a.seg_len;
-  const int threads = a.seg_len > 4096 || a.history_len > 4096 ? kThreadsMax : 256;
+  const int threads = a.seg_len > kShortSegmentMax || a.history_len > kFewTokens ? kThreadsMax : 256;
   const size_t lds = rules ? (size_t)a.seg_len * bits / 8 + biases_held(a.biases) * 8 : 0;
   const auto fn = !rules                ? adjust_kernel<XK, OK, IN_PLACE, 0, false, false>
                   : a.history == nullptr ? adjust_kernel<XK, OK, IN_PLACE, 16, false, true>

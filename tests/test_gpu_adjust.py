@@ -112,11 +112,12 @@ def test_adjust_history_lengths(history):
     check(2, 5003, "f32", history=history, t64=history % 2 == 1)
 
 
+@pytest.mark.parametrize("history", [4096, 4097, 16383, 16400])
 @pytest.mark.parametrize("biases", [0, 1300])
-def test_adjust_long_histories_of_many_rows(biases):
-    """The largest tables: 32-bit entries of the longest segment, without and with biases."""
+def test_adjust_long_histories_of_many_rows(history, biases):
+    """The longest segments and the largest tables, without and with biases."""
     m, V = 600, 33000
-    a = rules_of(m, V, 5, history=16400, biases=biases)
+    a = rules_of(m, V, 5, history=history, biases=biases)
     x = torch.randn((m, V), generator=torch.Generator().manual_seed(1))
     got = sk.adjust_logits(x.cuda(), sk.LogitRules(m, V, **device(a)))
     torch.cuda.synchronize()
