@@ -541,6 +541,11 @@ __device__ __forceinline__ void store_rows(const AdaptArgs& g, const R* rows_s, 
   }
 }
 
+constexpr int kLongSteps = 4;  // held of a long rank, where whole tiles of 64 rows take it
+// whether the next columns' fragments fit beside those held (else col_blocks is 1)
+template <int TK, int HELD>
+constexpr bool holds_next() { return HELD > 0 && (HELD < kLongSteps || TK == CK_BF16); }
+
 // A workgroup: 16 TR rows of a tile, col_blocks times kBlockCols columns, 64 of them
 // per wave.  HELD: steps of 32 ranks whose fragments of B stay in registers over the
 // tile's rows (0: the steps follow one another, with running totals of its 16 rows).
@@ -567,7 +572,7 @@ __global__ __launch_bounds__(kThreads) void adapter_up_kernel(AdaptArgs g, int c
   if (rank == 0 && g.out == g.base) return;  // nothing to add
   const float scale = tile.scale;
   const int steps = (rank + 31) / 32;
-  const int pitch = (g.rank + 31) / 32 * 32 + 8;
+  const int pitch = (HELD > 0 ? HELD : (g.rank + 31) / 32) * 32 + 8;
   const uint16_t* wb = (const uint16_t*)g.B + (int64_t)max(tile.adapter, 0) * g.n * g.rank;
   __syncthreads();
 
@@ -609,7 +614,7 @@ __global__ __launch_bounds__(kThreads) void adapter_up_kernel(AdaptArgs g, int c
     const int col = wave_col + cb * kBlockCols, c0 = col + low * kColTiles;
     if (col >= g.n) break;
     WeightFrags<TK> next_w[HELD > 0 ? HELD : 1];  // the next columns'
-    if (cb + 1 < col_blocks) {
+    if (holds_next<TK, HELD>() && cb + 1 < col_blocks) {
 #pragma unroll
       for (int b = 0; b < HELD; ++b)
         if (b < steps) load_frags<TK>(g, wb, rank, b, col + kBlockCols, lane, next_w[b]);
@@ -680,7 +685,7 @@ __global__ __launch_bounds__(kThreads) void adapter_up_kernel(AdaptArgs g, int c
 #pragma unroll 1
       for (int t = 0; t * 16 < tile.rows; ++t) sixteen_rows(t);
     }
-    if (cb + 1 < col_blocks) {
+    if (holds_next<TK, HELD>() && cb + 1 < col_blocks) {
 #pragma unroll
       for (int b = 0; b < HELD; ++b)
 #pragma unroll
@@ -844,8 +849,7 @@ hipError_t launch_one(const AdaptArgs& a, hipStream_t stream) {
 
 template <int TK, int TR, int BK>
 auto up_kernel_of(int rank) {
-  if constexpr (TR == 1)
-    if (rank > 64) return adapter_up_kernel<TK, TR, BK, 0>;
+  if (rank > 64) return adapter_up_kernel<TK, TR, BK, TR == 1 ? 0 : kLongSteps>;
   return rank <= 32 ? adapter_up_kernel<TK, TR, BK, 1> : adapter_up_kernel<TK, TR, BK, 2>;
 }
 template <int TK, int TR>
@@ -855,13 +859,17 @@ auto up_kernel(const AdaptArgs& a) {
 }
 
 // Workgroups of the up product that take 16 rows of a tile of 64 each: where whole tiles
-// would be too few for the chip, and for long ranks, whose totals of 64 rows leave a CU
-// too few waves.  Measured (us; whole tiles / 16 rows of each):
+// would be too few for the chip, and for long ranks, unless rows and columns are many and
+// four steps of B can be held: totals of 64 rows would leave a CU too few waves.  Measured
+// (us; whole tiles / 16 rows of each):
 //   pieces of 256 columns of a tile   48: 3002 x 74 22.1 / 15.7, 172: 2594 x 859 31.3 / 25.8,
 //   348: 849 x 1311 22.1 / 16.0, 576: 4096 x 2048 28.2 / 30.1, 924: 2683 x 5178 41.3 / 36.4,
 //   2190: 4096 x 7680 48.0 / 55.3
-//   rank 128  41: 2458 x 355 35.6 / 24.3, 1168: 4096 x 4096 86.0 / 76.2, 2190: 4096 x 7680
-//   105 / 109, 9600: 20000 x 7680 421 / 400; rank 256  4096 x 7680 221 / 180
+//   rank 128, four steps held  704: 900 x 8192 35.2 / 36.3, 736: 900 x 4096 40.5 / 37.4,
+//   1168: 4096 x 4096 62.3 / 61.2, 1504: 1000 x 8192 57.8 / 57.7, 2190: 4096 x 7680 84.6 / 99.3,
+//   f16 (one block of columns, two 131) 101 / 118
+//   rank 256, none held  4096 x 7680 221 / 180
+constexpr int64_t kLongPieces = 1536;
 constexpr int64_t kPartPieces = 512;
 
 template <int TK, int TR>
@@ -880,11 +888,16 @@ hipError_t launch_tiles(const AdaptArgs& a, hipStream_t stream) {
   // 4096 rows x 7680 (2190 pieces of 256 columns) once / twice / three times 49.8 / 48.6 /
   // 50.4 us, 2000 x 2560 (350 pieces) 22.2 / 25.7 / 30.5, 1 x 7680 8.1, four times 10.7.
   const int64_t all = (int64_t)tiles * ((a.n + kBlockCols - 1) / kBlockCols);
-  const int col_blocks = TR == 1 && all >= 4096 ? 4 : all >= 1536 ? 2 : 1;
+  const bool long_steps = TR > 1 && a.rank > 64 && a.rank <= 32 * kLongSteps && all >= kLongPieces;
+  const int col_blocks = TR == 1 && all >= 4096 ? 4 : all < 1536 || (long_steps && TK == CK_F16) ? 1 : 2;
   const unsigned cols = (unsigned)((a.n + kBlockCols * col_blocks - 1) / (kBlockCols * col_blocks));
-  const int parts = TR > 1 && (a.rank > 64 || all < kPartPieces) ? TR : 1;
-  const size_t planes = (size_t)kPlanes * 16 * (TR / parts) * ((a.rank + 31) / 32 * 32 + 8) * 2;
+  const int parts = TR > 1 && (a.rank > 64 ? !long_steps : all < kPartPieces) ? TR : 1;
+  const size_t planes = (size_t)kPlanes * 16 * (TR / parts) * ((long_steps ? kLongSteps : (a.rank + 31) / 32) * 32 + 8) * 2;
   const auto up = parts > 1 ? up_kernel<TK, 1>(a) : up_kernel<TK, TR>(a);
+  if (planes > 40 * 1024) {  // (with the static part past the 64 KiB that need no asking)
+    e = hipFuncSetAttribute((const void*)up, hipFuncAttributeMaxDynamicSharedMemorySize, 64 * 1024);
+    if (e != hipSuccess) return e;
+  }
   hipLaunchKernelGGL(up, dim3(cols, tiles, (unsigned)parts), dim3(kThreads), planes, stream, a, col_blocks);
   return hipGetLastError();
 }

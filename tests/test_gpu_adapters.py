@@ -105,6 +105,13 @@ def test_adapters_middle_batches(m, count):
     Case(m, 1024, 300, count, 8, "f16", "f32", ids=[0]).check()
 
 
+@pytest.mark.parametrize("rank,kind,base", [(72, "bf16", "f32"), (96, "f16", "f16"), (104, "f16", "f32"), (128, "bf16", "bf16"),
+                                            (128, "f16", None)])
+def test_adapters_long_ranks_of_many_rows(rank, kind, base):
+    """Whole tiles of 64 rows with a long rank."""
+    Case(700, 64, 17003, 12, rank, kind, base, ranks=[rank, rank - 3, 33, 64, 7, rank]).check("f32")
+
+
 @pytest.mark.parametrize("m", [16, 250, 600])
 def test_adapters_ids(m):
     """One adapter for all, none at all, runs, every row its own, ids out of range."""
