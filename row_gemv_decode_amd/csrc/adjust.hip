@@ -144,11 +144,13 @@ __global__ __launch_bounds__(kThreadsMax) void adjust_kernel(AdjustArgs g) {
   int held = 0, prompt = 0;
   Penalties pen = {1.0f, 0.0f, 0.0f};
   const int64_t bias_row = r * g.biases;
-  auto bias_off = [&](int i) -> int64_t {  // -1: not in the segment
-    const int64_t off = token_at(g.bias_ids, bias_row + i, g.tokens64) - first;
-    return off < len ? off : -1;
+  // a listed id's place in the segment, -1 for every id that does not lie in it (compared
+  // before anything is subtracted or cut: a list may be filled up with any id)
+  auto bias_off = [&](int i) -> int {
+    const int64_t id = token_at(g.bias_ids, bias_row + i, g.tokens64);
+    return id >= first && id < (int64_t)first + len ? (int)(id - first) : -1;
   };
-  int64_t my_bias = -1;
+  int my_bias = -1;
   float my_value = 0.0f;
   if constexpr (HISTORY) {
 #pragma unroll
@@ -232,13 +234,13 @@ __global__ __launch_bounds__(kThreadsMax) void adjust_kernel(AdjustArgs g) {
       }
     }
     for (int i = tid; BIASES && i < biases; i += threads) {
-      const int64_t off = i == tid ? my_bias : i < g.biases ? bias_off(i) : -1;
+      const int off = i == tid ? my_bias : i < g.biases ? bias_off(i) : -1;
       if (i < held_biases) {
-        bias_off_s[i] = (int)off;
+        bias_off_s[i] = off;
         bias_s[i] = i == tid ? my_value : i < g.biases ? g.bias_values[bias_row + i] : 0.0f;
       }
       if (off >= 0) {
-        const At at((int)off);
+        const At at(off);
         biased_s = 1;
         if ((at.of(atomicOr(&table_s[at.word], kBiased << at.shift)) & kBiased) != 0) twice_s = 1;
       }
@@ -317,9 +319,8 @@ __global__ __launch_bounds__(kThreadsMax) void adjust_kernel(AdjustArgs g) {
     __syncthreads();
     const bool twice = twice_s != 0;
     for (int i = tid; i < g.biases; i += threads) {
-      const int64_t o = i < held_biases ? bias_off_s[i] : bias_off(i);
-      if (o < 0) continue;
-      const int off = (int)o;
+      const int off = i < held_biases ? bias_off_s[i] : bias_off(i);
+      if (off < 0) continue;
       const At at(off);
       // the first to take the flag away writes the token's logit
       const uint32_t entry = at.of(atomicAnd(&table_s[at.word], ~(kBiased << at.shift)));
@@ -341,7 +342,7 @@ __global__ __launch_bounds__(kThreadsMax) void adjust_kernel(AdjustArgs g) {
         }
 #pragma unroll 1
         for (int k = held_biases; k < g.biases; ++k)
-          if (bias_off(k) == o) b += g.bias_values[bias_row + k];
+          if (bias_off(k) == off) b += g.bias_values[bias_row + k];
       }
       const float x = penalised(value_at<XK>(x_row, off), entry, pen) + b;
       store_out<OK>(o_row, off, allowed_at(mask, off) ? x : -INFINITY);

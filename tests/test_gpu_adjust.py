@@ -155,6 +155,40 @@ def test_adjust_biases_are_added_in_the_lists_order():
     assert out[0, 7] == 0.0 and out[1, 7] == 1.0 and out[0, 3] == 2.0
 
 
+def far_ids(kind, near, V):
+    """Ids outside 0 .. V - 1 that have the low 32 bits of a token's place in some segment,
+    or that leave their type's range when a segment's first token is taken from them."""
+    if kind == np.int32:
+        return [-(1 << 31), (1 << 31) - 1, -1, V, -V, -(1 << 31) + near]
+    high = [h << s for s in (32, 33, 40, 62) for h in (1, -1)] + [-(1 << 63)]
+    return [h + t for h in high for t in (0, near)] + [(1 << 63) - 1, -1, V, (1 << 31) + near, -(1 << 31) + near]
+
+
+@pytest.mark.parametrize("m,V", [(2, 500), (2, 9973), (40, 40000)])
+@pytest.mark.parametrize("biases", [60, 1100])
+@pytest.mark.parametrize("kind", [np.int32, np.int64])
+def test_adjust_ids_far_outside_the_vocabulary(kind, biases, m, V):
+    """Any id outside the vocabulary fills a list up and does not count in a history,
+    however far it lies: tokens 0 and `near` listed beside them, once and (row 1) twice,
+    before and behind them, in lists that LDS holds and longer ones."""
+    for near in (7, V - 3):
+        far = far_ids(kind, near, V)
+        a = {"bias_ids": np.resize(np.array(far, kind), (m, biases)),
+             "bias_values": np.random.default_rng(V).uniform(1, 8, (m, biases)).astype(np.float32)}
+        a["bias_ids"][:, 3], a["bias_ids"][::3, biases - 1] = near, 0
+        a["bias_ids"][1, biases // 2], a["bias_ids"][1, biases - 2] = near, 0
+        a["bias_ids"][m - 1, 0], a["bias_ids"][m - 1, 3] = near, -(1 << 31)
+        for history in (False, True):
+            if history:
+                a["history"] = np.resize(np.array(far + [near], kind), (m, 150))
+                a["frequency"] = np.full(m, 0.25, np.float32)
+            X = logits_of(m, V, "f32", 5)
+            rules = sk.LogitRules(m, V, **device(a))
+            compare(sk.adjust_logits(X[0], rules), X[1], a, "f32")
+            y = X[0].clone()
+            compare(sk.adjust_logits(y, rules, out=y), X[1], a, "f32")
+
+
 def test_adjust_optional_rules():
     """Every rule by itself; none at all gives the logits."""
     m, V = 4, 3001
