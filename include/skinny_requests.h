@@ -34,9 +34,9 @@ extern "C" {
  *   y            = h * weight / sqrt(mean(h^2) + eps)       in fp32
  *   out          = y, rounded to its type (nearest even)
  *   scales_g     = max(max |y_j| over group g / 448, 2^-126)
- *   q_j          = y_j / scales_g, rounded to 8 bits (e4m3, nearest even): q_j *
- *                  scales_g stands for y_j
- * The norm is that of the unrounded sum h, and q is rounded once, from fp32.
+ *   q_j          = y_j / scales_g in fp32, rounded to 8 bits (e4m3, nearest even):
+ *                  q_j * scales_g stands for y_j
+ * The norm is that of the unrounded sum h, and q is rounded from the unrounded y.
  * Groups are `group` (32, 64 or 128) consecutive columns, the row's last one
  * what is left, or the whole row (group 0).  A row's results do not depend on
  * the other rows: they are the same bits at every m.  mean(h^2) is held in

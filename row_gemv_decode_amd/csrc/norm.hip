@@ -21,10 +21,11 @@
 // copy reaches), 2000 x 7681 bf16 23.3 (5.3), 1983 x 896 bf16 on fp32 sums 5.8,
 // 1 x 5120 2.8.
 //
-// q is y times the reciprocal of its scale: the quotient rounded once more,
-// 2^-23 off at the most before it is rounded to 8 bits.  |y / s| is at most
-// 448 (1 + 2^-22), which rounds to 448, so nothing has to be clamped and a NaN
-// stays one.
+// q is the fp32 quotient y / s, rounded to 8 bits.  A product with 1 / s alone, 2^-23
+// off, moved 184 of 84 million codes across a border; the remainder's correction costs
+// two instructions per value (16384 x 5120 113 us with and without, 8192 x 8192 in groups
+// of 32 46.6 -> 47.7; divisions 55.6).  |y / s| is at most 448 (1 + 2^-22), which rounds
+// to 448, so nothing has to be clamped and a NaN stays one.
 #include "requests.h"
 #include "vector_io.h"
 #include "wave_ops.h"
@@ -144,13 +145,26 @@ __device__ __forceinline__ float max8(const float (&y)[8]) {
 
 __device__ __forceinline__ float scale_of(float top) { return fmaxf(top / kTop8, kLeastScale); }
 
-__device__ __forceinline__ void store8_q(uint8_t* row, int e0, int d, const float (&y)[8], float inv) {
+// y / s for inv = 1 / s: the product with inv, less what it misses y by, which an fma
+// gives exactly (Markstein 1990) while y is above 2^-103: below, the remainder's last
+// bits are lost and the quotient may be that of the product.  The signs keep that of a zero.
+__device__ __forceinline__ float quotient(float y, float s, float inv) {
+  const float q = y * inv;
+  const float past = __builtin_fmaf(q, s, -y);
+  return __builtin_fmaf(-past, inv, q);
+}
+
+__device__ __forceinline__ void store8_q(uint8_t* row, int e0, int d, const float (&y)[8], float s) {
+  const float inv = 1.0f / s;
   uint32_t w[2];
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
+    float t[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) t[e] = quotient(y[4 * q + e], s, inv);
     int v = 0;
-    v = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * q] * inv, y[4 * q + 1] * inv, v, false);
-    v = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * q + 2] * inv, y[4 * q + 3] * inv, v, true);
+    v = __builtin_amdgcn_cvt_pk_fp8_f32(t[0], t[1], v, false);
+    v = __builtin_amdgcn_cvt_pk_fp8_f32(t[2], t[3], v, true);
     w[q] = (uint32_t)v;
   }
   if (e0 + 8 <= d) {
@@ -253,10 +267,10 @@ __global__ __launch_bounds__(BLOCK ? 1024 : 256) void norm_kernel(NormArgs g) {
   }
   if (p.q == nullptr) return;
   if (row_scale) {
-    const float s = scale_of(row_top * inv), si = 1.0f / s;
+    const float s = scale_of(row_top * inv);
     if (active) {
 #pragma unroll
-      for (int c = 0; c < CH; ++c) store8_q(p.q, (c * step + place) * 8, d, h[c], si);
+      for (int c = 0; c < CH; ++c) store8_q(p.q, (c * step + place) * 8, d, h[c], s);
       if (place == 0) p.scales[0] = s;
     }
   } else {
@@ -267,7 +281,7 @@ __global__ __launch_bounds__(BLOCK ? 1024 : 256) void norm_kernel(NormArgs g) {
       const int e0 = (c * step + place) * 8;
       const float s = scale_of(lanes_reduce<true>(top[c], mine) * inv);
       if (active) {
-        store8_q(p.q, e0, d, h[c], 1.0f / s);
+        store8_q(p.q, e0, d, h[c], s);
         if ((place & (mine - 1)) == 0 && e0 < d) p.scales[e0 / g.group] = s;
       }
     }
@@ -327,7 +341,7 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(NormArgs g) {
         s = scale_of(lanes_reduce<true>(group_top, g.group >> 3) * inv);
         if ((e0 & (g.group - 1)) == 0 && e0 < d) p.scales[e0 / g.group] = s;
       }
-      store8_q(p.q, e0, d, y, 1.0f / s);
+      store8_q(p.q, e0, d, y, s);
     }
   }
 }

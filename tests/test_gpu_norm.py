@@ -87,6 +87,21 @@ def test_norm_scales(d, group):
     check(2, d, "f16", "f16", "f16", "f16", group)
 
 
+@pytest.mark.parametrize("m,d,group", [(2048, 5120, 0), (2048, 5120, 64), (20000, 512, 32), (250, 40000, 0), (250, 40000, 128)])
+def test_norm_codes_are_the_quotients(m, d, group):
+    """Every code is y / scale in fp32, rounded to 8 bits: a quotient off by a step in 24
+    bits shows as codes on the wrong side of a border, up to tens in ten million."""
+    gen = torch.Generator(device="cuda").manual_seed(m + group)
+    x = torch.randn((m, d), generator=gen, device="cuda")
+    x[:, 7] = -0.0
+    w = torch.rand(d, generator=gen, device="cuda") + 0.5
+    got = sk.rms_norm(x, w, out_dtype=torch.float32, quant=group)
+    y, s = got.out.cpu().numpy(), got.scales.cpu().numpy()
+    quot = torch.from_numpy(y / np.repeat(s, group or d, axis=1)[:, :d])
+    want = quot.to(torch.float8_e4m3fn).view(torch.uint8)
+    assert int((got.q.cpu().view(torch.uint8) != want).sum()) == 0
+
+
 @pytest.mark.parametrize("ok", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("xk,rk,wk", [("f32", "f32", "f32"), ("f32", None, None), ("f16", "f16", "f16"), ("f16", "f32", "f32"),
                                       ("bf16", "bf16", "bf16"), ("bf16", "f32", "bf16"), ("bf16", None, "f32"), ("f32", "bf16", "f16"), ("f32", "f16", "f32"), ("f16", "bf16", "bf16"),
