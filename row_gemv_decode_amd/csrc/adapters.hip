@@ -54,7 +54,7 @@ __device__ __forceinline__ int rank_of(const AdaptArgs& g, int a) {
 // hold: a wave counts them in LDS of its own.
 __device__ __forceinline__ bool later_tile(const AdaptArgs& g, int later, const int (&a)[kAdaptDirectRows / 64], int& adapter,
                                            int& before) {
-  __shared__ uint32_t counts_s[kWaves][kAdaptDirectRows];
+  __shared__ uint32_t counts_s[kWaves][kAdaptDirectRows] __attribute__((aligned(16)));
   const int lane = threadIdx.x & 63;
   uint32_t* counts = counts_s[threadIdx.x >> 6];
 #pragma unroll
@@ -555,7 +555,7 @@ constexpr bool holds_next() { return HELD > 0 && (HELD < kLongSteps || TK == CK_
 // adapter's rank.
 template <int TK, int TR, int BK, int HELD>
 __global__ __launch_bounds__(kThreads) void adapter_up_kernel(AdaptArgs g, int col_blocks) {
-  extern __shared__ uint16_t planes_s[];  // [planes][16 TR][pitch]
+  extern __shared__ uint16_t planes_s[] __attribute__((aligned(16)));  // [planes][16 TR][pitch]
   __shared__ uint32_t rows_s[16 * TR];
   __shared__ u32x4 slots_s[kWaves][64 * kColTiles];
   const int tid = threadIdx.x, lane = tid & 63;

@@ -117,7 +117,7 @@ constexpr int stream_elems() { return XK == CK_F32 || OK == CK_F32 ? 4 : 8; }
 // TABLE: 0 (mask only), or an entry's bits; HISTORY, BIASES: which of the two there are
 template <int XK, int OK, bool IN_PLACE, int TABLE, bool HISTORY, bool BIASES>
 __global__ __launch_bounds__(kThreadsMax) void adjust_kernel(AdjustArgs g) {
-  extern __shared__ uint32_t table_s[];
+  extern __shared__ uint32_t table_s[] __attribute__((aligned(16)));  // the table, then the first biases
   __shared__ int biased_s, twice_s;
   constexpr int CW = TABLE == 0 ? 16 : TABLE;
   using At = Entry<CW>;
