@@ -51,7 +51,11 @@ class Step:
         self.vocab, self.d = vocab, d
 
     def start(self, prompts):
-        """The requests' prompts, lists of token ids."""
+        """The requests' prompts, lists of token ids, of at least one token and no more than
+        the histories' room."""
+        room = self.history.shape[1]
+        if len(prompts) != len(self.lengths) or any(not 1 <= len(p) <= room or min(p) < 0 or max(p) >= self.vocab for p in prompts):
+            raise ValueError(f"takes {len(self.lengths)} prompts of 1 to {room} tokens below {self.vocab}")
         for i, p in enumerate(prompts):
             self.history[i, :len(p)] = torch.tensor(p, dtype=torch.int64, device=self.history.device)
             self.lengths[i] = self.prompts[i] = len(p)
@@ -77,12 +81,16 @@ class Step:
 
     def step(self):
         """The most likely tokens and their log probabilities, appended to the
-        histories."""
+        histories.  A history whose room is used up stays as it is, also where a captured
+        step is replayed."""
         _, logits = self.logits()
         tokens = logits.argmax(1)
         scores = sk.token_logprobs(logits, tokens)
-        self.history.scatter_(1, self.lengths.long().unsqueeze(1), tokens.unsqueeze(1))
-        self.lengths += 1
+        room = self.history.shape[1]
+        place = self.lengths.long().clamp(max=room - 1).unsqueeze(1)
+        free = self.lengths < room
+        self.history.scatter_(1, place, torch.where(free, tokens, self.history.gather(1, place).squeeze(1)).unsqueeze(1))
+        self.lengths += free
         return tokens, scores.logprob
 
 
@@ -91,8 +99,9 @@ def main():
     ap.add_argument("--requests", type=int, default=6)
     ap.add_argument("--steps", type=int, default=8)
     a = ap.parse_args()
-    s = Step(a.requests)
-    s.start([[17 * i + 1, 5, 9] for i in range(a.requests)])
+    prompts = [[17 * i + 1, 5, 9] for i in range(a.requests)]
+    s = Step(a.requests, room=max(len(p) for p in prompts) + a.steps)
+    s.start(prompts)
     s.adapters.copy_(torch.arange(a.requests, device="cuda") % 5 - 1)
     s.repetition.fill_(1.2)
     s.presence.fill_(0.3)

@@ -93,3 +93,36 @@ def test_a_captured_step_replays_the_eager_one(example):
         torch.cuda.synchronize()
         assert torch.equal(tokens, want_tokens) and torch.equal(lp, want_lp)
         assert torch.equal(s.history, e.history) and torch.equal(s.lengths, e.lengths)
+
+
+def test_full_histories_stay_as_they_are(example):
+    """Steps past the histories' room, eager and replayed: what is held stays."""
+    s = example.Step(3, d=512, vocab=5003, room=6)
+    s.start([[5, 9, 2], [7], [1, 2, 3, 4, 5, 6]])
+    s.step()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        s.step()
+    assert s.lengths.tolist() == [4, 2, 6]
+    held = s.history.clone()
+    for n in ([5, 3, 6], [6, 4, 6], [6, 5, 6], [6, 6, 6], [6, 6, 6]):
+        g.replay()
+        assert s.lengths.tolist() == n and s.history[2].tolist() == [1, 2, 3, 4, 5, 6]
+    assert torch.equal(s.history[0, :4], held[0, :4]) and torch.equal(s.history[1, :2], held[1, :2])
+    full = s.history.clone()
+    s.step()
+    assert torch.equal(s.history, full) and s.lengths.tolist() == [6, 6, 6]
+
+
+def test_prompts_that_do_not_fit_are_refused(example):
+    s = example.Step(2, d=512, vocab=5003, room=4)
+    for bad in ([[1, 2]], [[1], []], [[1], [1, 2, 3, 4, 5]], [[1], [2], [3]], [[1], [5003]], [[-1], [1]]):
+        with pytest.raises(ValueError):
+            s.start(bad)
+
+
+def test_example_runs_more_steps_than_its_usual_room(example, monkeypatch, capsys):
+    monkeypatch.setattr(example.sys, "argv", ["decode_requests.py", "--requests", "2", "--steps", "70"])
+    example.main()
+    lines = capsys.readouterr().out.splitlines()
+    assert len(lines) == 2 and all(len(line.split("[")[1].split(",")) == 73 for line in lines)
