@@ -15,7 +15,8 @@
  * synchronise and only enqueue kernels on `stream`, so they can be captured
  * in a HIP graph; every argument is checked on the host before any HIP call,
  * and on an error nothing is enqueued.  Unless stated otherwise non-finite
- * inputs are outside the contract.  A row stride of 0 means dense rows.
+ * inputs are outside the contract.  A row stride of 0 means dense rows; strides go
+ * up to 2^40 elements, and rows times stride up to 2^60.
  */
 #ifndef SKINNY_REQUESTS_H
 #define SKINNY_REQUESTS_H

@@ -13,8 +13,11 @@ using namespace skinny;
 
 namespace {
 
-constexpr int64_t kMaxStride = 1LL << 40;
 constexpr int64_t kMaxLen = 1 << 24;
+
+// a stride that no memory holds `rows` rows of (their bytes, and so the spans below, stay
+// within 2^62)
+bool too_far(int64_t rows, int64_t ld) { return ld > (1LL << 40) || ld > (1LL << 60) / rows; }
 
 int64_t round16(int64_t b) { return (b + 15) / 16 * 16; }
 
@@ -74,7 +77,7 @@ skinny_status skinny_rms_norm_run(int64_t m, int64_t d, const void* x, int64_t l
   const bool used[] = {true, residual != nullptr, residual_out != nullptr, out != nullptr, q != nullptr};
   for (int i = 0; i < 5; ++i) {
     if (!used[i] || *strides[i] == 0) *strides[i] = d;
-    if (*strides[i] > kMaxStride) return SKINNY_ERR_INVALID_ARG;
+    if (too_far(m, *strides[i])) return SKINNY_ERR_INVALID_ARG;
     if (*strides[i] < d) return SKINNY_ERR_SHAPE;
   }
   const int64_t xs = size_of(x_dtype), rs = size_of(r_dtype), os = size_of(out_dtype);
@@ -138,7 +141,7 @@ skinny_status skinny_adapters_run(const skinny_adapters* adapters, int64_t m, co
   if (ldx == 0) ldx = d.k;
   if (ldb == 0 || base == nullptr) ldb = d.n;
   if (ldo == 0) ldo = d.n;
-  if (ldx > kMaxStride || ldb > kMaxStride || ldo > kMaxStride) return SKINNY_ERR_INVALID_ARG;
+  if (too_far(m, ldx) || too_far(m, ldb) || too_far(m, ldo)) return SKINNY_ERR_INVALID_ARG;
   if (ldx < d.k || ldb < d.n || ldo < d.n) return SKINNY_ERR_SHAPE;
   const int64_t bs = size_of(base_dtype), os = size_of(out_dtype);
   if (ldx % 8 != 0 || !aligned(x, 16) || !aligned(d.A, 16) || !aligned(d.B, 16) || !aligned(d.ranks, 4) ||
@@ -210,7 +213,7 @@ skinny_status skinny_adjust_logits_run(int64_t m, int64_t vocab, const void* log
   const int64_t ldm = u.ldm == 0 || !mask ? words : u.ldm;
   if (ld == 0) ld = vocab;
   if (ldo == 0) ldo = vocab;
-  if (ld > kMaxStride || ldo > kMaxStride || ldh > kMaxStride || ldm > kMaxStride) return SKINNY_ERR_INVALID_ARG;
+  if (too_far(m, ld) || too_far(m, ldo) || too_far(m, ldh) || too_far(mask ? u.masks : 1, ldm)) return SKINNY_ERR_INVALID_ARG;
   if (ld < vocab || ldo < vocab || ldh < u.history_len || (mask && ldm < words) ||
       (mask && u.mask_rows == nullptr && u.masks < m))
     return SKINNY_ERR_SHAPE;

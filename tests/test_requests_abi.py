@@ -168,3 +168,20 @@ def test_adjust_refusals(kw, status):
 def test_adjust_nothing_in_place_is_no_launch():
     """No rule, in place: done before any HIP call."""
     assert adjust_run(out=at(1), ot=sk.BF16, **NO_HISTORY, **NO_BIAS, **NO_MASK) == sk.OK
+
+
+FAR = [(1 << 23, 1 << 40), ((1 << 23) + 1, 1 << 40), (1 << 30, (1 << 30) + 1), ((1 << 29) + 1, 1 << 35), (1 << 30, 1 << 40)]
+
+
+@pytest.mark.parametrize("m,ld", FAR)
+@pytest.mark.parametrize("name", ["ldx", "ldr", "ldro", "ldo", "ldq"])
+def test_norm_rows_further_apart_than_memory_are_refused(name, m, ld):
+    """Their bytes pass 63 bits, where the spans that must not overlap came out as any."""
+    assert norm_run(m=m, x=at(1), r=at(2), ro=at(3), out=at(4), q=at(5), **{name: ld}) == sk.ERR_INVALID_ARG
+    assert norm_run(m=m, r=None, ro=None, q=None, s=None, ldx=ld, out=at(1) + 128, ldo=64) == sk.ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("m,ld", FAR)
+def test_adjust_rows_further_apart_than_memory_are_refused(m, ld):
+    for kw in (dict(ld=ld), dict(ldo=ld), dict(ldh=ld), dict(ldm=ld, masks=m), dict(ld=ld, out=at(1) + 4096)):
+        assert adjust_run(**{"m": m, "vocab": 1000, **NO_BIAS, **kw}) == sk.ERR_INVALID_ARG
