@@ -109,9 +109,10 @@ typedef struct skinny_adapters {
  *              its element; may be base itself (the same rows and type), and
  *              overlaps nothing else
  *   workspace  device scratch of at least skinny_adapters_workspace_size bytes,
- *              16-byte aligned, of any contents.  Two runs in flight at once
- *              must not share one; a run is up to three launches over it, so two
- *              host threads must not enqueue runs on one workspace at once. */
+ *              16-byte aligned, of any contents, apart from every operand.  Two runs
+ *              in flight at once must not share one; a run is up to three launches
+ *              over it, so two host threads must not enqueue runs on one workspace
+ *              at once. */
 SKINNY_API skinny_status skinny_adapters_workspace_size(const skinny_adapters* adapters, int64_t m, size_t* bytes);
 SKINNY_API skinny_status skinny_adapters_run(const skinny_adapters* adapters, int64_t m, const void* x, int64_t ldx,
                                              const void* ids, int32_t ids64, const void* base, int64_t ldb,

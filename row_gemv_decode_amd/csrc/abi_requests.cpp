@@ -154,11 +154,12 @@ skinny_status skinny_adapters_run(const skinny_adapters* adapters, int64_t m, co
                      {d.ranks, 1, d.count, d.count, 4},
                      {d.scaling, 1, d.count, d.count, 4},
                      {ids, 1, m, m, ids64 != 0 ? 8 : 4}};
-  for (const Rows& r : in)
-    if (meet(to, r)) return SKINNY_ERR_INVALID_ARG;
-  const bool same = base == out && ldb == ldo && base_dtype == out_dtype;
-  if (!same && meet(to, Rows{base, m, ldb, d.n, bs})) return SKINNY_ERR_INVALID_ARG;
   const AdaptSizes s = adapt_sizes(d, m);
+  const Rows add = {base, m, ldb, d.n, bs}, ws = {workspace, 1, s.bytes, s.bytes, 1};
+  for (const Rows& r : in)
+    if (meet(to, r) || meet(ws, r)) return SKINNY_ERR_INVALID_ARG;
+  const bool same = base == out && ldb == ldo && base_dtype == out_dtype;
+  if ((!same && meet(to, add)) || meet(ws, add) || meet(ws, to)) return SKINNY_ERR_INVALID_ARG;
   if (workspace == nullptr || workspace_bytes < (size_t)s.bytes) return SKINNY_ERR_WORKSPACE;
   if (!aligned(workspace, 16)) return SKINNY_ERR_ALIGNMENT;
   AdaptArgs a{};

@@ -185,3 +185,10 @@ def test_norm_rows_further_apart_than_memory_are_refused(name, m, ld):
 def test_adjust_rows_further_apart_than_memory_are_refused(m, ld):
     for kw in (dict(ld=ld), dict(ldo=ld), dict(ldh=ld), dict(ldm=ld, masks=m), dict(ld=ld, out=at(1) + 4096)):
         assert adjust_run(**{"m": m, "vocab": 1000, **NO_BIAS, **kw}) == sk.ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("i", [1, 2, 3, 4, 5, 6, 7, 8])
+def test_adapters_workspace_apart_from_every_operand(i):
+    """A, B, ranks, scaling, x, ids, base, out: the workspace is written before they are read."""
+    assert adapt_run(ws=at(i)) == sk.ERR_INVALID_ARG
+    assert adapt_run(ws=at(i) - 64) == sk.ERR_INVALID_ARG
