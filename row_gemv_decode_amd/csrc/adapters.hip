@@ -872,6 +872,14 @@ auto up_kernel(const AdaptArgs& a) {
 constexpr int64_t kLongPieces = 1536;
 constexpr int64_t kPartPieces = 512;
 
+// A workgroup gets more than 64 KiB of LDS, the launch's part (at most 64 here) and the
+// kernel's own, on request.  The request is the same in every call: threads share it.
+template <typename F>
+hipError_t ask_for_lds(F fn, size_t launch_bytes, size_t own_bytes) {
+  if (launch_bytes + own_bytes <= 64 * 1024) return hipSuccess;
+  return hipFuncSetAttribute((const void*)fn, hipFuncAttributeMaxDynamicSharedMemorySize, 64 * 1024);
+}
+
 template <int TK, int TR>
 hipError_t launch_tiles(const AdaptArgs& a, hipStream_t stream) {
   const unsigned tiles = (unsigned)a.max_tiles;
@@ -881,8 +889,10 @@ hipError_t launch_tiles(const AdaptArgs& a, hipStream_t stream) {
   const size_t lds = (size_t)kWaves * entries * 64 * sizeof(f32x4);
   const auto down = nr == 1   ? adapter_down_kernel<TK, TR, 1>
                     : nr == 2 ? adapter_down_kernel<TK, TR, 2> : adapter_down_kernel<TK, TR, 4>;
+  hipError_t e = ask_for_lds(down, lds, 64 * sizeof(int));
+  if (e != hipSuccess) return e;
   hipLaunchKernelGGL(down, dim3(blocks, tiles), dim3(kThreads), lds, stream, a);
-  hipError_t e = hipGetLastError();
+  e = hipGetLastError();
   if (e != hipSuccess) return e;
   // Columns of a workgroup: 256 times what leaves about four workgroups for each CU.
   // 4096 rows x 7680 (2190 pieces of 256 columns) once / twice / three times 49.8 / 48.6 /
@@ -894,10 +904,8 @@ hipError_t launch_tiles(const AdaptArgs& a, hipStream_t stream) {
   const int parts = TR > 1 && (a.rank > 64 ? !long_steps : all < kPartPieces) ? TR : 1;
   const size_t planes = (size_t)kPlanes * 16 * (TR / parts) * ((long_steps ? kLongSteps : (a.rank + 31) / 32) * 32 + 8) * 2;
   const auto up = parts > 1 ? up_kernel<TK, 1>(a) : up_kernel<TK, TR>(a);
-  if (planes > 40 * 1024) {  // (with the static part past the 64 KiB that need no asking)
-    e = hipFuncSetAttribute((const void*)up, hipFuncAttributeMaxDynamicSharedMemorySize, 64 * 1024);
-    if (e != hipSuccess) return e;
-  }
+  e = ask_for_lds(up, planes, kWaves * 64 * kColTiles * sizeof(u32x4) + 16 * TR * sizeof(uint32_t));
+  if (e != hipSuccess) return e;
   hipLaunchKernelGGL(up, dim3(cols, tiles, (unsigned)parts), dim3(kThreads), planes, stream, a, col_blocks);
   return hipGetLastError();
 }
