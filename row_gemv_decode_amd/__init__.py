@@ -905,7 +905,7 @@ _new_norm = tuple.__new__  # (a named tuple's own constructor takes twice as lon
 def _input_stride(where, name, t, stream):
     """_input_rows, with 0 for the stride of rows that lie one behind the other (the
     library's word for dense rows), which costs the host less."""
-    return (t, 0) if t.is_contiguous() else _input_rows(where, name, t, stream)
+    return (t, 0) if t.is_contiguous() and t.dim() == 2 else _input_rows(where, name, t, stream)
 
 
 def _output_stride(where, name, t, index, shape, dtype):

@@ -88,6 +88,18 @@ def test_outputs_that_share_memory_are_refused(lib):
     assert lib.calls == []
 
 
+@pytest.mark.parametrize("shape", [(16,), (2, 3, 16), ()])
+def test_inputs_that_are_no_matrices_are_refused(lib, shape):
+    x, ids = torch.zeros(shape, dtype=half), torch.zeros(3, dtype=torch.int32)
+    for name, call in (("x", lambda: sk.rms_norm(x)), ("residual", lambda: sk.rms_norm(torch.zeros((3, 16)), residual=x)),
+                       ("x", lambda: sk.add_adapters(x, adapters(), ids)),
+                       ("base", lambda: sk.add_adapters(torch.zeros((3, 16), dtype=half), adapters(), ids, x)),
+                       ("logits", lambda: sk.adjust_logits(x, sk.LogitRules(3, 16)))):
+        with pytest.raises(ValueError, match=f"{name} must be a matrix"):
+            call()
+    assert lib.calls == []
+
+
 def test_norm_arguments(lib):
     x, r = torch.zeros((3, 40), dtype=half)[:, :32], torch.zeros((3, 32))
     got = sk.rms_norm(x, torch.ones(32), 1e-5, residual=r, residual_out=r, quant=0)
