@@ -889,7 +889,7 @@ hipError_t launch_tiles(const AdaptArgs& a, hipStream_t stream) {
   const size_t lds = (size_t)kWaves * entries * 64 * sizeof(f32x4);
   const auto down = nr == 1   ? adapter_down_kernel<TK, TR, 1>
                     : nr == 2 ? adapter_down_kernel<TK, TR, 2> : adapter_down_kernel<TK, TR, 4>;
-  hipError_t e = ask_for_lds(down, lds, 64 * sizeof(int));
+  hipError_t e = ask_for_lds(down, lds, TR > 1 ? 256 : 4352);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(down, dim3(blocks, tiles), dim3(kThreads), lds, stream, a);
   e = hipGetLastError();
