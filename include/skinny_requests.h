@@ -42,12 +42,14 @@ extern "C" {
  * what is left, or the whole row (group 0).  A row's results do not depend on
  * the other rows: they are the same bits at every m.  mean(h^2) is held in
  * fp32: rows whose sum of squares overflows it (|h| near 2^63) come out as 0.
- * A NaN or infinity stays in its row.
+ * A NaN or infinity stays in its row.  The 8-bit output is for an 8-bit product of
+ * the caller's own: this library's products take 16-bit rows and block formats.
  *   m, d          1 <= m <= 2^31, 1 <= d <= 2^24
  *   x             [m][ldx] SKINNY_F32, SKINNY_F16 or SKINNY_BF16 (x_dtype)
  *   residual      [m][ldr] of any of these types (r_dtype), or NULL
  *   weight        [d] of any of them (w_dtype), or NULL: 1 everywhere
- *   eps           >= 0, finite; with eps = 0 a row of zeros gives NaN
+ *   eps           >= 0, finite; with eps = 0 a row of zeros gives NaN, and rows of
+ *                 |h| below 2^-63 lose bits of their squares
  *   residual_out  [m][ldro] of r_dtype, or NULL; may be `residual` itself (the
  *                 same rows), not given without a residual
  *   out           [m][ldo] SKINNY_F32, SKINNY_F16 or SKINNY_BF16 (out_dtype), or
@@ -57,7 +59,7 @@ extern "C" {
  *   their element, strides are any from the rows' length on; beyond what is
  *   allowed above, outputs overlap neither one another nor an input, each
  *   counted from its first element to its last (else SKINNY_ERR_INVALID_ARG).
- * All device pointers.  One launch (past 2^31 threads, several). */
+ * All device pointers.  One launch (past 2^30 threads, several). */
 SKINNY_API skinny_status skinny_rms_norm_run(int64_t m, int64_t d, const void* x, int64_t ldx, int32_t x_dtype,
                                              const void* residual, int64_t ldr, int32_t r_dtype, const void* weight,
                                              int32_t w_dtype, float eps, void* residual_out, int64_t ldro, void* out,
@@ -96,9 +98,10 @@ typedef struct skinny_adapters {
  * is not read).  `base` is the shared projection's output, or NULL: 0.  Sums are
  * held in fp32, the inner values A x are carried in 24 bits, and the output is
  * rounded once.  Rows of one adapter are multiplied together wherever they
- * stand, so that an adapter's weights are read once per 16 rows (64 for larger
- * batches) that use it.  A row's results do not depend on the other rows' values; for
- * m <= SKINNY_GEMV_MAX_M they are the same bits at every m.
+ * stand: 16 of them share a read of its weights; past 256 rows 64 share one of A, and
+ * 64 one of B where tiles are many and ranks short (else 16).  A row's results do
+ * not depend on the other rows' values; for m <= SKINNY_GEMV_MAX_M they are the same
+ * bits at every m.
  *   m          1 <= m <= 2^20
  *   x          [m][ldx] of the adapters' dtype; ldx a multiple of 8; 16-byte
  *              aligned
@@ -174,7 +177,7 @@ typedef struct skinny_logit_rules {
  *   history_len  0 .. 2^24; biases 0 .. 2^16
  *   Everything is aligned to its element; strides are any from the rows' length on
  *   (ldm from ceil(vocab / 32) on).
- * All device pointers.  One launch (past 2^31 threads, several). */
+ * All device pointers.  One launch (past 2^30 threads, several). */
 SKINNY_API skinny_status skinny_adjust_logits_run(int64_t m, int64_t vocab, const void* logits, int64_t ld,
                                                   int32_t dtype, const skinny_logit_rules* rules, void* out,
                                                   int64_t ldo, int32_t out_dtype, void* stream);

@@ -6,9 +6,10 @@
 // Two launches.  The first ("down") gives the inner values A x of every row, the
 // second ("up") multiplies them by B and adds the base (a few rows with a small A take
 // both in one, see takes_one).  Rows of one adapter are
-// gathered into tiles, so that 16 rows share one read of the adapter's weights
-// (64 in batches of more than kAdaptDirectRows rows) and a matrix-core step has
-// rows to multiply.  For few rows each workgroup finds its tile in the list of
+// gathered into tiles, so that 16 rows share one read of the adapter's weights and a
+// matrix-core step has rows to multiply.  In batches of more than kAdaptDirectRows rows a
+// tile has 64, which share a read of A, and of B where launch_tiles gives whole tiles to a
+// workgroup.  For few rows each workgroup finds its tile in the list of
 // ids by itself, which costs no more than reading its own id would: a wave
 // compares 64 ids per ballot.  For many, one more launch before the two sorts
 // the rows by adapter.
@@ -18,8 +19,8 @@
 // adds them in order.  Up: the inner values keep 24 bits as three bf16 planes
 // (each the rounded remainder of the last), so that the result is that of fp32
 // products; bf16 weights then take three matrix-core steps, and f16 weights,
-// which are the exact sum of two bf16 numbers, five (the two products of the
-// lowest planes lie below 2^-24).  Planes in f16 would lose small inner values.
+// which are the exact sum of two bf16 numbers, five (the product of the two
+// lowest parts, at most 2^-24, is left out).  Planes in f16 would lose small inner values.
 // The work of both is bound by memory: by latency for a few rows, for many by x
 // in the one and base and out in the other.  Measured (bf16): 4096 rows of 12 prompts
 // with 8 adapters of rank 32, k 5120, n 7680: sort 5 us, down 11 (4.0 TB/s), up 27 (4.7

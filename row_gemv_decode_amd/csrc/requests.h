@@ -60,7 +60,7 @@ struct AdaptArgs {
   int32_t ids64;
   int32_t base_kind, out_kind;
   int32_t splits;        // of k over workgroups
-  int32_t split_len;     // elements of a split, a multiple of 32
+  int32_t split_len;     // elements of a split, a multiple of 256
   float* h;              // [splits][m][rank] partial inner values
   uint32_t* tile_count;  // batches past kAdaptDirectRows: how many tiles there are
   uint32_t* tiles;       // [max_tiles][4]: adapter, rows (0: no tile), rank, scaling
