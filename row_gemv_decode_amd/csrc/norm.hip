@@ -36,6 +36,7 @@ namespace {
 
 constexpr int kNone = -1;  // RK: no residual
 constexpr float kTop8 = 448.0f;  // largest e4m3 value
+constexpr float kLargest = 3.40282347e38f;
 constexpr float kLeastScale = 1.17549435e-38f;  // 2^-126: a group of zeros has codes 0, not NaN
 
 // sum or maximum over `lanes` (8 .. 64) consecutive lanes, in all of them; the
@@ -156,6 +157,7 @@ __device__ __forceinline__ float quotient(float y, float s, float inv) {
 
 __device__ __forceinline__ void store8_q(uint8_t* row, int e0, int d, const float (&y)[8], float s) {
   const float inv = 1.0f / s;
+  s = fminf(s, kLargest);  // (an infinite scale's quotients are 0, or its own NaN: by inv alone)
   uint32_t w[2];
 #pragma unroll
   for (int q = 0; q < 2; ++q) {

@@ -102,6 +102,24 @@ def test_norm_codes_are_the_quotients(m, d, group):
     assert int((got.q.cpu().view(torch.uint8) != want).sum()) == 0
 
 
+@pytest.mark.parametrize("d", [64, 5120, 40000])
+@pytest.mark.parametrize("group", [0, 32])
+def test_norm_codes_beside_an_overflow(d, group):
+    """A value past fp32 makes its group's scale infinite: the others' quotients are 0, its own
+    NaN; other groups and rows do not notice."""
+    x = torch.ones((3, d), device="cuda")
+    x[1, 1] = 1e18
+    w = torch.ones(d, device="cuda")
+    w[1] = 1e25
+    got = sk.rms_norm(x, w, out_dtype=torch.float32, quant=group)
+    y, s = got.out.cpu().numpy(), got.scales.cpu().numpy()
+    assert np.isinf(y[1, 1]) and np.isinf(s[1, 0]) and np.isfinite(s[0]).all()
+    with np.errstate(invalid="ignore"):
+        want = torch.from_numpy(y / np.repeat(s, group or d, axis=1)[:, :d]).to(torch.float8_e4m3fn).float()
+    assert torch.equal(got.q.cpu().float().nan_to_num(nan=1000.0), want.nan_to_num(nan=1000.0))
+    assert int(want.isnan().sum()) == 1 and not want[1, 2:group or d].any()
+
+
 @pytest.mark.parametrize("ok", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("xk,rk,wk", [("f32", "f32", "f32"), ("f32", None, None), ("f16", "f16", "f16"), ("f16", "f32", "f32"),
                                       ("bf16", "bf16", "bf16"), ("bf16", "f32", "bf16"), ("bf16", None, "f32"), ("f32", "bf16", "f16"), ("f32", "f16", "f32"), ("f16", "bf16", "bf16"),
